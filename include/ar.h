@@ -324,6 +324,107 @@ int ar_last_hip_error(void);
 /* AR_VERSION of the loaded library. */
 int ar_version(void);
 
+/* ---- the training step next to the collectives --------------------------------
+ *
+ * AdamW over many tensors at once (the update of the shards that a
+ * ReduceScatter leaves with their owners, before the AllGather of the result)
+ * and the router of a mixture of experts (what decides the AllToAll's
+ * exchange).  As above: device pointers, the caller's stream, argument errors
+ * reported before anything is enqueued, no allocation, no synchronisation;
+ * ar_debug_fail_launch counts these launches too.  None of these calls
+ * touches the byte counters or the choice of implementation.
+ */
+
+/* Elements that share one scale of an 8-bit state. */
+#define AR_ADAMW_BLOCK 256
+
+/* One tensor of an AdamW plan: `count` contiguous elements of each.
+ *   param       AR_FLOAT32 or AR_BFLOAT16, updated in place
+ *   grad        AR_FLOAT32 or AR_BFLOAT16, only read
+ *   copy        bfloat16 working copy of a float32 param, rewritten by every
+ *               step; NULL for none (all tensors of a plan or none)
+ *   exp_avg, exp_avg_sq    m and v: float32 (state_bits 32), or one code a
+ *               element (state_bits 8): int8 for m, uint8 for v
+ *   exp_avg_scale, exp_avg_sq_scale   state_bits 8: ceil(count / 256) float32
+ *               scales each; NULL for 32
+ * An 8-bit state holds m = a q |q| with q in [-127, 127] and v = (r u^2)^2
+ * with u in [0, 255], a and r the scales of the element's block of 256:
+ * a = max |m| / 127^2 and r = sqrt(max v) / 255^2 over the block.  A value
+ * is held as the code nearest to it (for v: nearest in sqrt(v)), a tie as
+ * the smaller code, a positive v never as 0.  The rounding of m and v to
+ * codes is decided in 64 bits and comes after the parameter's update, which
+ * uses their unrounded values.  A block whose m (or v) is not finite gets the
+ * scale NaN, so that all of it reads as NaN. */
+typedef struct {
+  void* param;
+  const void* grad;
+  void* copy;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  size_t count;
+} ar_adamw_tensor_t;
+
+/* Hyperparameters of one step.  `step` counts from 1. */
+typedef struct {
+  double lr;
+  double beta1;
+  double beta2;
+  double eps;
+  double weight_decay;
+  double grad_scale;   /* the gradients' factor, e.g. 1/N for a mean over N ranks */
+  int64_t step;
+  int clip;            /* nonzero: use the factor of the last ar_adamw_grad_norm */
+} ar_adamw_step_t;
+
+/* Bytes of a plan for these tensors; 0 on a bad argument (see ar_adamw_plan)
+ * or when the host runs out of memory. */
+size_t ar_adamw_plan_bytes(const ar_adamw_tensor_t* tensors, int ntensors, ar_dtype_t param_dtype,
+                           ar_dtype_t grad_dtype, int state_bits);
+
+/* Writes the plan of these tensors into `plan` (host memory of
+ * ar_adamw_plan_bytes bytes).  The caller copies all of it to device memory
+ * (16-byte aligned) and passes both to the calls below, which read the host
+ * plan's head and the device copy's tables; the device copy also holds the
+ * norm's partial sums, so calls on one plan must be ordered on one stream (or
+ * by events).  The tensors must stay where they are while the plan is used.
+ * Everything is checked here: AR_ERROR_INVALID_ARGUMENT for NULL or
+ * misaligned pointers, copies of some tensors only or of bfloat16 params,
+ * scales missing (8) or given (32), a written range that overlaps any other
+ * range; AR_ERROR_UNSUPPORTED for other types or state_bits, or more than
+ * 2^32 - 1 tiles of work.  A tensor of count 0 is skipped, its pointers not
+ * looked at. */
+ar_status_t ar_adamw_plan(const ar_adamw_tensor_t* tensors, int ntensors, ar_dtype_t param_dtype,
+                          ar_dtype_t grad_dtype, int state_bits, void* plan, size_t bytes);
+
+/* norm = |grad_scale| sqrt(sum g^2) over all tensors of the plan (products
+ * and sums in 64 bits, in an order fixed by the plan), written as float32 to
+ * the device address `norm` (may be NULL) and kept in the plan, with the
+ * factor c = min(1, max_norm / norm) (1 where norm is NaN) for a following
+ * ar_adamw_step with `clip`.  max_norm may be infinite (no clipping). */
+ar_status_t ar_adamw_grad_norm(const void* plan, void* device_plan, double max_norm,
+                               double grad_scale, float* norm, hipStream_t stream);
+
+/* One AdamW step in place, with G = c grad_scale g (c = 1 without `clip`;
+ * c grad_scale is one float32 factor):
+ *   m' = beta1 m + (1 - beta1) G       v' = beta2 v + (1 - beta2) G^2
+ *   p' = p - lr (weight_decay p + (m' / (1 - beta1^step)) /
+ *                                 (sqrt(v' / (1 - beta2^step)) + eps))
+ * rounded once to param's type, and to bfloat16 in `copy`.  With 32-bit
+ * states in float32, with 8-bit states m' and v' in float64.
+ * AR_ERROR_INVALID_ARGUMENT: a factor that is not finite, lr, eps or
+ * weight_decay negative, a beta outside [0, 1), step < 1.
+ * AR_ERROR_UNSUPPORTED: `stream` is being captured (a replayed step would
+ * repeat this step's bias corrections). */
+ar_status_t ar_adamw_step(const void* plan, void* device_plan, const ar_adamw_step_t* args,
+                          hipStream_t stream);
+
+/* The values of `count` 8-bit codes (int8 for m when is_signed, else uint8
+ * for v) as float32; code i belongs to scales[i / 256]. */
+ar_status_t ar_adamw_dequantize(const void* codes, const float* scales, size_t count,
+                                int is_signed, float* out, hipStream_t stream);
+
 /* ---- testing ---------------------------------------------------------------- */
 
 /* For callers' tests of their AR_ERROR_HIP handling (the error path of the

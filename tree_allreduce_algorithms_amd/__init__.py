@@ -1,6 +1,7 @@
-"""MI355X-native ring / tree collectives over N rank buffers on one GPU.
+"""MI355X-native ring / tree collectives over N rank buffers on one GPU, and the
+AdamW step that updates a rank's shard between them.
 
-The collectives live in a C-ABI shared library (``libar.so``: HIP kernels for
+The operators live in a C-ABI shared library (``libar.so``: HIP kernels for
 gfx950 plus the C ABI declared in ``include/ar.h``); this package is a thin
 ctypes binding with the same names.  The library is loaded on first use; if
 it has not been built the call raises.
@@ -36,3 +37,4 @@ from .binding import (  # noqa: F401
     set_impl,
     tree_allreduce,
 )
+from .training import AdamW, dequantize  # noqa: F401

@@ -21,9 +21,23 @@ COLLECTIVES = {"ring_allreduce": 0, "reduce_scatter": 1, "allgather": 2, "broadc
                "tree_allreduce": 4, "reduce": 5, "scatter": 6, "gather": 7, "alltoall": 8}
 IMPLS = {"fused": 0, "step": 1}
 
-# name -> (restype, argtypes), in the order include/ar.h declares them
 _VP, _I, _SZ, _U64P = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.POINTER(ctypes.c_uint64)
 _PP = ctypes.POINTER(ctypes.c_void_p)
+class AdamwTensor(ctypes.Structure):
+    """ar_adamw_tensor_t."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("param", "grad", "copy", "exp_avg", "exp_avg_sq",
+                                               "exp_avg_scale", "exp_avg_sq_scale")] + \
+               [("count", ctypes.c_size_t)]
+
+
+class AdamwStep(ctypes.Structure):
+    """ar_adamw_step_t."""
+    _fields_ = [(f, ctypes.c_double) for f in ("lr", "beta1", "beta2", "eps", "weight_decay",
+                                               "grad_scale")] + \
+               [("step", ctypes.c_int64), ("clip", ctypes.c_int)]
+
+
+# name -> (restype, argtypes), in the order include/ar.h declares them
 SIGNATURES = {
     "ar_ring_allreduce": (_I, [_PP, _I, _SZ, _I, _I, _VP]),
     "ar_reduce_scatter": (_I, [_PP, _I, _SZ, _I, _I, _VP]),
@@ -53,6 +67,11 @@ SIGNATURES = {
     "ar_status_string": (ctypes.c_char_p, [_I]),
     "ar_last_hip_error": (_I, []),
     "ar_version": (_I, []),
+    "ar_adamw_plan_bytes": (_SZ, [ctypes.POINTER(AdamwTensor), _I, _I, _I, _I]),
+    "ar_adamw_plan": (_I, [ctypes.POINTER(AdamwTensor), _I, _I, _I, _I, _VP, _SZ]),
+    "ar_adamw_grad_norm": (_I, [_VP, _VP, ctypes.c_double, ctypes.c_double, _VP, _VP]),
+    "ar_adamw_step": (_I, [_VP, _VP, ctypes.POINTER(AdamwStep), _VP]),
+    "ar_adamw_dequantize": (_I, [_VP, _VP, _SZ, _I, _VP, _VP]),
     "ar_debug_fail_launch": (_I, [_I]),
 }
 

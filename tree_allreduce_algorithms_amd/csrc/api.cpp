@@ -15,6 +15,7 @@
 
 #include "ar.h"
 #include "kernels.hpp"
+#include "launch.hpp"
 #include "plan.hpp"
 #include "plan_check.hpp"
 
@@ -58,15 +59,6 @@ thread_local int t_last_hip_error = 0;
 // the launch that takes it from 1 to 0 returns hipErrorLaunchFailure without
 // reaching the HIP runtime.
 std::atomic<int> g_fail_launch{0};
-
-template <class F>
-hipError_t enqueue(F&& launch_fn) {
-  int k = g_fail_launch.load(std::memory_order_relaxed);
-  while (k > 0 && !g_fail_launch.compare_exchange_weak(k, k - 1, std::memory_order_relaxed)) {
-  }
-  if (k == 1) return hipErrorLaunchFailure;
-  return launch_fn();
-}
 
 // Cost model coefficients (alpha_us per launch, gbps of HBM traffic) per
 // collective and implementation.  The AllReduce pairs are the least-squares
@@ -180,14 +172,14 @@ ar_status_t run(ar_collective_t coll, void* const* bufs, int n, size_t count, ar
   if (coll == AR_REDUCE) {
     // one implementation: the partials of the rounds live in registers, so
     // no rank other than the root is written
-    err = enqueue([&] { return ar::launch_tree_fold(ptrs, n, count, dtype, aop, root, false, vec, stream); });
+    err = ar::enqueue([&] { return ar::launch_tree_fold(ptrs, n, count, dtype, aop, root, false, vec, stream); });
   } else if (coll == AR_ALLTOALL) {
-    err = enqueue([&] { return ar::launch_alltoall(ptrs, n, count, dtype, vec, stream); });
+    err = ar::enqueue([&] { return ar::launch_alltoall(ptrs, n, count, dtype, vec, stream); });
   } else if (impl == AR_IMPL_STEP || coll == AR_SCATTER || coll == AR_GATHER) {
     // the literal schedule: one launch per step (the schedule is built only here)
     const std::vector<ar::Step> sched = ar::schedule_for(coll, n, count, root < 0 ? 0 : root);
     for (const ar::Step& s : sched) {
-      err = enqueue([&] { return ar::launch_step(ptrs, s, dtype, aop, vec, stream); });
+      err = ar::enqueue([&] { return ar::launch_step(ptrs, s, dtype, aop, vec, stream); });
       if (err != hipSuccess) break;
     }
   } else {
@@ -197,47 +189,61 @@ ar_status_t run(ar_collective_t coll, void* const* bufs, int n, size_t count, ar
           // fused ReduceScatter, then the owners' chunks fanned out: the same
           // bits as the one-pass fold (AllReduce = AllGather after
           // ReduceScatter), faster for many ranks
-          err = enqueue([&] { return ar::launch_ring_fold(ptrs, n, count, dtype, aop, false, vec, stream); });
+          err = ar::enqueue([&] { return ar::launch_ring_fold(ptrs, n, count, dtype, aop, false, vec, stream); });
           if (err == hipSuccess)
-            err = enqueue([&] { return ar::launch_fanout(ptrs, n, count, dtype, false, 0, vec, stream); });
+            err = ar::enqueue([&] { return ar::launch_fanout(ptrs, n, count, dtype, false, 0, vec, stream); });
         } else {
-          err = enqueue([&] { return ar::launch_ring_fold(ptrs, n, count, dtype, aop, true, vec, stream); });
+          err = ar::enqueue([&] { return ar::launch_ring_fold(ptrs, n, count, dtype, aop, true, vec, stream); });
         }
         break;
       case AR_REDUCE_SCATTER:
-        err = enqueue([&] { return ar::launch_ring_fold(ptrs, n, count, dtype, aop, false, vec, stream); });
+        err = ar::enqueue([&] { return ar::launch_ring_fold(ptrs, n, count, dtype, aop, false, vec, stream); });
         break;
       case AR_ALLGATHER:
-        err = enqueue([&] { return ar::launch_fanout(ptrs, n, count, dtype, false, 0, vec, stream); });
+        err = ar::enqueue([&] { return ar::launch_fanout(ptrs, n, count, dtype, false, 0, vec, stream); });
         break;
       case AR_BROADCAST:
-        err = enqueue([&] { return ar::launch_fanout(ptrs, n, count, dtype, true, root, vec, stream); });
+        err = ar::enqueue([&] { return ar::launch_fanout(ptrs, n, count, dtype, true, root, vec, stream); });
         break;
       case AR_TREE_ALLREDUCE:
         if (ar::allreduce_split(n, count, ar::itemsize(dtype))) {
           // both trees' folds stored into their roots, then each root's half
           // fanned out: the reduce and broadcast passes, the same bits as the
           // one-pass fold, faster for many ranks
-          err = enqueue([&] { return ar::launch_tree_fold(ptrs, n, count, dtype, aop, -1, true, vec, stream); });
+          err = ar::enqueue([&] { return ar::launch_tree_fold(ptrs, n, count, dtype, aop, -1, true, vec, stream); });
           if (err == hipSuccess)
-            err = enqueue([&] { return ar::launch_tree_broadcast(ptrs, n, count, dtype, vec, stream); });
+            err = ar::enqueue([&] { return ar::launch_tree_broadcast(ptrs, n, count, dtype, vec, stream); });
         } else {
-          err = enqueue([&] { return ar::launch_tree_fold(ptrs, n, count, dtype, aop, -1, false, vec, stream); });
+          err = ar::enqueue([&] { return ar::launch_tree_fold(ptrs, n, count, dtype, aop, -1, false, vec, stream); });
         }
         break;
       default:   // Reduce, Scatter, Gather and AllToAll are dispatched above
         break;
     }
   }
-  if (err != hipSuccess) {
-    t_last_hip_error = static_cast<int>(err);
-    return AR_ERROR_HIP;
-  }
+  if (err != hipSuccess) return ar::launch_status(err);
   add_counters(coll, n, count, root, ar::itemsize(dtype));
   return AR_SUCCESS;
 }
 
 }  // namespace
+
+namespace ar {
+
+bool take_launch_failure() {
+  int k = g_fail_launch.load(std::memory_order_relaxed);
+  while (k > 0 && !g_fail_launch.compare_exchange_weak(k, k - 1, std::memory_order_relaxed)) {
+  }
+  return k == 1;
+}
+
+ar_status_t launch_status(hipError_t err) {
+  if (err == hipSuccess) return AR_SUCCESS;
+  t_last_hip_error = static_cast<int>(err);
+  return AR_ERROR_HIP;
+}
+
+}  // namespace ar
 
 extern "C" {
 

@@ -1,0 +1,186 @@
+"""The training step next to the collectives: AdamW over many tensors at once.
+
+Argument marshalling only, as in ``binding``: the work is done by libar.so's
+HIP kernels, on the current stream unless a call names another.
+"""
+
+import ctypes
+
+from . import binding
+from .binding import DTYPES, SUCCESS, AdamwStep, AdamwTensor, ArError, lib
+
+BLOCK = 256   # elements that share one scale of an 8-bit state
+
+
+def _handle(stream, dev):
+    """hipStream_t of a torch stream, a raw handle, or (None) the current stream."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _flat(tensors, what, dev, dtypes, sizes):
+    """`tensors` as a list: contiguous GPU tensors of one of `dtypes` (all the
+    same) on `dev`, of these sizes."""
+    import torch
+    tensors = list(tensors)
+    if len(tensors) != len(sizes):
+        raise ValueError(f"{what}: {len(tensors)} tensors for {len(sizes)} parameters")
+    for t, n in zip(tensors, sizes):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{what} must be GPU tensors")
+        if t.dtype not in dtypes or t.dtype != tensors[0].dtype:
+            raise TypeError(f"{what}: unsupported or mixed dtype {t.dtype}")
+        if t.get_device() != dev or t.numel() != n:
+            raise ValueError(f"{what} must share the parameters' device and sizes")
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+    return tensors
+
+
+class AdamW:
+    """AdamW over many tensors, one launch a step (see ar_adamw_step).
+
+    ``params`` and ``grads`` are lists of contiguous GPU tensors (float32 or
+    bfloat16 each), for instance the shards that ``reduce_scatter`` leaves
+    with their owners; ``copies`` optionally lists bfloat16 working copies of
+    float32 params, rewritten by every step.  Everything is checked once,
+    here; the tensors' storage must not move while the object is in use, and
+    every step reads the gradients from the same ``grads``.
+
+    ``state_bits`` is 32 (``exp_avg`` and ``exp_avg_sq`` in float32) or 8
+    (int8 and uint8 codes, with one float32 scale per 256 elements of a tensor
+    in ``exp_avg_scale`` and ``exp_avg_sq_scale``; see ar_adamw_tensor_t and
+    ``dequantize``).  ``state`` hands over existing lists of these names, which
+    are updated in place; by default they start at zero.  ``steps`` counts the
+    steps taken so far.  ``grad_scale`` multiplies every gradient first, e.g.
+    ``1 / N`` where they are sums over N ranks.
+
+    Calls run on the current stream, or on ``stream``; those of one object must
+    be ordered.  ``grad_norm`` may be captured into a graph, ``step`` may not
+    (its bias corrections are those of one step).
+    """
+
+    def __init__(self, params, grads, copies=None, *, state_bits=32, state=None, steps=0,
+                 betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, grad_scale=1.0):
+        import torch
+        params = list(params)
+        if not params:
+            raise ValueError("need at least one parameter")
+        if not isinstance(params[0], torch.Tensor) or not params[0].is_cuda:
+            raise TypeError("params must be GPU tensors")
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, not {state_bits!r}")
+        if int(steps) != steps or steps < 0:
+            raise ValueError("steps must be a whole number of steps taken, at least 0")
+        dev = params[0].get_device()
+        sizes = [p.numel() for p in params]
+        real = (torch.float32, torch.bfloat16)
+        self.params = _flat(params, "params", dev, real, sizes)
+        self.grads = _flat(grads, "grads", dev, real, sizes)
+        self.copies = None
+        if copies is not None:
+            if params[0].dtype != torch.float32:
+                raise TypeError("copies are offered for float32 params only")
+            self.copies = _flat(copies, "copies", dev, (torch.bfloat16,), sizes)
+        kinds = {"exp_avg": (torch.float32, sizes), "exp_avg_sq": (torch.float32, sizes)}
+        if state_bits == 8:
+            blocks = [-(-n // BLOCK) for n in sizes]
+            kinds = {"exp_avg": (torch.int8, sizes), "exp_avg_sq": (torch.uint8, sizes),
+                     "exp_avg_scale": (torch.float32, blocks),
+                     "exp_avg_sq_scale": (torch.float32, blocks)}
+        if state is None:
+            state = {k: [torch.zeros(n, dtype=dt, device=params[0].device) for n in ns]
+                     for k, (dt, ns) in kinds.items()}
+        if set(state) != set(kinds):
+            raise ValueError(f"state must hold {sorted(kinds)}, not {sorted(state)}")
+        self.state = {k: _flat(state[k], k, dev, (dt,), ns) for k, (dt, ns) in kinds.items()}
+        self.state_bits, self.steps = state_bits, int(steps)
+        self._clip_ready = False
+        self._args = AdamwStep(0.0, float(betas[0]), float(betas[1]), float(eps),
+                               float(weight_decay), float(grad_scale), 0, 0)
+        self._grad_scale = float(grad_scale)
+
+        ptr = lambda k, i: self.state[k][i].data_ptr() if k in self.state else 0  # noqa: E731
+        table = (AdamwTensor * len(params))(*[
+            AdamwTensor(self.params[i].data_ptr(), self.grads[i].data_ptr(),
+                        self.copies[i].data_ptr() if self.copies else 0, ptr("exp_avg", i),
+                        ptr("exp_avg_sq", i), ptr("exp_avg_scale", i), ptr("exp_avg_sq_scale", i), n)
+            for i, n in enumerate(sizes)])
+        kind = (len(params), DTYPES[binding._torch_dtype_name(params[0])],
+                DTYPES[binding._torch_dtype_name(self.grads[0])], state_bits)
+        size = lib().ar_adamw_plan_bytes(table, *kind)
+        self._host = (ctypes.c_char * max(size, 16))()
+        binding._check(lib().ar_adamw_plan(table, *kind, self._host, size), "AdamW")
+        self._dev = dev
+        with binding._on_device(dev):
+            self._norm = torch.zeros((), dtype=torch.float32, device=params[0].device)
+            self._device = torch.frombuffer(self._host, dtype=torch.uint8).to(params[0].device)
+        self._call_args = (ctypes.addressof(self._host), self._device.data_ptr())
+        self._step_args = ctypes.byref(self._args)
+        self._fn_norm, self._fn_step = lib().ar_adamw_grad_norm, lib().ar_adamw_step
+
+    def grad_norm(self, max_norm=None, stream=None):
+        """The 2-norm over all gradients (times ``grad_scale``), a float32 GPU
+        scalar that the next call overwrites.  With ``max_norm`` the factor
+        ``min(1, max_norm / norm)`` is kept for ``step(clip=True)``; nothing
+        waits for the GPU."""
+        with binding._on_device(self._dev):
+            status = self._fn_norm(*self._call_args, float("inf") if max_norm is None else max_norm,
+                                   self._grad_scale, self._norm.data_ptr(), _handle(stream, self._dev))
+        if status != SUCCESS:
+            raise ArError(status, "grad_norm")
+        self._clip_ready = max_norm is not None
+        return self._norm
+
+    def step(self, lr, clip=False, stream=None):
+        """One step in place.  ``clip=True`` scales the gradients by the factor
+        of ``grad_norm(max_norm=...)``, which must have been called since the
+        step before."""
+        if clip and not self._clip_ready:
+            raise ValueError("step(clip=True) needs grad_norm(max_norm=...) on these gradients first")
+        args = self._args
+        args.lr, args.step, args.clip = lr, self.steps + 1, 1 if clip else 0
+        with binding._on_device(self._dev):
+            status = self._fn_step(*self._call_args, self._step_args, _handle(stream, self._dev))
+        if status != SUCCESS:
+            raise ArError(status, "step")
+        self.steps += 1
+        self._clip_ready = False
+
+
+def dequantize(codes, scales, stream=None):
+    """float32 values of the codes of an 8-bit AdamW state: int8 codes of
+    ``exp_avg`` or uint8 codes of ``exp_avg_sq``, with one scale per 256."""
+    import torch
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda or not scales.is_cuda:
+        raise TypeError("codes and scales must be GPU tensors")
+    if codes.dtype not in (torch.int8, torch.uint8) or scales.dtype != torch.float32:
+        raise TypeError(f"need int8 or uint8 codes and float32 scales, not {codes.dtype} and "
+                        f"{scales.dtype}")
+    n, dev = codes.numel(), codes.get_device()
+    if scales.numel() != -(-n // BLOCK) or scales.get_device() != dev:
+        raise ValueError(f"{n} codes need {-(-n // BLOCK)} scales on their device")
+    if not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError("codes and scales must be contiguous")
+    out = _empty(codes.shape, torch.float32, codes.device, stream)
+    with binding._on_device(dev):
+        status = lib().ar_adamw_dequantize(codes.data_ptr(), scales.data_ptr(), n,
+                                           1 if codes.dtype == torch.int8 else 0, out.data_ptr(),
+                                           _handle(stream, dev))
+    if status != SUCCESS:
+        raise ArError(status, "dequantize")
+    return out
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a kernel on `stream`: it belongs to that stream, so its
+    memory is not handed out again before the kernel there has run."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
