@@ -425,6 +425,61 @@ ar_status_t ar_adamw_step(const void* plan, void* device_plan, const ar_adamw_st
 ar_status_t ar_adamw_dequantize(const void* codes, const float* scales, size_t count,
                                 int is_signed, float* out, hipStream_t stream);
 
+#define AR_MAX_EXPERTS 1024
+#define AR_MAX_TOP_K 8
+
+/* Device memory of a router call's sums: AR_ROUTE_WORKSPACE bytes, 16-byte
+ * aligned, all zero before the call; the call leaves it zero again, so one
+ * workspace serves any number of calls ordered on one stream.  Two streams
+ * need two. */
+#define AR_ROUTE_WORKSPACE 270592
+
+/* Shape of a router call: `nranks` ranks (at most AR_MAX_RANKS) of `tokens`
+ * tokens each, whose logits over `experts` experts lie `row_stride` elements
+ * apart (row_stride >= experts).  nranks * tokens < 2^31. */
+typedef struct {
+  int nranks;
+  size_t tokens;
+  int experts;
+  size_t row_stride;
+  int top_k;          /* 1 .. min(experts, AR_MAX_TOP_K) */
+  int renormalize;
+  ar_dtype_t dtype;   /* of the logits: AR_FLOAT32 or AR_BFLOAT16 */
+} ar_route_shape_t;
+
+/* The router.  For each token with logits x: p = softmax(x); chosen are the
+ * top_k largest x above -infinity, a tie to the lowest index;
+ *   indices [nranks][tokens][top_k]  the chosen experts, largest first, -1
+ *           where fewer than top_k are above -infinity
+ *   weights [nranks][tokens][top_k]  their p, divided by their sum with
+ *           `renormalize`; 0 where the index is -1
+ *   counts  [nranks][experts]        tokens of the rank that chose the expert
+ *   loss    E / (K T^2) sum_e C_e S_e, with C_e the counts' sum over ranks,
+ *           S_e the sum of p_e over all tokens and T the tokens that live
+ *   share   [experts]                E C_e / (K T^2), for ar_route_grad
+ * `masks` (NULL, or one pointer a rank to `tokens` bytes): a token whose byte
+ * is 0, or with every logit -infinity, is no token: index -1, weight 0,
+ * nothing counted.  A token with a NaN or +infinite logit has NaN for every
+ * weight and makes loss NaN; a NaN is never chosen.  p and weights are computed in float32;
+ * the sums S are added up in float32 over the tokens of a block and over the
+ * blocks in fixed point (2^-32), so that no result depends on the order of
+ * execution.  Outputs are written whole. */
+ar_status_t ar_route(const void* const* logits, const uint8_t* const* masks,
+                     const ar_route_shape_t* shape, int32_t* indices, float* weights,
+                     int32_t* counts, float* loss, float* share, void* workspace,
+                     hipStream_t stream);
+
+/* Gradient of sum(dweights * weights) + dloss * loss with respect to the
+ * logits, the counts held fixed: dlogits [nranks][tokens][experts],
+ * contiguous, of the logits' type (one rounding).  logits, masks and shape
+ * are the forward call's, indices and share its outputs; dweights (NULL: 0)
+ * holds one pointer a rank to [tokens][top_k] float32, dloss (NULL: 0) a
+ * float32 on the device.  0 for a token that is none. */
+ar_status_t ar_route_grad(const void* const* logits, const uint8_t* const* masks,
+                          const ar_route_shape_t* shape, const int32_t* indices,
+                          const float* share, const float* const* dweights, const float* dloss,
+                          void* dlogits, hipStream_t stream);
+
 /* ---- testing ---------------------------------------------------------------- */
 
 /* For callers' tests of their AR_ERROR_HIP handling (the error path of the

@@ -1,0 +1,351 @@
+"""The router kernels against the definition in 64 bits, on the GPU.
+
+Indices and counts have to be equal.  The tolerances of the computed outputs
+count float32 roundings (half a step, 2^-24): exp(x - top) takes a
+difference, a constant and a product (3 half steps of the exponent, so a
+relative 3 |x - top| 2^-24) and one instruction (2 half steps); a row's sum is
+at most 48 additions deep; quotients and products add a few.
+"""
+
+import math
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import tree_allreduce_algorithms_amd as ar
+from tree_allreduce_algorithms_amd import training
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+F32, BF16 = torch.float32, torch.bfloat16
+H = 2.0 ** -24
+TINY = 1e-37       # results below float32's normal numbers may be taken as 0
+
+
+def announce(msg):
+    print(f"[gpu-route] {msg}", file=sys.__stderr__, flush=True)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu_ready():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    ar.lib()
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
+def definition(x, k, mask, renormalize, dw=None, dloss=0.0):
+    """Outputs of x [ranks, tokens, experts] in float64, and what the
+    tolerances need."""
+    ranks, tokens, experts = x.shape
+    x = np.where(mask[..., None], x, -np.inf)
+    live = np.any(x > -np.inf, -1)
+    top = np.where(live, x.max(-1, initial=-np.inf), 0.0)[..., None]
+    d = np.where(x > -np.inf, top - x, 0.0)                      # distances below the top
+    e = np.where(x > -np.inf, np.exp(-d), 0.0)
+    p = e / np.where(live, e.sum(-1), 1.0)[..., None]
+    order = np.argsort(-x, axis=-1, kind="stable")[..., :k]
+    chosen = np.take_along_axis(x, order, -1) > -np.inf
+    index = np.where(chosen, order, -1).astype(np.int32)
+    w = np.where(chosen, np.take_along_axis(p, order, -1), 0.0)
+    if renormalize:
+        w = w / np.where(live, w.sum(-1), 1.0)[..., None]
+    counts = np.zeros((ranks, experts), np.int64)
+    for r in range(ranks):
+        counts[r] = np.bincount(index[r][index[r] >= 0], minlength=experts)
+    n = max(1, int(live.sum()))
+    share = experts * counts.sum(0) / (k * float(n) ** 2)
+    loss = float((share * p.sum((0, 1))).sum())
+    spread = 3 * (p * d).sum(-1, keepdims=True)                  # of the row's sum, in half steps
+    dk = np.take_along_axis(d, order, -1)
+    out = {"index": index, "w": w, "counts": counts, "loss": loss, "share": share,
+           "w_err": H * (3 * dk + 2 * spread + 64) * w + TINY,
+           "loss_err": H * (128 + 64 + 2 * spread.max(initial=0) + 3 * 8) * loss + 2.0 ** -32 * share.sum() + TINY}
+    if dw is None:
+        return out
+    dw = np.where(chosen, dw, 0.0)
+    at = np.zeros_like(p)
+    coef = dloss * share
+    rel = H * (3 * d + 2 * spread + 128)
+    if renormalize:
+        np.put_along_axis(at, order, np.where(chosen, w * (dw - (w * dw).sum(-1, keepdims=True)), 0.0), -1)
+        dx = p * (coef - (p * coef).sum(-1, keepdims=True)) + at
+        err = p * (np.abs(coef) + (p * np.abs(coef)).sum(-1, keepdims=True)) * 2 * rel
+        aw = w * (np.abs(dw) + (w * np.abs(dw)).sum(-1, keepdims=True))
+        err_at = np.zeros_like(p)
+        np.put_along_axis(err_at, order, np.where(chosen, aw, 0.0), -1)
+        err = err + err_at * 2 * rel
+    else:
+        np.put_along_axis(at, order, dw, -1)
+        dp = coef + at
+        dx = p * (dp - (p * dp).sum(-1, keepdims=True))
+        err = p * (np.abs(dp) + (p * np.abs(dp)).sum(-1, keepdims=True)) * 2 * rel
+    out["dx"], out["dx_err"] = dx, err + TINY * (1 + np.abs(coef).max(initial=0) + np.abs(dw).max(initial=0))
+    return out
+
+
+def fill(kind, shape, rng):
+    x = rng.normal(0, 1.5, shape) + rng.normal(0, 0.5, shape[2])
+    if kind == "ruled out":          # some experts, in some rows all
+        gone = rng.random(shape) < rng.choice([0.0, 0.5, 0.95, 1.1], shape[:2])[..., None]
+        x = np.where(gone, -np.inf, x)
+    elif kind == "ties":
+        x = np.round(x)
+    elif kind == "equal":
+        x = np.zeros(shape)
+    elif kind == "lowest":           # masked by the type's lowest value instead of -infinity
+        x = np.where(rng.random(shape) < 0.7, -3.3895313892515355e38, x)
+    elif kind == "wide":
+        x = x * 1e4
+    elif kind == "near":             # neighbours in the last bits
+        x = (3.0 + rng.integers(0, 4, shape) * 2.0 ** -22) * rng.choice([1.0, 1.0, -1.0], shape)
+    elif kind == "zeros":            # zeros of both signs tie
+        x = rng.choice([0.0, -0.0, -1.0], shape)
+    return x
+
+
+def place(x, dtype, stride, offset):
+    """The ranks' logits on the device: rows `stride` apart, `offset` elements in."""
+    ranks, tokens, experts = x.shape
+    out = []
+    for r in range(ranks):
+        room = torch.full((max(1, tokens) * stride + offset,), 99.0, dtype=dtype, device=DEV)
+        view = room[offset:offset + max(1, tokens) * stride].view(max(1, tokens), stride)[:tokens, :experts]
+        view.copy_(torch.from_numpy(x[r]))
+        out.append(view)
+    return out
+
+
+def check(x, k, dtype, renormalize, mask=None, stride=None, offset=0, seed=0):
+    """Forward and gradient of one case against the definition."""
+    rng = np.random.default_rng(seed)
+    ranks, tokens, experts = x.shape
+    logits = place(x, dtype, stride or experts, offset)
+    x = np.stack([t.double().cpu().numpy() for t in logits]) if ranks else x
+    masks = None if mask is None else [torch.from_numpy(m).to(DEV) for m in mask]
+    full = np.ones(x.shape[:2], bool) if mask is None else mask
+    dw = rng.normal(0, 1, (ranks, tokens, k)).astype(np.float32)
+    dloss = np.float32(7.5)
+    want = definition(x, k, full, renormalize, dw.astype(np.float64), float(dloss))
+    r = ar.route(logits, k, mask=masks, renormalize=renormalize)
+    dx = ar.route_grad(logits, r, dweights=[torch.from_numpy(a).to(DEV) for a in dw],
+                       dloss=torch.tensor(dloss, device=DEV))
+    torch.cuda.synchronize()
+    assert np.array_equal(r.indices.cpu().numpy(), want["index"])
+    assert np.array_equal(r.counts.cpu().numpy(), want["counts"])
+    assert np.all(np.abs(r.weights.cpu().numpy() - want["w"]) <= want["w_err"])
+    assert np.all(np.abs(r.share.cpu().numpy() - want["share"]) <= 2 * H * want["share"])
+    assert abs(float(r.loss) - want["loss"]) <= want["loss_err"], (float(r.loss), want["loss"])
+    assert dx.dtype == dtype and dx.shape == x.shape
+    err = want["dx_err"] + (2.0 ** -8 if dtype == BF16 else 0) * (np.abs(want["dx"]) + want["dx_err"])
+    assert np.all(np.abs(dx.double().cpu().numpy() - want["dx"]) <= err)
+    for ws in training._route_workspaces.values():
+        assert not ws.any()
+    return r, dx
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("experts", [1, 2, 7, 8, 16, 61, 64, 65, 128, 200, 256, 300, 512, 1000, 1024])
+def test_experts(experts, renormalize, dtype):
+    announce(f"experts {experts} {renormalize} {dtype}")
+    rng = np.random.default_rng(experts)
+    for k in sorted({1, 2, 3, 6, 8}):
+        if k <= experts:
+            check(fill("plain", (3, 37, experts), rng), k, dtype, renormalize)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("kind", ["ruled out", "ties", "equal", "lowest", "wide", "near", "zeros"])
+@pytest.mark.parametrize("experts", [5, 61, 64, 256, 500, 777])
+def test_values(experts, kind, dtype):
+    announce(f"values {experts} {kind} {dtype}")
+    rng = np.random.default_rng(experts)
+    for k in (1, 4, 5, 8):
+        if k <= experts:
+            for renormalize in (False, True):
+                check(fill(kind, (2, 53, experts), rng), k, dtype, renormalize)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("ranks, tokens", [(1, 0), (3, 0), (1, 1), (64, 1), (64, 33), (5, 509), (1, 5000), (8, 2048)])
+def test_tokens_and_ranks(ranks, tokens, dtype):
+    announce(f"tokens {ranks} {tokens} {dtype}")
+    rng = np.random.default_rng(tokens + ranks)
+    check(fill("plain", (ranks, tokens, 40), rng), 4, dtype, True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("share", [0.0, 0.05, 0.5, 1.0])
+def test_masks(share, dtype):
+    announce(f"masks {share} {dtype}")
+    rng = np.random.default_rng(4)
+    mask = rng.random((4, 300)) >= share
+    for kind in ("plain", "ruled out"):
+        for renormalize in (False, True):
+            check(fill(kind, (4, 300, 96), rng), 3, dtype, renormalize, mask=mask)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("experts, stride, offset", [(64, 64, 1), (64, 65, 0), (64, 72, 0), (256, 300, 3),
+                                                      (61, 64, 0), (61, 61, 2), (512, 1024, 8), (8, 9, 1)])
+def test_strides_and_alignment(experts, stride, offset, dtype):
+    announce(f"strides {experts} {stride} {offset} {dtype}")
+    rng = np.random.default_rng(stride)
+    check(fill("plain", (2, 70, experts), rng), 2, dtype, True, stride=stride, offset=offset)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("experts", [8, 64, 256])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_what_is_not_finite_shows_in_its_row_only(dtype, experts, bad):
+    rng = np.random.default_rng(2)
+    x = fill("plain", (2, 40, experts), rng)
+    clean = place(x, dtype, experts, 0)
+    x[1, 7, 3] = bad
+    x[1, 9] = float("nan")
+    logits = place(x, dtype, experts, 0)
+    keep = torch.ones(2, 40, dtype=torch.bool, device=DEV)
+    keep[1, 7] = keep[1, 9] = False
+    one = torch.ones((), device=DEV)
+    for renormalize in (False, True):
+        r, c = (ar.route(t, 2, renormalize=renormalize) for t in (logits, clean))
+        assert torch.isnan(r.weights[~keep]).all() and math.isnan(float(r.loss))
+        assert torch.equal(r.weights[keep], c.weights[keep])
+        assert torch.equal(r.indices[keep], c.indices[keep])
+        assert (r.indices >= -1).all() and (r.indices < experts).all()
+        assert (r.indices[1, 9] == -1).all() and (r.indices[1, 7] == (3 if bad > 0 else -9)).any() == (bad > 0)
+        dw = [torch.ones(40, 2, device=DEV)] * 2
+        dx = ar.route_grad(logits, r, dweights=dw, dloss=one)
+        assert torch.isnan(dx[~keep]).all() and torch.isfinite(dx[keep]).all()
+        for ws in training._route_workspaces.values():
+            assert not ws.any()
+
+
+def test_gradient_is_that_of_differences():
+    """Central differences of the definition, choices and counts held fixed."""
+    rng = np.random.default_rng(8)
+    x, k, dloss, h = rng.normal(0, 1, (2, 3, 8)).astype(np.float32), 3, 5.0, 1e-5
+    dw = rng.normal(0, 1, (2, 3, k)).astype(np.float32)
+    mask = np.ones((2, 3), bool)
+    for renormalize in (False, True):
+        base = definition(x.astype(np.float64), k, mask, renormalize)
+
+        def value(y):
+            p = np.exp(y) / np.exp(y).sum(-1, keepdims=True)
+            w = np.take_along_axis(p, base["index"].astype(np.int64), -1)
+            if renormalize:
+                w = w / w.sum(-1, keepdims=True)
+            return (dw * w).sum() + dloss * (base["share"] * p.sum((0, 1))).sum()
+
+        num = np.zeros(x.shape)
+        for at in np.ndindex(*x.shape):
+            step = np.zeros(x.shape)
+            step[at] = h
+            num[at] = (value(x + step) - value(x - step)) / (2 * h)
+        logits = [torch.from_numpy(t).to(DEV) for t in x]
+        r = ar.route(logits, k, renormalize=renormalize)
+        dx = ar.route_grad(logits, r, dweights=[torch.from_numpy(t).to(DEV) for t in dw],
+                           dloss=torch.tensor(dloss, device=DEV))
+        # differences: h^2 f'''/6 and 2^-53 |f| / h; the kernel: 128 half steps of a few units
+        assert np.max(np.abs(dx.cpu().numpy() - num)) <= 1e-4
+        only_w = ar.route_grad(logits, r, dweights=[torch.from_numpy(t).to(DEV) for t in dw])
+        only_l = ar.route_grad(logits, r, dloss=torch.tensor(dloss, device=DEV))
+        assert torch.allclose(only_w + only_l, dx, atol=1e-5, rtol=0)
+        assert not ar.route_grad(logits, r).any()
+
+
+def test_refusals():
+    x = torch.zeros(6, 16, device=DEV)
+    ok = ar.route([x, x], 2)
+    cases = [(ValueError, lambda: ar.route([], 2)), (ValueError, lambda: ar.route([x], 0)),
+             (ValueError, lambda: ar.route([x], 9)), (ValueError, lambda: ar.route([x[:, :1]], 2)),
+             (TypeError, lambda: ar.route([x.half()], 2)), (TypeError, lambda: ar.route([x, x.bfloat16()], 2)),
+             (ValueError, lambda: ar.route([x, x[:5]], 2)), (ValueError, lambda: ar.route([x[0]], 2)),
+             (ValueError, lambda: ar.route([x.t()], 2)), (ValueError, lambda: ar.route([x[:1].expand(6, 16)], 2)),
+             (ValueError, lambda: ar.route([torch.zeros(2, 1025, device=DEV)], 2)),
+             (ValueError, lambda: ar.route([x], 2, mask=[])),
+             (TypeError, lambda: ar.route([x], 2, mask=[torch.ones(6, device=DEV)])),
+             (ValueError, lambda: ar.route([x], 2, mask=[torch.ones(5, device=DEV, dtype=torch.bool)])),
+             (ValueError, lambda: ar.route_grad([x], ok)), (ValueError, lambda: ar.route_grad([x[:, :8]] * 2, ok)),
+             (ValueError, lambda: ar.route_grad([x.bfloat16()] * 2, ok)),
+             (ValueError, lambda: ar.route_grad([x, x], ok, dweights=[x])),
+             (ValueError, lambda: ar.route_grad([x, x], ok, dweights=[x, x])),
+             (ValueError, lambda: ar.route_grad([x, x], ok, dloss=torch.zeros(2, device=DEV))),
+             (TypeError, lambda: ar.route([x.cpu()], 2))]
+    for i, (error, call) in enumerate(cases):
+        with pytest.raises(error):
+            call()
+            raise AssertionError(f"case {i} was taken")
+    ar.debug_fail_launch(1)
+    with pytest.raises(ar.ArError):
+        ar.route([x], 2)
+
+
+def test_side_streams_and_graph():
+    """Calls on several streams at once, and a captured call that is replayed
+    beside eager ones, give what the calls give alone."""
+    logits = [torch.randn(700, 64, device=DEV) for _ in range(3)]
+    dw = [torch.randn(700, 4, device=DEV) for _ in range(3)]
+    one = torch.ones((), device=DEV)
+
+    def both(stream=None):
+        r = ar.route(logits, 4, renormalize=True, stream=stream)
+        return r.indices, r.weights, r.counts, r.loss, ar.route_grad(logits, r, dw, one, stream=stream)
+
+    want = both()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [[both(s) for s in streams] for _ in range(5)]
+    torch.cuda.synchronize()
+    for row in got:
+        for outs in row:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = both()
+    for k in range(4):
+        for t in logits:
+            t.normal_()
+        want = both()
+        torch.cuda.synchronize()
+        graph.replay()
+        both()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), k
+
+
+def test_same_bits_every_time():
+    logits = [torch.randn(16_000, 256, device=DEV) for _ in range(4)]
+    first = ar.route(logits, 8)
+    for _ in range(5):
+        r = ar.route(logits, 8)
+        assert torch.equal(r.loss, first.loss) and torch.equal(r.weights, first.weights)
+
+
+def test_offsets_past_32_bits():
+    """Rows that lie 2^21 elements apart, and an output of more than 2^32 elements."""
+    tokens, experts, stride = 2100, 32, 1 << 21
+    room = torch.empty(tokens * stride, dtype=BF16, device=DEV)
+    far = room.view(tokens, stride)[:, :experts]
+    far.normal_()
+    near = far.contiguous()
+    a, b = ar.route([far], 4), ar.route([near], 4)
+    assert torch.equal(a.indices, b.indices) and torch.equal(a.weights, b.weights)
+    one = torch.ones((), device=DEV)
+    assert torch.equal(ar.route_grad([far], a, dloss=one), ar.route_grad([near], b, dloss=one))
+    del room, far
+    tokens, experts = (1 << 21) + 3, 1024
+    x = torch.zeros(2, tokens, experts, dtype=BF16, device=DEV)
+    x[1, -50:].normal_()
+    dw = torch.ones(tokens, 3, device=DEV)
+    r = ar.route(list(x), 3)
+    tail = ar.route([x[1, -50:]], 3)
+    assert torch.equal(r.indices[1, -50:], tail.indices[0]) and torch.equal(r.weights[1, -50:], tail.weights[0])
+    assert int(r.counts.sum()) == 2 * tokens * 3
+    dx = ar.route_grad(list(x), r, dweights=[dw, dw])
+    assert torch.equal(dx[1, -50:], ar.route_grad([x[1, -50:]], tail, dweights=[dw[-50:]])[0])

@@ -9,7 +9,7 @@ import pytest
 
 import tree_allreduce_algorithms_amd as ar
 from tree_allreduce_algorithms_amd import binding
-from tree_allreduce_algorithms_amd.binding import AdamwStep, AdamwTensor
+from tree_allreduce_algorithms_amd.binding import AdamwStep, AdamwTensor, RouteShape
 
 INT32, F32, BF16, ACC32 = 0, 1, 2, 3
 OK, INVALID, UNSUPPORTED, HIP = (binding.SUCCESS, binding.INVALID_ARGUMENT, binding.UNSUPPORTED,
@@ -188,3 +188,87 @@ def test_python_refusals_need_no_gpu():
         ar.AdamW([x], [x])
     with pytest.raises(TypeError, match="GPU"):
         ar.dequantize(x, x)
+
+
+# --- the router ---------------------------------------------------------------------
+
+def addresses(n, first=A):
+    return (ctypes.c_void_p * n)(*[first + i * GAP for i in range(n)]) if n else None
+
+
+def route_call(shape, logits="default", masks=None, outs=None, workspace=A + 200 * GAP):
+    outs = outs or [A + (100 + i) * GAP for i in range(5)]
+    logits = addresses(max(1, min(shape.nranks, 64))) if logits == "default" else logits
+    return ar.lib().ar_route(logits, masks, ctypes.byref(shape), *outs, workspace, None)
+
+
+def grad_call(shape, logits="default", masks=None, indices=A + 100 * GAP, share=A + 101 * GAP,
+              dweights=None, dloss=None, dlogits=A + 102 * GAP):
+    logits = addresses(max(1, min(shape.nranks, 64))) if logits == "default" else logits
+    return ar.lib().ar_route_grad(logits, masks, ctypes.byref(shape), indices, share, dweights, dloss,
+                                  dlogits, None)
+
+
+def shape(nranks=2, tokens=5, experts=16, row_stride=None, top_k=2, renormalize=0, dtype=F32):
+    return RouteShape(nranks, tokens, experts, experts if row_stride is None else row_stride, top_k,
+                      renormalize, dtype)
+
+
+@pytest.mark.parametrize("kw, want", [
+    ({"nranks": 0}, INVALID), ({"nranks": 65}, INVALID), ({"experts": 0}, INVALID),
+    ({"top_k": 0}, INVALID), ({"top_k": 17}, INVALID), ({"row_stride": 15}, INVALID),
+    ({"dtype": INT32}, UNSUPPORTED), ({"dtype": ACC32}, UNSUPPORTED),
+    ({"experts": 1025}, UNSUPPORTED), ({"top_k": 9}, UNSUPPORTED),
+    ({"tokens": 1 << 31}, UNSUPPORTED), ({"tokens": (1 << 30) - 1, "row_stride": 1 << 34}, INVALID)])
+def test_router_shape_refusals(kw, want):
+    assert route_call(shape(**kw)) == want
+    assert grad_call(shape(**kw)) == want
+
+
+def test_router_pointer_refusals():
+    s = shape()
+    two = lambda *p: (ctypes.c_void_p * 2)(*p)  # noqa: E731
+    for call in (route_call, grad_call):
+        assert call(s, logits=None) == INVALID
+        assert call(s, logits=two(A, None)) == INVALID
+        assert call(s, logits=two(A, A + GAP + 2)) == INVALID
+        assert call(s, masks=two(A, None)) == INVALID
+    good = [A + (100 + i) * GAP for i in range(5)]
+    for i in range(5):
+        for bad in (None, good[i] + 2):
+            assert route_call(s, outs=good[:i] + [bad] + good[i + 1:]) == INVALID
+    assert route_call(s, workspace=None) == INVALID
+    assert route_call(s, workspace=A + 8) == INVALID
+    assert grad_call(s, indices=None) == INVALID
+    assert grad_call(s, share=None) == INVALID
+    assert grad_call(s, dlogits=None) == INVALID
+    assert grad_call(s, dlogits=A + 2) == INVALID
+    assert grad_call(s, dloss=A + 2) == INVALID
+    assert grad_call(s, dweights=two(A, None)) == INVALID
+    assert grad_call(s, dweights=two(A, A + GAP + 2)) == INVALID
+    assert ar.lib().ar_route(addresses(2), None, None, *good, A, None) == INVALID
+
+
+def test_router_injected_launch_failures():
+    for call in (route_call, grad_call):
+        ar.debug_fail_launch(1)
+        assert call(shape()) == HIP
+        assert ar.lib().ar_last_hip_error() == 719
+    assert grad_call(shape(tokens=0), logits=addresses(2)) == OK       # nothing to do
+
+
+def test_router_python_refusals_need_no_gpu():
+    import torch
+    with pytest.raises(ValueError, match="ranks"):
+        ar.route([], 1)
+    with pytest.raises(TypeError, match="GPU"):
+        ar.route([torch.zeros(4, 8)], 1)
+
+
+def test_router_workspace_size_is_the_headers():
+    from tree_allreduce_algorithms_amd import training
+    text = open(os.path.join(os.path.dirname(binding.PKG), "include", "ar.h")).read()
+    for name, value in (("AR_ROUTE_WORKSPACE", training.ROUTE_WORKSPACE),
+                        ("AR_MAX_EXPERTS", training.MAX_EXPERTS), ("AR_MAX_TOP_K", training.MAX_TOP_K),
+                        ("AR_ADAMW_BLOCK", training.BLOCK)):
+        assert f"#define {name} {value}\n" in text

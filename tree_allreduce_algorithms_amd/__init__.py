@@ -1,5 +1,6 @@
-"""MI355X-native ring / tree collectives over N rank buffers on one GPU, and the
-AdamW step that updates a rank's shard between them.
+"""MI355X-native ring / tree collectives over N rank buffers on one GPU, with
+the AdamW step that updates a rank's shard between them and the router that
+sends tokens to experts.
 
 The operators live in a C-ABI shared library (``libar.so``: HIP kernels for
 gfx950 plus the C ABI declared in ``include/ar.h``); this package is a thin
@@ -37,4 +38,4 @@ from .binding import (  # noqa: F401
     set_impl,
     tree_allreduce,
 )
-from .training import AdamW, dequantize  # noqa: F401
+from .training import AdamW, Routing, dequantize, route, route_grad  # noqa: F401

@@ -37,6 +37,13 @@ class AdamwStep(ctypes.Structure):
                [("step", ctypes.c_int64), ("clip", ctypes.c_int)]
 
 
+class RouteShape(ctypes.Structure):
+    """ar_route_shape_t."""
+    _fields_ = [("nranks", ctypes.c_int), ("tokens", ctypes.c_size_t), ("experts", ctypes.c_int),
+                ("row_stride", ctypes.c_size_t), ("top_k", ctypes.c_int),
+                ("renormalize", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
 # name -> (restype, argtypes), in the order include/ar.h declares them
 SIGNATURES = {
     "ar_ring_allreduce": (_I, [_PP, _I, _SZ, _I, _I, _VP]),
@@ -72,6 +79,8 @@ SIGNATURES = {
     "ar_adamw_grad_norm": (_I, [_VP, _VP, ctypes.c_double, ctypes.c_double, _VP, _VP]),
     "ar_adamw_step": (_I, [_VP, _VP, ctypes.POINTER(AdamwStep), _VP]),
     "ar_adamw_dequantize": (_I, [_VP, _VP, _SZ, _I, _VP, _VP]),
+    "ar_route": (_I, [_VP, _VP, ctypes.POINTER(RouteShape)] + [_VP] * 7),
+    "ar_route_grad": (_I, [_VP, _VP, ctypes.POINTER(RouteShape)] + [_VP] * 6),
     "ar_debug_fail_launch": (_I, [_I]),
 }
 

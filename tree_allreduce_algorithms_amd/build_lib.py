@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libar.so")
 
 SOURCES = ["api.cpp", "plan.cpp", "ring_kernels.hip", "copy_kernels.hip", "tree_kernels.hip",
-           "step_kernels.hip", "train/adamw.cpp", "train/adamw_kernels.hip"]
+           "step_kernels.hip", "train/adamw.cpp", "train/adamw_kernels.hip", "train/route.cpp",
+           "train/route_kernels.hip"]
 
 COMPILE_FLAGS = [
     "--offload-arch=gfx950",

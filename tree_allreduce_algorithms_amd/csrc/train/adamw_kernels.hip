@@ -9,11 +9,11 @@
 // across its lanes and no LDS.
 #include "device_common.hpp"
 #include "train/adamw.hpp"
+#include "train/wave.hpp"
 
 namespace ar {
 namespace {
 
-constexpr int kWave = 64;
 constexpr int kQuad = 4;                                  // elements a lane holds of each step
 static_assert(kWave * kQuad == AR_ADAMW_BLOCK, "a wave's step is a block of an 8-bit state");
 static_assert(kBlock * kQuad == kAdamwStep, "a block's step");
@@ -97,25 +97,6 @@ __device__ __forceinline__ bool lanes_of(const AdamwTensor& t, uint64_t tile_beg
 
 // --- the norm --------------------------------------------------------------------
 
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-  for (int d = kWave / 2; d > 0; d /= 2) x += __shfl_xor(x, d);
-  return x;
-}
-
-// Sum over the block, in lane then wave order; every thread gets it.
-__device__ __forceinline__ double block_sum(double x) {
-  __shared__ double part[kBlock / kWave];
-  x = wave_sum(x);
-  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = x;
-  __syncthreads();
-  double s = part[0];
-#pragma unroll
-  for (int w = 1; w < kBlock / kWave; ++w) s += part[w];
-  __syncthreads();
-  return s;
-}
-
 // The squares are exact in 64 bits and are added up in 64 bits: the clipping
 // factor must be the float32 nearest to max_norm / norm, because 8-bit codes
 // are decided on what it scales.  Every block leaves a partial sum; the one
@@ -143,21 +124,15 @@ template <class G> __global__ __launch_bounds__(kBlock) void adamw_norm_kernel(A
       }
     }
   }
-  sum = block_sum(sum);
-  __shared__ bool last;
-  if (threadIdx.x == 0) {
+  sum = block_sum<kBlock>(sum);
+  if (threadIdx.x == 0)
     __hip_atomic_store(&partials[blockIdx.x], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const uint32_t before =
-        __hip_atomic_fetch_add(&head->arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-    last = before == gridDim.x - 1;
-  }
-  __syncthreads();
-  if (!last) return;
+  if (!last_to_arrive(&head->arrived, gridDim.x)) return;
 
   double all = 0.0;
   for (uint32_t i = threadIdx.x; i < gridDim.x; i += kBlock)
     all += __hip_atomic_load(&partials[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  all = block_sum(all);
+  all = block_sum<kBlock>(all);
   if (threadIdx.x == 0) {
     const double norm = fabs(a.grad_scale) * sqrt(all);
     const float c = norm > a.max_norm ? static_cast<float>(a.max_norm / norm) : 1.0f;
@@ -168,21 +143,6 @@ template <class G> __global__ __launch_bounds__(kBlock) void adamw_norm_kernel(A
 }
 
 // --- 8-bit states ------------------------------------------------------------------
-
-// Maximum over the wave's lanes: row shifts by 1, 2, 4, 8 and the two row
-// broadcasts leave it in lane 63.
-__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-#define AR_DPP_MAX(ctrl) \
-  x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), ctrl, 0xf, 0xf, false)))
-  AR_DPP_MAX(0x111);
-  AR_DPP_MAX(0x112);
-  AR_DPP_MAX(0x114);
-  AR_DPP_MAX(0x118);
-  AR_DPP_MAX(0x142);
-  AR_DPP_MAX(0x143);
-#undef AR_DPP_MAX
-  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), 63));
-}
 
 // Largest of the wave's doubles, none of them negative; a NaN counts as
 // larger than all.  Such numbers are ordered as their bits are: first the

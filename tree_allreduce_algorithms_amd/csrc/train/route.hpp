@@ -1,0 +1,57 @@
+// The expert router: what the entry points hand to the kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "kernels.hpp"
+
+namespace ar {
+
+// A router call's sums (AR_ROUTE_WORKSPACE bytes of device memory, zero
+// between calls).
+struct RouteSums {
+  uint64_t share[AR_MAX_EXPERTS];                  // S_e in steps of 2^-32
+  uint32_t counts[AR_MAX_RANKS * AR_MAX_EXPERTS];  // [rank][experts]
+  uint32_t tokens;                                 // that live
+  uint32_t not_finite;                             // a block's sum was not a number
+  uint32_t arrived;                                // blocks that have added their sums
+  uint32_t pad[61];
+};
+static_assert(sizeof(RouteSums) == AR_ROUTE_WORKSPACE, "the workspace's documented size");
+
+struct RouteArgs {
+  RankPtrs logits;
+  RankPtrs masks;                  // p[0] NULL: none
+  RouteSums* sums;
+  int32_t* indices;
+  float* weights;
+  int32_t* counts;
+  float* loss;
+  float* share;
+  uint64_t row_stride;             // elements
+  uint32_t tokens;                 // of a rank
+  uint32_t rows_per_block;         // blocks (x, rank): tokens [x, x + 1) * rows_per_block
+  int nranks, experts, top_k, renormalize;
+};
+
+struct RouteGradArgs {
+  RankPtrs logits;
+  RankPtrs masks;
+  RankPtrs dweights;               // p[0] NULL: none
+  const int32_t* indices;
+  const float* share;
+  const float* dloss;              // NULL: 0
+  void* dlogits;
+  uint64_t row_stride;
+  uint32_t tokens;
+  uint32_t rows_per_block;
+  int nranks, experts, top_k, renormalize;
+};
+
+// rows_per_block is set by the launchers.
+hipError_t launch_route(RouteArgs a, ar_dtype_t dtype, hipStream_t stream);
+hipError_t launch_route_grad(RouteGradArgs a, ar_dtype_t dtype, hipStream_t stream);
+
+}  // namespace ar

@@ -1,0 +1,60 @@
+// Reductions across a wave's 64 lanes or a block, shared by the training
+// kernels (gfx950).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace ar {
+namespace {
+
+constexpr int kWave = 64;
+
+// Maximum over the wave's lanes: row shifts by 1, 2, 4, 8 and the two row
+// broadcasts leave it in lane 63.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+#define AR_DPP_MAX(ctrl) \
+  x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), ctrl, 0xf, 0xf, false)))
+  AR_DPP_MAX(0x111);
+  AR_DPP_MAX(0x112);
+  AR_DPP_MAX(0x114);
+  AR_DPP_MAX(0x118);
+  AR_DPP_MAX(0x142);
+  AR_DPP_MAX(0x143);
+#undef AR_DPP_MAX
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), 63));
+}
+
+template <class T> __device__ __forceinline__ T wave_sum(T x) {
+#pragma unroll
+  for (int d = kWave / 2; d > 0; d /= 2) x += __shfl_xor(x, d);
+  return x;
+}
+
+// Sum over the block's waves, in wave order; every thread gets it.
+template <int BLOCK> __device__ __forceinline__ double block_sum(double x) {
+  __shared__ double part[BLOCK / kWave];
+  x = wave_sum(x);
+  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = x;
+  __syncthreads();
+  double s = part[0];
+#pragma unroll
+  for (int w = 1; w < BLOCK / kWave; ++w) s += part[w];
+  __syncthreads();
+  return s;
+}
+
+// True in every thread of the block that is the last of `blocks` to get here,
+// which then sees what the others stored before; `arrived` counts them from 0.
+__device__ __forceinline__ bool last_to_arrive(uint32_t* arrived, uint32_t blocks) {
+  __shared__ bool last;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == blocks - 1;
+  __syncthreads();
+  return last;
+}
+
+}  // namespace
+}  // namespace ar

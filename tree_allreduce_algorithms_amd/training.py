@@ -1,4 +1,5 @@
-"""The training step next to the collectives: AdamW over many tensors at once.
+"""The training step next to the collectives: AdamW over many tensors at once
+and the router of a mixture of experts.
 
 Argument marshalling only, as in ``binding``: the work is done by libar.so's
 HIP kernels, on the current stream unless a call names another.
@@ -7,9 +8,11 @@ HIP kernels, on the current stream unless a call names another.
 import ctypes
 
 from . import binding
-from .binding import DTYPES, SUCCESS, AdamwStep, AdamwTensor, ArError, lib
+from .binding import DTYPES, SUCCESS, AdamwStep, AdamwTensor, ArError, RouteShape, lib
 
 BLOCK = 256   # elements that share one scale of an 8-bit state
+MAX_EXPERTS, MAX_TOP_K = 1024, 8
+ROUTE_WORKSPACE = 270592   # AR_ROUTE_WORKSPACE
 
 
 def _handle(stream, dev):
@@ -154,6 +157,11 @@ def dequantize(codes, scales, stream=None):
     """float32 values of the codes of an 8-bit AdamW state: int8 codes of
     ``exp_avg`` or uint8 codes of ``exp_avg_sq``, with one scale per 256."""
     import torch
+    if stream is not None:
+        # the result belongs to that stream: its memory is not handed out
+        # again before the kernel there has run
+        with torch.cuda.stream(_torch_stream(stream, [codes])):
+            return dequantize(codes, scales)
     if not isinstance(codes, torch.Tensor) or not codes.is_cuda or not scales.is_cuda:
         raise TypeError("codes and scales must be GPU tensors")
     if codes.dtype not in (torch.int8, torch.uint8) or scales.dtype != torch.float32:
@@ -164,23 +172,168 @@ def dequantize(codes, scales, stream=None):
         raise ValueError(f"{n} codes need {-(-n // BLOCK)} scales on their device")
     if not codes.is_contiguous() or not scales.is_contiguous():
         raise ValueError("codes and scales must be contiguous")
-    out = _empty(codes.shape, torch.float32, codes.device, stream)
     with binding._on_device(dev):
+        out = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
         status = lib().ar_adamw_dequantize(codes.data_ptr(), scales.data_ptr(), n,
                                            1 if codes.dtype == torch.int8 else 0, out.data_ptr(),
-                                           _handle(stream, dev))
+                                           _handle(None, dev))
     if status != SUCCESS:
         raise ArError(status, "dequantize")
     return out
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor for a kernel on `stream`: it belongs to that stream, so its
-    memory is not handed out again before the kernel there has run."""
+# --- the router ------------------------------------------------------------------
+
+class Routing:
+    """What ``route`` found, for the expert exchange and for ``route_grad``:
+    ``indices`` [ranks, tokens, top_k] int32, ``weights`` (same shape, float32),
+    ``counts`` [ranks, experts] int32, ``loss`` (float32 scalar) and ``share``
+    [experts] float32 (see ar_route)."""
+
+    __slots__ = ("indices", "weights", "counts", "loss", "share", "_mask", "_shape")
+
+    def __init__(self, indices, weights, counts, loss, share, mask, shape):
+        self.indices, self.weights, self.counts = indices, weights, counts
+        self.loss, self.share, self._mask, self._shape = loss, share, mask, shape
+
+
+def _table(tensors):
+    """A host array of the tensors' addresses."""
+    return (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
+
+
+def _logits(logits):
+    """The ranks' logits as a list, checked: [tokens, experts] GPU tensors of
+    one type, size and row stride, experts next to each other."""
     import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+    logits = list(logits)
+    if not 1 <= len(logits) <= binding.MAX_RANKS:
+        raise ValueError(f"need the logits of 1 to {binding.MAX_RANKS} ranks")
+    first = logits[0]
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise TypeError("logits must be GPU tensors")
+    if first.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {first.dtype}")
+    shape, stride, dtype, dev = first.shape, first.stride(), first.dtype, first.device
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError("logits must be [tokens, experts]")
+    if stride[1] != 1 and shape[1] > 1 and shape[0] > 0 or (shape[0] > 1 and stride[0] < shape[1]):
+        raise ValueError("a token's logits must lie next to each other, tokens apart")
+    for t in logits:
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev:
+            raise TypeError("logits must share type and device")
+        if t.shape != shape or t.stride() != stride:
+            raise ValueError("logits must share shape and strides")
+    return logits, shape[0], shape[1], max(stride[0], shape[1])
+
+
+def _ranks(tensors, n, shape, dtype, dev, what):
+    """One contiguous tensor a rank, as a list and as a table of addresses."""
+    import torch
+    tensors = list(tensors)
+    if len(tensors) != n:
+        raise ValueError(f"{what}: {len(tensors)} tensors for {n} ranks")
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev:
+            raise TypeError(f"{what} must be {dtype} on the logits' device")
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous, {tuple(shape)} a rank")
+    return tensors, _table(tensors)
+
+
+_route_workspaces = {}   # (device, stream handle) -> zeroed workspace
+
+
+def _route_workspace(device, handle):
+    """The stream's workspace, which every call leaves zero.  A captured call
+    gets one of its own, cleared in the graph: its replays may run beside the
+    stream's other calls."""
+    import torch
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(ROUTE_WORKSPACE, dtype=torch.uint8, device=device)
+    key = (device, handle)
+    ws = _route_workspaces.get(key)
+    if ws is None:
+        ws = torch.zeros(ROUTE_WORKSPACE, dtype=torch.uint8, device=device)
+        _route_workspaces[key] = ws
+    return ws
+
+
+def route(logits, top_k, mask=None, renormalize=False, stream=None):
+    """Chooses ``top_k`` experts for every token (see ar_route).
+
+    ``logits`` lists one [tokens, experts] tensor a rank (float32 or bfloat16;
+    rows may be strided); ``mask`` optionally lists one boolean [tokens] tensor
+    a rank, False for what is no token.  Returns a ``Routing``.  Up to 1,024
+    experts and 8 choices."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream, logits)):
+            return route(logits, top_k, mask, renormalize)
+    logits, tokens, experts, row_stride = _logits(logits)
+    n, device = len(logits), logits[0].device
+    if not 1 <= top_k <= min(experts, MAX_TOP_K) or experts > MAX_EXPERTS:
+        raise ValueError(f"top_k must be 1 to {min(experts, MAX_TOP_K)} of at most {MAX_EXPERTS} "
+                         f"experts, not {top_k} of {experts}")
+    masks = None
+    if mask is not None:
+        mask, masks = _ranks(mask, n, (tokens,), torch.bool, device, "mask")
+    shape = RouteShape(n, tokens, experts, row_stride, top_k, 1 if renormalize else 0,
+                       1 if logits[0].dtype == torch.float32 else 2)
+    with binding._on_device(device.index):
+        handle = torch.cuda.current_stream(device).cuda_stream
+        indices = torch.empty((n, tokens, top_k), dtype=torch.int32, device=device)
+        weights = torch.empty((n, tokens, top_k), dtype=torch.float32, device=device)
+        counts = torch.empty((n, experts), dtype=torch.int32, device=device)
+        loss = torch.empty((), dtype=torch.float32, device=device)
+        share = torch.empty(experts, dtype=torch.float32, device=device)
+        status = lib().ar_route(_table(logits), masks, ctypes.byref(shape), indices.data_ptr(),
+                                weights.data_ptr(), counts.data_ptr(), loss.data_ptr(),
+                                share.data_ptr(), _route_workspace(device, handle).data_ptr(), handle)
+    if status != SUCCESS:
+        raise ArError(status, "route")
+    return Routing(indices, weights, counts, loss, share, (mask, masks), shape)
+
+
+def route_grad(logits, routing, dweights=None, dloss=None, stream=None):
+    """Gradient of ``sum(dweights * weights) + dloss * loss`` with respect to
+    the logits, [ranks, tokens, experts] of their type (see ar_route_grad).
+
+    ``logits`` are those that ``route`` took for ``routing``; ``dweights``
+    lists one float32 [tokens, top_k] tensor a rank, ``dloss`` is a float32 GPU
+    scalar; either may be left out."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream, logits)):
+            return route_grad(logits, routing, dweights, dloss)
+    logits, tokens, experts, row_stride = _logits(logits)
+    n, device, was = len(logits), logits[0].device, routing._shape
+    code = 1 if logits[0].dtype == torch.float32 else 2
+    if (n, tokens, experts, code) != (was.nranks, was.tokens, was.experts, was.dtype) or \
+            device != routing.indices.device:
+        raise ValueError("these are not the logits of this routing")
+    grads = None
+    if dweights is not None:
+        dweights, grads = _ranks(dweights, n, (tokens, was.top_k), torch.float32, device, "dweights")
+    if dloss is not None and (dloss.dtype != torch.float32 or dloss.device != device or dloss.numel() != 1):
+        raise ValueError("dloss must be one float32 on the logits' device")
+    shape = was
+    if row_stride != was.row_stride:
+        shape = RouteShape(n, tokens, experts, row_stride, was.top_k, was.renormalize, code)
+    with binding._on_device(device.index):
+        dlogits = torch.empty((n, tokens, experts), dtype=logits[0].dtype, device=device)
+        status = lib().ar_route_grad(_table(logits), routing._mask[1], ctypes.byref(shape),
+                                     routing.indices.data_ptr(), routing.share.data_ptr(), grads,
+                                     None if dloss is None else dloss.data_ptr(), dlogits.data_ptr(),
+                                     torch.cuda.current_stream(device).cuda_stream)
+    if status != SUCCESS:
+        raise ArError(status, "route_grad")
+    return dlogits
+
+
+def _torch_stream(stream, tensors):
+    """`stream`, or a raw handle on the device of the first of `tensors`, as a torch stream."""
+    import torch
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=tensors[0].device)
