@@ -393,7 +393,7 @@ size_t ar_adamw_plan_bytes(const ar_adamw_tensor_t* tensors, int ntensors, ar_dt
  * misaligned pointers, copies of some tensors only or of bfloat16 params,
  * scales missing (8) or given (32), a written range that overlaps any other
  * range; AR_ERROR_UNSUPPORTED for other types or state_bits, or more than
- * 2^32 - 1 tiles of work.  A tensor of count 0 is skipped, its pointers not
+ * 2^24 - 1 tiles of (up to) 4,096 elements of one tensor.  A tensor of count 0 is skipped, its pointers not
  * looked at. */
 ar_status_t ar_adamw_plan(const ar_adamw_tensor_t* tensors, int ntensors, ar_dtype_t param_dtype,
                           ar_dtype_t grad_dtype, int state_bits, void* plan, size_t bytes);

@@ -23,26 +23,19 @@ bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p
 struct Layout {
   uint32_t tensors = 0;     // with elements
   uint64_t tiles = 0;
-  uint32_t tile_elements = 0;
   uint64_t tensors_at = 0, tiles_at = 0, bytes = 0;
 };
 
-// Tiles long enough to amortise a block's start where there are plenty, one
-// step long where there are few.
+constexpr uint64_t sums_at() { return (sizeof(AdamwHead) + 255) / 256 * 256; }
+
 Layout layout_of(const ar_adamw_tensor_t* t, int n) {
   Layout l;
-  uint64_t steps = 0;
   for (int i = 0; i < n; ++i) {
     if (t[i].count == 0) continue;
     ++l.tensors;
-    steps += (t[i].count - 1) / ar::kAdamwStep + 1;
+    l.tiles += (t[i].count - 1) / ar::kAdamwTile + 1;
   }
-  uint64_t per = 1;
-  while (per < ar::kMaxTileSteps && steps >= 2 * per * ar::kMaxNormBlocks) per *= 2;
-  l.tile_elements = static_cast<uint32_t>(per * ar::kAdamwStep);
-  for (int i = 0; i < n; ++i)
-    if (t[i].count != 0) l.tiles += (t[i].count - 1) / l.tile_elements + 1;
-  l.tensors_at = align16(sizeof(AdamwHead)) + ar::kMaxNormBlocks * sizeof(double);
+  l.tensors_at = sums_at() + sizeof(ar::AdamwSums);
   l.tiles_at = align16(l.tensors_at + l.tensors * sizeof(AdamwTensor));
   l.bytes = align16(l.tiles_at + l.tiles * sizeof(AdamwTile));
   return l;
@@ -137,7 +130,7 @@ ar_status_t ar_adamw_plan(const ar_adamw_tensor_t* tensors, int ntensors, ar_dty
   if (st != AR_SUCCESS) return st;
   const Layout l = layout_of(tensors, ntensors);
   if (plan == nullptr || bytes < l.bytes || !aligned(plan, 8)) return AR_ERROR_INVALID_ARGUMENT;
-  if (l.tiles > std::numeric_limits<uint32_t>::max()) return AR_ERROR_UNSUPPORTED;
+  if (l.tiles > ar::kAdamwMaxTiles) return AR_ERROR_UNSUPPORTED;
 
   char* base = static_cast<char*>(plan);
   std::memset(base, 0, l.bytes);
@@ -145,15 +138,14 @@ ar_status_t ar_adamw_plan(const ar_adamw_tensor_t* tensors, int ntensors, ar_dty
   h->magic = ar::kAdamwMagic;
   h->tensors = l.tensors;
   h->tiles = static_cast<uint32_t>(l.tiles);
-  h->tile_elements = l.tile_elements;
+  h->tile_elements = ar::kAdamwTile;
   h->param_dtype = param_dtype;
   h->grad_dtype = grad_dtype;
   h->state_bits = state_bits;
   h->bytes = l.bytes;
-  h->partials_at = align16(sizeof(AdamwHead));
+  h->sums_at = sums_at();
   h->tensors_at = l.tensors_at;
   h->tiles_at = l.tiles_at;
-  h->factor = 1.0f;
   AdamwTensor* out = reinterpret_cast<AdamwTensor*>(base + l.tensors_at);
   AdamwTile* tile = reinterpret_cast<AdamwTile*>(base + l.tiles_at);
   const uintptr_t pquad = param_dtype == AR_FLOAT32 ? 16 : 8, gquad = grad_dtype == AR_FLOAT32 ? 16 : 8;
@@ -167,7 +159,7 @@ ar_status_t ar_adamw_plan(const ar_adamw_tensor_t* tensors, int ntensors, ar_dty
                      aligned(x.exp_avg, squad) && aligned(x.exp_avg_sq, squad);
     out[k] = {x.param, x.grad, x.copy, x.exp_avg, x.exp_avg_sq, x.exp_avg_scale, x.exp_avg_sq_scale,
               x.count, vec ? 1u : 0u, {0, 0, 0}};
-    const uint64_t n = (x.count - 1) / l.tile_elements + 1;
+    const uint64_t n = (x.count - 1) / ar::kAdamwTile + 1;
     for (uint64_t j = 0; j < n; ++j) *tile++ = {k, static_cast<uint32_t>(j)};
     ++k;
   }
@@ -181,11 +173,10 @@ ar_status_t ar_adamw_grad_norm(const void* plan, void* device_plan, double max_n
     return AR_ERROR_INVALID_ARGUMENT;
   ar::AdamwNormArgs a;
   a.plan = static_cast<char*>(device_plan);
-  a.partials_at = h->partials_at;
+  a.sums_at = h->sums_at;
   a.tensors_at = h->tensors_at;
   a.tiles_at = h->tiles_at;
   a.tiles = h->tiles;
-  a.tile_elements = h->tile_elements;
   a.max_norm = max_norm;
   a.grad_scale = grad_scale;
   a.norm = norm;
@@ -212,19 +203,21 @@ ar_status_t ar_adamw_step(const void* plan, void* device_plan, const ar_adamw_st
   ar::AdamwStepArgs a;
   a.plan = static_cast<char*>(device_plan);
   a.tensors_at = h->tensors_at;
+  a.sums_at = h->sums_at;
   a.tiles_at = h->tiles_at;
-  a.tile_elements = h->tile_elements;
   a.clip = s->clip != 0;
   a.factor = static_cast<float>(s->grad_scale);
-  a.lr = static_cast<float>(s->lr);
+  const double bc1 = 1.0 - std::pow(s->beta1, static_cast<double>(s->step));
+  const double bc2 = 1.0 - std::pow(s->beta2, static_cast<double>(s->step));
+  a.lr = static_cast<float>(s->lr * std::sqrt(bc2) / bc1);
+  a.eps = static_cast<float>(s->eps * std::sqrt(bc2));
   a.lr_wd = static_cast<float>(s->lr * s->weight_decay);
-  a.eps = static_cast<float>(s->eps);
-  a.bc1 = static_cast<float>(1.0 - std::pow(s->beta1, static_cast<double>(s->step)));
-  a.bc2 = static_cast<float>(1.0 - std::pow(s->beta2, static_cast<double>(s->step)));
   a.b1 = s->beta1;
   a.one_b1 = 1.0 - s->beta1;
   a.b2 = s->beta2;
   a.one_b2 = 1.0 - s->beta2;
+  a.root_b2 = std::sqrt(a.b2);
+  a.root_one_b2 = std::sqrt(a.one_b2);
   return ar::launch_status(ar::enqueue([&] {
     return ar::launch_adamw_step(a, h->tiles, static_cast<ar_dtype_t>(h->param_dtype),
                                  static_cast<ar_dtype_t>(h->grad_dtype), h->state_bits,

@@ -1,8 +1,8 @@
 // AdamW plans: what the host lays out and the kernels read.
 //
 // A plan is one image, identical in host and device memory:
-//   AdamwHead     sizes and types (host reads), and the norm's results
-//   partials      kMaxNormBlocks doubles (device only)
+//   AdamwHead     sizes and types (the host reads them)
+//   AdamwSums     the norm's partial sums and results (device only)
 //   tensors       one AdamwTensor per tensor that has elements
 //   tiles         one AdamwTile per unit of work
 // All offsets are from the image's start.
@@ -17,9 +17,16 @@
 namespace ar {
 
 constexpr uint32_t kAdamwMagic = 0x41573031u;
+constexpr uint32_t kAdamwTile = 4096;       // elements of a tile
+
+// One block a tile; a launch has less than 2^32 threads.
+constexpr uint32_t kAdamwMaxTiles = (1u << 24) - 1;
+
+// Blocks of a norm, and how many of them make a group: the sums of a group's
+// blocks, and those of the groups, are added up by one block.
 constexpr uint32_t kMaxNormBlocks = 2048;
-constexpr uint32_t kAdamwStep = 1024;       // elements a block handles at a time
-constexpr uint32_t kMaxTileSteps = 4;
+constexpr uint32_t kNormGroup = 64;
+constexpr uint32_t kNormGroups = kMaxNormBlocks / kNormGroup;
 
 struct AdamwHead {
   uint32_t magic;
@@ -31,14 +38,19 @@ struct AdamwHead {
   int32_t state_bits;
   int32_t has_copy;
   uint64_t bytes;
-  uint64_t partials_at;
+  uint64_t sums_at;
   uint64_t tensors_at;
   uint64_t tiles_at;
-  // device side: the last norm's factor, and how many blocks of the running
-  // norm have left their partial sum (0 between calls)
-  float factor;
-  uint32_t arrived;
-  uint64_t pad;
+};
+
+struct AdamwSums {
+  double of_block[kMaxNormBlocks];
+  double of_group[kNormGroups];
+  // how many have left their sum, 0 between calls; each in a line of its own
+  struct alignas(256) Counter {
+    uint32_t count;
+  } arrived[kNormGroups], groups_arrived;
+  alignas(256) float factor;                // of the last norm
 };
 
 struct AdamwTensor {
@@ -56,13 +68,13 @@ struct AdamwTensor {
 
 struct AdamwTile {
   uint32_t tensor;
-  uint32_t index;    // elements [index, index + 1) * tile_elements of it
+  uint32_t index;    // elements [index, index + 1) * kAdamwTile of it
 };
 
 struct AdamwNormArgs {
   char* plan;
-  uint64_t partials_at, tensors_at, tiles_at;
-  uint32_t tiles, tile_elements;
+  uint64_t sums_at, tensors_at, tiles_at;
+  uint32_t tiles;
   double max_norm;
   double grad_scale;
   float* norm;
@@ -70,12 +82,14 @@ struct AdamwNormArgs {
 
 struct AdamwStepArgs {
   char* plan;
-  uint64_t tensors_at, tiles_at;
-  uint32_t tile_elements;
+  uint64_t sums_at, tensors_at, tiles_at;
   int clip;
-  float factor;                     // without clip
-  float lr, lr_wd, eps, bc1, bc2;   // bc = 1 - beta^step
-  double b1, one_b1, b2, one_b2;
+  float factor;               // without clip
+  float lr_wd;
+  float lr, eps;              // with the bias corrections, see updated()
+  double b1, one_b1;          // beta, 1 - beta
+  double b2, one_b2;
+  double root_b2, root_one_b2;
 };
 
 hipError_t launch_adamw_norm(const AdamwNormArgs& a, ar_dtype_t grad_dtype, hipStream_t stream);

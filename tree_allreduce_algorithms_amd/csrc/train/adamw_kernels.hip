@@ -2,11 +2,11 @@
 // states.
 //
 // All three are streams: each element's values are read once and written
-// once, by one lane, so HBM bandwidth is what bounds them.  Work is cut into
-// tiles of one tensor (the plan's table), a tile into steps of 1,024
-// elements, 256 for each of the block's four waves: a wave's 256 elements are
-// one block of an 8-bit state, whose maxima therefore need one reduction
-// across its lanes and no LDS.
+// once, by one lane, so HBM bandwidth is what should bound them.  Work is cut
+// into tiles of kAdamwTile elements of one tensor (the plan's table), one
+// quarter for each of the block's four waves, sixteen elements a lane.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "train/adamw.hpp"
 #include "train/wave.hpp"
@@ -14,64 +14,93 @@
 namespace ar {
 namespace {
 
-constexpr int kQuad = 4;                                  // elements a lane holds of each step
-static_assert(kWave * kQuad == AR_ADAMW_BLOCK, "a wave's step is a block of an 8-bit state");
-static_assert(kBlock * kQuad == kAdamwStep, "a block's step");
+constexpr int kWaveElements = kAdamwTile / (kBlock / kWave);
+constexpr int kQuads = kWaveElements / kWave / 4;          // of a lane
+static_assert(kWaveElements == 4 * AR_ADAMW_BLOCK && kQuads == 4, "a wave's part is four blocks of an 8-bit state");
 
 // --- accesses ------------------------------------------------------------------
 
-// Four consecutive elements in one access, past the caches where it is 16
-// bytes (nothing here is used twice).
+// Four consecutive elements, one access where they are aligned and all exist.
 template <class T> struct Quad {
-  T e[kQuad];
+  T e[4];
 };
 
-template <class T> __device__ __forceinline__ Quad<T> load_quad(const T* p) {
-  using Raw = uint32_t __attribute__((ext_vector_type(sizeof(T))));   // sizeof(T) words
-  if constexpr (sizeof(T) == 1) {
-    return __builtin_bit_cast(Quad<T>, __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p)));
-  } else {
-    return __builtin_bit_cast(Quad<T>, __builtin_nontemporal_load(reinterpret_cast<const Raw*>(p)));
-  }
-}
-template <class T> __device__ __forceinline__ void store_quad(T* p, const Quad<T>& v) {
-  using Raw = uint32_t __attribute__((ext_vector_type(sizeof(T))));
-  if constexpr (sizeof(T) == 1) {
-    __builtin_nontemporal_store(__builtin_bit_cast(uint32_t, v), reinterpret_cast<uint32_t*>(p));
-  } else {
-    __builtin_nontemporal_store(__builtin_bit_cast(Raw, v), reinterpret_cast<Raw*>(p));
-  }
-}
+// Four bytes of codes are a quarter of what a lane group touches of a line at
+// a time, so they go through the caches; wider ones stream past (nothing here
+// is used twice).
+template <class T> struct Raw {
+  using type = uint32_t __attribute__((ext_vector_type(sizeof(T))));
+};
+template <> struct Raw<int8_t> {
+  using type = uint32_t;
+};
+template <> struct Raw<uint8_t> {
+  using type = uint32_t;
+};
 
-// The lane's four elements of a wave's 256: neighbours where the tensor is
-// aligned and the 256 are whole, else 64 apart, each only if it exists.
-struct Lanes {
-  uint64_t base;      // the wave's first element
-  uint32_t live;      // how many of the 256 exist
-  bool quad;
-  __device__ uint32_t at(int j) const {
-    const uint32_t lane = threadIdx.x % kWave;
-    return quad ? lane * kQuad + j : j * kWave + lane;
-  }
-  template <class T> __device__ Quad<T> load(const void* p) const {
-    const T* q = static_cast<const T*>(p) + base;
-    if (quad) return load_quad<T>(q + threadIdx.x % kWave * kQuad);
+// A pointer out of the plan's table is to global memory, which the compiler
+// cannot see; an access that might be to LDS as well (flat) costs more.
+#define AR_GLOBAL __attribute__((address_space(1)))
+
+// Which elements of a tensor a lane has: kQuads runs of four, `step` apart.
+// WHOLE: all of the wave's elements exist, and the tensor's pointers allow
+// quads.  Only the last wave of a tensor takes the other path, or one whose
+// tensors are aligned to their elements only.
+template <bool WHOLE> struct Lanes {
+  uint64_t first, count;
+  uint32_t step;
+  bool vec;       // the tensor's pointers allow quads
+  __device__ uint64_t at(int q) const { return first + q * step; }
+  template <class T> __device__ __forceinline__ Quad<T> load(const void* p, int q) const {
+    using R = typename Raw<T>::type;
+    const AR_GLOBAL T* x = (const AR_GLOBAL T*)p + at(q);
+    if (WHOLE || (vec && at(q) + 4 <= count)) {
+      if constexpr (sizeof(T) == 1)
+        return __builtin_bit_cast(Quad<T>, *(const AR_GLOBAL R*)x);
+      else
+        return __builtin_bit_cast(Quad<T>, __builtin_nontemporal_load((const AR_GLOBAL R*)x));
+    }
     Quad<T> v;
 #pragma unroll
-    for (int j = 0; j < kQuad; ++j) v.e[j] = at(j) < live ? q[at(j)] : T(0);
+    for (int i = 0; i < 4; ++i) v.e[i] = at(q) + i < count ? x[i] : T(0);
     return v;
   }
-  template <class T> __device__ void store(void* p, const Quad<T>& v) const {
-    T* q = static_cast<T*>(p) + base;
-    if (quad) {
-      store_quad<T>(q + threadIdx.x % kWave * kQuad, v);
+  template <class T> __device__ __forceinline__ void store(void* p, int q, const Quad<T>& v) const {
+    using R = typename Raw<T>::type;
+    AR_GLOBAL T* x = (AR_GLOBAL T*)p + at(q);
+    if (WHOLE || (vec && at(q) + 4 <= count)) {
+      if constexpr (sizeof(T) == 1)
+        *(AR_GLOBAL R*)x = __builtin_bit_cast(R, v);
+      else
+        __builtin_nontemporal_store(__builtin_bit_cast(R, v), (AR_GLOBAL R*)x);
     } else {
 #pragma unroll
-      for (int j = 0; j < kQuad; ++j)
-        if (at(j) < live) q[at(j)] = v.e[j];
+      for (int i = 0; i < 4; ++i)
+        if (at(q) + i < count) x[i] = v.e[i];
     }
   }
 };
+
+// The wave's first element of a tile.
+__device__ __forceinline__ uint64_t wave_begin(const AdamwTile& tile) {
+  return static_cast<uint64_t>(tile.index) * kAdamwTile + wave_uniform(threadIdx.x / kWave) * kWaveElements;
+}
+
+__device__ __forceinline__ bool whole(uint64_t begin, uint64_t count, bool vec) {
+  return vec && begin + kWaveElements <= count;
+}
+
+// A wave's elements spread so that each of its accesses is one run.
+template <bool WHOLE> __device__ __forceinline__ Lanes<WHOLE> runs_of(uint64_t begin, uint64_t count, bool vec) {
+  return {begin + threadIdx.x % kWave * 4, count, 4 * kWave, vec};
+}
+
+// The same elements, each row of 16 lanes with one block of 256: an access is
+// four runs of 16 quads, and a block's maximum needs the row only.
+template <bool WHOLE> __device__ __forceinline__ Lanes<WHOLE> rows_of(uint64_t begin, uint64_t count, bool vec) {
+  const uint32_t lane = threadIdx.x % kWave;
+  return {begin + lane / 16 * AR_ADAMW_BLOCK + lane % 16 * 4, count, 64, vec};
+}
 
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(uint16_t x) { return bf16_widen(x); }
@@ -85,207 +114,289 @@ template <class T> __device__ __forceinline__ Quad<T> narrow(const Quad<float>& 
   }
 }
 
-// The wave's part of step `s` of a tile; false where nothing of it exists.
-__device__ __forceinline__ bool lanes_of(const AdamwTensor& t, uint64_t tile_begin, uint32_t s, Lanes* l) {
-  l->base = tile_begin + s * kAdamwStep + threadIdx.x / kWave * AR_ADAMW_BLOCK;
-  if (l->base >= t.count) return false;
-  const uint64_t left = t.count - l->base;
-  l->live = left < AR_ADAMW_BLOCK ? static_cast<uint32_t>(left) : AR_ADAMW_BLOCK;
-  l->quad = t.vec != 0 && l->live == AR_ADAMW_BLOCK;
-  return true;
-}
-
 // --- the norm --------------------------------------------------------------------
+
+template <bool WHOLE, class G>
+__device__ __forceinline__ void add_squares(const AdamwTensor& t, uint64_t begin, double* sum) {
+  const Lanes<WHOLE> l = runs_of<WHOLE>(begin, t.count, t.vec != 0);
+  Quad<G> g[kQuads];
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q) g[q] = l.template load<G>(t.g, q);
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double x = widen(g[q].e[i]);
+      sum[i] = fma(x, x, sum[i]);
+    }
+}
 
 // The squares are exact in 64 bits and are added up in 64 bits: the clipping
 // factor must be the float32 nearest to max_norm / norm, because 8-bit codes
-// are decided on what it scales.  Every block leaves a partial sum; the one
-// that arrives last adds them up in their order and sets the factor, so a
-// norm is one launch and its bits do not depend on which block that is.
+// are decided on what it scales.  Every block leaves a partial sum; the last
+// block of each group adds up the group's, the last group the groups', each
+// in their order, so a norm is one launch and its bits do not depend on which
+// block comes last.  (One counter for all blocks would take the 2,048 of a
+// large norm 40 us: an atomic on one address measured 20 ns.)
 template <class G> __global__ __launch_bounds__(kBlock) void adamw_norm_kernel(AdamwNormArgs a) {
   const AdamwTensor* tensors = reinterpret_cast<const AdamwTensor*>(a.plan + a.tensors_at);
   const AdamwTile* tiles = reinterpret_cast<const AdamwTile*>(a.plan + a.tiles_at);
-  double* partials = reinterpret_cast<double*>(a.plan + a.partials_at);
-  AdamwHead* head = reinterpret_cast<AdamwHead*>(a.plan);
+  AdamwSums* sums = reinterpret_cast<AdamwSums*>(a.plan + a.sums_at);
 
-  double sum = 0.0;
+  double sum[4] = {0.0, 0.0, 0.0, 0.0};
   for (uint32_t i = blockIdx.x; i < a.tiles; i += gridDim.x) {
     const AdamwTile tile = tiles[i];
     const AdamwTensor& t = tensors[tile.tensor];
-    const uint64_t begin = static_cast<uint64_t>(tile.index) * a.tile_elements;
-    for (uint32_t s = 0; s < a.tile_elements / kAdamwStep; ++s) {
-      Lanes l;
-      if (!lanes_of(t, begin, s, &l)) break;
-      const Quad<G> g = l.load<G>(t.g);
-#pragma unroll
-      for (int j = 0; j < kQuad; ++j) {
-        const double x = widen(g.e[j]);
-        sum = fma(x, x, sum);
-      }
-    }
+    const uint64_t begin = wave_begin(tile);
+    if (begin >= t.count) continue;
+    if (whole(begin, t.count, t.vec != 0))
+      add_squares<true, G>(t, begin, sum);
+    else
+      add_squares<false, G>(t, begin, sum);
   }
-  sum = block_sum<kBlock>(sum);
-  if (threadIdx.x == 0)
-    __hip_atomic_store(&partials[blockIdx.x], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if (!last_to_arrive(&head->arrived, gridDim.x)) return;
+  double all = block_sum<kBlock>((sum[0] + sum[1]) + (sum[2] + sum[3]));
 
-  double all = 0.0;
-  for (uint32_t i = threadIdx.x; i < gridDim.x; i += kBlock)
-    all += __hip_atomic_load(&partials[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  all = block_sum<kBlock>(all);
+  const uint32_t group = blockIdx.x / kNormGroup, groups = (gridDim.x - 1) / kNormGroup + 1;
+  const uint32_t first = group * kNormGroup, members = min(kNormGroup, gridDim.x - first);
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) shared_store(&sums->of_block[blockIdx.x], all);
+    if (!last_to_arrive(&sums->arrived[group].count, members)) return;
+    all = block_sum<kBlock>(threadIdx.x < members ? shared_load(&sums->of_block[first + threadIdx.x]) : 0.0);
+    if (threadIdx.x == 0) {
+      sums->arrived[group].count = 0;
+      shared_store(&sums->of_group[group], all);
+    }
+    if (!last_to_arrive(&sums->groups_arrived.count, groups)) return;
+    all = block_sum<kBlock>(threadIdx.x < groups ? shared_load(&sums->of_group[threadIdx.x]) : 0.0);
+    if (threadIdx.x == 0) sums->groups_arrived.count = 0;
+  }
   if (threadIdx.x == 0) {
     const double norm = fabs(a.grad_scale) * sqrt(all);
     const float c = norm > a.max_norm ? static_cast<float>(a.max_norm / norm) : 1.0f;
-    head->factor = static_cast<float>(c * a.grad_scale);
-    head->arrived = 0;
+    sums->factor = static_cast<float>(c * a.grad_scale);
     if (a.norm != nullptr) *a.norm = static_cast<float>(norm);
   }
 }
 
 // --- 8-bit states ------------------------------------------------------------------
 
-// Largest of the wave's doubles, none of them negative; a NaN counts as
-// larger than all.  Such numbers are ordered as their bits are: first the
-// high words, then the low words of the lanes that have the highest.
-__device__ __forceinline__ double wave_max(double x) {
+// Maximum over each row of 16 lanes, by rotations: every lane gets it.
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+#define AR_DPP_MAX(ctrl) \
+  x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), ctrl, 0xf, 0xf, false)))
+  AR_DPP_MAX(0x121);
+  AR_DPP_MAX(0x122);
+  AR_DPP_MAX(0x124);
+  AR_DPP_MAX(0x128);
+#undef AR_DPP_MAX
+  return x;
+}
+
+// Largest of a row's doubles, none of them negative; a NaN counts as larger
+// than all.  Such numbers are ordered as their bits are: first the high
+// words, then the low words of the lanes that have the highest.
+__device__ __forceinline__ double row_max(double x) {
   const uint64_t bits = __builtin_bit_cast(uint64_t, x);
   const uint32_t hi = static_cast<uint32_t>(bits >> 32), lo = static_cast<uint32_t>(bits);
-  const uint32_t top = wave_max(hi);
-  const uint32_t low = wave_max(hi == top ? lo : 0u);
+  const uint32_t top = row_max(hi);
+  const uint32_t low = row_max(hi == top ? lo : 0u);
   return __builtin_bit_cast(double, static_cast<uint64_t>(top) << 32 | low);
 }
 
-__device__ __forceinline__ double larger(double x, double y) {
-  const uint64_t a = __builtin_bit_cast(uint64_t, x), b = __builtin_bit_cast(uint64_t, y);
-  return __builtin_bit_cast(double, a > b ? a : b);
+// Values between the codes j and j + 1 round to j up to the middle between
+// their squares, j^2 + j + 1/2 (in units of the scale).  A float32 root of
+// the value in those units is off by far less than 1/2, and the border lies
+// between (j + 1/2)^2 and (j + 3/4)^2, so the only border in doubt is that
+// above j = floor(root); it is decided in float64, where scale * border is
+// exact.  An 8-bit step thus rounds as the definition in 64 bits does, at the
+// price of about ten float64 instructions a value.
+//
+// Scales are one per block and therefore the same in a row's lanes, which
+// share the cost of computing them over sixteen elements each.
+__device__ __forceinline__ uint32_t floor_root(float t) {
+  return static_cast<uint32_t>(__builtin_amdgcn_sqrtf(t));
 }
 
-// Values between the codes j and j + 1 round to j up to the middle between
-// their squares, j^2 + j + 1/2 = (j + 1/2)^2 + 1/4 (in units of the scale).
-// y = sqrt(t - 1/4) in float32 is off by far less than 1/2, so the only
-// border that can be wrong is that between j and j + 1 with j = floor(y); it
-// is decided in float64, where scale * border is exact.
-__device__ __forceinline__ float border_below(float t, float most) {
-  return fminf(floorf(__builtin_amdgcn_sqrtf(fmaxf(t - 0.25f, 0.0f))), most);
+// The float32 nearest to x / d: one correction step makes the quotient as
+// good as a division's.
+__device__ __forceinline__ float quotient(double x, double d, double inv_d) {
+  const double q = x * inv_d;
+  return static_cast<float>(fma(fma(-q, d, x), inv_d, q));
 }
 
 struct ScaleM {
-  double a, inv;
-  bool ok;
+  double a, half, inv;
+  float stored;
   // `top`: the block's largest |m|
-  __device__ explicit ScaleM(double top, float* scale) {
-    const float s = static_cast<float>(top / 16129.0);
-    ok = s > 0.0f && s < __builtin_inff();
-    *scale = s < __builtin_inff() ? s : __builtin_nanf("");
-    a = s;
-    inv = 1.0 / a;
+  __device__ explicit ScaleM(double top) {
+    const float s = quotient(top, 16129.0, 1.0 / 16129.0);
+    const bool ok = s > 0.0f && s < __builtin_inff();
+    stored = s < __builtin_inff() ? s : __builtin_nanf("");
+    a = ok ? s : __builtin_inf();                 // no value is above its borders
+    half = a * 0.5;
+    inv = ok ? __builtin_amdgcn_rcp(a) : 0.0;
   }
-  __device__ int8_t code(double m) const {
+  __device__ __forceinline__ uint32_t code(double m) const {
     const double x = fabs(m);
-    const float j = border_below(static_cast<float>(x * inv), 126.0f);
-    const float border = fmaf(j, j, j) + 0.5f;
-    const int q = static_cast<int>(j) + (x > a * static_cast<double>(border) ? 1 : 0);
-    return static_cast<int8_t>(ok ? (m < 0.0 ? -q : q) : 0);
+    const uint32_t j = floor_root(static_cast<float>(x * inv));
+    const double border = fma(a, static_cast<double>(j * j + j), half);
+    const int q = min(static_cast<int>(j + (x > border ? 1 : 0)), 127);
+    const int sign = static_cast<int>(__builtin_bit_cast(uint64_t, m) >> 32) >> 31;
+    return static_cast<uint32_t>((q ^ sign) - sign);
   }
 };
 
 struct ScaleV {
-  double r, inv2;
-  bool ok;
+  double r, half, inv2, zero;
+  float stored;
   // `top`: the block's largest v
-  __device__ explicit ScaleV(double top, float* scale) {
-    const float s = static_cast<float>(sqrt(top) / 65025.0);
-    ok = s > 0.0f && s < __builtin_inff();
-    *scale = s < __builtin_inff() ? s : __builtin_nanf("");
-    r = s;
-    inv2 = 1.0 / (r * r);
+  __device__ explicit ScaleV(double top) {
+    const float s = quotient(sqrt(top), 65025.0, 1.0 / 65025.0);
+    const bool ok = s > 0.0f && s < __builtin_inff();
+    stored = s < __builtin_inff() ? s : __builtin_nanf("");
+    r = ok ? s : __builtin_inf();
+    half = r * 0.5;
+    inv2 = ok ? __builtin_amdgcn_rcp(r * r) : 0.0;
+    zero = ok ? 0.0 : __builtin_inf();
   }
-  __device__ uint8_t code(double v) const {
-    const float t = __builtin_amdgcn_sqrtf(static_cast<float>(v * inv2));
-    const float j = border_below(t, 254.0f);
-    const double border = r * static_cast<double>(fmaf(j, j, j) + 0.5f);
-    int u = static_cast<int>(j) + (v > border * border ? 1 : 0);
-    if (u == 0 && v > 0.0) u = 1;
-    return static_cast<uint8_t>(ok ? u : 0);
+  __device__ __forceinline__ uint32_t code(double v) const {
+    const uint32_t j = floor_root(__builtin_amdgcn_sqrtf(static_cast<float>(v * inv2)));
+    const double border = fma(r, static_cast<double>(j * j + j), half);
+    const uint32_t u = min(j + (v > border * border ? 1u : 0u), 255u);
+    return max(u, v > zero ? 1u : 0u);
   }
 };
 
-__device__ __forceinline__ double value_m(int8_t code, double a) {
-  const int q = code;
-  return static_cast<double>(q * (q < 0 ? -q : q)) * a;
+// Four codes as a word; the upper bytes of each are dropped.
+__device__ __forceinline__ uint32_t pack(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), hi = __builtin_amdgcn_perm(d, c, 0x04000c0cu);
+  return lo | hi;
 }
-__device__ __forceinline__ double value_v(uint8_t code, double r) {
-  const uint32_t u = code;
-  const double s = static_cast<double>(u * u) * r;
-  return s * s;
+
+// What a code stands for in units of its scale (m) or its scale's root (v).
+__device__ __forceinline__ double units(int8_t code) {
+  const float q = static_cast<float>(code);
+  return q * fabsf(q);
+}
+__device__ __forceinline__ double units(uint8_t code) {
+  const float u = static_cast<float>(code);
+  return u * u;
 }
 
 // --- the step ------------------------------------------------------------------------
 
+// u = (m / bc1) / (sqrt(v / bc2) + eps), with the two corrections moved to
+// the factor in front and to eps.  The root and the reciprocal are single
+// instructions, off by one step of the last place each; the root takes a
+// subnormal v (a root below 1.1e-19) as 0.
 __device__ __forceinline__ float updated(float p, float m, float v, const AdamwStepArgs& a) {
-  const float u = (m / a.bc1) / (sqrtf(v / a.bc2) + a.eps);
+  const float u = m * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v) + a.eps);
   return p - fmaf(a.lr_wd, p, a.lr * u);
 }
 
-template <class P, class G, bool COPY, int BITS>
-__global__ __launch_bounds__(kBlock) void adamw_step_kernel(AdamwStepArgs a) {
-  const AdamwTensor* tensors = reinterpret_cast<const AdamwTensor*>(a.plan + a.tensors_at);
-  const AdamwTile tile = reinterpret_cast<const AdamwTile*>(a.plan + a.tiles_at)[blockIdx.x];
-  const AdamwTensor& t = tensors[tile.tensor];
-  const float c = a.clip ? reinterpret_cast<const AdamwHead*>(a.plan)->factor : a.factor;
-  const uint64_t begin = static_cast<uint64_t>(tile.index) * a.tile_elements;
-
-  for (uint32_t s = 0; s < a.tile_elements / kAdamwStep; ++s) {
-    Lanes l;
-    if (!lanes_of(t, begin, s, &l)) break;
-    const Quad<P> p = l.load<P>(t.p);
-    const Quad<G> g = l.load<G>(t.g);
+template <bool WHOLE, class P, class G, bool COPY>
+__device__ __forceinline__ void step32(const AdamwStepArgs& a, const AdamwTensor& t, uint64_t begin, float c) {
+  const Lanes<WHOLE> l = runs_of<WHOLE>(begin, t.count, t.vec != 0);
+  const float b1 = static_cast<float>(a.b1), one_b1 = static_cast<float>(a.one_b1);
+  const float b2 = static_cast<float>(a.b2), one_b2 = static_cast<float>(a.one_b2);
+  Quad<P> p[kQuads];
+  Quad<G> g[kQuads];
+  Quad<float> m[kQuads], v[kQuads];
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q) {
+    p[q] = l.template load<P>(t.p, q);
+    g[q] = l.template load<G>(t.g, q);
+    m[q] = l.template load<float>(t.m, q);
+    v[q] = l.template load<float>(t.v, q);
+  }
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q) {
     Quad<float> out;
-    if constexpr (BITS == 32) {
-      Quad<float> m = l.load<float>(t.m), v = l.load<float>(t.v);
-      const float b1 = static_cast<float>(a.b1), one_b1 = static_cast<float>(a.one_b1);
-      const float b2 = static_cast<float>(a.b2), one_b2 = static_cast<float>(a.one_b2);
 #pragma unroll
-      for (int j = 0; j < kQuad; ++j) {
-        const float x = widen(g.e[j]) * c;
-        m.e[j] = fmaf(b1, m.e[j], one_b1 * x);
-        v.e[j] = fmaf(b2, v.e[j], one_b2 * x * x);
-        out.e[j] = updated(widen(p.e[j]), m.e[j], v.e[j], a);
-      }
-      l.store<float>(t.m, m);
-      l.store<float>(t.v, v);
-    } else {
-      const uint64_t block = l.base / AR_ADAMW_BLOCK;
-      const Quad<int8_t> qm = l.load<int8_t>(t.m);
-      const Quad<uint8_t> qv = l.load<uint8_t>(t.v);
-      const double am = t.ms[block], rv = t.vs[block];
-      double m[kQuad], v[kQuad], top_m = 0.0, top_v = 0.0;
-      // m and v in float64: a code changes where a value crosses a border
-#pragma unroll
-      for (int j = 0; j < kQuad; ++j) {
-        const double x = static_cast<double>(widen(g.e[j])) * static_cast<double>(c);
-        m[j] = a.b1 * value_m(qm.e[j], am) + a.one_b1 * x;
-        v[j] = a.b2 * value_v(qv.e[j], rv) + a.one_b2 * x * x;
-        if (!l.quad && l.at(j) >= l.live) m[j] = v[j] = 0.0;
-        top_m = larger(top_m, fabs(m[j]));
-        top_v = larger(top_v, v[j]);
-        out.e[j] = updated(widen(p.e[j]), static_cast<float>(m[j]), static_cast<float>(v[j]), a);
-      }
-      // every lane stores the same scale to the same place
-      const ScaleM sm(wave_max(top_m), &t.ms[block]);
-      const ScaleV sv(wave_max(top_v), &t.vs[block]);
-      Quad<int8_t> nm;
-      Quad<uint8_t> nv;
-#pragma unroll
-      for (int j = 0; j < kQuad; ++j) {
-        nm.e[j] = sm.code(m[j]);
-        nv.e[j] = sv.code(v[j]);
-      }
-      l.store<int8_t>(t.m, nm);
-      l.store<uint8_t>(t.v, nv);
+    for (int i = 0; i < 4; ++i) {
+      const float x = widen(g[q].e[i]) * c;
+      m[q].e[i] = fmaf(b1, m[q].e[i], one_b1 * x);
+      v[q].e[i] = fmaf(b2, v[q].e[i], one_b2 * x * x);
+      out.e[i] = updated(widen(p[q].e[i]), m[q].e[i], v[q].e[i], a);
     }
-    l.store<P>(t.p, narrow<P>(out));
-    if constexpr (COPY) l.store<uint16_t>(t.copy, narrow<uint16_t>(out));
+    l.template store<float>(t.m, q, m[q]);
+    l.template store<float>(t.v, q, v[q]);
+    l.template store<P>(t.p, q, narrow<P>(out));
+    if constexpr (COPY) l.template store<uint16_t>(t.copy, q, narrow<uint16_t>(out));
+  }
+}
+
+template <bool WHOLE, class P, class G, bool COPY>
+__device__ __forceinline__ void step8(const AdamwStepArgs& a, const AdamwTensor& t, uint64_t begin, double c) {
+  const Lanes<WHOLE> l = rows_of<WHOLE>(begin, t.count, t.vec != 0);
+  const uint64_t block = begin / AR_ADAMW_BLOCK + threadIdx.x % kWave / 16;
+  const bool exists = WHOLE || block * AR_ADAMW_BLOCK < t.count;
+  AR_GLOBAL float* ms = (AR_GLOBAL float*)t.ms + block;
+  AR_GLOBAL float* vs = (AR_GLOBAL float*)t.vs + block;
+  const double am = exists ? *ms : 0.0f, rv = exists ? *vs : 0.0f;
+
+  // m and v in float64 (a code changes where a value crosses a border), the
+  // factors of a block's sixteen elements a lane taken together first
+  const double old_m = a.b1 * am, old_v = a.root_b2 * rv;
+  const double new_m = a.one_b1 * c, new_v = a.root_one_b2 * c;
+  double m[kQuads][4], v[kQuads][4], top_m = 0.0, top_v = 0.0, sum_v = 0.0;
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q) {
+    const Quad<P> p = l.template load<P>(t.p, q);
+    const Quad<G> g = l.template load<G>(t.g, q);
+    const Quad<int8_t> qm = l.template load<int8_t>(t.m, q);
+    const Quad<uint8_t> qv = l.template load<uint8_t>(t.v, q);
+    Quad<float> out;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double x = widen(g.e[i]), old = units(qv.e[i]) * old_v, now = x * new_v;
+      m[q][i] = fma(new_m, x, units(qm.e[i]) * old_m);
+      v[q][i] = fma(now, now, old * old);
+      top_m = fmax(top_m, fabs(m[q][i]));
+      top_v = fmax(top_v, v[q][i]);
+      sum_v += v[q][i];
+      out.e[i] = updated(widen(p.e[i]), static_cast<float>(m[q][i]), static_cast<float>(v[q][i]), a);
+    }
+    l.template store<P>(t.p, q, narrow<P>(out));
+    if constexpr (COPY) l.template store<uint16_t>(t.copy, q, narrow<uint16_t>(out));
+  }
+  // a maximum leaves a NaN out; a NaN is in v where the gradient or v's scale
+  // is one, and in m where the gradient or m's scale is
+  if (sum_v != sum_v) top_v = sum_v;
+  if (sum_v != sum_v || am != am) top_m = __builtin_nan("");
+  const ScaleM sm(row_max(top_m));
+  const ScaleV sv(row_max(top_v));
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q) {
+    const uint32_t nm = pack(sm.code(m[q][0]), sm.code(m[q][1]), sm.code(m[q][2]), sm.code(m[q][3]));
+    const uint32_t nv = pack(sv.code(v[q][0]), sv.code(v[q][1]), sv.code(v[q][2]), sv.code(v[q][3]));
+    l.template store<int8_t>(t.m, q, __builtin_bit_cast(Quad<int8_t>, nm));
+    l.template store<uint8_t>(t.v, q, __builtin_bit_cast(Quad<uint8_t>, nv));
+  }
+  if (exists && threadIdx.x % 16 == 0) {
+    *ms = sm.stored;
+    *vs = sv.stored;
+  }
+}
+
+template <int BITS, class P, class G, bool COPY>
+__global__ __launch_bounds__(kBlock) void adamw_step_kernel(AdamwStepArgs a) {
+  const AdamwTile tile = reinterpret_cast<const AdamwTile*>(a.plan + a.tiles_at)[blockIdx.x];
+  const AdamwTensor t = reinterpret_cast<const AdamwTensor*>(a.plan + a.tensors_at)[tile.tensor];
+  const float c = a.clip ? reinterpret_cast<const AdamwSums*>(a.plan + a.sums_at)->factor : a.factor;
+  const uint64_t begin = wave_begin(tile);
+  if (begin >= t.count) return;
+  const bool all = whole(begin, t.count, t.vec != 0);
+  if constexpr (BITS == 32) {
+    if (all)
+      step32<true, P, G, COPY>(a, t, begin, c);
+    else
+      step32<false, P, G, COPY>(a, t, begin, c);
+  } else {
+    if (all)
+      step8<true, P, G, COPY>(a, t, begin, c);
+    else
+      step8<false, P, G, COPY>(a, t, begin, c);
   }
 }
 
@@ -293,31 +404,40 @@ __global__ __launch_bounds__(kBlock) void adamw_step_kernel(AdamwStepArgs a) {
 
 // One rounding per value: the products are taken in float64 (m's is exact
 // there) and rounded to float32.
-template <bool SIGNED>
-__global__ __launch_bounds__(kBlock) void adamw_dequantize_kernel(const void* codes, const float* scales,
-                                                                  uint64_t count, int quads, float* out) {
-  using C = typename std::conditional<SIGNED, int8_t, uint8_t>::type;
-  const uint64_t blocks = (count - 1) / AR_ADAMW_BLOCK + 1;
-  const uint64_t stride = static_cast<uint64_t>(gridDim.x) * (kBlock / kWave);
-  for (uint64_t b = static_cast<uint64_t>(blockIdx.x) * (kBlock / kWave) + threadIdx.x / kWave;
-       b < blocks; b += stride) {
-    Lanes l;
-    l.base = b * AR_ADAMW_BLOCK;
-    const uint64_t left = count - l.base;
-    l.live = left < AR_ADAMW_BLOCK ? static_cast<uint32_t>(left) : AR_ADAMW_BLOCK;
-    l.quad = quads != 0 && l.live == AR_ADAMW_BLOCK;
-    const double scale = scales[b];
-    const Quad<C> q = l.load<C>(codes);
+template <bool WHOLE, class C>
+__device__ __forceinline__ void decode(const C* codes, const float* scales, uint64_t begin, uint64_t count,
+                                       bool vec, float* out) {
+  const Lanes<WHOLE> l = runs_of<WHOLE>(begin, count, vec);
+  Quad<C> code[kQuads];
+  float scale[kQuads];
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q) {
+    code[q] = l.template load<C>(codes, q);
+    const uint64_t first = begin + q * l.step;      // of the block that the wave's q-th run is
+    scale[q] = WHOLE || first < count ? scales[first / AR_ADAMW_BLOCK] : 0.0f;
+  }
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q) {
     Quad<float> x;
 #pragma unroll
-    for (int j = 0; j < kQuad; ++j) {
-      if constexpr (SIGNED)
-        x.e[j] = static_cast<float>(value_m(q.e[j], scale));
-      else
-        x.e[j] = static_cast<float>(value_v(q.e[j], scale));
+    for (int i = 0; i < 4; ++i) {
+      const double y = units(code[q].e[i]) * static_cast<double>(scale[q]);
+      x.e[i] = static_cast<float>(std::is_signed<C>::value ? y : y * y);
     }
-    l.store<float>(out, x);
+    l.template store<float>(out, q, x);
   }
+}
+
+template <class C>
+__global__ __launch_bounds__(kBlock) void adamw_dequantize_kernel(const C* codes, const float* scales,
+                                                                  uint64_t count, int vec, float* out) {
+  const AdamwTile tile = {0, blockIdx.x};
+  const uint64_t begin = wave_begin(tile);
+  if (begin >= count) return;
+  if (whole(begin, count, vec != 0))
+    decode<true>(codes, scales, begin, count, true, out);
+  else
+    decode<false>(codes, scales, begin, count, vec != 0, out);
 }
 
 template <class A> hipError_t launch1(void (*kernel)(A), uint64_t blocks, const A& a, hipStream_t stream) {
@@ -327,11 +447,8 @@ template <class A> hipError_t launch1(void (*kernel)(A), uint64_t blocks, const 
                          dim3(kBlock), args, 0, stream);
 }
 
-template <int BITS>
-void (*step_kernel_for(bool p32, bool g32, bool copy))(AdamwStepArgs) {
-  if (!p32) return g32 ? adamw_step_kernel<uint16_t, float, false, BITS> : adamw_step_kernel<uint16_t, uint16_t, false, BITS>;
-  if (copy) return g32 ? adamw_step_kernel<float, float, true, BITS> : adamw_step_kernel<float, uint16_t, true, BITS>;
-  return g32 ? adamw_step_kernel<float, float, false, BITS> : adamw_step_kernel<float, uint16_t, false, BITS>;
+template <class P, class G, bool COPY> auto step_kernel(int bits) {
+  return bits == 32 ? adamw_step_kernel<32, P, G, COPY> : adamw_step_kernel<8, P, G, COPY>;
 }
 
 }  // namespace
@@ -345,19 +462,25 @@ hipError_t launch_adamw_norm(const AdamwNormArgs& a, ar_dtype_t grad_dtype, hipS
 hipError_t launch_adamw_step(const AdamwStepArgs& a, uint32_t tiles, ar_dtype_t param_dtype,
                              ar_dtype_t grad_dtype, int state_bits, bool copy, hipStream_t stream) {
   const bool p32 = param_dtype == AR_FLOAT32, g32 = grad_dtype == AR_FLOAT32;
-  return launch1(state_bits == 32 ? step_kernel_for<32>(p32, g32, copy) : step_kernel_for<8>(p32, g32, copy),
-                 tiles, a, stream);
+  void (*fn)(AdamwStepArgs);
+  if (!p32)
+    fn = g32 ? step_kernel<uint16_t, float, false>(state_bits) : step_kernel<uint16_t, uint16_t, false>(state_bits);
+  else if (copy)
+    fn = g32 ? step_kernel<float, float, true>(state_bits) : step_kernel<float, uint16_t, true>(state_bits);
+  else
+    fn = g32 ? step_kernel<float, float, false>(state_bits) : step_kernel<float, uint16_t, false>(state_bits);
+  return launch1(fn, tiles, a, stream);
 }
 
 hipError_t launch_adamw_dequantize(const void* codes, const float* scales, uint64_t count,
                                    bool is_signed, float* out, hipStream_t stream) {
-  const uint64_t blocks = ((count - 1) / AR_ADAMW_BLOCK) / (kBlock / kWave) + 1;
-  const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>(blocks, 1u << 20));
-  int quads = reinterpret_cast<uintptr_t>(codes) % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
-  void* args[] = {&codes, &scales, &count, &quads, &out};
-  const void* fn = is_signed ? reinterpret_cast<const void*>(&adamw_dequantize_kernel<true>)
-                             : reinterpret_cast<const void*>(&adamw_dequantize_kernel<false>);
-  return hipLaunchKernel(fn, dim3(grid), dim3(kBlock), args, 0, stream);
+  const uint64_t blocks = (count - 1) / kAdamwTile + 1;
+  if (blocks > kAdamwMaxTiles) return hipErrorInvalidValue;          // more codes than memory holds
+  int vec = reinterpret_cast<uintptr_t>(codes) % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+  void* args[] = {&codes, &scales, &count, &vec, &out};
+  const void* fn = is_signed ? reinterpret_cast<const void*>(&adamw_dequantize_kernel<int8_t>)
+                             : reinterpret_cast<const void*>(&adamw_dequantize_kernel<uint8_t>);
+  return hipLaunchKernel(fn, dim3(static_cast<uint32_t>(blocks)), dim3(kBlock), args, 0, stream);
 }
 
 }  // namespace ar

@@ -140,38 +140,36 @@ template <class T, int V> __global__ __launch_bounds__(kBlock) void route_kernel
     if (s >= 0.0f) {
       const uint64_t fixed = static_cast<uint64_t>(static_cast<double>(s) * 4294967296.0 + 0.5);
       if (fixed != 0)
-        __hip_atomic_fetch_add(&a.sums->share[e], fixed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        shared_add(&a.sums->share[e], fixed);
     } else {
-      __hip_atomic_store(&a.sums->not_finite, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      shared_store(&a.sums->not_finite, 1u);
     }
     if (hist[e] != 0)
-      __hip_atomic_fetch_add(&a.sums->counts[rank * a.experts + e], hist[e], __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
+      shared_add(&a.sums->counts[rank * a.experts + e], hist[e]);
   }
   if (threadIdx.x == 0) {
     uint32_t n = 0;
     for (int w = 0; w < kWaves; ++w) n += tokens[w];
-    __hip_atomic_fetch_add(&a.sums->tokens, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    shared_add(&a.sums->tokens, n);
   }
-  __threadfence();
   if (!last_to_arrive(&a.sums->arrived, gridDim.x * gridDim.y)) return;
 
   // the last block: counts, shares and loss, and the workspace zero again
   RouteSums* ws = a.sums;
-  const double n = __hip_atomic_load(&ws->tokens, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const bool bad = __hip_atomic_load(&ws->not_finite, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0;
+  const double n = shared_load(&ws->tokens);
+  const bool bad = shared_load(&ws->not_finite) != 0;
   const double unit = n > 0 ? a.experts / (a.top_k * n * n) : 0.0;
   double loss = 0.0;
   for (int e = threadIdx.x; e < a.experts; e += kBlock) {
     uint64_t chosen = 0;
     for (int r = 0; r < a.nranks; ++r) {
       const int at = r * a.experts + e;
-      const uint32_t c = __hip_atomic_load(&ws->counts[at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      const uint32_t c = shared_load(&ws->counts[at]);
       ws->counts[at] = 0;
       a.counts[at] = static_cast<int32_t>(c);
       chosen += c;
     }
-    const uint64_t fixed = __hip_atomic_load(&ws->share[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint64_t fixed = shared_load(&ws->share[e]);
     ws->share[e] = 0;
     const double share = unit * static_cast<double>(chosen);
     a.share[e] = static_cast<float>(share);
