@@ -429,10 +429,10 @@ ar_status_t ar_adamw_dequantize(const void* codes, const float* scales, size_t c
 #define AR_MAX_TOP_K 8
 
 /* Device memory of a router call's sums: AR_ROUTE_WORKSPACE bytes, 16-byte
- * aligned, all zero before the call; the call leaves it zero again, so one
- * workspace serves any number of calls ordered on one stream.  Two streams
- * need two. */
-#define AR_ROUTE_WORKSPACE 270592
+ * aligned, all zero before its first call; a call leaves it ready for the
+ * next, so one workspace serves any number of calls ordered on one stream.
+ * Two streams need two. */
+#define AR_ROUTE_WORKSPACE 5000192
 
 /* Shape of a router call: `nranks` ranks (at most AR_MAX_RANKS) of `tokens`
  * tokens each, whose logits over `experts` experts lie `row_stride` elements
@@ -460,10 +460,10 @@ typedef struct {
  * `masks` (NULL, or one pointer a rank to `tokens` bytes): a token whose byte
  * is 0, or with every logit -infinity, is no token: index -1, weight 0,
  * nothing counted.  A token with a NaN or +infinite logit has NaN for every
- * weight and makes loss NaN; a NaN is never chosen.  p and weights are computed in float32;
- * the sums S are added up in float32 over the tokens of a block and over the
- * blocks in fixed point (2^-32), so that no result depends on the order of
- * execution.  Outputs are written whole. */
+ * weight and makes loss NaN; a NaN is never chosen.  p and weights are
+ * computed in float32; the sums S are added up in float32 over the tokens of
+ * a block and in float64 beyond, in an order that depends on the shape alone.
+ * Outputs are written whole. */
 ar_status_t ar_route(const void* const* logits, const uint8_t* const* masks,
                      const ar_route_shape_t* shape, int32_t* indices, float* weights,
                      int32_t* counts, float* loss, float* share, void* workspace,

@@ -120,6 +120,12 @@ def place(x, dtype, stride, offset):
     return out
 
 
+def counters_are_zero():
+    """The workspaces' 65 counters of arrived blocks, ready for the next call."""
+    for ws in training._route_workspaces.values():
+        assert not ws[:65 * 256].any()
+
+
 def check(x, k, dtype, renormalize, mask=None, stride=None, offset=0, seed=0):
     """Forward and gradient of one case against the definition."""
     rng = np.random.default_rng(seed)
@@ -143,8 +149,7 @@ def check(x, k, dtype, renormalize, mask=None, stride=None, offset=0, seed=0):
     assert dx.dtype == dtype and dx.shape == x.shape
     err = want["dx_err"] + (2.0 ** -8 if dtype == BF16 else 0) * (np.abs(want["dx"]) + want["dx_err"])
     assert np.all(np.abs(dx.double().cpu().numpy() - want["dx"]) <= err)
-    for ws in training._route_workspaces.values():
-        assert not ws.any()
+    counters_are_zero()
     return r, dx
 
 
@@ -222,8 +227,7 @@ def test_what_is_not_finite_shows_in_its_row_only(dtype, experts, bad):
         dw = [torch.ones(40, 2, device=DEV)] * 2
         dx = ar.route_grad(logits, r, dweights=dw, dloss=one)
         assert torch.isnan(dx[~keep]).all() and torch.isfinite(dx[keep]).all()
-        for ws in training._route_workspaces.values():
-            assert not ws.any()
+        counters_are_zero()
 
 
 def test_gradient_is_that_of_differences():

@@ -67,6 +67,7 @@ ar_status_t ar_route(const void* const* logits, const uint8_t* const* masks,
   fill(&a.logits, logits, shape);
   fill(&a.masks, masks, shape);
   fill_shape(&a, shape);
+  a.group = 0;
   a.sums = static_cast<ar::RouteSums*>(workspace);
   a.indices = indices;
   a.weights = weights;

@@ -9,17 +9,25 @@
 
 namespace ar {
 
-// A router call's sums (AR_ROUTE_WORKSPACE bytes of device memory, zero
-// between calls).
+// A router call's sums (AR_ROUTE_WORKSPACE bytes of device memory).  Every
+// block leaves a row of S_e and of counts; the last block of a group adds up
+// the group's rows, the last group the groups'.  The counters are 0 between
+// calls, each in a line of its own; the rest needs no clearing.
+constexpr int kRouteBlocks = 512;
+constexpr int kRouteGroups = 64;
+
 struct RouteSums {
-  uint64_t share[AR_MAX_EXPERTS];                  // S_e in steps of 2^-32
-  uint32_t counts[AR_MAX_RANKS * AR_MAX_EXPERTS];  // [rank][experts]
-  uint32_t tokens;                                 // that live
-  uint32_t not_finite;                             // a block's sum was not a number
-  uint32_t arrived;                                // blocks that have added their sums
-  uint32_t pad[61];
+  struct alignas(256) Counter {
+    uint32_t count;
+  } arrived[kRouteGroups], groups_arrived;
+  uint32_t tokens_of_block[kRouteBlocks];            // that live
+  uint32_t tokens_of_group[kRouteGroups];
+  double share_of_group[kRouteGroups * AR_MAX_EXPERTS];    // [group][experts]
+  uint32_t counts_of_group[kRouteGroups * AR_MAX_EXPERTS];
+  float share_of_block[kRouteBlocks * AR_MAX_EXPERTS];     // [block][experts]
+  uint32_t counts_of_block[kRouteBlocks * AR_MAX_EXPERTS];
 };
-static_assert(sizeof(RouteSums) == AR_ROUTE_WORKSPACE, "the workspace's documented size");
+static_assert(sizeof(RouteSums) <= AR_ROUTE_WORKSPACE, "the workspace's documented size");
 
 struct RouteArgs {
   RankPtrs logits;
@@ -33,6 +41,7 @@ struct RouteArgs {
   uint64_t row_stride;             // elements
   uint32_t tokens;                 // of a rank
   uint32_t rows_per_block;         // blocks (x, rank): tokens [x, x + 1) * rows_per_block
+  uint32_t group;                  // blocks of a rank whose sums are joined first
   int nranks, experts, top_k, renormalize;
 };
 
@@ -50,8 +59,8 @@ struct RouteGradArgs {
   int nranks, experts, top_k, renormalize;
 };
 
-// rows_per_block is set by the launchers.
-hipError_t launch_route(RouteArgs a, ar_dtype_t dtype, hipStream_t stream);
-hipError_t launch_route_grad(RouteGradArgs a, ar_dtype_t dtype, hipStream_t stream);
+// rows_per_block and group are set by the launchers.
+hipError_t launch_route(const RouteArgs& a, ar_dtype_t dtype, hipStream_t stream);
+hipError_t launch_route_grad(const RouteGradArgs& a, ar_dtype_t dtype, hipStream_t stream);
 
 }  // namespace ar

@@ -1,8 +1,11 @@
 // Expert router kernels (gfx950): the choice of experts with its weights,
 // counts and balance loss, and the gradient of the logits.
 //
-// A token's logits are one row.  A wave takes a row at a time, lane l the
-// columns l, l + 64, ...; the row is read once and stays in registers.
+// A token's logits are one row, held by G lanes of a wave (8 up to 256
+// experts), V = 4 to 32 values each, so that a wave has 8 rows at a time: a
+// row's maximum and sums then take three steps across lanes, shared by 8
+// rows, where a wave a row would take six for each.  Rows are read in
+// 16-byte accesses whatever their alignment.
 #include "device_common.hpp"
 #include "train/route.hpp"
 #include "train/wave.hpp"
@@ -12,286 +15,605 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kWaves = kBlock / kWave;
+constexpr int kNone = INT32_MIN;
 
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(uint16_t x) { return bf16_widen(x); }
-template <class T> __device__ __forceinline__ T narrow(float x) {
-  if constexpr (sizeof(T) == 4)
-    return x;
-  else
-    return bf16_round(x);
-}
 
-// exp(x - top): 0 for x = -infinity, NaN for a NaN.
-__device__ __forceinline__ float exp_from(float x, float top) {
-  return __builtin_amdgcn_exp2f((x - top) * kLog2e);
-}
+// --- lanes of a row ----------------------------------------------------------------
 
-// Order-preserving bits of a logit; 0 for -infinity and NaN, which are never
-// chosen.
-__device__ __forceinline__ uint32_t order_key(float x) {
-  const uint32_t b = __float_as_uint(x + 0.0f);   // -0 and 0 are equal
-  const uint32_t key = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-  return x > -__builtin_inff() ? key : 0u;
-}
-__device__ __forceinline__ float from_key(uint32_t key) {
-  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
-}
-
-// The tokens [begin, end) of a block.
-struct Rows {
-  uint32_t begin, end;
-  template <class A> __device__ explicit Rows(const A& a) {
-    begin = blockIdx.x * a.rows_per_block;
-    end = min(begin + a.rows_per_block, a.tokens);
-  }
+// Lane g of a row's G = 2^LG has C chunks of W consecutive columns, chunk c
+// at column (c G + g) W, so that G lanes read one run.
+template <class T, int LG, int C> struct Shape {
+  static constexpr int G = 1 << LG;
+  static constexpr int W = 16 / sizeof(T);
+  static constexpr int V = C * W;
+  static constexpr int kColumns = G * V;
+  static constexpr int kRows = kWave / G;           // of a wave
+  static __device__ int lane() { return threadIdx.x & (G - 1); }
+  static __device__ int column(int v) { return ((v / W) * G + lane()) * W + v % W; }
 };
 
-template <class T, int V>
-__device__ __forceinline__ void load_row(const T* row, int experts, bool live, float* x) {
-  const int lane = threadIdx.x % kWave;
+template <int CTRL> __device__ __forceinline__ int dpp(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, CTRL, 0xf, 0xf, false);
+}
+// The value of the lane across step S of a row: pairs, pairs of pairs, then
+// mirrored halves of 8 and 16, and lanes 16 apart.
+template <int S> __device__ __forceinline__ int across(int x) {
+  if constexpr (S == 0)
+    return dpp<0xB1>(x);
+  else if constexpr (S == 1)
+    return dpp<0x4E>(x);
+  else if constexpr (S == 2)
+    return dpp<0x141>(x);
+  else if constexpr (S == 3)
+    return dpp<0x140>(x);
+  else
+    return __shfl_xor(x, 16);
+}
+template <int LG, int S = 0> __device__ __forceinline__ int row_max(int x) {
+  if constexpr (S < LG)
+    return row_max<LG, S + 1>(max(x, across<S>(x)));
+  else
+    return x;
+}
+template <int LG, int S = 0> __device__ __forceinline__ float row_sum(float x) {
+  if constexpr (S < LG)
+    return row_sum<LG, S + 1>(x + __int_as_float(across<S>(__float_as_int(x))));
+  else
+    return x;
+}
+
+// A row's chunks as they lie in memory; -infinity beyond its end.
+using Chunk = uint32_t __attribute__((ext_vector_type(4)));
+template <class T> struct Loose;
+template <> struct Loose<float> {
+  typedef Chunk type __attribute__((aligned(4)));
+};
+template <> struct Loose<uint16_t> {
+  typedef Chunk type __attribute__((aligned(2)));
+};
+
+template <class T> __device__ __forceinline__ Chunk minus_infinity() {
+  const uint32_t w = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+  return Chunk{w, w, w, w};
+}
+
+template <class S, class T, int C>
+__device__ __forceinline__ void load_chunks(const T* row, int experts, Chunk (&raw)[C]) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int col = lane + v * kWave;
-    x[v] = live && col < experts ? widen(row[col]) : -__builtin_inff();
+  for (int c = 0; c < C; ++c) {
+    const int col = (c * S::G + S::lane()) * S::W;
+    if (col + S::W <= experts) {
+      raw[c] = *reinterpret_cast<const typename Loose<T>::type*>(row + col);
+    } else {
+      raw[c] = minus_infinity<T>();
+      T e[S::W];
+      __builtin_memcpy(e, &raw[c], 16);
+#pragma unroll
+      for (int w = 0; w < S::W; ++w)
+        if (col + w < experts) e[w] = row[col + w];
+      __builtin_memcpy(&raw[c], e, 16);
+    }
   }
 }
 
-template <class T, int V> __global__ __launch_bounds__(kBlock) void route_kernel(RouteArgs a) {
-  __shared__ uint32_t hist[V * kWave];
-  __shared__ float sums[kWaves][V * kWave];
+template <class T> __device__ __forceinline__ float value_of(const Chunk& raw, int w) {
+  if constexpr (sizeof(T) == 4)
+    return __uint_as_float(raw[w]);
+  else
+    return __uint_as_float(w % 2 == 0 ? raw[w / 2] << 16 : raw[w / 2] & 0xffff0000u);
+}
+
+// --- the choice ----------------------------------------------------------------------
+
+// A logit as an integer of the same order, 0 for both zeros.  With `bias`, a
+// negative one is moved up by that much, so that dropping the low bits keeps
+// -infinity apart from the lowest finite number.
+__device__ __forceinline__ int order(float x, int bias) {
+  const int b = __float_as_int(x);
+  return b < 0 ? static_cast<int>(0x80000000u + bias - static_cast<uint32_t>(b)) : b;
+}
+__device__ __forceinline__ float from_order(int key) {
+  return __uint_as_float(key < 0 ? 0x80000000u - static_cast<uint32_t>(key) : static_cast<uint32_t>(key));
+}
+constexpr int kMinusInfinity = -0x7f800000;         // order(-infinity, 0)
+
+__device__ __forceinline__ void sort2(int& a, int& b) {
+  const int hi = max(a, b), lo = min(a, b);
+  a = hi;
+  b = lo;
+}
+
+// Batcher's odd-even merge sort (Knuth, The Art of Computer Programming 3,
+// 5.2.2), descending.
+template <int N> __device__ __forceinline__ void sort(int* x) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k && i + j + k < N; ++i)
+          if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) sort2(x[i + j], x[i + j + k]);
+}
+
+// The N largest of two descending lists of N, into the first: the larger of
+// each pair of opposite ends, which is a bitonic list, and its merge.
+template <int N> __device__ __forceinline__ void merge(int* x, const int* y) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = max(x[i], y[N - 1 - i]);
+#pragma unroll
+  for (int k = N / 2; k >= 1; k /= 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((i & k) == 0) sort2(x[i], x[i + k]);
+}
+
+// What was chosen for a row: lane k of the row has the k-th column, -1 for
+// none; `top` is the largest logit or near it (within 8 where it is not it).
+struct Choice {
+  int index;
+  float top;
+};
+
+// The row's L largest by keys of 32 bits: the order of the logit in the high
+// bits, its column (the lowest the largest) in the low ones.  Each lane sorts
+// its values in lists of L and merges them, then the row's heads are popped
+// one by one.  bfloat16 fits the high bits and keys are exact; of a float32
+// log2(columns) bits are cut off, and false is returned for rows where two
+// neighbours among the top_k + 1 largest agree in what is left, or where
+// something is out of the ordinary (a top beyond 2^16 or not finite).
+template <class T, int LG, int C, int L>
+__device__ __forceinline__ bool choose(const float (&x)[Shape<T, LG, C>::V], int top_k, Choice* out) {
+  using S = Shape<T, LG, C>;
+  constexpr bool kExact = sizeof(T) == 2;
+  constexpr int kLow = S::kColumns - 1;              // of a key: columns - 1 - column
+  constexpr int N = L < S::V ? L : S::V;
+  int list[N];
+#pragma unroll
+  for (int v0 = 0; v0 < S::V; v0 += N) {
+    int part[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int v = v0 + i;
+      const int low = kLow - ((v / S::W) * S::G * S::W + v % S::W);   // of lane 0
+      const int key = order(x[v], kExact ? 0 : kLow);
+      part[i] = kExact ? key | low : (key & ~kLow) | low;
+    }
+    sort<N>(part);
+    if (v0 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) list[i] = part[i];
+    } else {
+      merge<N>(list, part);
+    }
+  }
+  // the lane's share of the column: its bits are ones so far
+  const int lane = S::lane();
+#pragma unroll
+  for (int i = 0; i < N; ++i) list[i] -= lane * S::W;
+
+  int mine = kNone, popped = 0, before = 0, first = 0;
+  bool clear = true;
+#pragma unroll
+  for (int k = 0; k <= L; ++k) {
+    if (k == L && kExact) break;
+    const int m = row_max<LG>(list[0]);
+    if (k == 0) first = m;
+    // neighbours k - 1 and k
+    if (!kExact && k > 0 && k <= top_k) clear = clear && ((before ^ m) & ~kLow) != 0;
+    before = m;
+    if (k == L) break;
+    if (lane == k) mine = m;
+    const bool me = list[0] == m;
+    popped += me ? 1 : 0;
+#pragma unroll
+    for (int i = 0; i + 1 < N; ++i) list[i] = me ? list[i + 1] : list[i];
+    list[N - 1] = me ? kNone : list[N - 1];
+  }
+  // a lane that gave L values may hold the next one too
+  if (!kExact && N == L && N < S::V)
+    clear = clear && (top_k < L || row_max<LG>(popped) < N);
+  constexpr int kBig = 0x47800000;                   // 2^16
+  const int top = first & ~kLow;
+  clear = clear && static_cast<uint32_t>(top + kBig) <= 2u * kBig;
+  out->top = from_order(top);
+  out->index = lane < top_k && (mine & ~kLow) > kMinusInfinity ? kLow - (mine & kLow) : -1;
+  return clear;
+}
+
+// The same for any row, by top_k searches over all values: exact, NaN never
+// chosen, about three times the work.
+template <class T, int LG, int C>
+__device__ __forceinline__ Choice choose_slowly(const float (&x)[Shape<T, LG, C>::V], int top_k) {
+  using S = Shape<T, LG, C>;
+  int key[S::V];
+#pragma unroll
+  for (int v = 0; v < S::V; ++v) key[v] = x[v] > -__builtin_inff() ? order(x[v], 0) : kNone;
+  Choice out = {-1, 0.0f};
+  for (int k = 0; k < top_k; ++k) {
+    int best = kNone;
+#pragma unroll
+    for (int v = 0; v < S::V; ++v) best = max(best, key[v]);
+    best = row_max<LG>(best);
+    int first = -S::kColumns;                        // minus the lowest column of the best
+#pragma unroll
+    for (int v = S::V - 1; v >= 0; --v)
+      if (key[v] == best) first = -S::column(v);
+    const int col = -row_max<LG>(first);
+    if (best != kNone) {
+      if (k == 0) out.top = from_order(best);
+      if (S::lane() == k) out.index = col;
+    }
+#pragma unroll
+    for (int v = 0; v < S::V; ++v)
+      if (S::column(v) == col) key[v] = kNone;
+  }
+  return out;
+}
+
+// --- forward ----------------------------------------------------------------------------
+
+// Adds up rows [0, n) of a table with `experts` columns by the block: the sum
+// of column e goes to put(e, sum).
+template <class X, class Y, class Put>
+__device__ __forceinline__ void column_sums(const X* rows, int n, int experts, const Put& put) {
+  for (int e = threadIdx.x; e < experts; e += kBlock) {
+    Y s = 0;
+    int i = 0;
+    for (; i + 8 <= n; i += 8) {
+      X x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = shared_load(&rows[static_cast<size_t>(i + u) * experts + e]);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += x[u];
+    }
+    for (; i < n; ++i) s += shared_load(&rows[static_cast<size_t>(i) * experts + e]);
+    put(e, s);
+  }
+}
+
+template <class T, int LG, int C, int L>
+__global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
+  using S = Shape<T, LG, C>;
+  constexpr int V = S::V;
+  __shared__ uint32_t hist[S::kColumns];
+  __shared__ float sums[kWaves][S::kColumns];
   __shared__ uint32_t tokens[kWaves];
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int wave = wave_uniform(threadIdx.x / kWave), lane = S::lane();
   const int rank = blockIdx.y;
-  for (int i = threadIdx.x; i < V * kWave; i += kBlock) hist[i] = 0;
+  const T* logits = static_cast<const T*>(a.logits.p[rank]);
+  const uint8_t* masks = static_cast<const uint8_t*>(a.masks.p[rank]);
+  for (int i = threadIdx.x; i < S::kColumns; i += kBlock) hist[i] = 0;
   __syncthreads();
 
   float total[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) total[v] = 0.0f;
   uint32_t live_rows = 0;
-  const Rows rows(a);
-  for (uint32_t i = rows.begin + wave; i < rows.end; i += kWaves) {
-    const uint8_t* mask = static_cast<const uint8_t*>(a.masks.p[rank]);
-    const bool masked = mask != nullptr && mask[i] == 0;
-    float x[V];
-    load_row<T, V>(static_cast<const T*>(a.logits.p[rank]) + i * a.row_stride, a.experts, !masked, x);
-    uint32_t key[V];
+  const uint32_t begin = blockIdx.x * a.rows_per_block;
+  const uint32_t end = min(begin + a.rows_per_block, a.tokens);
+  // a wave's rows are neighbours; rows past the end are read as the last one
+  const uint32_t sub = wave * S::kRows + threadIdx.x % kWave / S::G;
+  for (uint32_t first = begin; first < end; first += kWaves * S::kRows) {
+    const uint32_t i = min(first + sub, end - 1);
+    const bool token = first + sub < end && (masks == nullptr || masks[i] != 0);
+    const T* row = logits + i * a.row_stride;
+    Chunk raw[C];
+    load_chunks<S>(row, a.experts, raw);
+    if (__any(!token)) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = order_key(x[v]);
-
-    // the largest key, then its lowest column, top_k times; lane k keeps the k-th
-    int index = -1;
-    float value = 0.0f, top = 0.0f;
-    for (int k = 0; k < a.top_k; ++k) {
-      uint32_t best = 0;
-#pragma unroll
-      for (int v = 0; v < V; ++v) best = max(best, key[v]);
-      best = wave_max(best);
-      if (best == 0) break;
-      uint32_t first = 0;       // counted from the end: the largest is the lowest column
-#pragma unroll
-      for (int v = V - 1; v >= 0; --v)
-        if (key[v] == best) first = AR_MAX_EXPERTS - (lane + v * kWave);
-      const int col = AR_MAX_EXPERTS - static_cast<int>(wave_max(first));
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (col == lane + v * kWave) key[v] = 0;
-      if (k == 0) top = from_key(best);
-      if (lane == k) {
-        index = col;
-        value = from_key(best);
-      }
+      for (int c = 0; c < C; ++c)
+        if (!token) raw[c] = minus_infinity<T>();
     }
+    float x[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = value_of<T>(raw[v / S::W], v % S::W);
 
-    float e[V], sum = 0.0f;
+    Choice choice;
+    const bool clear = choose<T, LG, C, L>(x, a.top_k, &choice);
+    if (__any(token && !clear)) {
+      const Choice exact = choose_slowly<T, LG, C>(x, a.top_k);
+      if (!clear) choice = exact;       // what a row gets does not depend on its neighbours
+    }
+    if (!token) choice = {-1, 0.0f};
+
+    // exp(x - top) = 2^(x log2(e) - top log2(e)): rounding the second product
+    // scales a row's values by one factor, which the sum takes out.  Tops
+    // beyond 2^20, where that factor could overflow, are subtracted first.
+    float top = choice.top;
+    const float away = fabsf(top) <= 0x1p20f ? 0.0f : top;
+    if (__any(away != 0.0f)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] -= away;
+      top -= away;
+    }
+    const float shift = top * kLog2e;
+    const float xk = choice.index >= 0 ? widen(row[choice.index]) - away : -__builtin_inff();
+    float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      e[v] = exp_from(x[v], top);
-      sum += e[v];
+      x[v] = __builtin_amdgcn_exp2f(fmaf(x[v], kLog2e, -shift));
+      sum += x[v];
     }
-    sum = wave_sum(sum);
+    sum = row_sum<LG>(sum);
     const bool live = sum != 0.0f;          // a NaN lives
-    const float inv = live ? 1.0f / sum : 0.0f;
+    const float inv = live ? __builtin_amdgcn_rcpf(sum) : 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) total[v] = fmaf(e[v], inv, total[v]);
-    live_rows += live ? 1 : 0;
+    for (int v = 0; v < V; ++v) total[v] = fmaf(x[v], inv, total[v]);
+    live_rows += live && lane == 0 ? 1 : 0;
 
-    const float mine = index >= 0 ? exp_from(value, top) : 0.0f;
+    const float mine = __builtin_amdgcn_exp2f(fmaf(xk, kLog2e, -shift));
     float weight = mine * inv;
-    if (a.renormalize) weight = live ? mine / wave_sum(mine) : 0.0f;
+    if (a.renormalize) weight = live ? mine * __builtin_amdgcn_rcpf(row_sum<LG>(mine)) : 0.0f;
     if (sum != sum) weight = sum;
-    if (lane < a.top_k) {
+    if (lane < a.top_k && first + sub < end) {
       const uint64_t at = (static_cast<uint64_t>(rank) * a.tokens + i) * a.top_k + lane;
-      a.indices[at] = index;
+      a.indices[at] = choice.index;
       a.weights[at] = weight;
-      if (index >= 0) atomicAdd(&hist[index], 1u);
+      if (choice.index >= 0) atomicAdd(&hist[choice.index], 1u);
     }
   }
 
-  // the block's sums into the call's
+  // the block's row of sums
 #pragma unroll
-  for (int v = 0; v < V; ++v) sums[wave][lane + v * kWave] = total[v];
-  if (lane == 0) tokens[wave] = live_rows;
+  for (int d = S::G; d < kWave; d *= 2) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) total[v] += __shfl_xor(total[v], d);
+  }
+  live_rows = wave_sum(live_rows);
+  if (threadIdx.x % kWave < S::G) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) sums[wave][S::column(v)] = total[v];
+    if (lane == 0) tokens[wave] = live_rows;
+  }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.experts; e += kBlock) {
-    float s = sums[0][e];
-    for (int w = 1; w < kWaves; ++w) s += sums[w][e];
-    if (s >= 0.0f) {
-      const uint64_t fixed = static_cast<uint64_t>(static_cast<double>(s) * 4294967296.0 + 0.5);
-      if (fixed != 0)
-        shared_add(&a.sums->share[e], fixed);
-    } else {
-      shared_store(&a.sums->not_finite, 1u);
-    }
-    if (hist[e] != 0)
-      shared_add(&a.sums->counts[rank * a.experts + e], hist[e]);
-  }
-  if (threadIdx.x == 0) {
-    uint32_t n = 0;
-    for (int w = 0; w < kWaves; ++w) n += tokens[w];
-    shared_add(&a.sums->tokens, n);
-  }
-  if (!last_to_arrive(&a.sums->arrived, gridDim.x * gridDim.y)) return;
 
-  // the last block: counts, shares and loss, and the workspace zero again
   RouteSums* ws = a.sums;
-  const double n = shared_load(&ws->tokens);
-  const bool bad = shared_load(&ws->not_finite) != 0;
-  const double unit = n > 0 ? a.experts / (a.top_k * n * n) : 0.0;
+  const uint32_t groups_of_rank = (gridDim.x - 1) / a.group + 1, groups = groups_of_rank * gridDim.y;
+  const uint32_t my_group = rank * groups_of_rank + blockIdx.x / a.group;
+  const uint32_t in_group = min(a.group, gridDim.x - blockIdx.x / a.group * a.group);
+  const uint32_t block = rank * gridDim.x + blockIdx.x, block0 = block - blockIdx.x % a.group;
+  uint32_t n = tokens[0] + tokens[1] + tokens[2] + tokens[3];
+  auto of_wave = [&](int e) { return (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]); };
+  static_assert(kWaves == 4, "four waves' sums");
+
+  if (in_group > 1) {
+    for (int e = threadIdx.x; e < a.experts; e += kBlock) {
+      shared_store(&ws->share_of_block[static_cast<size_t>(block) * a.experts + e], of_wave(e));
+      shared_store(&ws->counts_of_block[static_cast<size_t>(block) * a.experts + e], hist[e]);
+    }
+    if (threadIdx.x == 0) shared_store(&ws->tokens_of_block[block], n);
+    if (!last_to_arrive(&ws->arrived[my_group].count, in_group)) return;
+    if (threadIdx.x == 0) ws->arrived[my_group].count = 0;
+    const float* share = ws->share_of_block + static_cast<size_t>(block0) * a.experts;
+    const uint32_t* counts = ws->counts_of_block + static_cast<size_t>(block0) * a.experts;
+    column_sums<float, double>(share, in_group, a.experts, [&](int e, double s) {
+      shared_store(&ws->share_of_group[static_cast<size_t>(my_group) * a.experts + e], s);
+    });
+    column_sums<uint32_t, uint32_t>(counts, in_group, a.experts, [&](int e, uint32_t s) {
+      shared_store(&ws->counts_of_group[static_cast<size_t>(my_group) * a.experts + e], s);
+    });
+    n = 0;
+    for (uint32_t b = 0; b < in_group; ++b) n += shared_load(&ws->tokens_of_block[block0 + b]);
+  } else {
+    for (int e = threadIdx.x; e < a.experts; e += kBlock) {
+      shared_store(&ws->share_of_group[static_cast<size_t>(my_group) * a.experts + e], static_cast<double>(of_wave(e)));
+      shared_store(&ws->counts_of_group[static_cast<size_t>(my_group) * a.experts + e], hist[e]);
+    }
+  }
+  if (threadIdx.x == 0) shared_store(&ws->tokens_of_group[my_group], n);
+  if (!last_to_arrive(&ws->groups_arrived.count, groups)) return;
+  if (threadIdx.x == 0) ws->groups_arrived.count = 0;
+
+  // the last block: counts, shares and loss
+  const double live = wave_sum(threadIdx.x % kWave < groups ? shared_load(&ws->tokens_of_group[threadIdx.x % kWave]) : 0u);
+  const double unit = live > 0 ? a.experts / (a.top_k * live * live) : 0.0;
   double loss = 0.0;
   for (int e = threadIdx.x; e < a.experts; e += kBlock) {
     uint64_t chosen = 0;
     for (int r = 0; r < a.nranks; ++r) {
-      const int at = r * a.experts + e;
-      const uint32_t c = shared_load(&ws->counts[at]);
-      ws->counts[at] = 0;
-      a.counts[at] = static_cast<int32_t>(c);
+      uint32_t c = 0;
+      for (uint32_t g = r * groups_of_rank; g < (r + 1) * groups_of_rank; ++g)
+        c += shared_load(&ws->counts_of_group[static_cast<size_t>(g) * a.experts + e]);
+      a.counts[r * a.experts + e] = static_cast<int32_t>(c);
       chosen += c;
     }
-    const uint64_t fixed = shared_load(&ws->share[e]);
-    ws->share[e] = 0;
-    const double share = unit * static_cast<double>(chosen);
-    a.share[e] = static_cast<float>(share);
-    loss += share * (static_cast<double>(fixed) / 4294967296.0);
+    a.share[e] = static_cast<float>(unit * static_cast<double>(chosen));
+    sums[0][e] = static_cast<float>(unit * static_cast<double>(chosen));
   }
-  loss = block_sum<kBlock>(loss);      // its barriers come after every thread's reads above
-  if (threadIdx.x == 0) {
-    *a.loss = bad ? __builtin_nanf("") : static_cast<float>(loss);
-    ws->tokens = ws->not_finite = ws->arrived = 0;
-  }
+  column_sums<double, double>(ws->share_of_group, groups, a.experts,
+                              [&](int e, double s) { loss += s * static_cast<double>(sums[0][e]); });
+  loss = block_sum<kBlock>(loss);
+  if (threadIdx.x == 0) *a.loss = static_cast<float>(loss);
 }
 
-template <class T, int V> __global__ __launch_bounds__(kBlock) void route_grad_kernel(RouteGradArgs a) {
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+// --- gradient ----------------------------------------------------------------------------
+
+template <class T, int LG, int C>
+__global__ __launch_bounds__(kBlock, 2) void route_grad_kernel(RouteGradArgs a) {
+  using S = Shape<T, LG, C>;
+  constexpr int V = S::V, W = S::W;
+  // what the chosen experts' weights add, a row of columns for each row of
+  // logits; zero but for the entries in use.  The pad keeps two rows' same
+  // columns out of each other's banks.
+  constexpr int kPitch = S::kColumns + 32;
+  __shared__ float spread[kWaves * S::kRows * kPitch];
+  const int wave = wave_uniform(threadIdx.x / kWave), lane = S::lane();
   const int rank = blockIdx.y;
+  const uint32_t sub = wave * S::kRows + threadIdx.x % kWave / S::G;
+  float* at = spread + sub * kPitch;
+  const T* logits = static_cast<const T*>(a.logits.p[rank]);
+  const uint8_t* masks = static_cast<const uint8_t*>(a.masks.p[rank]);
+  const float* dweights = static_cast<const float*>(a.dweights.p[rank]);
   const float dloss = a.dloss != nullptr ? *a.dloss : 0.0f;
   float coef[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int col = lane + v * kWave;
-    coef[v] = col < a.experts ? dloss * a.share[col] : 0.0f;
+    at[S::column(v)] = 0.0f;
+    coef[v] = S::column(v) < a.experts ? dloss * a.share[S::column(v)] : 0.0f;
   }
-  const Rows rows(a);
-  for (uint32_t i = rows.begin + wave; i < rows.end; i += kWaves) {
-    const uint8_t* mask = static_cast<const uint8_t*>(a.masks.p[rank]);
-    const bool masked = mask != nullptr && mask[i] == 0;
-    const T* row = static_cast<const T*>(a.logits.p[rank]) + i * a.row_stride;
-    float x[V], top = -__builtin_inff();
-    load_row<T, V>(row, a.experts, !masked, x);
-#pragma unroll
-    for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
-    const uint32_t top_key = wave_max(order_key(top));
-    top = top_key != 0 ? from_key(top_key) : 0.0f;
-    float p[V], sum = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      p[v] = exp_from(x[v], top);
-      sum += p[v];
-    }
-    sum = wave_sum(sum);
-    const bool live = sum != 0.0f;
-    const float inv = live ? 1.0f / sum : 0.0f;
-
-    // lane k has the k-th chosen expert's part
+  const uint32_t begin = blockIdx.x * a.rows_per_block;
+  const uint32_t end = min(begin + a.rows_per_block, a.tokens);
+  for (uint32_t first = begin; first < end; first += kWaves * S::kRows) {
+    const uint32_t i = min(first + sub, end - 1);
+    const uint64_t token = static_cast<uint64_t>(rank) * a.tokens + i;
+    const T* row = logits + i * a.row_stride;
+    const bool counts = masks == nullptr || masks[i] != 0;
     int index = -1;
     float dw = 0.0f;
-    const uint64_t token = static_cast<uint64_t>(rank) * a.tokens + i;
-    if (lane < a.top_k && a.dweights.p[0] != nullptr && live) {
+    if (dweights != nullptr && lane < a.top_k) {
       index = a.indices[token * a.top_k + lane];
       if (static_cast<uint32_t>(index) >= static_cast<uint32_t>(a.experts)) index = -1;
-      if (index >= 0)
-        dw = static_cast<const float*>(a.dweights.p[rank])[static_cast<uint64_t>(i) * a.top_k + lane];
+      if (index >= 0) dw = dweights[static_cast<uint64_t>(i) * a.top_k + lane];
     }
+    Chunk raw[C];
+    load_chunks<S>(row, a.experts, raw);
+    if (__any(!counts)) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (!counts) raw[c] = minus_infinity<T>();
+    }
+    float p[V], top = -__builtin_inff();
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      p[v] = value_of<T>(raw[v / W], v % W);
+      top = fmaxf(top, p[v]);
+    }
+    const int top_key = row_max<LG>(order(top, 0));
+    top = top_key > kMinusInfinity ? from_order(top_key) : 0.0f;
+    const float away = fabsf(top) <= 0x1p20f ? 0.0f : top;
+    if (__any(away != 0.0f)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) p[v] -= away;
+      top -= away;
+    }
+    const float shift = top * kLog2e;
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      p[v] = __builtin_amdgcn_exp2f(fmaf(p[v], kLog2e, -shift));
+      sum += p[v];
+    }
+    sum = row_sum<LG>(sum);
+    const bool live = sum != 0.0f;
+    const float inv = live ? __builtin_amdgcn_rcpf(sum) : 0.0f;
+
     float add = dw;                // to dp of its expert, or (renormalized) to dx
     if (a.renormalize) {
-      const float e = index >= 0 ? exp_from(widen(row[index]), top) : 0.0f;
-      const float all = wave_sum(e);
-      const float w = all > 0.0f ? e / all : 0.0f;
-      add = w * (dw - wave_sum(w * dw));
+      const float x = index >= 0 && live ? widen(row[index]) - away : -__builtin_inff();
+      const float e = __builtin_amdgcn_exp2f(fmaf(x, kLog2e, -shift));
+      const float all = row_sum<LG>(e);
+      const float w = all > 0.0f ? e * __builtin_amdgcn_rcpf(all) : 0.0f;
+      add = w * (dw - row_sum<LG>(w * dw));
     }
-    float at[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) at[v] = 0.0f;
-    for (int k = 0; k < a.top_k; ++k) {
-      const int col = __shfl(index, k);
-      const float y = __shfl(add, k);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (col == lane + v * kWave) at[v] = y;
-    }
-    float dot = 0.0f;
+    // a row's lanes are of one wave, whose LDS accesses happen in order
+    if (index >= 0) at[index] = add;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    float dot = 0.0f, here[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+      here[v] = at[S::column(v)];
       p[v] *= inv;
-      dot = fmaf(p[v], a.renormalize ? coef[v] : coef[v] + at[v], dot);
+      dot = fmaf(p[v], a.renormalize ? coef[v] : coef[v] + here[v], dot);
     }
-    dot = wave_sum(dot);
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    if (index >= 0) at[index] = 0.0f;
+    dot = row_sum<LG>(dot);
+    if (first + sub >= end) continue;
     T* out = static_cast<T*>(a.dlogits) + token * a.experts;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int col = lane + v * kWave;
-      const float dx = a.renormalize ? fmaf(p[v], coef[v] - dot, at[v]) : p[v] * (coef[v] + at[v] - dot);
-      if (col < a.experts) out[col] = narrow<T>(live ? dx : 0.0f);
+    for (int c = 0; c < C; ++c) {
+      float dx[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const int v = c * W + w;
+        dx[w] = a.renormalize ? fmaf(p[v], coef[v] - dot, here[v]) : p[v] * (coef[v] + here[v] - dot);
+        if (!live) dx[w] = 0.0f;
+      }
+      const int col = (c * S::G + lane) * W;
+      Chunk o;
+      if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) o[w] = __float_as_uint(dx[w]);
+      } else {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) o[w] = bf16x2_round(dx[2 * w], dx[2 * w + 1]);
+      }
+      if (col + W <= a.experts) {
+        *reinterpret_cast<typename Loose<T>::type*>(out + col) = o;
+      } else {
+        T e[W];
+        __builtin_memcpy(e, &o, 16);
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          if (col + w < a.experts) out[col + w] = e[w];
+      }
     }
   }
 }
 
-// Enough blocks to fill the chip, each with rows for all its waves.
-template <class A> dim3 grid_of(A* a) {
-  const uint32_t most = std::max<uint32_t>(1, 2048 / a->nranks);
-  const uint32_t blocks = std::max<uint32_t>(1, std::min((a->tokens + kWaves - 1) / kWaves, most));
-  a->rows_per_block = (a->tokens + blocks - 1) / blocks;
-  return dim3(a->tokens == 0 ? 1 : (a->tokens + a->rows_per_block - 1) / a->rows_per_block, a->nranks);
+// --- launches -----------------------------------------------------------------------------
+
+// One block of a rank takes rows_per_block tokens, a whole number of the
+// rows that its waves hold at a time; at most `most` blocks in all (or one a
+// rank).
+template <class A> dim3 grid_of(A* a, uint32_t rows, uint32_t most) {
+  const uint32_t wanted = std::max(1u, (a->tokens + rows - 1) / rows);
+  const uint32_t blocks = std::min(wanted, std::max<uint32_t>(1, most / a->nranks));
+  const uint32_t each = (wanted + blocks - 1) / blocks;
+  a->rows_per_block = each * rows;
+  return dim3((wanted + each - 1) / each, a->nranks);
 }
 
-template <class A>
-hipError_t launch_rows(const void* kernel, dim3 grid, A* a, hipStream_t stream) {
+hipError_t launch_rows(const void* kernel, dim3 grid, void* a, hipStream_t stream) {
   void* args[] = {a};
   return hipLaunchKernel(kernel, grid, dim3(kBlock), args, 0, stream);
 }
 
-#define AR_BY_EXPERTS(kernel, T, e)                                              \
-  ((e) <= 64    ? reinterpret_cast<const void*>(&kernel<T, 1>)                   \
-   : (e) <= 128 ? reinterpret_cast<const void*>(&kernel<T, 2>)                   \
-   : (e) <= 256 ? reinterpret_cast<const void*>(&kernel<T, 4>)                   \
-   : (e) <= 512 ? reinterpret_cast<const void*>(&kernel<T, 8>)                   \
-                : reinterpret_cast<const void*>(&kernel<T, 16>))
-
-}  // namespace
-
-hipError_t launch_route(RouteArgs a, ar_dtype_t dtype, hipStream_t stream) {
-  const void* fn = dtype == AR_FLOAT32 ? AR_BY_EXPERTS(route_kernel, float, a.experts)
-                                       : AR_BY_EXPERTS(route_kernel, uint16_t, a.experts);
-  const dim3 grid = grid_of(&a);
+template <class T, int LG, int C> hipError_t route_as(RouteArgs a, hipStream_t stream) {
+  const dim3 grid = grid_of(&a, kWaves * Shape<T, LG, C>::kRows, kRouteBlocks);
+  // few blocks are all joined by the last one
+  a.group = grid.x * grid.y <= 32 ? 1 : 16;
+  const void* fn = a.top_k <= 2   ? reinterpret_cast<const void*>(&route_kernel<T, LG, C, 2>)
+                   : a.top_k <= 4 ? reinterpret_cast<const void*>(&route_kernel<T, LG, C, 4>)
+                                  : reinterpret_cast<const void*>(&route_kernel<T, LG, C, 8>);
   return launch_rows(fn, grid, &a, stream);
 }
 
-hipError_t launch_route_grad(RouteGradArgs a, ar_dtype_t dtype, hipStream_t stream) {
-  const void* fn = dtype == AR_FLOAT32 ? AR_BY_EXPERTS(route_grad_kernel, float, a.experts)
-                                       : AR_BY_EXPERTS(route_grad_kernel, uint16_t, a.experts);
-  const dim3 grid = grid_of(&a);
-  return launch_rows(fn, grid, &a, stream);
+template <class T, int LG, int C> hipError_t route_grad_as(RouteGradArgs a, hipStream_t stream) {
+  const dim3 grid = grid_of(&a, kWaves * Shape<T, LG, C>::kRows, 1024);
+  return launch_rows(reinterpret_cast<const void*>(&route_grad_kernel<T, LG, C>), grid, &a, stream);
+}
+
+// The smallest arrangement that holds a row: 8 lanes of 1 to 8 chunks, then
+// 16 and 32 lanes.
+#define AR_BY_EXPERTS(call, e, a, dtype, stream)                                          \
+  if (dtype == AR_FLOAT32)                                                                \
+    return e <= 32    ? call<float, 3, 1>(a, stream)                                      \
+           : e <= 64  ? call<float, 3, 2>(a, stream)                                      \
+           : e <= 128 ? call<float, 3, 4>(a, stream)                                      \
+           : e <= 256 ? call<float, 3, 8>(a, stream)                                      \
+           : e <= 512 ? call<float, 4, 8>(a, stream)                                      \
+                      : call<float, 5, 8>(a, stream);                                     \
+  return e <= 64    ? call<uint16_t, 3, 1>(a, stream)                                     \
+         : e <= 128 ? call<uint16_t, 3, 2>(a, stream)                                     \
+         : e <= 256 ? call<uint16_t, 3, 4>(a, stream)                                     \
+         : e <= 512 ? call<uint16_t, 4, 4>(a, stream)                                     \
+                    : call<uint16_t, 5, 4>(a, stream)
+
+}  // namespace
+
+hipError_t launch_route(const RouteArgs& a, ar_dtype_t dtype, hipStream_t stream) {
+  AR_BY_EXPERTS(route_as, a.experts, a, dtype, stream);
+}
+
+hipError_t launch_route_grad(const RouteGradArgs& a, ar_dtype_t dtype, hipStream_t stream) {
+  AR_BY_EXPERTS(route_grad_as, a.experts, a, dtype, stream);
 }
 
 }  // namespace ar

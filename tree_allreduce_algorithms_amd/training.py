@@ -12,7 +12,7 @@ from .binding import DTYPES, SUCCESS, AdamwStep, AdamwTensor, ArError, RouteShap
 
 BLOCK = 256   # elements that share one scale of an 8-bit state
 MAX_EXPERTS, MAX_TOP_K = 1024, 8
-ROUTE_WORKSPACE = 270592   # AR_ROUTE_WORKSPACE
+ROUTE_WORKSPACE = 5000192   # AR_ROUTE_WORKSPACE
 
 
 def _handle(stream, dev):
@@ -241,11 +241,11 @@ def _ranks(tensors, n, shape, dtype, dev, what):
     return tensors, _table(tensors)
 
 
-_route_workspaces = {}   # (device, stream handle) -> zeroed workspace
+_route_workspaces = {}   # (device, stream handle) -> workspace
 
 
 def _route_workspace(device, handle):
-    """The stream's workspace, which every call leaves zero.  A captured call
+    """The stream's workspace, which every call leaves ready for the next.  A captured call
     gets one of its own, cleared in the graph: its replays may run beside the
     stream's other calls."""
     import torch
