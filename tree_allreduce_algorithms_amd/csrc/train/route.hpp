@@ -22,10 +22,9 @@ struct RouteSums {
   } arrived[kRouteGroups], groups_arrived;
   uint32_t tokens_of_block[kRouteBlocks];            // that live
   uint32_t tokens_of_group[kRouteGroups];
-  double share_of_group[kRouteGroups * AR_MAX_EXPERTS];    // [group][experts]
-  uint32_t counts_of_group[kRouteGroups * AR_MAX_EXPERTS];
-  float share_of_block[kRouteBlocks * AR_MAX_EXPERTS];     // [block][experts]
-  uint32_t counts_of_block[kRouteBlocks * AR_MAX_EXPERTS];
+  // [group or block][experts]: S_e as float32 in the high word, counts in the low
+  uint64_t of_group[kRouteGroups * AR_MAX_EXPERTS];
+  uint64_t of_block[kRouteBlocks * AR_MAX_EXPERTS];
 };
 static_assert(sizeof(RouteSums) <= AR_ROUTE_WORKSPACE, "the workspace's documented size");
 

@@ -139,11 +139,8 @@ template <int N> __device__ __forceinline__ void sort(int* x) {
           if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) sort2(x[i + j], x[i + j + k]);
 }
 
-// The N largest of two descending lists of N, into the first: the larger of
-// each pair of opposite ends, which is a bitonic list, and its merge.
-template <int N> __device__ __forceinline__ void merge(int* x, const int* y) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = max(x[i], y[N - 1 - i]);
+// Merge of a bitonic list, descending.
+template <int N> __device__ __forceinline__ void merge(int* x) {
 #pragma unroll
   for (int k = N / 2; k >= 1; k /= 2)
 #pragma unroll
@@ -151,87 +148,124 @@ template <int N> __device__ __forceinline__ void merge(int* x, const int* y) {
       if ((i & k) == 0) sort2(x[i], x[i + k]);
 }
 
+// The N largest of two descending lists of N, into the first: the larger of
+// each pair of opposite ends, which is a bitonic list.
+template <int N> __device__ __forceinline__ void join(int* x, const int* y) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = max(x[i], y[N - 1 - i]);
+  merge<N>(x);
+}
+
+// The row's L largest from each lane's N (descending), for every lane.
+template <int LG, int L, int N, int S = 0> __device__ __forceinline__ void join_row(int* x) {
+  if constexpr (S < LG) {
+    if constexpr (N < L) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[2 * N - 1 - i] = across<S>(x[i]);
+      merge<2 * N>(x);
+      join_row<LG, L, 2 * N, S + 1>(x);
+    } else {
+      int y[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] = across<S>(x[i]);
+      join<N>(x, y);
+      join_row<LG, L, N, S + 1>(x);
+    }
+  }
+}
+
 // What was chosen for a row: lane k of the row has the k-th column, -1 for
-// none; `top` is the largest logit or near it (within 8 where it is not it).
+// none.  `top` is the largest logit, or (within 2^16) the end of its interval
+// of keys, at most 8 away: any number near it serves the softmax.
 struct Choice {
   int index;
   float top;
 };
 
+template <class T, int LG, int C> struct Keys {
+  static constexpr bool kExact = sizeof(T) == 2;
+  static constexpr int kLow = Shape<T, LG, C>::kColumns - 1;
+  static constexpr int kBig = 0x47800000;            // 2^16
+  // The order of a logit without the low bits; -infinity is by itself.
+  static __device__ __forceinline__ int high(float x) { return order(x, kExact ? 0 : kLow) & ~kLow; }
+  static __device__ __forceinline__ bool big(int high) { return static_cast<uint32_t>(high + kBig) > 2u * kBig; }
+};
+
 // The row's L largest by keys of 32 bits: the order of the logit in the high
 // bits, its column (the lowest the largest) in the low ones.  Each lane sorts
-// its values in lists of L and merges them, then the row's heads are popped
-// one by one.  bfloat16 fits the high bits and keys are exact; of a float32
-// log2(columns) bits are cut off, and false is returned for rows where two
-// neighbours among the top_k + 1 largest agree in what is left, or where
-// something is out of the ordinary (a top beyond 2^16 or not finite).
+// its values in lists of L and joins them, then the lanes join theirs.
+// bfloat16 fits the high bits and keys are exact; of a float32 log2(columns)
+// bits are cut off, and false is returned where two neighbours among the
+// top_k + 1 largest agree in what is left.  So it is, for all rows of a wave
+// or some, where a top is beyond 2^16 or not finite.
 template <class T, int LG, int C, int L>
-__device__ __forceinline__ bool choose(const float (&x)[Shape<T, LG, C>::V], int top_k, Choice* out) {
+__device__ __forceinline__ bool choose(const float (&x)[Shape<T, LG, C>::V], int top_k, bool token, Choice* out) {
   using S = Shape<T, LG, C>;
-  constexpr bool kExact = sizeof(T) == 2;
-  constexpr int kLow = S::kColumns - 1;              // of a key: columns - 1 - column
+  using K = Keys<T, LG, C>;
+  constexpr int kLow = K::kLow;                      // of a key: columns - 1 - column
   constexpr int N = L < S::V ? L : S::V;
-  int list[N];
+  const int lane = S::lane();
+  int list[L], key[S::V];
 #pragma unroll
-  for (int v0 = 0; v0 < S::V; v0 += N) {
-    int part[N];
+  for (int v = 0; v < S::V; ++v) {
+    const int low = kLow - ((v / S::W) * S::G * S::W + v % S::W);   // of lane 0
+    key[v] = K::kExact ? order(x[v], 0) | low : K::high(x[v]) | low;
+  }
+  bool clear = true;
+  int part[S::V];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int v = v0 + i;
-      const int low = kLow - ((v / S::W) * S::G * S::W + v % S::W);   // of lane 0
-      const int key = order(x[v], kExact ? 0 : kLow);
-      part[i] = kExact ? key | low : (key & ~kLow) | low;
-    }
-    sort<N>(part);
-    if (v0 == 0) {
+  for (int v = 0; v < S::V; ++v) part[v] = key[v];
 #pragma unroll
-      for (int i = 0; i < N; ++i) list[i] = part[i];
-    } else {
-      merge<N>(list, part);
-    }
+  for (int v = 0; v < S::V; v += N) {
+    sort<N>(part + v);
+    if (v > 0) join<N>(part, part + v);
   }
   // the lane's share of the column: its bits are ones so far
-  const int lane = S::lane();
 #pragma unroll
-  for (int i = 0; i < N; ++i) list[i] -= lane * S::W;
+  for (int i = 0; i < N; ++i) list[i] = part[i] - lane * S::W;
+  join_row<LG, L, N>(list);
 
-  int mine = kNone, popped = 0, before = 0, first = 0;
-  bool clear = true;
+  const int top = list[0] & ~kLow;
+  clear = !K::big(top);
+  int mine = list[0];
 #pragma unroll
-  for (int k = 0; k <= L; ++k) {
-    if (k == L && kExact) break;
-    const int m = row_max<LG>(list[0]);
-    if (k == 0) first = m;
-    // neighbours k - 1 and k
-    if (!kExact && k > 0 && k <= top_k) clear = clear && ((before ^ m) & ~kLow) != 0;
-    before = m;
-    if (k == L) break;
-    if (lane == k) mine = m;
-    const bool me = list[0] == m;
-    popped += me ? 1 : 0;
+  for (int k = 1; k < L; ++k) mine = lane == k ? list[k] : mine;
+  if constexpr (!K::kExact) {
+    int last = list[0];
 #pragma unroll
-    for (int i = 0; i + 1 < N; ++i) list[i] = me ? list[i + 1] : list[i];
-    list[N - 1] = me ? kNone : list[N - 1];
+    for (int k = 1; k < L; ++k) {
+      if (k <= top_k) clear = clear && ((list[k - 1] ^ list[k]) & ~kLow) != 0;
+      if (k < top_k) last = list[k];
+    }
+    // with top_k = L the next largest is not in the list: as many values as
+    // were chosen must reach the last one's interval
+    if (top_k == L) {
+      const int floor = token ? last & ~kLow : INT32_MAX;
+      int reach = 0;
+#pragma unroll
+      for (int v = 0; v < S::V; ++v) reach += __popcll(__ballot(key[v] >= floor));
+      clear = clear && reach == __popcll(__ballot(token && lane == 0)) * L;
+    }
   }
-  // a lane that gave L values may hold the next one too
-  if (!kExact && N == L && N < S::V)
-    clear = clear && (top_k < L || row_max<LG>(popped) < N);
-  constexpr int kBig = 0x47800000;                   // 2^16
-  const int top = first & ~kLow;
-  clear = clear && static_cast<uint32_t>(top + kBig) <= 2u * kBig;
   out->top = from_order(top);
   out->index = lane < top_k && (mine & ~kLow) > kMinusInfinity ? kLow - (mine & kLow) : -1;
   return clear;
 }
 
 // The same for any row, by top_k searches over all values: exact, NaN never
-// chosen, about three times the work.
+// chosen, about three times the work.  Within 2^16 its top is the one above,
+// so that a row's results do not depend on which of the two its wave took.
 template <class T, int LG, int C>
 __device__ __forceinline__ Choice choose_slowly(const float (&x)[Shape<T, LG, C>::V], int top_k) {
   using S = Shape<T, LG, C>;
+  using K = Keys<T, LG, C>;
   int key[S::V];
 #pragma unroll
-  for (int v = 0; v < S::V; ++v) key[v] = x[v] > -__builtin_inff() ? order(x[v], 0) : kNone;
+  for (int v = 0; v < S::V; ++v) {
+    float y = x[v];
+    asm volatile("" : "+v"(y));                      // keeps this work on this path
+    key[v] = y > -__builtin_inff() ? order(y, 0) : kNone;
+  }
   Choice out = {-1, 0.0f};
   for (int k = 0; k < top_k; ++k) {
     int best = kNone;
@@ -244,7 +278,10 @@ __device__ __forceinline__ Choice choose_slowly(const float (&x)[Shape<T, LG, C>
       if (key[v] == best) first = -S::column(v);
     const int col = -row_max<LG>(first);
     if (best != kNone) {
-      if (k == 0) out.top = from_order(best);
+      if (k == 0) {
+        const int high = K::high(from_order(best));
+        out.top = K::big(high) ? from_order(best) : from_order(high);
+      }
       if (S::lane() == k) out.index = col;
     }
 #pragma unroll
@@ -256,31 +293,48 @@ __device__ __forceinline__ Choice choose_slowly(const float (&x)[Shape<T, LG, C>
 
 // --- forward ----------------------------------------------------------------------------
 
-// Adds up rows [0, n) of a table with `experts` columns by the block: the sum
-// of column e goes to put(e, sum).
-template <class X, class Y, class Put>
-__device__ __forceinline__ void column_sums(const X* rows, int n, int experts, const Put& put) {
-  for (int e = threadIdx.x; e < experts; e += kBlock) {
-    Y s = 0;
-    int i = 0;
-    for (; i + 8 <= n; i += 8) {
-      X x[8];
+__device__ __forceinline__ uint64_t pair_of(float s, uint32_t count) {
+  return static_cast<uint64_t>(__float_as_uint(s)) << 32 | count;
+}
+__device__ __forceinline__ float sum_in(uint64_t pair) { return __uint_as_float(static_cast<uint32_t>(pair >> 32)); }
+__device__ __forceinline__ uint32_t count_in(uint64_t pair) { return static_cast<uint32_t>(pair); }
+
+// Reads n rows (row, row + stride, ...) of a table, column e, several at a
+// time (they come from memory, about a microsecond each if one by one), and
+// hands them to take() in order.
+template <class Take>
+__device__ __forceinline__ void read_rows(const uint64_t* table, int row, int n, int stride, int experts, int e,
+                                          const Take& take) {
+  constexpr int kAtOnce = 8;
+  for (int i = 0; i < n; i += kAtOnce) {
+    uint64_t x[kAtOnce];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] = shared_load(&rows[static_cast<size_t>(i + u) * experts + e]);
+    for (int u = 0; u < kAtOnce; ++u)
+      x[u] = shared_load(&table[static_cast<size_t>(row + min(i + u, n - 1) * stride) * experts + e]);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) s += x[u];
-    }
-    for (; i < n; ++i) s += shared_load(&rows[static_cast<size_t>(i) * experts + e]);
-    put(e, s);
+    for (int u = 0; u < kAtOnce; ++u)
+      if (i + u < n) take(x[u]);
   }
 }
+
+// How the last block's threads share the columns: E of them (a power of two)
+// at a time, in P slices of rows.
+struct Slices {
+  int E, P, e, slice;
+  __device__ explicit Slices(int experts) {
+    E = min(kBlock, 1 << (32 - __clz(max(experts - 1, 1))));
+    P = kBlock / E;
+    e = threadIdx.x & (E - 1);
+    slice = threadIdx.x / E;
+  }
+};
 
 template <class T, int LG, int C, int L>
 __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
   using S = Shape<T, LG, C>;
   constexpr int V = S::V;
   __shared__ uint32_t hist[S::kColumns];
-  __shared__ float sums[kWaves][S::kColumns];
+  __shared__ float sums[kWaves * kWave * V];          // [wave and row of it][columns]
   __shared__ uint32_t tokens[kWaves];
   const int wave = wave_uniform(threadIdx.x / kWave), lane = S::lane();
   const int rank = blockIdx.y;
@@ -297,12 +351,22 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
   const uint32_t end = min(begin + a.rows_per_block, a.tokens);
   // a wave's rows are neighbours; rows past the end are read as the last one
   const uint32_t sub = wave * S::kRows + threadIdx.x % kWave / S::G;
+  Chunk next[C];
+  bool next_token = false;
+  auto fetch = [&](uint32_t first) {
+    const uint32_t i = min(first + sub, end - 1);
+    next_token = first + sub < end && (masks == nullptr || masks[i] != 0);
+    load_chunks<S>(logits + i * a.row_stride, a.experts, next);
+  };
+  if (begin < end) fetch(begin);
   for (uint32_t first = begin; first < end; first += kWaves * S::kRows) {
     const uint32_t i = min(first + sub, end - 1);
-    const bool token = first + sub < end && (masks == nullptr || masks[i] != 0);
+    const bool token = next_token;
     const T* row = logits + i * a.row_stride;
     Chunk raw[C];
-    load_chunks<S>(row, a.experts, raw);
+#pragma unroll
+    for (int c = 0; c < C; ++c) raw[c] = next[c];
+    if (first + kWaves * S::kRows < end) fetch(first + kWaves * S::kRows);
     if (__any(!token)) {
 #pragma unroll
       for (int c = 0; c < C; ++c)
@@ -313,11 +377,8 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
     for (int v = 0; v < V; ++v) x[v] = value_of<T>(raw[v / S::W], v % S::W);
 
     Choice choice;
-    const bool clear = choose<T, LG, C, L>(x, a.top_k, &choice);
-    if (__any(token && !clear)) {
-      const Choice exact = choose_slowly<T, LG, C>(x, a.top_k);
-      if (!clear) choice = exact;       // what a row gets does not depend on its neighbours
-    }
+    const bool clear = choose<T, LG, C, L>(x, a.top_k, token, &choice);
+    if (__any(token && !clear)) choice = choose_slowly<T, LG, C>(x, a.top_k);
     if (!token) choice = {-1, 0.0f};
 
     // exp(x - top) = 2^(x log2(e) - top log2(e)): rounding the second product
@@ -358,17 +419,11 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
   }
 
   // the block's row of sums
+  float* mine = sums + (wave * S::kRows + threadIdx.x % kWave / S::G) * S::kColumns;
 #pragma unroll
-  for (int d = S::G; d < kWave; d *= 2) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) total[v] += __shfl_xor(total[v], d);
-  }
+  for (int v = 0; v < V; ++v) mine[S::column(v)] = total[v];
   live_rows = wave_sum(live_rows);
-  if (threadIdx.x % kWave < S::G) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) sums[wave][S::column(v)] = total[v];
-    if (lane == 0) tokens[wave] = live_rows;
-  }
+  if (threadIdx.x % kWave == 0) tokens[wave] = live_rows;
   __syncthreads();
 
   RouteSums* ws = a.sums;
@@ -377,57 +432,109 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
   const uint32_t in_group = min(a.group, gridDim.x - blockIdx.x / a.group * a.group);
   const uint32_t block = rank * gridDim.x + blockIdx.x, block0 = block - blockIdx.x % a.group;
   uint32_t n = tokens[0] + tokens[1] + tokens[2] + tokens[3];
-  auto of_wave = [&](int e) { return (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]); };
   static_assert(kWaves == 4, "four waves' sums");
+  // one group of one block in all joins its own row only; with one block a
+  // group, the groups' rows are the blocks'
+  uint64_t* my_rows = in_group > 1 ? ws->of_block + static_cast<size_t>(block) * a.experts
+                                   : ws->of_group + static_cast<size_t>(my_group) * a.experts;
+  for (int e = threadIdx.x; e < a.experts; e += kBlock) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWaves * S::kRows; ++i) s += sums[i * S::kColumns + e];
+    shared_store(&my_rows[e], pair_of(s, hist[e]));
+  }
+  if (threadIdx.x == 0) shared_store(in_group > 1 ? &ws->tokens_of_block[block] : &ws->tokens_of_group[my_group], n);
 
+  __shared__ double part_s[kBlock];
+  __shared__ uint32_t part_c[kBlock], of_rank[kBlock];
+  const Slices t(a.experts);
   if (in_group > 1) {
-    for (int e = threadIdx.x; e < a.experts; e += kBlock) {
-      shared_store(&ws->share_of_block[static_cast<size_t>(block) * a.experts + e], of_wave(e));
-      shared_store(&ws->counts_of_block[static_cast<size_t>(block) * a.experts + e], hist[e]);
-    }
-    if (threadIdx.x == 0) shared_store(&ws->tokens_of_block[block], n);
     if (!last_to_arrive(&ws->arrived[my_group].count, in_group)) return;
-    if (threadIdx.x == 0) ws->arrived[my_group].count = 0;
-    const float* share = ws->share_of_block + static_cast<size_t>(block0) * a.experts;
-    const uint32_t* counts = ws->counts_of_block + static_cast<size_t>(block0) * a.experts;
-    column_sums<float, double>(share, in_group, a.experts, [&](int e, double s) {
-      shared_store(&ws->share_of_group[static_cast<size_t>(my_group) * a.experts + e], s);
-    });
-    column_sums<uint32_t, uint32_t>(counts, in_group, a.experts, [&](int e, uint32_t s) {
-      shared_store(&ws->counts_of_group[static_cast<size_t>(my_group) * a.experts + e], s);
-    });
-    n = 0;
-    for (uint32_t b = 0; b < in_group; ++b) n += shared_load(&ws->tokens_of_block[block0 + b]);
-  } else {
-    for (int e = threadIdx.x; e < a.experts; e += kBlock) {
-      shared_store(&ws->share_of_group[static_cast<size_t>(my_group) * a.experts + e], static_cast<double>(of_wave(e)));
-      shared_store(&ws->counts_of_group[static_cast<size_t>(my_group) * a.experts + e], hist[e]);
+    n = threadIdx.x < in_group ? shared_load(&ws->tokens_of_block[block0 + threadIdx.x]) : 0u;
+    for (int e0 = 0; e0 < a.experts; e0 += t.E) {
+      const int e = min(e0 + t.e, a.experts - 1);
+      double s = 0.0;
+      uint32_t c = 0;
+      const int rows = (static_cast<int>(in_group) - t.slice + t.P - 1) / t.P;
+      read_rows(ws->of_block, block0 + t.slice, rows, t.P, a.experts, e, [&](uint64_t x) {
+        s += sum_in(x);
+        c += count_in(x);
+      });
+      part_s[threadIdx.x] = s;
+      part_c[threadIdx.x] = c;
+      __syncthreads();
+      if (t.slice == 0 && e0 + t.e < a.experts) {
+        for (int i = 1; i < t.P; ++i) {
+          s += part_s[i * t.E + t.e];
+          c += part_c[i * t.E + t.e];
+        }
+        shared_store(&ws->of_group[static_cast<size_t>(my_group) * a.experts + e], pair_of(static_cast<float>(s), c));
+      }
+      __syncthreads();
+    }
+    n = wave_sum(n);                       // at most 16 blocks: the first wave has them all
+    if (threadIdx.x == 0) {
+      ws->arrived[my_group].count = 0;
+      shared_store(&ws->tokens_of_group[my_group], n);
     }
   }
-  if (threadIdx.x == 0) shared_store(&ws->tokens_of_group[my_group], n);
   if (!last_to_arrive(&ws->groups_arrived.count, groups)) return;
-  if (threadIdx.x == 0) ws->groups_arrived.count = 0;
 
   // the last block: counts, shares and loss
-  const double live = wave_sum(threadIdx.x % kWave < groups ? shared_load(&ws->tokens_of_group[threadIdx.x % kWave]) : 0u);
+  const uint32_t lane_tokens = threadIdx.x % kWave < groups ? shared_load(&ws->tokens_of_group[threadIdx.x % kWave]) : 0u;
+  const double live = wave_sum(lane_tokens);
   const double unit = live > 0 ? a.experts / (a.top_k * live * live) : 0.0;
+  // q slices a rank where there are more slices than ranks, else whole ranks a slice
+  const int q = max(1, t.P / a.nranks), together = t.P / q;
+  const int first_rank = q > 1 ? t.slice / q : t.slice * a.nranks / t.P;
+  const int end_rank = q > 1 ? (first_rank < min(a.nranks, together) ? first_rank + 1 : first_rank)
+                             : (t.slice + 1) * a.nranks / t.P;
+  const int per_rank = static_cast<int>(groups_of_rank), part = q > 1 ? t.slice % q : 0;
   double loss = 0.0;
-  for (int e = threadIdx.x; e < a.experts; e += kBlock) {
-    uint64_t chosen = 0;
-    for (int r = 0; r < a.nranks; ++r) {
-      uint32_t c = 0;
-      for (uint32_t g = r * groups_of_rank; g < (r + 1) * groups_of_rank; ++g)
-        c += shared_load(&ws->counts_of_group[static_cast<size_t>(g) * a.experts + e]);
-      a.counts[r * a.experts + e] = static_cast<int32_t>(c);
-      chosen += c;
+  for (int e0 = 0; e0 < a.experts; e0 += t.E) {
+    const int e = min(e0 + t.e, a.experts - 1);
+    const bool mine = e0 + t.e < a.experts;
+    double s = 0.0;
+    uint32_t chosen = 0, c = 0;
+    of_rank[threadIdx.x] = 0;
+    __syncthreads();
+    int rank_of_row = first_rank, left = per_rank;
+    const int rows = q > 1 ? (end_rank > first_rank ? (per_rank - part + q - 1) / q : 0)
+                           : (end_rank - first_rank) * per_rank;
+    read_rows(ws->of_group, first_rank * per_rank + part, rows, q, a.experts, e, [&](uint64_t x) {
+      s += sum_in(x);
+      c += count_in(x);
+      chosen += count_in(x);
+      if (q == 1 && --left == 0) {
+        if (mine) a.counts[rank_of_row * a.experts + e] = static_cast<int32_t>(c);
+        ++rank_of_row;
+        left = per_rank;
+        c = 0;
+      }
+    });
+    if (q > 1 && rows > 0) atomicAdd(&of_rank[first_rank * t.E + t.e], c);
+    part_s[threadIdx.x] = s;
+    part_c[threadIdx.x] = chosen;
+    __syncthreads();
+    if (q > 1 && t.slice < a.nranks && mine)
+      a.counts[t.slice * a.experts + e] = static_cast<int32_t>(of_rank[threadIdx.x]);
+    if (t.slice == 0 && mine) {
+      uint64_t all = chosen;
+      for (int i = 1; i < t.P; ++i) {
+        s += part_s[i * t.E + t.e];
+        all += part_c[i * t.E + t.e];
+      }
+      const float share = static_cast<float>(unit * static_cast<double>(all));
+      a.share[e] = share;
+      loss += s * share;
     }
-    a.share[e] = static_cast<float>(unit * static_cast<double>(chosen));
-    sums[0][e] = static_cast<float>(unit * static_cast<double>(chosen));
+    __syncthreads();
   }
-  column_sums<double, double>(ws->share_of_group, groups, a.experts,
-                              [&](int e, double s) { loss += s * static_cast<double>(sums[0][e]); });
   loss = block_sum<kBlock>(loss);
-  if (threadIdx.x == 0) *a.loss = static_cast<float>(loss);
+  if (threadIdx.x == 0) {
+    *a.loss = static_cast<float>(loss);
+    ws->groups_arrived.count = 0;
+  }
 }
 
 // --- gradient ----------------------------------------------------------------------------
