@@ -64,6 +64,13 @@ template <int LG, int S = 0> __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
+// A wave's LDS accesses happen in the order of its program; this keeps the
+// compiler from changing that.
+__device__ __forceinline__ void wave_in_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // A row's chunks as they lie in memory; -infinity beyond its end.
 using Chunk = uint32_t __attribute__((ext_vector_type(4)));
 template <class T> struct Loose;
@@ -79,16 +86,22 @@ template <class T> __device__ __forceinline__ Chunk minus_infinity() {
   return Chunk{w, w, w, w};
 }
 
+// Whether all lanes' parts of chunk c exist.  Launches take the smallest
+// arrangement that holds a row, so the lower half of the chunks always do.
+template <class S, int C> __device__ __forceinline__ bool whole_chunk(int c, int experts) {
+  return c < C / 2 || (c + 1) * S::G * S::W <= experts;
+}
+
 template <class S, class T, int C>
 __device__ __forceinline__ void load_chunks(const T* row, int experts, Chunk (&raw)[C]) {
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int col = (c * S::G + S::lane()) * S::W;
-    if (col + S::W <= experts) {
+    if (whole_chunk<S, C>(c, experts)) {
       raw[c] = *reinterpret_cast<const typename Loose<T>::type*>(row + col);
     } else {
-      raw[c] = minus_infinity<T>();
       T e[S::W];
+      raw[c] = minus_infinity<T>();
       __builtin_memcpy(e, &raw[c], 16);
 #pragma unroll
       for (int w = 0; w < S::W; ++w)
@@ -175,11 +188,12 @@ template <int LG, int L, int N, int S = 0> __device__ __forceinline__ void join_
 }
 
 // What was chosen for a row: lane k of the row has the k-th column, -1 for
-// none.  `top` is the largest logit, or (within 2^16) the end of its interval
+// none, and its logit (where a float32 key has cut it, only the interval).
+// `top` is the largest logit, or (within 2^16) the end of its interval
 // of keys, at most 8 away: any number near it serves the softmax.
 struct Choice {
   int index;
-  float top;
+  float value, top;
 };
 
 template <class T, int LG, int C> struct Keys {
@@ -248,6 +262,7 @@ __device__ __forceinline__ bool choose(const float (&x)[Shape<T, LG, C>::V], int
     }
   }
   out->top = from_order(top);
+  out->value = from_order(mine & ~kLow);
   out->index = lane < top_k && (mine & ~kLow) > kMinusInfinity ? kLow - (mine & kLow) : -1;
   return clear;
 }
@@ -266,7 +281,7 @@ __device__ __forceinline__ Choice choose_slowly(const float (&x)[Shape<T, LG, C>
     asm volatile("" : "+v"(y));                      // keeps this work on this path
     key[v] = y > -__builtin_inff() ? order(y, 0) : kNone;
   }
-  Choice out = {-1, 0.0f};
+  Choice out = {-1, 0.0f, 0.0f};
   for (int k = 0; k < top_k; ++k) {
     int best = kNone;
 #pragma unroll
@@ -282,7 +297,10 @@ __device__ __forceinline__ Choice choose_slowly(const float (&x)[Shape<T, LG, C>
         const int high = K::high(from_order(best));
         out.top = K::big(high) ? from_order(best) : from_order(high);
       }
-      if (S::lane() == k) out.index = col;
+      if (S::lane() == k) {
+        out.index = col;
+        out.value = from_order(best);
+      }
     }
 #pragma unroll
     for (int v = 0; v < S::V; ++v)
@@ -302,10 +320,9 @@ __device__ __forceinline__ uint32_t count_in(uint64_t pair) { return static_cast
 // Reads n rows (row, row + stride, ...) of a table, column e, several at a
 // time (they come from memory, about a microsecond each if one by one), and
 // hands them to take() in order.
-template <class Take>
+template <int kAtOnce, class Take>
 __device__ __forceinline__ void read_rows(const uint64_t* table, int row, int n, int stride, int experts, int e,
                                           const Take& take) {
-  constexpr int kAtOnce = 8;
   for (int i = 0; i < n; i += kAtOnce) {
     uint64_t x[kAtOnce];
 #pragma unroll
@@ -351,6 +368,7 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
   const uint32_t end = min(begin + a.rows_per_block, a.tokens);
   // a wave's rows are neighbours; rows past the end are read as the last one
   const uint32_t sub = wave * S::kRows + threadIdx.x % kWave / S::G;
+  float* row_sums = sums + sub * S::kColumns;
   Chunk next[C];
   bool next_token = false;
   auto fetch = [&](uint32_t first) {
@@ -362,7 +380,6 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
   for (uint32_t first = begin; first < end; first += kWaves * S::kRows) {
     const uint32_t i = min(first + sub, end - 1);
     const bool token = next_token;
-    const T* row = logits + i * a.row_stride;
     Chunk raw[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) raw[c] = next[c];
@@ -378,8 +395,18 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
 
     Choice choice;
     const bool clear = choose<T, LG, C, L>(x, a.top_k, token, &choice);
-    if (__any(token && !clear)) choice = choose_slowly<T, LG, C>(x, a.top_k);
-    if (!token) choice = {-1, 0.0f};
+    if (__any(token && !clear)) {
+      choice = choose_slowly<T, LG, C>(x, a.top_k);
+    } else if (sizeof(T) == 4) {
+      // the whole float32, by way of LDS: reading it again from memory would
+      // wait for the rows that are being read ahead
+#pragma unroll
+      for (int v = 0; v < V; ++v) row_sums[S::column(v)] = x[v];
+      wave_in_order();
+      choice.value = row_sums[max(choice.index, 0)];
+      wave_in_order();
+    }
+    if (!token) choice = {-1, 0.0f, 0.0f};
 
     // exp(x - top) = 2^(x log2(e) - top log2(e)): rounding the second product
     // scales a row's values by one factor, which the sum takes out.  Tops
@@ -392,7 +419,7 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
       top -= away;
     }
     const float shift = top * kLog2e;
-    const float xk = choice.index >= 0 ? widen(row[choice.index]) - away : -__builtin_inff();
+    const float xk = choice.index >= 0 ? choice.value - away : -__builtin_inff();
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -419,9 +446,8 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
   }
 
   // the block's row of sums
-  float* mine = sums + (wave * S::kRows + threadIdx.x % kWave / S::G) * S::kColumns;
 #pragma unroll
-  for (int v = 0; v < V; ++v) mine[S::column(v)] = total[v];
+  for (int v = 0; v < V; ++v) row_sums[S::column(v)] = total[v];
   live_rows = wave_sum(live_rows);
   if (threadIdx.x % kWave == 0) tokens[wave] = live_rows;
   __syncthreads();
@@ -433,15 +459,28 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
   const uint32_t block = rank * gridDim.x + blockIdx.x, block0 = block - blockIdx.x % a.group;
   uint32_t n = tokens[0] + tokens[1] + tokens[2] + tokens[3];
   static_assert(kWaves == 4, "four waves' sums");
-  // one group of one block in all joins its own row only; with one block a
-  // group, the groups' rows are the blocks'
+  // with one block a group, the groups' rows are the blocks'
   uint64_t* my_rows = in_group > 1 ? ws->of_block + static_cast<size_t>(block) * a.experts
                                    : ws->of_group + static_cast<size_t>(my_group) * a.experts;
+  const double only_unit = n > 0 ? a.experts / (a.top_k * (static_cast<double>(n) * n)) : 0.0;
+  double loss = 0.0;
   for (int e = threadIdx.x; e < a.experts; e += kBlock) {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < kWaves * S::kRows; ++i) s += sums[i * S::kColumns + e];
-    shared_store(&my_rows[e], pair_of(s, hist[e]));
+    if (groups == 1 && in_group == 1) {       // the only block
+      const float share = static_cast<float>(only_unit * hist[e]);
+      a.counts[e] = static_cast<int32_t>(hist[e]);
+      a.share[e] = share;
+      loss += static_cast<double>(s) * share;
+    } else {
+      shared_store(&my_rows[e], pair_of(s, hist[e]));
+    }
+  }
+  if (groups == 1 && in_group == 1) {
+    loss = block_sum<kBlock>(loss);
+    if (threadIdx.x == 0) *a.loss = static_cast<float>(loss);
+    return;
   }
   if (threadIdx.x == 0) shared_store(in_group > 1 ? &ws->tokens_of_block[block] : &ws->tokens_of_group[my_group], n);
 
@@ -456,7 +495,7 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
       double s = 0.0;
       uint32_t c = 0;
       const int rows = (static_cast<int>(in_group) - t.slice + t.P - 1) / t.P;
-      read_rows(ws->of_block, block0 + t.slice, rows, t.P, a.experts, e, [&](uint64_t x) {
+      read_rows<16>(ws->of_block, block0 + t.slice, rows, t.P, a.experts, e, [&](uint64_t x) {
         s += sum_in(x);
         c += count_in(x);
       });
@@ -490,7 +529,6 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
   const int end_rank = q > 1 ? (first_rank < min(a.nranks, together) ? first_rank + 1 : first_rank)
                              : (t.slice + 1) * a.nranks / t.P;
   const int per_rank = static_cast<int>(groups_of_rank), part = q > 1 ? t.slice % q : 0;
-  double loss = 0.0;
   for (int e0 = 0; e0 < a.experts; e0 += t.E) {
     const int e = min(e0 + t.e, a.experts - 1);
     const bool mine = e0 + t.e < a.experts;
@@ -501,7 +539,7 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
     int rank_of_row = first_rank, left = per_rank;
     const int rows = q > 1 ? (end_rank > first_rank ? (per_rank - part + q - 1) / q : 0)
                            : (end_rank - first_rank) * per_rank;
-    read_rows(ws->of_group, first_rank * per_rank + part, rows, q, a.experts, e, [&](uint64_t x) {
+    read_rows<32>(ws->of_group, first_rank * per_rank + part, rows, q, a.experts, e, [&](uint64_t x) {
       s += sum_in(x);
       c += count_in(x);
       chosen += count_in(x);
@@ -539,7 +577,7 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
 
 // --- gradient ----------------------------------------------------------------------------
 
-template <class T, int LG, int C>
+template <class T, int LG, int C, bool RENORMALIZE>
 __global__ __launch_bounds__(kBlock, 2) void route_grad_kernel(RouteGradArgs a) {
   using S = Shape<T, LG, C>;
   constexpr int V = S::V, W = S::W;
@@ -609,26 +647,23 @@ __global__ __launch_bounds__(kBlock, 2) void route_grad_kernel(RouteGradArgs a) 
     const float inv = live ? __builtin_amdgcn_rcpf(sum) : 0.0f;
 
     float add = dw;                // to dp of its expert, or (renormalized) to dx
-    if (a.renormalize) {
+    if constexpr (RENORMALIZE) {
       const float x = index >= 0 && live ? widen(row[index]) - away : -__builtin_inff();
       const float e = __builtin_amdgcn_exp2f(fmaf(x, kLog2e, -shift));
       const float all = row_sum<LG>(e);
       const float w = all > 0.0f ? e * __builtin_amdgcn_rcpf(all) : 0.0f;
       add = w * (dw - row_sum<LG>(w * dw));
     }
-    // a row's lanes are of one wave, whose LDS accesses happen in order
     if (index >= 0) at[index] = add;
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_in_order();
     float dot = 0.0f, here[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       here[v] = at[S::column(v)];
       p[v] *= inv;
-      dot = fmaf(p[v], a.renormalize ? coef[v] : coef[v] + here[v], dot);
+      dot = fmaf(p[v], RENORMALIZE ? coef[v] : coef[v] + here[v], dot);
     }
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_in_order();
     if (index >= 0) at[index] = 0.0f;
     dot = row_sum<LG>(dot);
     if (first + sub >= end) continue;
@@ -639,8 +674,7 @@ __global__ __launch_bounds__(kBlock, 2) void route_grad_kernel(RouteGradArgs a) 
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const int v = c * W + w;
-        dx[w] = a.renormalize ? fmaf(p[v], coef[v] - dot, here[v]) : p[v] * (coef[v] + here[v] - dot);
-        if (!live) dx[w] = 0.0f;
+        dx[w] = RENORMALIZE ? fmaf(p[v], coef[v] - dot, here[v]) : p[v] * (coef[v] + here[v] - dot);
       }
       const int col = (c * S::G + lane) * W;
       Chunk o;
@@ -651,7 +685,8 @@ __global__ __launch_bounds__(kBlock, 2) void route_grad_kernel(RouteGradArgs a) 
 #pragma unroll
         for (int w = 0; w < 4; ++w) o[w] = bf16x2_round(dx[2 * w], dx[2 * w + 1]);
       }
-      if (col + W <= a.experts) {
+      if (__any(!live) && !live) o = Chunk{0, 0, 0, 0};
+      if (whole_chunk<S, C>(c, a.experts)) {
         *reinterpret_cast<typename Loose<T>::type*>(out + col) = o;
       } else {
         T e[W];
@@ -694,7 +729,9 @@ template <class T, int LG, int C> hipError_t route_as(RouteArgs a, hipStream_t s
 
 template <class T, int LG, int C> hipError_t route_grad_as(RouteGradArgs a, hipStream_t stream) {
   const dim3 grid = grid_of(&a, kWaves * Shape<T, LG, C>::kRows, 1024);
-  return launch_rows(reinterpret_cast<const void*>(&route_grad_kernel<T, LG, C>), grid, &a, stream);
+  const void* fn = a.renormalize ? reinterpret_cast<const void*>(&route_grad_kernel<T, LG, C, true>)
+                                 : reinterpret_cast<const void*>(&route_grad_kernel<T, LG, C, false>);
+  return launch_rows(fn, grid, &a, stream);
 }
 
 // The smallest arrangement that holds a row: 8 lanes of 1 to 8 chunks, then
