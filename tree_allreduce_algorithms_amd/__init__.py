@@ -38,4 +38,14 @@ from .binding import (  # noqa: F401
     set_impl,
     tree_allreduce,
 )
-from .training import AdamW, Routing, dequantize, route, route_grad  # noqa: F401
+
+_TRAINING = ("AdamW", "Routing", "dequantize", "route", "route_grad")
+
+
+def __getattr__(name):
+    # these need torch, which the collectives' raw calls do without
+    if name in _TRAINING:
+        from . import training
+        globals().update({n: getattr(training, n) for n in _TRAINING})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -6,6 +6,9 @@ HIP kernels, on the current stream unless a call names another.
 """
 
 import ctypes
+from array import array
+
+import torch
 
 from . import binding
 from .binding import DTYPES, SUCCESS, AdamwStep, AdamwTensor, ArError, RouteShape, lib
@@ -13,20 +16,35 @@ from .binding import DTYPES, SUCCESS, AdamwStep, AdamwTensor, ArError, RouteShap
 BLOCK = 256   # elements that share one scale of an 8-bit state
 MAX_EXPERTS, MAX_TOP_K = 1024, 8
 ROUTE_WORKSPACE = 5000192   # AR_ROUTE_WORKSPACE
+_INF = float("inf")
+
+
+def _current_stream(dev):
+    """hipStream_t of the current stream of device `dev`."""
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# the same number without a stream object around it, where torch offers it
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
 def _handle(stream, dev):
     """hipStream_t of a torch stream, a raw handle, or (None) the current stream."""
-    import torch
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _current_stream(dev)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream_of(stream, dev):
+    """`stream` (a torch stream or a raw handle), or the current one of device `dev`."""
+    if stream is None:
+        return torch.cuda.current_stream(dev)
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=dev)
 
 
 def _flat(tensors, what, dev, dtypes, sizes):
     """`tensors` as a list: contiguous GPU tensors of one of `dtypes` (all the
     same) on `dev`, of these sizes."""
-    import torch
     tensors = list(tensors)
     if len(tensors) != len(sizes):
         raise ValueError(f"{what}: {len(tensors)} tensors for {len(sizes)} parameters")
@@ -67,7 +85,6 @@ class AdamW:
 
     def __init__(self, params, grads, copies=None, *, state_bits=32, state=None, steps=0,
                  betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, grad_scale=1.0):
-        import torch
         params = list(params)
         if not params:
             raise ValueError("need at least one parameter")
@@ -120,18 +137,24 @@ class AdamW:
         with binding._on_device(dev):
             self._norm = torch.zeros((), dtype=torch.float32, device=params[0].device)
             self._device = torch.frombuffer(self._host, dtype=torch.uint8).to(params[0].device)
-        self._call_args = (ctypes.addressof(self._host), self._device.data_ptr())
+        self._host_ptr, self._device_ptr = ctypes.addressof(self._host), self._device.data_ptr()
+        self._norm_ptr = self._norm.data_ptr()
         self._step_args = ctypes.byref(self._args)
         self._fn_norm, self._fn_step = lib().ar_adamw_grad_norm, lib().ar_adamw_step
+
+    def _run(self, fn, *args):
+        if torch.cuda.current_device() == self._dev:
+            return fn(self._host_ptr, self._device_ptr, *args)
+        with binding._on_device(self._dev):
+            return fn(self._host_ptr, self._device_ptr, *args)
 
     def grad_norm(self, max_norm=None, stream=None):
         """The 2-norm over all gradients (times ``grad_scale``), a float32 GPU
         scalar that the next call overwrites.  With ``max_norm`` the factor
         ``min(1, max_norm / norm)`` is kept for ``step(clip=True)``; nothing
         waits for the GPU."""
-        with binding._on_device(self._dev):
-            status = self._fn_norm(*self._call_args, float("inf") if max_norm is None else max_norm,
-                                   self._grad_scale, self._norm.data_ptr(), _handle(stream, self._dev))
+        status = self._run(self._fn_norm, _INF if max_norm is None else max_norm, self._grad_scale,
+                           self._norm_ptr, _handle(stream, self._dev))
         if status != SUCCESS:
             raise ArError(status, "grad_norm")
         self._clip_ready = max_norm is not None
@@ -145,8 +168,7 @@ class AdamW:
             raise ValueError("step(clip=True) needs grad_norm(max_norm=...) on these gradients first")
         args = self._args
         args.lr, args.step, args.clip = lr, self.steps + 1, 1 if clip else 0
-        with binding._on_device(self._dev):
-            status = self._fn_step(*self._call_args, self._step_args, _handle(stream, self._dev))
+        status = self._run(self._fn_step, self._step_args, _handle(stream, self._dev))
         if status != SUCCESS:
             raise ArError(status, "step")
         self.steps += 1
@@ -156,27 +178,27 @@ class AdamW:
 def dequantize(codes, scales, stream=None):
     """float32 values of the codes of an 8-bit AdamW state: int8 codes of
     ``exp_avg`` or uint8 codes of ``exp_avg_sq``, with one scale per 256."""
-    import torch
     if stream is not None:
         # the result belongs to that stream: its memory is not handed out
         # again before the kernel there has run
-        with torch.cuda.stream(_torch_stream(stream, [codes])):
+        with torch.cuda.stream(_stream_of(stream, codes.device)):
             return dequantize(codes, scales)
     if not isinstance(codes, torch.Tensor) or not codes.is_cuda or not scales.is_cuda:
         raise TypeError("codes and scales must be GPU tensors")
-    if codes.dtype not in (torch.int8, torch.uint8) or scales.dtype != torch.float32:
-        raise TypeError(f"need int8 or uint8 codes and float32 scales, not {codes.dtype} and "
-                        f"{scales.dtype}")
+    kind = codes.dtype
+    if (kind is not torch.int8 and kind is not torch.uint8) or scales.dtype is not torch.float32:
+        raise TypeError(f"need int8 or uint8 codes and float32 scales, not {kind} and {scales.dtype}")
     n, dev = codes.numel(), codes.get_device()
     if scales.numel() != -(-n // BLOCK) or scales.get_device() != dev:
         raise ValueError(f"{n} codes need {-(-n // BLOCK)} scales on their device")
     if not codes.is_contiguous() or not scales.is_contiguous():
         raise ValueError("codes and scales must be contiguous")
-    with binding._on_device(dev):
-        out = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
-        status = lib().ar_adamw_dequantize(codes.data_ptr(), scales.data_ptr(), n,
-                                           1 if codes.dtype == torch.int8 else 0, out.data_ptr(),
-                                           _handle(None, dev))
+    if torch.cuda.current_device() != dev:
+        with binding._on_device(dev):
+            return dequantize(codes, scales)
+    out = torch.empty_like(codes, dtype=torch.float32)
+    status = lib().ar_adamw_dequantize(codes.data_ptr(), scales.data_ptr(), n, kind is torch.int8,
+                                       out.data_ptr(), _current_stream(dev))
     if status != SUCCESS:
         raise ArError(status, "dequantize")
     return out
@@ -197,65 +219,65 @@ class Routing:
         self.loss, self.share, self._mask, self._shape = loss, share, mask, shape
 
 
-def _table(tensors):
-    """A host array of the tensors' addresses."""
-    return (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
-
-
 def _logits(logits):
-    """The ranks' logits as a list, checked: [tokens, experts] GPU tensors of
-    one type, size and row stride, experts next to each other."""
-    import torch
-    logits = list(logits)
-    if not 1 <= len(logits) <= binding.MAX_RANKS:
+    """The ranks' logits, checked: (addresses, device index, dtype, tokens,
+    experts, row stride) of [tokens, experts] GPU tensors of one type, shape
+    and strides, experts next to each other."""
+    n = len(logits)
+    if not 1 <= n <= binding.MAX_RANKS:
         raise ValueError(f"need the logits of 1 to {binding.MAX_RANKS} ranks")
     first = logits[0]
     if not isinstance(first, torch.Tensor) or not first.is_cuda:
         raise TypeError("logits must be GPU tensors")
-    if first.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"unsupported dtype {first.dtype}")
-    shape, stride, dtype, dev = first.shape, first.stride(), first.dtype, first.device
+    shape, stride, dtype, dev = first.shape, first.stride(), first.dtype, first.get_device()
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise TypeError(f"unsupported dtype {dtype}")
     if len(shape) != 2 or shape[1] < 1:
         raise ValueError("logits must be [tokens, experts]")
-    if stride[1] != 1 and shape[1] > 1 and shape[0] > 0 or (shape[0] > 1 and stride[0] < shape[1]):
+    tokens, experts = shape
+    if (stride[1] != 1 and experts > 1 and tokens > 0) or (tokens > 1 and stride[0] < experts):
         raise ValueError("a token's logits must lie next to each other, tokens apart")
+    ptrs = array("Q")
     for t in logits:
-        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev:
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
             raise TypeError("logits must share type and device")
         if t.shape != shape or t.stride() != stride:
             raise ValueError("logits must share shape and strides")
-    return logits, shape[0], shape[1], max(stride[0], shape[1])
+        ptrs.append(t.data_ptr())
+    return ptrs, dev, dtype, tokens, experts, max(stride[0], experts)
 
 
 def _ranks(tensors, n, shape, dtype, dev, what):
-    """One contiguous tensor a rank, as a list and as a table of addresses."""
-    import torch
-    tensors = list(tensors)
+    """Addresses of one contiguous tensor a rank."""
     if len(tensors) != n:
         raise ValueError(f"{what}: {len(tensors)} tensors for {n} ranks")
+    ptrs = array("Q")
     for t in tensors:
-        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev:
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
             raise TypeError(f"{what} must be {dtype} on the logits' device")
         if t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{what} must be contiguous, {tuple(shape)} a rank")
-    return tensors, _table(tensors)
+        ptrs.append(t.data_ptr())
+    return ptrs
+
+
+def _address(ptrs):
+    return None if ptrs is None else ptrs.buffer_info()[0]
 
 
 _route_workspaces = {}   # (device, stream handle) -> workspace
 
 
 def _route_workspace(device, handle):
-    """The stream's workspace, which every call leaves ready for the next.  A captured call
-    gets one of its own, cleared in the graph: its replays may run beside the
-    stream's other calls."""
-    import torch
+    """The stream's workspace, which every call leaves ready for the next.  A
+    captured call gets one of its own, cleared in the graph: its replays may
+    run beside the stream's other calls."""
     if torch.cuda.is_current_stream_capturing():
         return torch.zeros(ROUTE_WORKSPACE, dtype=torch.uint8, device=device)
-    key = (device, handle)
-    ws = _route_workspaces.get(key)
+    ws = _route_workspaces.get((device, handle))
     if ws is None:
         ws = torch.zeros(ROUTE_WORKSPACE, dtype=torch.uint8, device=device)
-        _route_workspaces[key] = ws
+        _route_workspaces[device, handle] = ws
     return ws
 
 
@@ -266,30 +288,31 @@ def route(logits, top_k, mask=None, renormalize=False, stream=None):
     rows may be strided); ``mask`` optionally lists one boolean [tokens] tensor
     a rank, False for what is no token.  Returns a ``Routing``.  Up to 1,024
     experts and 8 choices."""
-    import torch
-    if stream is not None:
-        with torch.cuda.stream(_torch_stream(stream, logits)):
+    logits = list(logits)
+    ptrs, dev, dtype, tokens, experts, row_stride = _logits(logits)
+    if stream is not None or torch.cuda.current_device() != dev:
+        with torch.cuda.stream(_stream_of(stream, dev)):
             return route(logits, top_k, mask, renormalize)
-    logits, tokens, experts, row_stride = _logits(logits)
-    n, device = len(logits), logits[0].device
+    n = len(ptrs)
     if not 1 <= top_k <= min(experts, MAX_TOP_K) or experts > MAX_EXPERTS:
         raise ValueError(f"top_k must be 1 to {min(experts, MAX_TOP_K)} of at most {MAX_EXPERTS} "
                          f"experts, not {top_k} of {experts}")
     masks = None
     if mask is not None:
-        mask, masks = _ranks(mask, n, (tokens,), torch.bool, device, "mask")
+        mask = list(mask)
+        masks = _ranks(mask, n, (tokens,), torch.bool, dev, "mask")
     shape = RouteShape(n, tokens, experts, row_stride, top_k, 1 if renormalize else 0,
-                       1 if logits[0].dtype == torch.float32 else 2)
-    with binding._on_device(device.index):
-        handle = torch.cuda.current_stream(device).cuda_stream
-        indices = torch.empty((n, tokens, top_k), dtype=torch.int32, device=device)
-        weights = torch.empty((n, tokens, top_k), dtype=torch.float32, device=device)
-        counts = torch.empty((n, experts), dtype=torch.int32, device=device)
-        loss = torch.empty((), dtype=torch.float32, device=device)
-        share = torch.empty(experts, dtype=torch.float32, device=device)
-        status = lib().ar_route(_table(logits), masks, ctypes.byref(shape), indices.data_ptr(),
-                                weights.data_ptr(), counts.data_ptr(), loss.data_ptr(),
-                                share.data_ptr(), _route_workspace(device, handle).data_ptr(), handle)
+                       DTYPES["float32" if dtype is torch.float32 else "bfloat16"])
+    device = logits[0].device
+    indices = torch.empty((n, tokens, top_k), dtype=torch.int32, device=device)
+    weights = torch.empty((n, tokens, top_k), dtype=torch.float32, device=device)
+    counts = torch.empty((n, experts), dtype=torch.int32, device=device)
+    loss = torch.empty((), dtype=torch.float32, device=device)
+    share = torch.empty(experts, dtype=torch.float32, device=device)
+    handle = _current_stream(dev)
+    status = lib().ar_route(_address(ptrs), _address(masks), ctypes.byref(shape), indices.data_ptr(),
+                            weights.data_ptr(), counts.data_ptr(), loss.data_ptr(), share.data_ptr(),
+                            _route_workspace(device, handle).data_ptr(), handle)
     if status != SUCCESS:
         raise ArError(status, "route")
     return Routing(indices, weights, counts, loss, share, (mask, masks), shape)
@@ -302,38 +325,29 @@ def route_grad(logits, routing, dweights=None, dloss=None, stream=None):
     ``logits`` are those that ``route`` took for ``routing``; ``dweights``
     lists one float32 [tokens, top_k] tensor a rank, ``dloss`` is a float32 GPU
     scalar; either may be left out."""
-    import torch
-    if stream is not None:
-        with torch.cuda.stream(_torch_stream(stream, logits)):
+    logits = list(logits)
+    ptrs, dev, dtype, tokens, experts, row_stride = _logits(logits)
+    if stream is not None or torch.cuda.current_device() != dev:
+        with torch.cuda.stream(_stream_of(stream, dev)):
             return route_grad(logits, routing, dweights, dloss)
-    logits, tokens, experts, row_stride = _logits(logits)
-    n, device, was = len(logits), logits[0].device, routing._shape
-    code = 1 if logits[0].dtype == torch.float32 else 2
-    if (n, tokens, experts, code) != (was.nranks, was.tokens, was.experts, was.dtype) or \
-            device != routing.indices.device:
+    n, shape = len(ptrs), routing._shape
+    code = DTYPES["float32" if dtype is torch.float32 else "bfloat16"]
+    if (n, tokens, experts, code) != (shape.nranks, shape.tokens, shape.experts, shape.dtype) or \
+            dev != routing.indices.get_device():
         raise ValueError("these are not the logits of this routing")
     grads = None
     if dweights is not None:
-        dweights, grads = _ranks(dweights, n, (tokens, was.top_k), torch.float32, device, "dweights")
-    if dloss is not None and (dloss.dtype != torch.float32 or dloss.device != device or dloss.numel() != 1):
+        grads = _ranks(list(dweights), n, (tokens, shape.top_k), torch.float32, dev, "dweights")
+    if dloss is not None and (dloss.dtype is not torch.float32 or dloss.get_device() != dev or
+                              dloss.numel() != 1):
         raise ValueError("dloss must be one float32 on the logits' device")
-    shape = was
-    if row_stride != was.row_stride:
-        shape = RouteShape(n, tokens, experts, row_stride, was.top_k, was.renormalize, code)
-    with binding._on_device(device.index):
-        dlogits = torch.empty((n, tokens, experts), dtype=logits[0].dtype, device=device)
-        status = lib().ar_route_grad(_table(logits), routing._mask[1], ctypes.byref(shape),
-                                     routing.indices.data_ptr(), routing.share.data_ptr(), grads,
-                                     None if dloss is None else dloss.data_ptr(), dlogits.data_ptr(),
-                                     torch.cuda.current_stream(device).cuda_stream)
+    if row_stride != shape.row_stride:
+        shape = RouteShape(n, tokens, experts, row_stride, shape.top_k, shape.renormalize, code)
+    dlogits = torch.empty((n, tokens, experts), dtype=dtype, device=logits[0].device)
+    status = lib().ar_route_grad(_address(ptrs), _address(routing._mask[1]), ctypes.byref(shape),
+                                 routing.indices.data_ptr(), routing.share.data_ptr(), _address(grads),
+                                 None if dloss is None else dloss.data_ptr(), dlogits.data_ptr(),
+                                 _current_stream(dev))
     if status != SUCCESS:
         raise ArError(status, "route_grad")
     return dlogits
-
-
-def _torch_stream(stream, tensors):
-    """`stream`, or a raw handle on the device of the first of `tensors`, as a torch stream."""
-    import torch
-    if hasattr(stream, "cuda_stream"):
-        return stream
-    return torch.cuda.ExternalStream(int(stream), device=tensors[0].device)
