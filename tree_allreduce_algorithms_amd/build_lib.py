@@ -1,15 +1,18 @@
-"""Build libar.so (HIP kernels for gfx950 + the C ABI) in-tree with hipcc.
+"""Build libar.so (HIP kernels for gfx950 + the C ABI) in-tree with hipcc, and
+_training.so (the training calls on torch tensors) with the host compiler.
 
 Usage: ``python -m tree_allreduce_algorithms_amd.build_lib`` (or call
 ``build()``).  hipcc cross-compiles for gfx950 without a GPU present.  Each
 source compiles to its own object in parallel (the kernel files instantiate
-many dtype x op x unroll variants), then one hipcc call links the library.
+many dtype x op x unroll variants), then one hipcc call links the library and
+one compiler call the module that calls it.
 """
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libar.so")
+MODULE = os.path.join(PKG, "_training.so")
 
 SOURCES = ["api.cpp", "plan.cpp", "ring_kernels.hip", "copy_kernels.hip", "tree_kernels.hip",
            "step_kernels.hip", "train/adamw.cpp", "train/adamw_kernels.hip", "train/route.cpp",
@@ -46,6 +50,20 @@ def hipcc():
 
 def sources():
     return [os.path.join(CSRC, s) for s in SOURCES]
+
+
+def module_command(out):
+    """The compiler call that builds the module, from torch's own headers and libraries."""
+    from torch.utils import cpp_extension
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no host C++ compiler (g++) found")
+    includes = [INCLUDE, *cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+            *[a for i in includes for a in ("-isystem", i)],
+            os.path.join(CSRC, "train", "torch_calls.cpp"), "-o", out, "-L", PKG, "-lar",
+            "-Wl,-rpath,$ORIGIN", *[f"-L{p}" for p in cpp_extension.library_paths()],
+            "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def build(verbose=False, jobs=None):
@@ -79,6 +97,11 @@ def build(verbose=False, jobs=None):
         if proc.returncode != 0:
             raise RuntimeError(f"link failed ({proc.returncode}):\n{proc.stdout}\n{proc.stderr}")
     os.replace(tmp, LIB)
+    tmp = MODULE + ".tmp"
+    proc = subprocess.run(module_command(tmp), capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"module failed ({proc.returncode}):\n{proc.stdout}\n{proc.stderr}")
+    os.replace(tmp, MODULE)
     return LIB
 
 

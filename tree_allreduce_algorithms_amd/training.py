@@ -2,20 +2,38 @@
 and the router of a mixture of experts.
 
 Argument marshalling only, as in ``binding``: the work is done by libar.so's
-HIP kernels, on the current stream unless a call names another.
+HIP kernels, on the current stream unless a call names another.  The calls
+that take lists of tensors or allocate their results go through _training.so,
+which is built with the library.
 """
 
 import ctypes
-from array import array
+import importlib.util
+import os
 
 import torch
 
 from . import binding
-from .binding import DTYPES, SUCCESS, AdamwStep, AdamwTensor, ArError, RouteShape, lib
+from .binding import DTYPES, SUCCESS, AdamwStep, AdamwTensor, ArError, lib
 
 BLOCK = 256   # elements that share one scale of an 8-bit state
 MAX_EXPERTS, MAX_TOP_K = 1024, 8
 ROUTE_WORKSPACE = 5000192   # AR_ROUTE_WORKSPACE
+
+
+def _load_module():
+    path = os.path.join(binding.PKG, "_training.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is not built; run "
+                           "`python -m tree_allreduce_algorithms_amd.build_lib` first")
+    lib()       # the library that it calls, from the same folder
+    spec = importlib.util.spec_from_file_location("_training", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+_training = _load_module()
 _INF = float("inf")
 
 
@@ -178,27 +196,15 @@ class AdamW:
 def dequantize(codes, scales, stream=None):
     """float32 values of the codes of an 8-bit AdamW state: int8 codes of
     ``exp_avg`` or uint8 codes of ``exp_avg_sq``, with one scale per 256."""
-    if stream is not None:
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
+        raise TypeError("codes and scales must be GPU tensors")
+    dev = codes.get_device()
+    if stream is not None or torch.cuda.current_device() != dev:
         # the result belongs to that stream: its memory is not handed out
         # again before the kernel there has run
-        with torch.cuda.stream(_stream_of(stream, codes.device)):
+        with torch.cuda.stream(_stream_of(stream, dev)):
             return dequantize(codes, scales)
-    if not isinstance(codes, torch.Tensor) or not codes.is_cuda or not scales.is_cuda:
-        raise TypeError("codes and scales must be GPU tensors")
-    kind = codes.dtype
-    if (kind is not torch.int8 and kind is not torch.uint8) or scales.dtype is not torch.float32:
-        raise TypeError(f"need int8 or uint8 codes and float32 scales, not {kind} and {scales.dtype}")
-    n, dev = codes.numel(), codes.get_device()
-    if scales.numel() != -(-n // BLOCK) or scales.get_device() != dev:
-        raise ValueError(f"{n} codes need {-(-n // BLOCK)} scales on their device")
-    if not codes.is_contiguous() or not scales.is_contiguous():
-        raise ValueError("codes and scales must be contiguous")
-    if torch.cuda.current_device() != dev:
-        with binding._on_device(dev):
-            return dequantize(codes, scales)
-    out = torch.empty_like(codes, dtype=torch.float32)
-    status = lib().ar_adamw_dequantize(codes.data_ptr(), scales.data_ptr(), n, kind is torch.int8,
-                                       out.data_ptr(), _current_stream(dev))
+    status, out = _training.dequantize(codes, scales, _current_stream(dev))
     if status != SUCCESS:
         raise ArError(status, "dequantize")
     return out
@@ -210,75 +216,35 @@ class Routing:
     """What ``route`` found, for the expert exchange and for ``route_grad``:
     ``indices`` [ranks, tokens, top_k] int32, ``weights`` (same shape, float32),
     ``counts`` [ranks, experts] int32, ``loss`` (float32 scalar) and ``share``
-    [experts] float32 (see ar_route)."""
+    [experts] float32 (see ar_route).  It keeps the masks, which must be as
+    they were when ``route_grad`` looks at them again."""
 
-    __slots__ = ("indices", "weights", "counts", "loss", "share", "_mask", "_shape")
+    __slots__ = ("indices", "weights", "counts", "loss", "share", "_dtype", "_mask", "_renormalize")
 
-    def __init__(self, indices, weights, counts, loss, share, mask, shape):
+    def __init__(self, indices, weights, counts, loss, share, dtype, mask, renormalize):
         self.indices, self.weights, self.counts = indices, weights, counts
-        self.loss, self.share, self._mask, self._shape = loss, share, mask, shape
+        self.loss, self.share, self._dtype = loss, share, dtype
+        self._mask, self._renormalize = mask, renormalize
 
 
-def _logits(logits):
-    """The ranks' logits, checked: (addresses, device index, dtype, tokens,
-    experts, row stride) of [tokens, experts] GPU tensors of one type, shape
-    and strides, experts next to each other."""
-    n = len(logits)
-    if not 1 <= n <= binding.MAX_RANKS:
-        raise ValueError(f"need the logits of 1 to {binding.MAX_RANKS} ranks")
-    first = logits[0]
-    if not isinstance(first, torch.Tensor) or not first.is_cuda:
-        raise TypeError("logits must be GPU tensors")
-    shape, stride, dtype, dev = first.shape, first.stride(), first.dtype, first.get_device()
-    if dtype is not torch.float32 and dtype is not torch.bfloat16:
-        raise TypeError(f"unsupported dtype {dtype}")
-    if len(shape) != 2 or shape[1] < 1:
-        raise ValueError("logits must be [tokens, experts]")
-    tokens, experts = shape
-    if (stride[1] != 1 and experts > 1 and tokens > 0) or (tokens > 1 and stride[0] < experts):
-        raise ValueError("a token's logits must lie next to each other, tokens apart")
-    ptrs = array("Q")
-    for t in logits:
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
-            raise TypeError("logits must share type and device")
-        if t.shape != shape or t.stride() != stride:
-            raise ValueError("logits must share shape and strides")
-        ptrs.append(t.data_ptr())
-    return ptrs, dev, dtype, tokens, experts, max(stride[0], experts)
+_route_workspaces = {}   # (device index, stream handle) -> workspace
 
 
-def _ranks(tensors, n, shape, dtype, dev, what):
-    """Addresses of one contiguous tensor a rank."""
-    if len(tensors) != n:
-        raise ValueError(f"{what}: {len(tensors)} tensors for {n} ranks")
-    ptrs = array("Q")
-    for t in tensors:
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
-            raise TypeError(f"{what} must be {dtype} on the logits' device")
-        if t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous, {tuple(shape)} a rank")
-        ptrs.append(t.data_ptr())
-    return ptrs
-
-
-def _address(ptrs):
-    return None if ptrs is None else ptrs.buffer_info()[0]
-
-
-_route_workspaces = {}   # (device, stream handle) -> workspace
-
-
-def _route_workspace(device, handle):
+def _route_workspace(dev, handle):
     """The stream's workspace, which every call leaves ready for the next.  A
     captured call gets one of its own, cleared in the graph: its replays may
     run beside the stream's other calls."""
     if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(ROUTE_WORKSPACE, dtype=torch.uint8, device=device)
-    ws = _route_workspaces.get((device, handle))
+        return torch.zeros(ROUTE_WORKSPACE, dtype=torch.uint8, device=f"cuda:{dev}")
+    ws = _route_workspaces.get((dev, handle))
     if ws is None:
-        ws = torch.zeros(ROUTE_WORKSPACE, dtype=torch.uint8, device=device)
-        _route_workspaces[device, handle] = ws
+        ws = torch.zeros(ROUTE_WORKSPACE, dtype=torch.uint8, device=f"cuda:{dev}")
+        _route_workspaces[dev, handle] = ws
     return ws
+
+
+def _list(tensors):
+    return tensors if tensors is None or type(tensors) is list else list(tensors)
 
 
 def route(logits, top_k, mask=None, renormalize=False, stream=None):
@@ -288,34 +254,17 @@ def route(logits, top_k, mask=None, renormalize=False, stream=None):
     rows may be strided); ``mask`` optionally lists one boolean [tokens] tensor
     a rank, False for what is no token.  Returns a ``Routing``.  Up to 1,024
     experts and 8 choices."""
-    logits = list(logits)
-    ptrs, dev, dtype, tokens, experts, row_stride = _logits(logits)
+    logits, mask = _list(logits), _list(mask)
+    dev = _training.device(logits)
     if stream is not None or torch.cuda.current_device() != dev:
         with torch.cuda.stream(_stream_of(stream, dev)):
             return route(logits, top_k, mask, renormalize)
-    n = len(ptrs)
-    if not 1 <= top_k <= min(experts, MAX_TOP_K) or experts > MAX_EXPERTS:
-        raise ValueError(f"top_k must be 1 to {min(experts, MAX_TOP_K)} of at most {MAX_EXPERTS} "
-                         f"experts, not {top_k} of {experts}")
-    masks = None
-    if mask is not None:
-        mask = list(mask)
-        masks = _ranks(mask, n, (tokens,), torch.bool, dev, "mask")
-    shape = RouteShape(n, tokens, experts, row_stride, top_k, 1 if renormalize else 0,
-                       DTYPES["float32" if dtype is torch.float32 else "bfloat16"])
-    device = logits[0].device
-    indices = torch.empty((n, tokens, top_k), dtype=torch.int32, device=device)
-    weights = torch.empty((n, tokens, top_k), dtype=torch.float32, device=device)
-    counts = torch.empty((n, experts), dtype=torch.int32, device=device)
-    loss = torch.empty((), dtype=torch.float32, device=device)
-    share = torch.empty(experts, dtype=torch.float32, device=device)
     handle = _current_stream(dev)
-    status = lib().ar_route(_address(ptrs), _address(masks), ctypes.byref(shape), indices.data_ptr(),
-                            weights.data_ptr(), counts.data_ptr(), loss.data_ptr(), share.data_ptr(),
-                            _route_workspace(device, handle).data_ptr(), handle)
+    workspace = _route_workspace(dev, handle)
+    status, *outputs = _training.route(logits, top_k, mask, renormalize, workspace.data_ptr(), handle)
     if status != SUCCESS:
         raise ArError(status, "route")
-    return Routing(indices, weights, counts, loss, share, (mask, masks), shape)
+    return Routing(*outputs, logits[0].dtype, mask, renormalize)
 
 
 def route_grad(logits, routing, dweights=None, dloss=None, stream=None):
@@ -325,29 +274,14 @@ def route_grad(logits, routing, dweights=None, dloss=None, stream=None):
     ``logits`` are those that ``route`` took for ``routing``; ``dweights``
     lists one float32 [tokens, top_k] tensor a rank, ``dloss`` is a float32 GPU
     scalar; either may be left out."""
-    logits = list(logits)
-    ptrs, dev, dtype, tokens, experts, row_stride = _logits(logits)
+    logits, dweights = _list(logits), _list(dweights)
+    dev = _training.device(logits)
     if stream is not None or torch.cuda.current_device() != dev:
         with torch.cuda.stream(_stream_of(stream, dev)):
             return route_grad(logits, routing, dweights, dloss)
-    n, shape = len(ptrs), routing._shape
-    code = DTYPES["float32" if dtype is torch.float32 else "bfloat16"]
-    if (n, tokens, experts, code) != (shape.nranks, shape.tokens, shape.experts, shape.dtype) or \
-            dev != routing.indices.get_device():
-        raise ValueError("these are not the logits of this routing")
-    grads = None
-    if dweights is not None:
-        grads = _ranks(list(dweights), n, (tokens, shape.top_k), torch.float32, dev, "dweights")
-    if dloss is not None and (dloss.dtype is not torch.float32 or dloss.get_device() != dev or
-                              dloss.numel() != 1):
-        raise ValueError("dloss must be one float32 on the logits' device")
-    if row_stride != shape.row_stride:
-        shape = RouteShape(n, tokens, experts, row_stride, shape.top_k, shape.renormalize, code)
-    dlogits = torch.empty((n, tokens, experts), dtype=dtype, device=logits[0].device)
-    status = lib().ar_route_grad(_address(ptrs), _address(routing._mask[1]), ctypes.byref(shape),
-                                 routing.indices.data_ptr(), routing.share.data_ptr(), _address(grads),
-                                 None if dloss is None else dloss.data_ptr(), dlogits.data_ptr(),
-                                 _current_stream(dev))
+    status, dlogits = _training.route_grad(logits, routing._dtype, routing.indices, routing.share,
+                                           routing._mask, routing._renormalize, dweights, dloss,
+                                           _current_stream(dev))
     if status != SUCCESS:
         raise ArError(status, "route_grad")
     return dlogits
