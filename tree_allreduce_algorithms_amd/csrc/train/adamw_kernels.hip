@@ -209,12 +209,15 @@ __device__ __forceinline__ double row_max(double x) {
 // between (j + 1/2)^2 and (j + 3/4)^2, so the only border in doubt is that
 // above j = floor(root); it is decided in float64, where scale * border is
 // exact.  An 8-bit step thus rounds as the definition in 64 bits does, at the
-// price of about ten float64 instructions a value.
+// price of a few float64 instructions a value.
 //
 // Scales are one per block and therefore the same in a row's lanes, which
 // share the cost of computing them over sixteen elements each.
 __device__ __forceinline__ uint32_t floor_root(float t) {
   return static_cast<uint32_t>(__builtin_amdgcn_sqrtf(t));
+}
+__device__ __forceinline__ double below_border(uint32_t j) {       // j^2 + j
+  return static_cast<double>(__umul24(j, j) + j);
 }
 
 // The float32 nearest to x / d: one correction step makes the quotient as
@@ -224,9 +227,14 @@ __device__ __forceinline__ float quotient(double x, double d, double inv_d) {
   return static_cast<float>(fma(fma(-q, d, x), inv_d, q));
 }
 
+// The roots' arguments come from float32 numbers that the step has anyway,
+// |m| and sqrt(v).  Where a scale is `tiny`, they could be subnormal (which
+// root and reciprocal take as 0) or the scale's reciprocal infinite, and the
+// arguments are taken in float64 instead.
 struct ScaleM {
-  double a, half, inv;
-  float stored;
+  double a, half;
+  float stored, inv;
+  bool tiny;
   // `top`: the block's largest |m|
   __device__ explicit ScaleM(double top) {
     const float s = quotient(top, 16129.0, 1.0 / 16129.0);
@@ -234,21 +242,24 @@ struct ScaleM {
     stored = s < __builtin_inff() ? s : __builtin_nanf("");
     a = ok ? s : __builtin_inf();                 // no value is above its borders
     half = a * 0.5;
-    inv = ok ? __builtin_amdgcn_rcp(a) : 0.0;
+    inv = ok ? __builtin_amdgcn_rcpf(s) : 0.0f;
+    tiny = ok && s < 1e-30f;
   }
-  __device__ __forceinline__ uint32_t code(double m) const {
+  template <bool TINY> __device__ __forceinline__ uint32_t code(double m, float m32) const {
     const double x = fabs(m);
-    const uint32_t j = floor_root(static_cast<float>(x * inv));
-    const double border = fma(a, static_cast<double>(j * j + j), half);
-    const int q = min(static_cast<int>(j + (x > border ? 1 : 0)), 127);
-    const int sign = static_cast<int>(__builtin_bit_cast(uint64_t, m) >> 32) >> 31;
-    return static_cast<uint32_t>((q ^ sign) - sign);
+    const float t = TINY ? static_cast<float>(tiny ? x * __builtin_amdgcn_rcp(a) : x * inv) : fabsf(m32) * inv;
+    const uint32_t j = floor_root(t);
+    uint32_t q = j + (x > fma(a, below_border(j), half) ? 1u : 0u);
+    if (TINY) q = min(q, 127u);                   // a subnormal scale may be half of what it should be
+    const uint32_t sign = static_cast<uint32_t>(static_cast<int>(__builtin_bit_cast(uint64_t, m) >> 32) >> 31);
+    return (q ^ sign) - sign;
   }
 };
 
 struct ScaleV {
-  double r, half, inv2, zero;
-  float stored;
+  double r, half, zero;
+  float stored, inv;
+  bool tiny;
   // `top`: the block's largest v
   __device__ explicit ScaleV(double top) {
     const float s = quotient(sqrt(top), 65025.0, 1.0 / 65025.0);
@@ -256,13 +267,16 @@ struct ScaleV {
     stored = s < __builtin_inff() ? s : __builtin_nanf("");
     r = ok ? s : __builtin_inf();
     half = r * 0.5;
-    inv2 = ok ? __builtin_amdgcn_rcp(r * r) : 0.0;
     zero = ok ? 0.0 : __builtin_inf();
+    inv = ok ? __builtin_amdgcn_rcpf(s) : 0.0f;
+    tiny = ok && s < 1e-18f;
   }
-  __device__ __forceinline__ uint32_t code(double v) const {
-    const uint32_t j = floor_root(__builtin_amdgcn_sqrtf(static_cast<float>(v * inv2)));
-    const double border = fma(r, static_cast<double>(j * j + j), half);
-    const uint32_t u = min(j + (v > border * border ? 1u : 0u), 255u);
+  template <bool TINY> __device__ __forceinline__ uint32_t code(double v, float root) const {
+    const float t = TINY ? static_cast<float>(__builtin_amdgcn_sqrt(v) * (tiny ? __builtin_amdgcn_rcp(r) : inv)) : root * inv;
+    const uint32_t j = floor_root(t);
+    const double border = fma(r, below_border(j), half);
+    uint32_t u = j + (v > border * border ? 1u : 0u);
+    if (TINY) u = min(u, 255u);
     return max(u, v > zero ? 1u : 0u);
   }
 };
@@ -289,8 +303,8 @@ __device__ __forceinline__ double units(uint8_t code) {
 // the factor in front and to eps.  The root and the reciprocal are single
 // instructions, off by one step of the last place each; the root takes a
 // subnormal v (a root below 1.1e-19) as 0.
-__device__ __forceinline__ float updated(float p, float m, float v, const AdamwStepArgs& a) {
-  const float u = m * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v) + a.eps);
+__device__ __forceinline__ float updated(float p, float m, float root_v, const AdamwStepArgs& a) {
+  const float u = m * __builtin_amdgcn_rcpf(root_v + a.eps);
   return p - fmaf(a.lr_wd, p, a.lr * u);
 }
 
@@ -317,12 +331,36 @@ __device__ __forceinline__ void step32(const AdamwStepArgs& a, const AdamwTensor
       const float x = widen(g[q].e[i]) * c;
       m[q].e[i] = fmaf(b1, m[q].e[i], one_b1 * x);
       v[q].e[i] = fmaf(b2, v[q].e[i], one_b2 * x * x);
-      out.e[i] = updated(widen(p[q].e[i]), m[q].e[i], v[q].e[i], a);
+      out.e[i] = updated(widen(p[q].e[i]), m[q].e[i], __builtin_amdgcn_sqrtf(v[q].e[i]), a);
     }
     l.template store<float>(t.m, q, m[q]);
     l.template store<float>(t.v, q, v[q]);
     l.template store<P>(t.p, q, narrow<P>(out));
     if constexpr (COPY) l.template store<uint16_t>(t.copy, q, narrow<uint16_t>(out));
+  }
+}
+
+// The update from m and v, and their codes.
+template <bool TINY, class P, bool COPY, class L>
+__device__ __forceinline__ void finish8(const AdamwStepArgs& a, const AdamwTensor& t, const L& l,
+                                        const Quad<P> (&p)[kQuads], const double (&m)[kQuads][4],
+                                        const double (&v)[kQuads][4], const ScaleM& sm, const ScaleV& sv) {
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q) {
+    Quad<float> out;
+    uint32_t nm[4], nv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float m32 = static_cast<float>(m[q][i]);
+      const float root = __builtin_amdgcn_sqrtf(static_cast<float>(v[q][i]));
+      out.e[i] = updated(widen(p[q].e[i]), m32, root, a);
+      nm[i] = sm.template code<TINY>(m[q][i], m32);
+      nv[i] = sv.template code<TINY>(v[q][i], root);
+    }
+    l.template store<P>(t.p, q, narrow<P>(out));
+    if constexpr (COPY) l.template store<uint16_t>(t.copy, q, narrow<uint16_t>(out));
+    l.template store<int8_t>(t.m, q, __builtin_bit_cast(Quad<int8_t>, pack(nm[0], nm[1], nm[2], nm[3])));
+    l.template store<uint8_t>(t.v, q, __builtin_bit_cast(Quad<uint8_t>, pack(nv[0], nv[1], nv[2], nv[3])));
   }
 }
 
@@ -339,14 +377,14 @@ __device__ __forceinline__ void step8(const AdamwStepArgs& a, const AdamwTensor&
   // factors of a block's sixteen elements a lane taken together first
   const double old_m = a.b1 * am, old_v = a.root_b2 * rv;
   const double new_m = a.one_b1 * c, new_v = a.root_one_b2 * c;
+  Quad<P> p[kQuads];
   double m[kQuads][4], v[kQuads][4], top_m = 0.0, top_v = 0.0, sum_v = 0.0;
 #pragma unroll
   for (int q = 0; q < kQuads; ++q) {
-    const Quad<P> p = l.template load<P>(t.p, q);
+    p[q] = l.template load<P>(t.p, q);
     const Quad<G> g = l.template load<G>(t.g, q);
     const Quad<int8_t> qm = l.template load<int8_t>(t.m, q);
     const Quad<uint8_t> qv = l.template load<uint8_t>(t.v, q);
-    Quad<float> out;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const double x = widen(g.e[i]), old = units(qv.e[i]) * old_v, now = x * new_v;
@@ -355,10 +393,7 @@ __device__ __forceinline__ void step8(const AdamwStepArgs& a, const AdamwTensor&
       top_m = fmax(top_m, fabs(m[q][i]));
       top_v = fmax(top_v, v[q][i]);
       sum_v += v[q][i];
-      out.e[i] = updated(widen(p.e[i]), static_cast<float>(m[q][i]), static_cast<float>(v[q][i]), a);
     }
-    l.template store<P>(t.p, q, narrow<P>(out));
-    if constexpr (COPY) l.template store<uint16_t>(t.copy, q, narrow<uint16_t>(out));
   }
   // a maximum leaves a NaN out; a NaN is in v where the gradient or v's scale
   // is one, and in m where the gradient or m's scale is
@@ -366,13 +401,10 @@ __device__ __forceinline__ void step8(const AdamwStepArgs& a, const AdamwTensor&
   if (sum_v != sum_v || am != am) top_m = __builtin_nan("");
   const ScaleM sm(row_max(top_m));
   const ScaleV sv(row_max(top_v));
-#pragma unroll
-  for (int q = 0; q < kQuads; ++q) {
-    const uint32_t nm = pack(sm.code(m[q][0]), sm.code(m[q][1]), sm.code(m[q][2]), sm.code(m[q][3]));
-    const uint32_t nv = pack(sv.code(v[q][0]), sv.code(v[q][1]), sv.code(v[q][2]), sv.code(v[q][3]));
-    l.template store<int8_t>(t.m, q, __builtin_bit_cast(Quad<int8_t>, nm));
-    l.template store<uint8_t>(t.v, q, __builtin_bit_cast(Quad<uint8_t>, nv));
-  }
+  if (!WHOLE || __any(sm.tiny || sv.tiny))
+    finish8<true, P, COPY>(a, t, l, p, m, v, sm, sv);
+  else
+    finish8<false, P, COPY>(a, t, l, p, m, v, sm, sv);
   if (exists && threadIdx.x % 16 == 0) {
     *ms = sm.stored;
     *vs = sv.stored;
@@ -380,7 +412,7 @@ __device__ __forceinline__ void step8(const AdamwStepArgs& a, const AdamwTensor&
 }
 
 template <int BITS, class P, class G, bool COPY>
-__global__ __launch_bounds__(kBlock) void adamw_step_kernel(AdamwStepArgs a) {
+__global__ __launch_bounds__(kBlock, 3) void adamw_step_kernel(AdamwStepArgs a) {
   const AdamwTile tile = reinterpret_cast<const AdamwTile*>(a.plan + a.tiles_at)[blockIdx.x];
   const AdamwTensor t = reinterpret_cast<const AdamwTensor*>(a.plan + a.tensors_at)[tile.tensor];
   const float c = a.clip ? reinterpret_cast<const AdamwSums*>(a.plan + a.sums_at)->factor : a.factor;
