@@ -150,11 +150,13 @@ ar_status_t ar_adamw_plan(const ar_adamw_tensor_t* tensors, int ntensors, ar_dty
   AdamwTile* tile = reinterpret_cast<AdamwTile*>(base + l.tiles_at);
   const uintptr_t pquad = param_dtype == AR_FLOAT32 ? 16 : 8, gquad = grad_dtype == AR_FLOAT32 ? 16 : 8;
   const uintptr_t squad = state_bits == 32 ? 16 : 4;
+  const uint64_t read = (param_dtype == AR_FLOAT32 ? 4 : 2) + (grad_dtype == AR_FLOAT32 ? 4 : 2) + state_bits / 4;
   uint32_t k = 0;
   for (int i = 0; i < ntensors; ++i) {
     const ar_adamw_tensor_t& x = tensors[i];
     if (x.count == 0) continue;
     h->has_copy = x.copy != nullptr;
+    h->touched += x.count * read;
     const bool vec = aligned(x.param, pquad) && aligned(x.grad, gquad) && aligned(x.copy, 8) &&
                      aligned(x.exp_avg, squad) && aligned(x.exp_avg_sq, squad);
     out[k] = {x.param, x.grad, x.copy, x.exp_avg, x.exp_avg_sq, x.exp_avg_scale, x.exp_avg_sq_scale,
@@ -221,7 +223,7 @@ ar_status_t ar_adamw_step(const void* plan, void* device_plan, const ar_adamw_st
   return ar::launch_status(ar::enqueue([&] {
     return ar::launch_adamw_step(a, h->tiles, static_cast<ar_dtype_t>(h->param_dtype),
                                  static_cast<ar_dtype_t>(h->grad_dtype), h->state_bits,
-                                 h->has_copy != 0, stream);
+                                 h->has_copy != 0, h->touched <= ar::kKeepBytes, stream);
   }));
 }
 

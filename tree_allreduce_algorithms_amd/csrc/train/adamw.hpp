@@ -19,13 +19,19 @@ namespace ar {
 constexpr uint32_t kAdamwMagic = 0x41573031u;
 constexpr uint32_t kAdamwTile = 4096;       // elements of a tile
 
-// One block a tile; a launch has less than 2^32 threads.
-constexpr uint32_t kAdamwMaxTiles = (1u << 24) - 1;
+// At most four blocks a tile; a launch has less than 2^32 threads.
+constexpr uint32_t kAdamwMaxTiles = (1u << 22) - 1;
+
+// A 32-bit step whose reads come to this much or less goes through the caches
+// for them, a longer one past them.  Norm and step, float32 throughout: 256 MiB
+// 83 us through and 97 past, 320 MiB 103 and 122, 400 MiB 154 and 145, 1 GiB
+// 391 and 369.
+constexpr uint64_t kKeepBytes = 320ull << 20;
 
 // Blocks of a norm, and how many of them make a group: the sums of a group's
 // blocks, and those of the groups, are added up by one block.
-constexpr uint32_t kMaxNormBlocks = 2048;
-constexpr uint32_t kNormGroup = 64;
+constexpr uint32_t kMaxNormBlocks = 1024;
+constexpr uint32_t kNormGroup = 32;
 constexpr uint32_t kNormGroups = kMaxNormBlocks / kNormGroup;
 
 struct AdamwHead {
@@ -41,6 +47,7 @@ struct AdamwHead {
   uint64_t sums_at;
   uint64_t tensors_at;
   uint64_t tiles_at;
+  uint64_t touched;       // bytes that a step reads
 };
 
 struct AdamwSums {
@@ -94,7 +101,7 @@ struct AdamwStepArgs {
 
 hipError_t launch_adamw_norm(const AdamwNormArgs& a, ar_dtype_t grad_dtype, hipStream_t stream);
 hipError_t launch_adamw_step(const AdamwStepArgs& a, uint32_t tiles, ar_dtype_t param_dtype,
-                             ar_dtype_t grad_dtype, int state_bits, bool copy, hipStream_t stream);
+                             ar_dtype_t grad_dtype, int state_bits, bool copy, bool keep, hipStream_t stream);
 hipError_t launch_adamw_dequantize(const void* codes, const float* scales, uint64_t count,
                                    bool is_signed, float* out, hipStream_t stream);
 

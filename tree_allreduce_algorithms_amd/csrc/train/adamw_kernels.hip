@@ -44,31 +44,31 @@ template <> struct Raw<uint8_t> {
 
 // Which elements of a tensor a lane has: kQuads runs of four, `step` apart.
 // WHOLE: all of the wave's elements exist, and the tensor's pointers allow
-// quads.  Only the last wave of a tensor takes the other path, or one whose
-// tensors are aligned to their elements only.
+// quads.  Only the last wave of a tensor goes element by element, or those of
+// arrays that are aligned to their elements only.
 template <bool WHOLE> struct Lanes {
   uint64_t first, count;
   uint32_t step;
-  bool vec;       // the tensor's pointers allow quads
   __device__ uint64_t at(int q) const { return first + q * step; }
   template <class T> __device__ __forceinline__ Quad<T> load(const void* p, int q) const {
     using R = typename Raw<T>::type;
-    const AR_GLOBAL T* x = (const AR_GLOBAL T*)p + at(q);
-    if (WHOLE || (vec && at(q) + 4 <= count)) {
+    if constexpr (WHOLE) {
+      const AR_GLOBAL T* x = (const AR_GLOBAL T*)p + at(q);
       if constexpr (sizeof(T) == 1)
         return __builtin_bit_cast(Quad<T>, *(const AR_GLOBAL R*)x);
       else
         return __builtin_bit_cast(Quad<T>, __builtin_nontemporal_load((const AR_GLOBAL R*)x));
     }
+    // past the end the last element again, so that no access waits for a branch
     Quad<T> v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v.e[i] = at(q) + i < count ? x[i] : T(0);
+    for (int i = 0; i < 4; ++i) v.e[i] = ((const AR_GLOBAL T*)p)[at(q) + i < count ? at(q) + i : count - 1];
     return v;
   }
   template <class T> __device__ __forceinline__ void store(void* p, int q, const Quad<T>& v) const {
     using R = typename Raw<T>::type;
     AR_GLOBAL T* x = (AR_GLOBAL T*)p + at(q);
-    if (WHOLE || (vec && at(q) + 4 <= count)) {
+    if constexpr (WHOLE) {
       if constexpr (sizeof(T) == 1)
         *(AR_GLOBAL R*)x = __builtin_bit_cast(R, v);
       else
@@ -91,15 +91,15 @@ __device__ __forceinline__ bool whole(uint64_t begin, uint64_t count, bool vec) 
 }
 
 // A wave's elements spread so that each of its accesses is one run.
-template <bool WHOLE> __device__ __forceinline__ Lanes<WHOLE> runs_of(uint64_t begin, uint64_t count, bool vec) {
-  return {begin + threadIdx.x % kWave * 4, count, 4 * kWave, vec};
+template <bool WHOLE> __device__ __forceinline__ Lanes<WHOLE> runs_of(uint64_t begin, uint64_t count) {
+  return {begin + threadIdx.x % kWave * 4, count, 4 * kWave};
 }
 
 // The same elements, each row of 16 lanes with one block of 256: an access is
 // four runs of 16 quads, and a block's maximum needs the row only.
-template <bool WHOLE> __device__ __forceinline__ Lanes<WHOLE> rows_of(uint64_t begin, uint64_t count, bool vec) {
+template <bool WHOLE> __device__ __forceinline__ Lanes<WHOLE> rows_of(uint64_t begin, uint64_t count) {
   const uint32_t lane = threadIdx.x % kWave;
-  return {begin + lane / 16 * AR_ADAMW_BLOCK + lane % 16 * 4, count, 64, vec};
+  return {begin + lane / 16 * AR_ADAMW_BLOCK + lane % 16 * 4, count, 64};
 }
 
 __device__ __forceinline__ float widen(float x) { return x; }
@@ -118,7 +118,7 @@ template <class T> __device__ __forceinline__ Quad<T> narrow(const Quad<float>& 
 
 template <bool WHOLE, class G>
 __device__ __forceinline__ void add_squares(const AdamwTensor& t, uint64_t begin, double* sum) {
-  const Lanes<WHOLE> l = runs_of<WHOLE>(begin, t.count, t.vec != 0);
+  const Lanes<WHOLE> l = runs_of<WHOLE>(begin, t.count);
   Quad<G> g[kQuads];
 #pragma unroll
   for (int q = 0; q < kQuads; ++q) g[q] = l.template load<G>(t.g, q);
@@ -126,7 +126,7 @@ __device__ __forceinline__ void add_squares(const AdamwTensor& t, uint64_t begin
   for (int q = 0; q < kQuads; ++q)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const double x = widen(g[q].e[i]);
+      const double x = WHOLE || l.at(q) + i < t.count ? widen(g[q].e[i]) : 0.0f;
       sum[i] = fma(x, x, sum[i]);
     }
 }
@@ -136,8 +136,9 @@ __device__ __forceinline__ void add_squares(const AdamwTensor& t, uint64_t begin
 // are decided on what it scales.  Every block leaves a partial sum; the last
 // block of each group adds up the group's, the last group the groups', each
 // in their order, so a norm is one launch and its bits do not depend on which
-// block comes last.  (One counter for all blocks would take the 2,048 of a
-// large norm 40 us: an atomic on one address measured 20 ns.)
+// block comes last.  1,024 blocks in groups of 32 measured 175 us for 300M
+// float32 (6.9 TB/s) and 87 us for 300M bfloat16; 2,048 in groups of 64 175
+// and 97, 512 in groups of 16 167 and 130.
 template <class G> __global__ __launch_bounds__(kBlock) void adamw_norm_kernel(AdamwNormArgs a) {
   const AdamwTensor* tensors = reinterpret_cast<const AdamwTensor*>(a.plan + a.tensors_at);
   const AdamwTile* tiles = reinterpret_cast<const AdamwTile*>(a.plan + a.tiles_at);
@@ -162,13 +163,13 @@ template <class G> __global__ __launch_bounds__(kBlock) void adamw_norm_kernel(A
     if (threadIdx.x == 0) shared_store(&sums->of_block[blockIdx.x], all);
     if (!last_to_arrive(&sums->arrived[group].count, members)) return;
     all = block_sum<kBlock>(threadIdx.x < members ? shared_load(&sums->of_block[first + threadIdx.x]) : 0.0);
-    if (threadIdx.x == 0) {
-      sums->arrived[group].count = 0;
-      shared_store(&sums->of_group[group], all);
+    if (threadIdx.x == 0) sums->arrived[group].count = 0;
+    if (groups > 1) {
+      if (threadIdx.x == 0) shared_store(&sums->of_group[group], all);
+      if (!last_to_arrive(&sums->groups_arrived.count, groups)) return;
+      all = block_sum<kBlock>(threadIdx.x < groups ? shared_load(&sums->of_group[threadIdx.x]) : 0.0);
+      if (threadIdx.x == 0) sums->groups_arrived.count = 0;
     }
-    if (!last_to_arrive(&sums->groups_arrived.count, groups)) return;
-    all = block_sum<kBlock>(threadIdx.x < groups ? shared_load(&sums->of_group[threadIdx.x]) : 0.0);
-    if (threadIdx.x == 0) sums->groups_arrived.count = 0;
   }
   if (threadIdx.x == 0) {
     const double norm = fabs(a.grad_scale) * sqrt(all);
@@ -308,36 +309,101 @@ __device__ __forceinline__ float updated(float p, float m, float root_v, const A
   return p - fmaf(a.lr_wd, p, a.lr * u);
 }
 
-template <bool WHOLE, class P, class G, bool COPY>
-__device__ __forceinline__ void step32(const AdamwStepArgs& a, const AdamwTensor& t, uint64_t begin, float c) {
-  const Lanes<WHOLE> l = runs_of<WHOLE>(begin, t.count, t.vec != 0);
+// Four elements of the 32-bit step.
+template <class P, class G>
+__device__ __forceinline__ Quad<float> step_quad(const AdamwStepArgs& a, const Quad<P>& p, const Quad<G>& g, float c,
+                                                 Quad<float>& m, Quad<float>& v) {
   const float b1 = static_cast<float>(a.b1), one_b1 = static_cast<float>(a.one_b1);
   const float b2 = static_cast<float>(a.b2), one_b2 = static_cast<float>(a.one_b2);
-  Quad<P> p[kQuads];
-  Quad<G> g[kQuads];
-  Quad<float> m[kQuads], v[kQuads];
+  Quad<float> out;
 #pragma unroll
-  for (int q = 0; q < kQuads; ++q) {
-    p[q] = l.template load<P>(t.p, q);
-    g[q] = l.template load<G>(t.g, q);
-    m[q] = l.template load<float>(t.m, q);
-    v[q] = l.template load<float>(t.v, q);
+  for (int i = 0; i < 4; ++i) {
+    const float x = widen(g.e[i]) * c;
+    m.e[i] = fmaf(b1, m.e[i], one_b1 * x);
+    v.e[i] = fmaf(b2, v.e[i], one_b2 * x * x);
+    out.e[i] = updated(widen(p.e[i]), m.e[i], __builtin_amdgcn_sqrtf(v.e[i]), a);
+  }
+  return out;
+}
+
+// One array's kPiece elements between memory and LDS, by one wave.
+constexpr int kPiece = kBlock * 4;
+template <class T, bool KEEP> __device__ __forceinline__ void stage(const void* from, uint64_t begin, Raw16* to) {
+  const AR_GLOBAL Raw16* x = (const AR_GLOBAL Raw16*)((const AR_GLOBAL T*)from + begin) + threadIdx.x % kWave;
+  constexpr int N = kPiece * sizeof(T) / 16 / kWave;
+  Raw16 r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (KEEP)
+      r[i] = x[i * kWave];
+    else
+      r[i] = __builtin_nontemporal_load(x + i * kWave);
   }
 #pragma unroll
-  for (int q = 0; q < kQuads; ++q) {
-    Quad<float> out;
+  for (int i = 0; i < N; ++i) to[threadIdx.x % kWave + i * kWave] = r[i];
+}
+template <class T> __device__ __forceinline__ void unstage(const Raw16* from, void* to, uint64_t begin) {
+  AR_GLOBAL Raw16* x = (AR_GLOBAL Raw16*)((AR_GLOBAL T*)to + begin) + threadIdx.x % kWave;
+  constexpr int N = kPiece * sizeof(T) / 16 / kWave;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = widen(g[q].e[i]) * c;
-      m[q].e[i] = fmaf(b1, m[q].e[i], one_b1 * x);
-      v[q].e[i] = fmaf(b2, v[q].e[i], one_b2 * x * x);
-      out.e[i] = updated(widen(p[q].e[i]), m[q].e[i], __builtin_amdgcn_sqrtf(v[q].e[i]), a);
-    }
-    l.template store<float>(t.m, q, m[q]);
-    l.template store<float>(t.v, q, v[q]);
-    l.template store<P>(t.p, q, narrow<P>(out));
-    if constexpr (COPY) l.template store<uint16_t>(t.copy, q, narrow<uint16_t>(out));
-  }
+  for (int i = 0; i < N; ++i)
+    __builtin_nontemporal_store(from[threadIdx.x % kWave + i * kWave], x + i * kWave);
+}
+
+// The 32-bit step of kPiece elements by a block, through LDS: wave w reads
+// and writes the w-th of the arrays only.
+template <class P, class G, bool COPY, bool KEEP>
+__device__ __forceinline__ void step32_staged(const AdamwStepArgs& a, const AdamwTensor& t, uint64_t begin, float c) {
+  __shared__ Raw16 lds[4][kPiece / 4];
+  const int wave = wave_uniform(threadIdx.x / kWave);
+  if (wave == 0) stage<P, KEEP>(t.p, begin, lds[0]);
+  else if (wave == 1) stage<G, KEEP>(t.g, begin, lds[1]);
+  else if (wave == 2) stage<float, KEEP>(t.m, begin, lds[2]);
+  else stage<float, KEEP>(t.v, begin, lds[3]);
+  __syncthreads();
+  Quad<P>* p = reinterpret_cast<Quad<P>*>(lds[0]) + threadIdx.x;
+  Quad<G>* g = reinterpret_cast<Quad<G>*>(lds[1]) + threadIdx.x;
+  Quad<float>* m = reinterpret_cast<Quad<float>*>(lds[2]) + threadIdx.x;
+  Quad<float>* v = reinterpret_cast<Quad<float>*>(lds[3]) + threadIdx.x;
+  Quad<float> nm = *m, nv = *v;
+  const Quad<float> out = step_quad<P, G>(a, *p, *g, c, nm, nv);
+  *m = nm;
+  *v = nv;
+  *p = narrow<P>(out);
+  if constexpr (COPY && sizeof(G) == 4) __syncthreads();          // the copy takes the gradient's place
+  if constexpr (COPY) reinterpret_cast<Quad<uint16_t>*>(lds[1])[threadIdx.x] = narrow<uint16_t>(out);
+  __syncthreads();
+  if (wave == 0) unstage<P>(lds[0], t.p, begin);
+  else if (wave == 1) { if constexpr (COPY) unstage<uint16_t>(lds[1], t.copy, begin); }
+  else if (wave == 2) unstage<float>(lds[2], t.m, begin);
+  else unstage<float>(lds[3], t.v, begin);
+}
+
+// The same without LDS, where not all of the elements exist or the arrays are
+// aligned to their elements only.
+template <class P, class G, bool COPY>
+__device__ __forceinline__ void step32_loose(const AdamwStepArgs& a, const AdamwTensor& t, uint64_t begin, float c) {
+  const Lanes<false> l = {begin + threadIdx.x * 4, t.count, 0};
+  Quad<float> m = l.template load<float>(t.m, 0), v = l.template load<float>(t.v, 0);
+  const Quad<float> out = step_quad<P, G>(a, l.template load<P>(t.p, 0), l.template load<G>(t.g, 0), c, m, v);
+  l.template store<float>(t.m, 0, m);
+  l.template store<float>(t.v, 0, v);
+  l.template store<P>(t.p, 0, narrow<P>(out));
+  if constexpr (COPY) l.template store<uint16_t>(t.copy, 0, narrow<uint16_t>(out));
+}
+
+template <class P, class G, bool COPY, bool KEEP>
+__global__ __launch_bounds__(kBlock) void adamw_step_kernel(AdamwStepArgs a) {
+  constexpr uint32_t kPieces = kAdamwTile / kPiece;
+  const AdamwTile tile = reinterpret_cast<const AdamwTile*>(a.plan + a.tiles_at)[blockIdx.x / kPieces];
+  const AdamwTensor t = reinterpret_cast<const AdamwTensor*>(a.plan + a.tensors_at)[tile.tensor];
+  const float c = a.clip ? reinterpret_cast<const AdamwSums*>(a.plan + a.sums_at)->factor : a.factor;
+  const uint64_t begin = static_cast<uint64_t>(tile.index) * kAdamwTile + blockIdx.x % kPieces * kPiece;
+  if (begin >= t.count) return;
+  if (t.vec != 0 && begin + kPiece <= t.count)
+    step32_staged<P, G, COPY, KEEP>(a, t, begin, c);
+  else
+    step32_loose<P, G, COPY>(a, t, begin, c);
 }
 
 // The update from m and v, and their codes.
@@ -366,12 +432,15 @@ __device__ __forceinline__ void finish8(const AdamwStepArgs& a, const AdamwTenso
 
 template <bool WHOLE, class P, class G, bool COPY>
 __device__ __forceinline__ void step8(const AdamwStepArgs& a, const AdamwTensor& t, uint64_t begin, double c) {
-  const Lanes<WHOLE> l = rows_of<WHOLE>(begin, t.count, t.vec != 0);
+  const Lanes<WHOLE> l = rows_of<WHOLE>(begin, t.count);
   const uint64_t block = begin / AR_ADAMW_BLOCK + threadIdx.x % kWave / 16;
   const bool exists = WHOLE || block * AR_ADAMW_BLOCK < t.count;
-  AR_GLOBAL float* ms = (AR_GLOBAL float*)t.ms + block;
-  AR_GLOBAL float* vs = (AR_GLOBAL float*)t.vs + block;
-  const double am = exists ? *ms : 0.0f, rv = exists ? *vs : 0.0f;
+  // what a lane has past the tensor's end is its last element, in the block
+  // of that element too, and stays out of memory
+  const uint64_t held = exists ? block : (t.count - 1) / AR_ADAMW_BLOCK;
+  AR_GLOBAL float* ms = (AR_GLOBAL float*)t.ms + held;
+  AR_GLOBAL float* vs = (AR_GLOBAL float*)t.vs + held;
+  const double am = *ms, rv = *vs;
 
   // m and v in float64 (a code changes where a value crosses a border), the
   // factors of a block's sixteen elements a lane taken together first
@@ -411,25 +480,20 @@ __device__ __forceinline__ void step8(const AdamwStepArgs& a, const AdamwTensor&
   }
 }
 
-template <int BITS, class P, class G, bool COPY>
-__global__ __launch_bounds__(kBlock, 3) void adamw_step_kernel(AdamwStepArgs a) {
-  const AdamwTile tile = reinterpret_cast<const AdamwTile*>(a.plan + a.tiles_at)[blockIdx.x];
+template <class P, class G, bool COPY>
+__global__ __launch_bounds__(kBlock, 3) void adamw8_step_kernel(AdamwStepArgs a) {
+  // from the end, where the norm has just been, and where the last tile's
+  // elements one by one would keep the rest waiting (6.5M elements: 25.1 us
+  // in order, 22.5 from the end; 300M 803 and 798)
+  const AdamwTile tile = reinterpret_cast<const AdamwTile*>(a.plan + a.tiles_at)[gridDim.x - 1 - blockIdx.x];
   const AdamwTensor t = reinterpret_cast<const AdamwTensor*>(a.plan + a.tensors_at)[tile.tensor];
   const float c = a.clip ? reinterpret_cast<const AdamwSums*>(a.plan + a.sums_at)->factor : a.factor;
   const uint64_t begin = wave_begin(tile);
   if (begin >= t.count) return;
-  const bool all = whole(begin, t.count, t.vec != 0);
-  if constexpr (BITS == 32) {
-    if (all)
-      step32<true, P, G, COPY>(a, t, begin, c);
-    else
-      step32<false, P, G, COPY>(a, t, begin, c);
-  } else {
-    if (all)
-      step8<true, P, G, COPY>(a, t, begin, c);
-    else
-      step8<false, P, G, COPY>(a, t, begin, c);
-  }
+  if (whole(begin, t.count, t.vec != 0))
+    step8<true, P, G, COPY>(a, t, begin, c);
+  else
+    step8<false, P, G, COPY>(a, t, begin, c);
 }
 
 // --- decoding ---------------------------------------------------------------------------
@@ -438,15 +502,15 @@ __global__ __launch_bounds__(kBlock, 3) void adamw_step_kernel(AdamwStepArgs a) 
 // there) and rounded to float32.
 template <bool WHOLE, class C>
 __device__ __forceinline__ void decode(const C* codes, const float* scales, uint64_t begin, uint64_t count,
-                                       bool vec, float* out) {
-  const Lanes<WHOLE> l = runs_of<WHOLE>(begin, count, vec);
+                                       float* out) {
+  const Lanes<WHOLE> l = runs_of<WHOLE>(begin, count);
   Quad<C> code[kQuads];
   float scale[kQuads];
 #pragma unroll
   for (int q = 0; q < kQuads; ++q) {
     code[q] = l.template load<C>(codes, q);
     const uint64_t first = begin + q * l.step;      // of the block that the wave's q-th run is
-    scale[q] = WHOLE || first < count ? scales[first / AR_ADAMW_BLOCK] : 0.0f;
+    scale[q] = scales[(WHOLE || first < count ? first : count - 1) / AR_ADAMW_BLOCK];
   }
 #pragma unroll
   for (int q = 0; q < kQuads; ++q) {
@@ -467,9 +531,9 @@ __global__ __launch_bounds__(kBlock) void adamw_dequantize_kernel(const C* codes
   const uint64_t begin = wave_begin(tile);
   if (begin >= count) return;
   if (whole(begin, count, vec != 0))
-    decode<true>(codes, scales, begin, count, true, out);
+    decode<true>(codes, scales, begin, count, out);
   else
-    decode<false>(codes, scales, begin, count, vec != 0, out);
+    decode<false>(codes, scales, begin, count, out);
 }
 
 template <class A> hipError_t launch1(void (*kernel)(A), uint64_t blocks, const A& a, hipStream_t stream) {
@@ -479,8 +543,10 @@ template <class A> hipError_t launch1(void (*kernel)(A), uint64_t blocks, const 
                          dim3(kBlock), args, 0, stream);
 }
 
-template <class P, class G, bool COPY> auto step_kernel(int bits) {
-  return bits == 32 ? adamw_step_kernel<32, P, G, COPY> : adamw_step_kernel<8, P, G, COPY>;
+template <class P, class G, bool COPY> auto step_kernel(int bits, bool keep) {
+  return bits == 8 ? adamw8_step_kernel<P, G, COPY>
+         : keep    ? adamw_step_kernel<P, G, COPY, true>
+                   : adamw_step_kernel<P, G, COPY, false>;
 }
 
 }  // namespace
@@ -492,16 +558,16 @@ hipError_t launch_adamw_norm(const AdamwNormArgs& a, ar_dtype_t grad_dtype, hipS
 }
 
 hipError_t launch_adamw_step(const AdamwStepArgs& a, uint32_t tiles, ar_dtype_t param_dtype,
-                             ar_dtype_t grad_dtype, int state_bits, bool copy, hipStream_t stream) {
+                             ar_dtype_t grad_dtype, int state_bits, bool copy, bool keep, hipStream_t stream) {
   const bool p32 = param_dtype == AR_FLOAT32, g32 = grad_dtype == AR_FLOAT32;
   void (*fn)(AdamwStepArgs);
   if (!p32)
-    fn = g32 ? step_kernel<uint16_t, float, false>(state_bits) : step_kernel<uint16_t, uint16_t, false>(state_bits);
+    fn = g32 ? step_kernel<uint16_t, float, false>(state_bits, keep) : step_kernel<uint16_t, uint16_t, false>(state_bits, keep);
   else if (copy)
-    fn = g32 ? step_kernel<float, float, true>(state_bits) : step_kernel<float, uint16_t, true>(state_bits);
+    fn = g32 ? step_kernel<float, float, true>(state_bits, keep) : step_kernel<float, uint16_t, true>(state_bits, keep);
   else
-    fn = g32 ? step_kernel<float, float, false>(state_bits) : step_kernel<float, uint16_t, false>(state_bits);
-  return launch1(fn, tiles, a, stream);
+    fn = g32 ? step_kernel<float, float, false>(state_bits, keep) : step_kernel<float, uint16_t, false>(state_bits, keep);
+  return launch1(fn, state_bits == 32 ? tiles * (kAdamwTile / kPiece) : tiles, a, stream);
 }
 
 hipError_t launch_adamw_dequantize(const void* codes, const float* scales, uint64_t count,
