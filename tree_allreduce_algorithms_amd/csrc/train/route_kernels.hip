@@ -205,15 +205,19 @@ template <class T, int LG, int C> struct Keys {
   static __device__ __forceinline__ bool big(int high) { return static_cast<uint32_t>(high + kBig) > 2u * kBig; }
 };
 
+// How far the keys have decided a row.
+enum Decided { kDecided, kOrderOpen, kOpen };
+
 // The row's L largest by keys of 32 bits: the order of the logit in the high
 // bits, its column (the lowest the largest) in the low ones.  Each lane sorts
 // its values in lists of L and joins them, then the lanes join theirs.
-// bfloat16 fits the high bits and keys are exact; of a float32 log2(columns)
-// bits are cut off, and false is returned where two neighbours among the
-// top_k + 1 largest agree in what is left.  So it is, for all rows of a wave
-// or some, where a top is beyond 2^16 or not finite.
+// bfloat16 fits the high bits and keys are exact.  Of a float32 log2(columns)
+// bits are cut off: where neighbours among the top_k largest agree in what is
+// left their order is open (kOrderOpen), where the top_k-th agrees with the
+// next one the choice is (kOpen).  So it is where the top is beyond 2^16 or
+// not finite; a row of -infinity only is decided.
 template <class T, int LG, int C, int L>
-__device__ __forceinline__ bool choose(const float (&x)[Shape<T, LG, C>::V], int top_k, bool token, Choice* out) {
+__device__ __forceinline__ Decided choose(const float (&x)[Shape<T, LG, C>::V], int top_k, bool token, Choice* out) {
   using S = Shape<T, LG, C>;
   using K = Keys<T, LG, C>;
   constexpr int kLow = K::kLow;                      // of a key: columns - 1 - column
@@ -225,7 +229,6 @@ __device__ __forceinline__ bool choose(const float (&x)[Shape<T, LG, C>::V], int
     const int low = kLow - ((v / S::W) * S::G * S::W + v % S::W);   // of lane 0
     key[v] = K::kExact ? order(x[v], 0) | low : K::high(x[v]) | low;
   }
-  bool clear = true;
   int part[S::V];
 #pragma unroll
   for (int v = 0; v < S::V; ++v) part[v] = key[v];
@@ -240,7 +243,8 @@ __device__ __forceinline__ bool choose(const float (&x)[Shape<T, LG, C>::V], int
   join_row<LG, L, N>(list);
 
   const int top = list[0] & ~kLow;
-  clear = !K::big(top);
+  const bool any = top > kMinusInfinity;
+  bool open = any && K::big(top), order_open = false;
   int mine = list[0];
 #pragma unroll
   for (int k = 1; k < L; ++k) mine = lane == k ? list[k] : mine;
@@ -248,23 +252,49 @@ __device__ __forceinline__ bool choose(const float (&x)[Shape<T, LG, C>::V], int
     int last = list[0];
 #pragma unroll
     for (int k = 1; k < L; ++k) {
-      if (k <= top_k) clear = clear && ((list[k - 1] ^ list[k]) & ~kLow) != 0;
+      const bool agree = list[k] > (kMinusInfinity | kLow) && ((list[k - 1] ^ list[k]) & ~kLow) == 0;
+      if (k < top_k) order_open = order_open || agree;
+      if (k == top_k) open = open || agree;
       if (k < top_k) last = list[k];
     }
     // with top_k = L the next largest is not in the list: as many values as
     // were chosen must reach the last one's interval
     if (top_k == L) {
-      const int floor = token ? last & ~kLow : INT32_MAX;
+      const bool counts = token && last > (kMinusInfinity | kLow);
+      const int floor = counts ? last & ~kLow : INT32_MAX;
       int reach = 0;
 #pragma unroll
       for (int v = 0; v < S::V; ++v) reach += __popcll(__ballot(key[v] >= floor));
-      clear = clear && reach == __popcll(__ballot(token && lane == 0)) * L;
+      open = open || reach != __popcll(__ballot(counts && lane == 0)) * L;
     }
   }
-  out->top = from_order(top);
+  out->top = any ? from_order(top) : 0.0f;
   out->value = from_order(mine & ~kLow);
   out->index = lane < top_k && (mine & ~kLow) > kMinusInfinity ? kLow - (mine & kLow) : -1;
-  return clear;
+  return open ? kOpen : order_open ? kOrderOpen : kDecided;
+}
+
+// Puts the row's chosen (lane k has the k-th, with its whole logit) in order;
+// `room` is L pairs of LDS for the row.
+template <class S, int L> __device__ __forceinline__ void reorder(Choice* c, int2* room) {
+  const int lane = S::lane();
+  const int key = c->index >= 0 ? order(c->value, 0) : kNone;
+  if (lane < L) room[lane] = make_int2(key, c->index);
+  wave_in_order();
+  int rank = 0;
+#pragma unroll
+  for (int k = 0; k < L; ++k) {
+    const int2 other = room[k];
+    rank += other.x > key || (other.x == key && (c->index < 0 ? k < lane : other.y < c->index)) ? 1 : 0;
+  }
+  wave_in_order();
+  if (lane < L) room[rank] = make_int2(key, c->index);
+  wave_in_order();
+  if (lane < L) {
+    const int2 at = room[lane];
+    c->index = at.y;
+    c->value = from_order(at.x);
+  }
 }
 
 // The same for any row, by top_k searches over all values: exact, NaN never
@@ -309,6 +339,17 @@ __device__ __forceinline__ Choice choose_slowly(const float (&x)[Shape<T, LG, C>
   return out;
 }
 
+// a plus what lies 32 (16) lanes across, in the lower half (the even rows of
+// 16), and b's in the upper half (the odd rows).
+__device__ __forceinline__ float swap32_and_add(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float swap16_and_add(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
 // --- forward ----------------------------------------------------------------------------
 
 __device__ __forceinline__ uint64_t pair_of(float s, uint32_t count) {
@@ -319,18 +360,19 @@ __device__ __forceinline__ uint32_t count_in(uint64_t pair) { return static_cast
 
 // Reads n rows (row, row + stride, ...) of a table, column e, several at a
 // time (they come from memory, about a microsecond each if one by one), and
-// hands them to take() in order.
+// hands them to take() in order.  `most` is the largest n of the block.
 template <int kAtOnce, class Take>
-__device__ __forceinline__ void read_rows(const uint64_t* table, int row, int n, int stride, int experts, int e,
-                                          const Take& take) {
-  for (int i = 0; i < n; i += kAtOnce) {
+__device__ __forceinline__ void read_rows(const uint64_t* table, int row, int n, int most, int stride, int experts,
+                                          int e, const Take& take) {
+  for (int i = 0; i < most; i += kAtOnce) {
     uint64_t x[kAtOnce];
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u)
-      x[u] = shared_load(&table[static_cast<size_t>(row + min(i + u, n - 1) * stride) * experts + e]);
+      if (i + u < most)
+        x[u] = shared_load(&table[static_cast<size_t>(row + max(min(i + u, n - 1), 0) * stride) * experts + e]);
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u)
-      if (i + u < n) take(x[u]);
+      if (i + u < most && i + u < n) take(x[u]);
   }
 }
 
@@ -351,7 +393,7 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
   using S = Shape<T, LG, C>;
   constexpr int V = S::V;
   __shared__ uint32_t hist[S::kColumns];
-  __shared__ float sums[kWaves * kWave * V];          // [wave and row of it][columns]
+  __shared__ float rows_lds[sizeof(T) == 4 ? kWaves * kWave * V : 1];
   __shared__ uint32_t tokens[kWaves];
   const int wave = wave_uniform(threadIdx.x / kWave), lane = S::lane();
   const int rank = blockIdx.y;
@@ -368,7 +410,6 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
   const uint32_t end = min(begin + a.rows_per_block, a.tokens);
   // a wave's rows are neighbours; rows past the end are read as the last one
   const uint32_t sub = wave * S::kRows + threadIdx.x % kWave / S::G;
-  float* row_sums = sums + sub * S::kColumns;
   Chunk next[C];
   bool next_token = false;
   auto fetch = [&](uint32_t first) {
@@ -376,13 +417,27 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
     next_token = first + sub < end && (masks == nullptr || masks[i] != 0);
     load_chunks<S>(logits + i * a.row_stride, a.experts, next);
   };
+  // A row's results are stored when the next one's work begins, before the
+  // reads ahead: memory answers in order, so whoever waits for a read waits for
+  // all stores before it, which are then a whole row's work old.
+  int done_index = -1;
+  float done_weight = 0.0f;
+  uint32_t done_first = end;
+  auto store_done = [&] {
+    if (lane < a.top_k && done_first + sub < end) {
+      const uint64_t at = (static_cast<uint64_t>(rank) * a.tokens + done_first + sub) * a.top_k + lane;
+      a.indices[at] = done_index;
+      a.weights[at] = done_weight;
+      if (done_index >= 0) atomicAdd(&hist[done_index], 1u);
+    }
+  };
   if (begin < end) fetch(begin);
   for (uint32_t first = begin; first < end; first += kWaves * S::kRows) {
-    const uint32_t i = min(first + sub, end - 1);
     const bool token = next_token;
     Chunk raw[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) raw[c] = next[c];
+    store_done();
     if (first + kWaves * S::kRows < end) fetch(first + kWaves * S::kRows);
     if (__any(!token)) {
 #pragma unroll
@@ -394,17 +449,19 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
     for (int v = 0; v < V; ++v) x[v] = value_of<T>(raw[v / S::W], v % S::W);
 
     Choice choice;
-    const bool clear = choose<T, LG, C, L>(x, a.top_k, token, &choice);
-    if (__any(token && !clear)) {
+    const Decided decided = choose<T, LG, C, L>(x, a.top_k, token, &choice);
+    if (__any(token && decided == kOpen)) {
       choice = choose_slowly<T, LG, C>(x, a.top_k);
-    } else if (sizeof(T) == 4) {
+    } else if constexpr (sizeof(T) == 4) {
       // the whole float32, by way of LDS: reading it again from memory would
       // wait for the rows that are being read ahead
+      float* room = rows_lds + sub * S::kColumns;
 #pragma unroll
-      for (int v = 0; v < V; ++v) row_sums[S::column(v)] = x[v];
+      for (int v = 0; v < V; ++v) room[S::column(v)] = x[v];
       wave_in_order();
-      choice.value = row_sums[max(choice.index, 0)];
+      choice.value = room[max(choice.index, 0)];
       wave_in_order();
+      if (__any(token && decided == kOrderOpen)) reorder<S, L>(&choice, reinterpret_cast<int2*>(room));
     }
     if (!token) choice = {-1, 0.0f, 0.0f};
 
@@ -431,24 +488,37 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
     const float inv = live ? __builtin_amdgcn_rcpf(sum) : 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) total[v] = fmaf(x[v], inv, total[v]);
-    live_rows += live && lane == 0 ? 1 : 0;
+    live_rows += static_cast<uint32_t>(__popcll(__ballot(live && lane == 0)));
 
     const float mine = __builtin_amdgcn_exp2f(fmaf(xk, kLog2e, -shift));
     float weight = mine * inv;
     if (a.renormalize) weight = live ? mine * __builtin_amdgcn_rcpf(row_sum<LG>(mine)) : 0.0f;
     if (sum != sum) weight = sum;
-    if (lane < a.top_k && first + sub < end) {
-      const uint64_t at = (static_cast<uint64_t>(rank) * a.tokens + i) * a.top_k + lane;
-      a.indices[at] = choice.index;
-      a.weights[at] = weight;
-      if (choice.index >= 0) atomicAdd(&hist[choice.index], 1u);
-    }
+    done_index = choice.index;
+    done_weight = weight;
+    done_first = first;
   }
+  store_done();
 
-  // the block's row of sums
+  // the wave's rows added up, two registers into one at a step: halves of the
+  // wave, then rows of 16 lanes, change places between the two, so that each
+  // lane is left with the sums of other columns
+  __shared__ float sums[kWaves][S::kColumns];
+  if constexpr (S::G == 8) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) row_sums[S::column(v)] = total[v];
-  live_rows = wave_sum(live_rows);
+    for (int v = 0; v < V; ++v) total[v] += __int_as_float(dpp<0x128>(__float_as_int(total[v])));
+  }
+#pragma unroll
+  for (int v = 0; v < V / 2; ++v) total[v] = swap32_and_add(total[v], total[v + V / 2]);
+  constexpr int N = S::G <= 16 ? V / 4 : V / 2;
+  if constexpr (S::G <= 16) {
+#pragma unroll
+    for (int v = 0; v < N; ++v) total[v] = swap16_and_add(total[v], total[v + N]);
+  }
+  const int first_v = (threadIdx.x & 32 ? V / 2 : 0) + (S::G <= 16 && (threadIdx.x & 16) ? V / 4 : 0);
+#pragma unroll
+  for (int v = 0; v < N; ++v)
+    if (S::G > 8 || (threadIdx.x & 8) == 0) sums[wave][S::column(first_v + v)] = total[v];
   if (threadIdx.x % kWave == 0) tokens[wave] = live_rows;
   __syncthreads();
 
@@ -465,9 +535,7 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
   const double only_unit = n > 0 ? a.experts / (a.top_k * (static_cast<double>(n) * n)) : 0.0;
   double loss = 0.0;
   for (int e = threadIdx.x; e < a.experts; e += kBlock) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kWaves * S::kRows; ++i) s += sums[i * S::kColumns + e];
+    const float s = (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]);
     if (groups == 1 && in_group == 1) {       // the only block
       const float share = static_cast<float>(only_unit * hist[e]);
       a.counts[e] = static_cast<int32_t>(hist[e]);
@@ -495,7 +563,7 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
       double s = 0.0;
       uint32_t c = 0;
       const int rows = (static_cast<int>(in_group) - t.slice + t.P - 1) / t.P;
-      read_rows<16>(ws->of_block, block0 + t.slice, rows, t.P, a.experts, e, [&](uint64_t x) {
+      read_rows<16>(ws->of_block, block0 + t.slice, rows, (in_group + t.P - 1) / t.P, t.P, a.experts, e, [&](uint64_t x) {
         s += sum_in(x);
         c += count_in(x);
       });
@@ -521,14 +589,13 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
 
   // the last block: counts, shares and loss
   const uint32_t lane_tokens = threadIdx.x % kWave < groups ? shared_load(&ws->tokens_of_group[threadIdx.x % kWave]) : 0u;
-  const double live = wave_sum(lane_tokens);
-  const double unit = live > 0 ? a.experts / (a.top_k * live * live) : 0.0;
   // q slices a rank where there are more slices than ranks, else whole ranks a slice
   const int q = max(1, t.P / a.nranks), together = t.P / q;
   const int first_rank = q > 1 ? t.slice / q : t.slice * a.nranks / t.P;
   const int end_rank = q > 1 ? (first_rank < min(a.nranks, together) ? first_rank + 1 : first_rank)
                              : (t.slice + 1) * a.nranks / t.P;
   const int per_rank = static_cast<int>(groups_of_rank), part = q > 1 ? t.slice % q : 0;
+  const int most = q > 1 ? (per_rank + q - 1) / q : (a.nranks + t.P - 1) / t.P * per_rank;
   for (int e0 = 0; e0 < a.experts; e0 += t.E) {
     const int e = min(e0 + t.e, a.experts - 1);
     const bool mine = e0 + t.e < a.experts;
@@ -539,7 +606,7 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
     int rank_of_row = first_rank, left = per_rank;
     const int rows = q > 1 ? (end_rank > first_rank ? (per_rank - part + q - 1) / q : 0)
                            : (end_rank - first_rank) * per_rank;
-    read_rows<32>(ws->of_group, first_rank * per_rank + part, rows, q, a.experts, e, [&](uint64_t x) {
+    read_rows<32>(ws->of_group, min(first_rank, a.nranks - 1) * per_rank + part, rows, most, q, a.experts, e, [&](uint64_t x) {
       s += sum_in(x);
       c += count_in(x);
       chosen += count_in(x);
@@ -556,7 +623,9 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
     __syncthreads();
     if (q > 1 && t.slice < a.nranks && mine)
       a.counts[t.slice * a.experts + e] = static_cast<int32_t>(of_rank[threadIdx.x]);
+    const double live = wave_sum(lane_tokens);
     if (t.slice == 0 && mine) {
+      const double unit = live > 0 ? a.experts / (a.top_k * live * live) : 0.0;
       uint64_t all = chosen;
       for (int i = 1; i < t.P; ++i) {
         s += part_s[i * t.E + t.e];
