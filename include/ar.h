@@ -432,7 +432,7 @@ ar_status_t ar_adamw_dequantize(const void* codes, const float* scales, size_t c
  * aligned, all zero before its first call; a call leaves it ready for the
  * next, so one workspace serves any number of calls ordered on one stream.
  * Two streams need two. */
-#define AR_ROUTE_WORKSPACE 5000192
+#define AR_ROUTE_WORKSPACE 2655744
 
 /* Shape of a router call: `nranks` ranks (at most AR_MAX_RANKS) of `tokens`
  * tokens each, whose logits over `experts` experts lie `row_stride` elements

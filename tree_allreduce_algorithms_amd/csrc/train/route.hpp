@@ -13,7 +13,7 @@ namespace ar {
 // block leaves a row of S_e and of counts; the last block of a group adds up
 // the group's rows, the last group the groups'.  The counters are 0 between
 // calls, each in a line of its own; the rest needs no clearing.
-constexpr int kRouteBlocks = 512;
+constexpr int kRouteBlocks = 256;
 constexpr int kRouteGroups = 64;
 
 struct RouteSums {

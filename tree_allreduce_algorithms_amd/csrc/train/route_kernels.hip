@@ -15,6 +15,8 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kWaves = kBlock / kWave;
+constexpr int kRouteBlock = 512;                 // threads of the forward kernel
+constexpr int kRouteWaves = kRouteBlock / kWave;
 constexpr int kNone = INT32_MIN;
 
 __device__ __forceinline__ float widen(float x) { return x; }
@@ -381,25 +383,25 @@ __device__ __forceinline__ void read_rows(const uint64_t* table, int row, int n,
 struct Slices {
   int E, P, e, slice;
   __device__ explicit Slices(int experts) {
-    E = min(kBlock, 1 << (32 - __clz(max(experts - 1, 1))));
-    P = kBlock / E;
+    E = min(kRouteBlock, 1 << (32 - __clz(max(experts - 1, 1))));
+    P = kRouteBlock / E;
     e = threadIdx.x & (E - 1);
     slice = threadIdx.x / E;
   }
 };
 
 template <class T, int LG, int C, int L>
-__global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
+__global__ __launch_bounds__(kRouteBlock, 2) void route_kernel(RouteArgs a) {
   using S = Shape<T, LG, C>;
   constexpr int V = S::V;
   __shared__ uint32_t hist[S::kColumns];
-  __shared__ float rows_lds[sizeof(T) == 4 ? kWaves * kWave * V : 1];
-  __shared__ uint32_t tokens[kWaves];
+  __shared__ alignas(16) float rows_lds[sizeof(T) == 4 ? kRouteWaves * kWave * V : 1];
+  __shared__ uint32_t tokens[kRouteWaves];
   const int wave = wave_uniform(threadIdx.x / kWave), lane = S::lane();
   const int rank = blockIdx.y;
   const T* logits = static_cast<const T*>(a.logits.p[rank]);
   const uint8_t* masks = static_cast<const uint8_t*>(a.masks.p[rank]);
-  for (int i = threadIdx.x; i < S::kColumns; i += kBlock) hist[i] = 0;
+  for (int i = threadIdx.x; i < S::kColumns; i += kRouteBlock) hist[i] = 0;
   __syncthreads();
 
   float total[V];
@@ -432,13 +434,13 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
     }
   };
   if (begin < end) fetch(begin);
-  for (uint32_t first = begin; first < end; first += kWaves * S::kRows) {
+  for (uint32_t first = begin; first < end; first += kRouteWaves * S::kRows) {
     const bool token = next_token;
     Chunk raw[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) raw[c] = next[c];
     store_done();
-    if (first + kWaves * S::kRows < end) fetch(first + kWaves * S::kRows);
+    if (first + kRouteWaves * S::kRows < end) fetch(first + kRouteWaves * S::kRows);
     if (__any(!token)) {
 #pragma unroll
       for (int c = 0; c < C; ++c)
@@ -503,7 +505,7 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
   // the wave's rows added up, two registers into one at a step: halves of the
   // wave, then rows of 16 lanes, change places between the two, so that each
   // lane is left with the sums of other columns
-  __shared__ float sums[kWaves][S::kColumns];
+  __shared__ float sums[kRouteWaves][S::kColumns];
   if constexpr (S::G == 8) {
 #pragma unroll
     for (int v = 0; v < V; ++v) total[v] += __int_as_float(dpp<0x128>(__float_as_int(total[v])));
@@ -527,15 +529,18 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
   const uint32_t my_group = rank * groups_of_rank + blockIdx.x / a.group;
   const uint32_t in_group = min(a.group, gridDim.x - blockIdx.x / a.group * a.group);
   const uint32_t block = rank * gridDim.x + blockIdx.x, block0 = block - blockIdx.x % a.group;
-  uint32_t n = tokens[0] + tokens[1] + tokens[2] + tokens[3];
-  static_assert(kWaves == 4, "four waves' sums");
+  uint32_t n = 0;
+#pragma unroll
+  for (int w = 0; w < kRouteWaves; ++w) n += tokens[w];
   // with one block a group, the groups' rows are the blocks'
   uint64_t* my_rows = in_group > 1 ? ws->of_block + static_cast<size_t>(block) * a.experts
                                    : ws->of_group + static_cast<size_t>(my_group) * a.experts;
   const double only_unit = n > 0 ? a.experts / (a.top_k * (static_cast<double>(n) * n)) : 0.0;
   double loss = 0.0;
-  for (int e = threadIdx.x; e < a.experts; e += kBlock) {
-    const float s = (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]);
+  for (int e = threadIdx.x; e < a.experts; e += kRouteBlock) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kRouteWaves; ++w) s += sums[w][e];
     if (groups == 1 && in_group == 1) {       // the only block
       const float share = static_cast<float>(only_unit * hist[e]);
       a.counts[e] = static_cast<int32_t>(hist[e]);
@@ -546,15 +551,16 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
     }
   }
   if (groups == 1 && in_group == 1) {
-    loss = block_sum<kBlock>(loss);
+    loss = block_sum<kRouteBlock>(loss);
     if (threadIdx.x == 0) *a.loss = static_cast<float>(loss);
     return;
   }
   if (threadIdx.x == 0) shared_store(in_group > 1 ? &ws->tokens_of_block[block] : &ws->tokens_of_group[my_group], n);
 
-  __shared__ double part_s[kBlock];
-  __shared__ uint32_t part_c[kBlock], of_rank[kBlock];
+  __shared__ double part_s[kRouteBlock];
+  __shared__ uint32_t part_c[kRouteBlock], of_rank[kRouteBlock];
   const Slices t(a.experts);
+  of_rank[threadIdx.x] = 0;
   if (in_group > 1) {
     if (!last_to_arrive(&ws->arrived[my_group].count, in_group)) return;
     n = threadIdx.x < in_group ? shared_load(&ws->tokens_of_block[block0 + threadIdx.x]) : 0u;
@@ -601,8 +607,6 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
     const bool mine = e0 + t.e < a.experts;
     double s = 0.0;
     uint32_t chosen = 0, c = 0;
-    of_rank[threadIdx.x] = 0;
-    __syncthreads();
     int rank_of_row = first_rank, left = per_rank;
     const int rows = q > 1 ? (end_rank > first_rank ? (per_rank - part + q - 1) / q : 0)
                            : (end_rank - first_rank) * per_rank;
@@ -637,7 +641,7 @@ __global__ __launch_bounds__(kBlock, 2) void route_kernel(RouteArgs a) {
     }
     __syncthreads();
   }
-  loss = block_sum<kBlock>(loss);
+  loss = block_sum<kRouteBlock>(loss);
   if (threadIdx.x == 0) {
     *a.loss = static_cast<float>(loss);
     ws->groups_arrived.count = 0;
@@ -781,26 +785,26 @@ template <class A> dim3 grid_of(A* a, uint32_t rows, uint32_t most) {
   return dim3((wanted + each - 1) / each, a->nranks);
 }
 
-hipError_t launch_rows(const void* kernel, dim3 grid, void* a, hipStream_t stream) {
+hipError_t launch_rows(const void* kernel, dim3 grid, int threads, void* a, hipStream_t stream) {
   void* args[] = {a};
-  return hipLaunchKernel(kernel, grid, dim3(kBlock), args, 0, stream);
+  return hipLaunchKernel(kernel, grid, dim3(threads), args, 0, stream);
 }
 
 template <class T, int LG, int C> hipError_t route_as(RouteArgs a, hipStream_t stream) {
-  const dim3 grid = grid_of(&a, kWaves * Shape<T, LG, C>::kRows, kRouteBlocks);
+  const dim3 grid = grid_of(&a, kRouteWaves * Shape<T, LG, C>::kRows, kRouteBlocks);
   // few blocks are all joined by the last one
-  a.group = grid.x * grid.y <= 32 ? 1 : 16;
+  a.group = grid.x * grid.y <= kRouteGroups ? 1 : 16;
   const void* fn = a.top_k <= 2   ? reinterpret_cast<const void*>(&route_kernel<T, LG, C, 2>)
                    : a.top_k <= 4 ? reinterpret_cast<const void*>(&route_kernel<T, LG, C, 4>)
                                   : reinterpret_cast<const void*>(&route_kernel<T, LG, C, 8>);
-  return launch_rows(fn, grid, &a, stream);
+  return launch_rows(fn, grid, kRouteBlock, &a, stream);
 }
 
 template <class T, int LG, int C> hipError_t route_grad_as(RouteGradArgs a, hipStream_t stream) {
   const dim3 grid = grid_of(&a, kWaves * Shape<T, LG, C>::kRows, 1024);
   const void* fn = a.renormalize ? reinterpret_cast<const void*>(&route_grad_kernel<T, LG, C, true>)
                                  : reinterpret_cast<const void*>(&route_grad_kernel<T, LG, C, false>);
-  return launch_rows(fn, grid, &a, stream);
+  return launch_rows(fn, grid, kBlock, &a, stream);
 }
 
 // The smallest arrangement that holds a row: 8 lanes of 1 to 8 chunks, then
