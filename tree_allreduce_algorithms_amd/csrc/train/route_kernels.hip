@@ -251,23 +251,27 @@ __device__ __forceinline__ Decided choose(const float (&x)[Shape<T, LG, C>::V], 
 #pragma unroll
   for (int k = 1; k < L; ++k) mine = lane == k ? list[k] : mine;
   if constexpr (!K::kExact) {
+    constexpr int kNothing = kMinusInfinity | kLow;   // the largest key of -infinity
+    uint32_t apart = UINT32_MAX;                      // least difference of neighbours
     int last = list[0];
 #pragma unroll
     for (int k = 1; k < L; ++k) {
-      const bool agree = list[k] > (kMinusInfinity | kLow) && ((list[k - 1] ^ list[k]) & ~kLow) == 0;
-      if (k < top_k) order_open = order_open || agree;
-      if (k == top_k) open = open || agree;
+      const uint32_t differ = static_cast<uint32_t>(list[k - 1] ^ list[k]);
+      apart = min(apart, differ);
+      if (k == top_k) open = open || (differ <= kLow && list[k] > kNothing);
       if (k < top_k) last = list[k];
     }
-    // with top_k = L the next largest is not in the list: as many values as
-    // were chosen must reach the last one's interval
+    order_open = apart <= kLow;                       // of what was not chosen too: no matter
+    // with top_k = L the next largest is not in the list: no more values than
+    // were chosen may reach the last one's interval, none of them a lane's L-th
     if (top_k == L) {
-      const bool counts = token && last > (kMinusInfinity | kLow);
+      const bool counts = token && last > kNothing;
       const int floor = counts ? last & ~kLow : INT32_MAX;
       int reach = 0;
 #pragma unroll
-      for (int v = 0; v < S::V; ++v) reach += __popcll(__ballot(key[v] >= floor));
-      open = open || reach != __popcll(__ballot(counts && lane == 0)) * L;
+      for (int i = 0; i < N; ++i) reach += __popcll(__ballot(part[i] >= floor));
+      open = open || reach != __popcll(__ballot(counts && lane == 0)) * L ||
+             (N < S::V && __any(part[N - 1] >= floor));
     }
   }
   out->top = any ? from_order(top) : 0.0f;
@@ -651,14 +655,15 @@ __global__ __launch_bounds__(kRouteBlock, 2) void route_kernel(RouteArgs a) {
 // --- gradient ----------------------------------------------------------------------------
 
 template <class T, int LG, int C, bool RENORMALIZE>
-__global__ __launch_bounds__(kBlock, 2) void route_grad_kernel(RouteGradArgs a) {
+__global__ __launch_bounds__(kBlock, 4) void route_grad_kernel(RouteGradArgs a) {
   using S = Shape<T, LG, C>;
   constexpr int V = S::V, W = S::W;
   // what the chosen experts' weights add, a row of columns for each row of
   // logits; zero but for the entries in use.  The pad keeps two rows' same
   // columns out of each other's banks.
   constexpr int kPitch = S::kColumns + 32;
-  __shared__ float spread[kWaves * S::kRows * kPitch];
+  __shared__ alignas(16) float spread[kWaves * S::kRows * kPitch];
+  __shared__ alignas(16) float coef[S::kColumns];    // of every row: dloss times the expert's share
   const int wave = wave_uniform(threadIdx.x / kWave), lane = S::lane();
   const int rank = blockIdx.y;
   const uint32_t sub = wave * S::kRows + threadIdx.x % kWave / S::G;
@@ -667,12 +672,10 @@ __global__ __launch_bounds__(kBlock, 2) void route_grad_kernel(RouteGradArgs a) 
   const uint8_t* masks = static_cast<const uint8_t*>(a.masks.p[rank]);
   const float* dweights = static_cast<const float*>(a.dweights.p[rank]);
   const float dloss = a.dloss != nullptr ? *a.dloss : 0.0f;
-  float coef[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    at[S::column(v)] = 0.0f;
-    coef[v] = S::column(v) < a.experts ? dloss * a.share[S::column(v)] : 0.0f;
-  }
+  for (int v = 0; v < V; ++v) at[S::column(v)] = 0.0f;
+  for (int e = threadIdx.x; e < S::kColumns; e += kBlock) coef[e] = e < a.experts ? dloss * a.share[e] : 0.0f;
+  __syncthreads();
   const uint32_t begin = blockIdx.x * a.rows_per_block;
   const uint32_t end = min(begin + a.rows_per_block, a.tokens);
   for (uint32_t first = begin; first < end; first += kWaves * S::kRows) {
@@ -729,12 +732,14 @@ __global__ __launch_bounds__(kBlock, 2) void route_grad_kernel(RouteGradArgs a) 
     }
     if (index >= 0) at[index] = add;
     wave_in_order();
+    // the part of dx (renormalized) or of dp that is given, dp's from the loss
     float dot = 0.0f, here[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       here[v] = at[S::column(v)];
+      if (!RENORMALIZE) here[v] += coef[S::column(v)];
       p[v] *= inv;
-      dot = fmaf(p[v], RENORMALIZE ? coef[v] : coef[v] + here[v], dot);
+      dot = fmaf(p[v], RENORMALIZE ? coef[S::column(v)] : here[v], dot);
     }
     wave_in_order();
     if (index >= 0) at[index] = 0.0f;
@@ -747,7 +752,7 @@ __global__ __launch_bounds__(kBlock, 2) void route_grad_kernel(RouteGradArgs a) 
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const int v = c * W + w;
-        dx[w] = RENORMALIZE ? fmaf(p[v], coef[v] - dot, here[v]) : p[v] * (coef[v] + here[v] - dot);
+        dx[w] = RENORMALIZE ? fmaf(p[v], coef[S::column(v)] - dot, here[v]) : p[v] * (here[v] - dot);
       }
       const int col = (c * S::G + lane) * W;
       Chunk o;
@@ -760,7 +765,9 @@ __global__ __launch_bounds__(kBlock, 2) void route_grad_kernel(RouteGradArgs a) 
       }
       if (__any(!live) && !live) o = Chunk{0, 0, 0, 0};
       if (whole_chunk<S, C>(c, a.experts)) {
-        *reinterpret_cast<typename Loose<T>::type*>(out + col) = o;
+        // past the caches, which then still hold logits of the forward pass:
+        // 42 us against 48 for 131,072 rows of 256 float32
+        __builtin_nontemporal_store(o, reinterpret_cast<typename Loose<T>::type*>(out + col));
       } else {
         T e[W];
         __builtin_memcpy(e, &o, 16);
