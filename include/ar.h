@@ -432,7 +432,7 @@ ar_status_t ar_adamw_dequantize(const void* codes, const float* scales, size_t c
  * aligned, all zero before its first call; a call leaves it ready for the
  * next, so one workspace serves any number of calls ordered on one stream.
  * Two streams need two. */
-#define AR_ROUTE_WORKSPACE 2655744
+#define AR_ROUTE_WORKSPACE 2386432
 
 /* Shape of a router call: `nranks` ranks (at most AR_MAX_RANKS) of `tokens`
  * tokens each, whose logits over `experts` experts lie `row_stride` elements
@@ -462,8 +462,8 @@ typedef struct {
  * nothing counted.  A token with a NaN or +infinite logit has NaN for every
  * weight and makes loss NaN; a NaN is never chosen.  p and weights are
  * computed in float32; the sums S are added up in float32 over the tokens of
- * a block and in float64 beyond, in an order that depends on the shape alone.
- * Outputs are written whole. */
+ * a block, in float64 over some blocks and in fixed point (2^-32) beyond, in
+ * ways that depend on the shape alone.  Outputs are written whole. */
 ar_status_t ar_route(const void* const* logits, const uint8_t* const* masks,
                      const ar_route_shape_t* shape, int32_t* indices, float* weights,
                      int32_t* counts, float* loss, float* share, void* workspace,

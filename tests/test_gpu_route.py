@@ -121,9 +121,9 @@ def place(x, dtype, stride, offset):
 
 
 def counters_are_zero():
-    """The workspaces' 65 counters of arrived blocks, ready for the next call."""
+    """The workspaces' counters and totals, ready for the next call."""
     for ws in training._route_workspaces.values():
-        assert not ws[:65 * 256].any()
+        assert not ws[:65 * 256 + 8 + 1024 * 8 + 64 * 1024 * 4].any()
 
 
 def check(x, k, dtype, renormalize, mask=None, stride=None, offset=0, seed=0):

@@ -10,9 +10,10 @@
 namespace ar {
 
 // A router call's sums (AR_ROUTE_WORKSPACE bytes of device memory).  Every
-// block leaves a row of S_e and of counts; the last block of a group adds up
-// the group's rows, the last group the groups'.  The counters are 0 between
-// calls, each in a line of its own; the rest needs no clearing.
+// block leaves a row of S_e and of counts; the last block of a group adds the
+// group's up and onto the totals, whole numbers, in which the order of adding
+// does not show.  Totals and counters are 0 between calls, the counters each in
+// a line of its own; the rows need no clearing.
 constexpr int kRouteBlocks = 256;
 constexpr int kRouteGroups = 64;
 
@@ -20,10 +21,12 @@ struct RouteSums {
   struct alignas(256) Counter {
     uint32_t count;
   } arrived[kRouteGroups], groups_arrived;
-  uint32_t tokens_of_block[kRouteBlocks];            // that live
-  uint32_t tokens_of_group[kRouteGroups];
-  // [group or block][experts]: S_e as float32 in the high word, counts in the low
-  uint64_t of_group[kRouteGroups * AR_MAX_EXPERTS];
+  uint32_t tokens;                                 // that live
+  uint32_t not_finite;                             // a sum of probabilities was not
+  uint64_t share[AR_MAX_EXPERTS];                  // S_e in steps of 2^-32
+  uint32_t counts[AR_MAX_RANKS * AR_MAX_EXPERTS];  // [rank][experts]
+  uint32_t tokens_of_block[kRouteBlocks];
+  // [block][experts]: S_e as float32 in the high word, counts in the low
   uint64_t of_block[kRouteBlocks * AR_MAX_EXPERTS];
 };
 static_assert(sizeof(RouteSums) <= AR_ROUTE_WORKSPACE, "the workspace's documented size");

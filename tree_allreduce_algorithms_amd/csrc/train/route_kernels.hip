@@ -394,6 +394,12 @@ struct Slices {
   }
 };
 
+// E / (K T^2) of T tokens.
+__device__ __forceinline__ double unit_of(const RouteArgs& a, uint32_t tokens) {
+  const double n = tokens;
+  return n > 0 ? a.experts / (a.top_k * n * n) : 0.0;
+}
+
 template <class T, int LG, int C, int L>
 __global__ __launch_bounds__(kRouteBlock, 2) void route_kernel(RouteArgs a) {
   using S = Shape<T, LG, C>;
@@ -536,119 +542,111 @@ __global__ __launch_bounds__(kRouteBlock, 2) void route_kernel(RouteArgs a) {
   uint32_t n = 0;
 #pragma unroll
   for (int w = 0; w < kRouteWaves; ++w) n += tokens[w];
-  // with one block a group, the groups' rows are the blocks'
-  uint64_t* my_rows = in_group > 1 ? ws->of_block + static_cast<size_t>(block) * a.experts
-                                   : ws->of_group + static_cast<size_t>(my_group) * a.experts;
-  const double only_unit = n > 0 ? a.experts / (a.top_k * (static_cast<double>(n) * n)) : 0.0;
-  double loss = 0.0;
-  for (int e = threadIdx.x; e < a.experts; e += kRouteBlock) {
+  auto of_waves = [&](int e) {
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < kRouteWaves; ++w) s += sums[w][e];
-    if (groups == 1 && in_group == 1) {       // the only block
-      const float share = static_cast<float>(only_unit * hist[e]);
+    return s;
+  };
+
+  if (groups == 1 && in_group == 1) {         // the only block
+    const double unit = unit_of(a, n);
+    double loss = 0.0;
+    for (int e = threadIdx.x; e < a.experts; e += kRouteBlock) {
+      const float share = static_cast<float>(unit * hist[e]);
       a.counts[e] = static_cast<int32_t>(hist[e]);
       a.share[e] = share;
-      loss += static_cast<double>(s) * share;
-    } else {
-      shared_store(&my_rows[e], pair_of(s, hist[e]));
+      loss += static_cast<double>(of_waves(e)) * share;
     }
-  }
-  if (groups == 1 && in_group == 1) {
     loss = block_sum<kRouteBlock>(loss);
     if (threadIdx.x == 0) *a.loss = static_cast<float>(loss);
     return;
   }
-  if (threadIdx.x == 0) shared_store(in_group > 1 ? &ws->tokens_of_block[block] : &ws->tokens_of_group[my_group], n);
 
-  __shared__ double part_s[kRouteBlock];
-  __shared__ uint32_t part_c[kRouteBlock], of_rank[kRouteBlock];
-  const Slices t(a.experts);
-  of_rank[threadIdx.x] = 0;
+  // a group's sums onto the totals
+  auto add = [&](int e, double s, uint32_t count) {
+    if (s >= 0.0) {
+      const uint64_t fixed = static_cast<uint64_t>(s * 4294967296.0 + 0.5);
+      if (fixed != 0) shared_add(&ws->share[e], fixed);
+    } else {
+      shared_store(&ws->not_finite, 1u);
+    }
+    if (count != 0) shared_add(&ws->counts[rank * a.experts + e], count);
+  };
   if (in_group > 1) {
+    __shared__ double part_s[kRouteBlock];
+    __shared__ uint32_t part_c[kRouteBlock];
+    for (int e = threadIdx.x; e < a.experts; e += kRouteBlock)
+      shared_store(&ws->of_block[static_cast<size_t>(block) * a.experts + e], pair_of(of_waves(e), hist[e]));
+    if (threadIdx.x == 0) shared_store(&ws->tokens_of_block[block], n);
     if (!last_to_arrive(&ws->arrived[my_group].count, in_group)) return;
     n = threadIdx.x < in_group ? shared_load(&ws->tokens_of_block[block0 + threadIdx.x]) : 0u;
+    const Slices t(a.experts);
     for (int e0 = 0; e0 < a.experts; e0 += t.E) {
       const int e = min(e0 + t.e, a.experts - 1);
       double s = 0.0;
       uint32_t c = 0;
       const int rows = (static_cast<int>(in_group) - t.slice + t.P - 1) / t.P;
-      read_rows<16>(ws->of_block, block0 + t.slice, rows, (in_group + t.P - 1) / t.P, t.P, a.experts, e, [&](uint64_t x) {
-        s += sum_in(x);
-        c += count_in(x);
-      });
-      part_s[threadIdx.x] = s;
-      part_c[threadIdx.x] = c;
-      __syncthreads();
-      if (t.slice == 0 && e0 + t.e < a.experts) {
-        for (int i = 1; i < t.P; ++i) {
-          s += part_s[i * t.E + t.e];
-          c += part_c[i * t.E + t.e];
-        }
-        shared_store(&ws->of_group[static_cast<size_t>(my_group) * a.experts + e], pair_of(static_cast<float>(s), c));
+      read_rows<16>(ws->of_block, block0 + t.slice, rows, (in_group + t.P - 1) / t.P, t.P, a.experts, e,
+                    [&](uint64_t x) {
+                      s += sum_in(x);
+                      c += count_in(x);
+                    });
+      if (t.P > 1) {
+        part_s[threadIdx.x] = s;
+        part_c[threadIdx.x] = c;
+        __syncthreads();
+        if (t.slice == 0)
+          for (int i = 1; i < min(t.P, static_cast<int>(in_group)); ++i) {
+            s += part_s[i * t.E + t.e];
+            c += part_c[i * t.E + t.e];
+          }
       }
-      __syncthreads();
+      if (t.slice == 0 && e0 + t.e < a.experts) add(e, s, c);
     }
     n = wave_sum(n);                       // at most 16 blocks: the first wave has them all
-    if (threadIdx.x == 0) {
-      ws->arrived[my_group].count = 0;
-      shared_store(&ws->tokens_of_group[my_group], n);
-    }
+    if (threadIdx.x == 0) ws->arrived[my_group].count = 0;
+  } else {
+    for (int e = threadIdx.x; e < a.experts; e += kRouteBlock) add(e, of_waves(e), hist[e]);
   }
+  if (threadIdx.x == 0) shared_add(&ws->tokens, n);
   if (!last_to_arrive(&ws->groups_arrived.count, groups)) return;
 
-  // the last block: counts, shares and loss
-  const uint32_t lane_tokens = threadIdx.x % kWave < groups ? shared_load(&ws->tokens_of_group[threadIdx.x % kWave]) : 0u;
-  // q slices a rank where there are more slices than ranks, else whole ranks a slice
-  const int q = max(1, t.P / a.nranks), together = t.P / q;
-  const int first_rank = q > 1 ? t.slice / q : t.slice * a.nranks / t.P;
-  const int end_rank = q > 1 ? (first_rank < min(a.nranks, together) ? first_rank + 1 : first_rank)
-                             : (t.slice + 1) * a.nranks / t.P;
-  const int per_rank = static_cast<int>(groups_of_rank), part = q > 1 ? t.slice % q : 0;
-  const int most = q > 1 ? (per_rank + q - 1) / q : (a.nranks + t.P - 1) / t.P * per_rank;
-  for (int e0 = 0; e0 < a.experts; e0 += t.E) {
-    const int e = min(e0 + t.e, a.experts - 1);
-    const bool mine = e0 + t.e < a.experts;
-    double s = 0.0;
-    uint32_t chosen = 0, c = 0;
-    int rank_of_row = first_rank, left = per_rank;
-    const int rows = q > 1 ? (end_rank > first_rank ? (per_rank - part + q - 1) / q : 0)
-                           : (end_rank - first_rank) * per_rank;
-    read_rows<32>(ws->of_group, min(first_rank, a.nranks - 1) * per_rank + part, rows, most, q, a.experts, e, [&](uint64_t x) {
-      s += sum_in(x);
-      c += count_in(x);
-      chosen += count_in(x);
-      if (q == 1 && --left == 0) {
-        if (mine) a.counts[rank_of_row * a.experts + e] = static_cast<int32_t>(c);
-        ++rank_of_row;
-        left = per_rank;
-        c = 0;
+  // the last block: counts, shares and loss, and the totals 0 again
+  const uint32_t live = shared_load(&ws->tokens), bad = shared_load(&ws->not_finite);
+  for (int e = threadIdx.x; e < a.experts; e += kRouteBlock) hist[e] = 0;
+  __syncthreads();
+  const int all = a.nranks * a.experts;
+  constexpr int kAtOnce = 8;
+  for (int i0 = threadIdx.x; i0 < all; i0 += kAtOnce * kRouteBlock) {
+    uint32_t c[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+      if (i0 + u * kRouteBlock < all) c[u] = shared_load(&ws->counts[i0 + u * kRouteBlock]);
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + u * kRouteBlock;
+      if (i < all) {
+        a.counts[i] = static_cast<int32_t>(c[u]);
+        ws->counts[i] = 0;
+        if (c[u] != 0) atomicAdd(&hist[i % a.experts], c[u]);
       }
-    });
-    if (q > 1 && rows > 0) atomicAdd(&of_rank[first_rank * t.E + t.e], c);
-    part_s[threadIdx.x] = s;
-    part_c[threadIdx.x] = chosen;
-    __syncthreads();
-    if (q > 1 && t.slice < a.nranks && mine)
-      a.counts[t.slice * a.experts + e] = static_cast<int32_t>(of_rank[threadIdx.x]);
-    const double live = wave_sum(lane_tokens);
-    if (t.slice == 0 && mine) {
-      const double unit = live > 0 ? a.experts / (a.top_k * live * live) : 0.0;
-      uint64_t all = chosen;
-      for (int i = 1; i < t.P; ++i) {
-        s += part_s[i * t.E + t.e];
-        all += part_c[i * t.E + t.e];
-      }
-      const float share = static_cast<float>(unit * static_cast<double>(all));
-      a.share[e] = share;
-      loss += s * share;
     }
-    __syncthreads();
+  }
+  __syncthreads();
+  const double unit = unit_of(a, live);
+  double loss = 0.0;
+  for (int e = threadIdx.x; e < a.experts; e += kRouteBlock) {
+    const double s = static_cast<double>(shared_load(&ws->share[e])) / 4294967296.0;
+    ws->share[e] = 0;
+    const float share = static_cast<float>(unit * hist[e]);
+    a.share[e] = share;
+    loss += s * share;
   }
   loss = block_sum<kRouteBlock>(loss);
   if (threadIdx.x == 0) {
-    *a.loss = static_cast<float>(loss);
-    ws->groups_arrived.count = 0;
+    *a.loss = bad ? __builtin_nanf("") : static_cast<float>(loss);
+    ws->tokens = ws->not_finite = ws->groups_arrived.count = 0;
   }
 }
 

@@ -18,7 +18,7 @@ from .binding import DTYPES, SUCCESS, AdamwStep, AdamwTensor, ArError, lib
 
 BLOCK = 256   # elements that share one scale of an 8-bit state
 MAX_EXPERTS, MAX_TOP_K = 1024, 8
-ROUTE_WORKSPACE = 2655744   # AR_ROUTE_WORKSPACE
+ROUTE_WORKSPACE = 2386432   # AR_ROUTE_WORKSPACE
 
 
 def _load_module():
