@@ -10,6 +10,8 @@ which is built with the library.
 import ctypes
 import importlib.util
 import os
+from array import array
+from itertools import chain
 
 import torch
 
@@ -66,10 +68,11 @@ def _flat(tensors, what, dev, dtypes, sizes):
     tensors = list(tensors)
     if len(tensors) != len(sizes):
         raise ValueError(f"{what}: {len(tensors)} tensors for {len(sizes)} parameters")
+    kind = getattr(tensors[0], "dtype", None)
     for t, n in zip(tensors, sizes):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{what} must be GPU tensors")
-        if t.dtype not in dtypes or t.dtype != tensors[0].dtype:
+        if t.dtype is not kind or kind not in dtypes:
             raise TypeError(f"{what}: unsupported or mixed dtype {t.dtype}")
         if t.get_device() != dev or t.numel() != n:
             raise ValueError(f"{what} must share the parameters' device and sizes")
@@ -140,12 +143,14 @@ class AdamW:
                                float(weight_decay), float(grad_scale), 0, 0)
         self._grad_scale = float(grad_scale)
 
-        ptr = lambda k, i: self.state[k][i].data_ptr() if k in self.state else 0  # noqa: E731
-        table = (AdamwTensor * len(params))(*[
-            AdamwTensor(self.params[i].data_ptr(), self.grads[i].data_ptr(),
-                        self.copies[i].data_ptr() if self.copies else 0, ptr("exp_avg", i),
-                        ptr("exp_avg_sq", i), ptr("exp_avg_scale", i), ptr("exp_avg_sq_scale", i), n)
-            for i, n in enumerate(sizes)])
+        # a row of ar_adamw_tensor_t per tensor
+        none = [0] * len(params)
+        columns = [[t.data_ptr() for t in ts] if ts else none
+                   for ts in (self.params, self.grads, self.copies,
+                              *(self.state.get(k) for k in ("exp_avg", "exp_avg_sq", "exp_avg_scale",
+                                                            "exp_avg_sq_scale")))]
+        rows = array("Q", chain.from_iterable(zip(*columns, sizes)))
+        table = (AdamwTensor * len(params)).from_buffer(rows)
         kind = (len(params), DTYPES[binding._torch_dtype_name(params[0])],
                 DTYPES[binding._torch_dtype_name(self.grads[0])], state_bits)
         size = lib().ar_adamw_plan_bytes(table, *kind)
