@@ -162,11 +162,13 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!check_ranks(a[2], "mask", at::kBool, {tokens}, *first, s.nranks, &masks, &masked)) return nullptr;
   s.top_k = static_cast<int>(k);
   s.renormalize = PyObject_IsTrue(a[3]);
-  const auto real = first->options().dtype(at::kFloat), whole = first->options().dtype(at::kInt);
-  const at::Tensor indices = at::empty({s.nranks, tokens, k}, whole), weights = at::empty({s.nranks, tokens, k}, real);
-  // the small ones together: whoever keeps the loss keeps little else
-  const int64_t n_counts = static_cast<int64_t>(s.nranks) * s.experts;
-  const at::Tensor small = at::empty({n_counts + s.experts + 1}, real);
+  // indices and weights in one allocation, the small ones in another: whoever
+  // keeps the loss keeps little else
+  const int64_t n_choices = s.nranks * tokens * k, n_counts = static_cast<int64_t>(s.nranks) * s.experts;
+  const at::Tensor choices = at::empty({2 * n_choices}, first->options().dtype(at::kFloat));
+  const at::Tensor small = at::empty({n_counts + s.experts + 1}, choices.options());
+  const at::Tensor indices = part_of(choices, at::kInt, {s.nranks, tokens, k}, 0);
+  const at::Tensor weights = part_of(choices, at::kFloat, {s.nranks, tokens, k}, n_choices);
   const at::Tensor counts = part_of(small, at::kInt, {s.nranks, s.experts}, 0);
   const at::Tensor share = part_of(small, at::kFloat, {s.experts}, n_counts);
   const at::Tensor loss = part_of(small, at::kFloat, {}, n_counts + s.experts);

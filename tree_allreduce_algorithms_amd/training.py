@@ -44,8 +44,10 @@ def _current_stream(dev):
     return torch.cuda.current_stream(dev).cuda_stream
 
 
-# the same number without a stream object around it, where torch offers it
+# the same numbers without objects and initialisation around them, where torch
+# offers that (a GPU tensor is at hand, so the device is initialised)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _handle(stream, dev):
@@ -165,19 +167,18 @@ class AdamW:
         self._step_args = ctypes.byref(self._args)
         self._fn_norm, self._fn_step = lib().ar_adamw_grad_norm, lib().ar_adamw_step
 
-    def _run(self, fn, *args):
-        if torch.cuda.current_device() == self._dev:
-            return fn(self._host_ptr, self._device_ptr, *args)
-        with binding._on_device(self._dev):
-            return fn(self._host_ptr, self._device_ptr, *args)
-
     def grad_norm(self, max_norm=None, stream=None):
         """The 2-norm over all gradients (times ``grad_scale``), a float32 GPU
         scalar that the next call overwrites.  With ``max_norm`` the factor
         ``min(1, max_norm / norm)`` is kept for ``step(clip=True)``; nothing
         waits for the GPU."""
-        status = self._run(self._fn_norm, _INF if max_norm is None else max_norm, self._grad_scale,
-                           self._norm_ptr, _handle(stream, self._dev))
+        dev = self._dev
+        if _current_device() != dev:
+            with binding._on_device(dev):
+                return self.grad_norm(max_norm, stream)
+        status = self._fn_norm(self._host_ptr, self._device_ptr, _INF if max_norm is None else max_norm,
+                               self._grad_scale, self._norm_ptr,
+                               _current_stream(dev) if stream is None else _handle(stream, dev))
         if status != SUCCESS:
             raise ArError(status, "grad_norm")
         self._clip_ready = max_norm is not None
@@ -189,9 +190,14 @@ class AdamW:
         step before."""
         if clip and not self._clip_ready:
             raise ValueError("step(clip=True) needs grad_norm(max_norm=...) on these gradients first")
+        dev = self._dev
+        if _current_device() != dev:
+            with binding._on_device(dev):
+                return self.step(lr, clip, stream)
         args = self._args
         args.lr, args.step, args.clip = lr, self.steps + 1, 1 if clip else 0
-        status = self._run(self._fn_step, self._step_args, _handle(stream, self._dev))
+        status = self._fn_step(self._host_ptr, self._device_ptr, self._step_args,
+                               _current_stream(dev) if stream is None else _handle(stream, dev))
         if status != SUCCESS:
             raise ArError(status, "step")
         self.steps += 1
@@ -201,10 +207,10 @@ class AdamW:
 def dequantize(codes, scales, stream=None):
     """float32 values of the codes of an 8-bit AdamW state: int8 codes of
     ``exp_avg`` or uint8 codes of ``exp_avg_sq``, with one scale per 256."""
-    if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
+    dev = codes.get_device() if isinstance(codes, torch.Tensor) else -1
+    if dev < 0:
         raise TypeError("codes and scales must be GPU tensors")
-    dev = codes.get_device()
-    if stream is not None or torch.cuda.current_device() != dev:
+    if stream is not None or _current_device() != dev:
         # the result belongs to that stream: its memory is not handed out
         # again before the kernel there has run
         with torch.cuda.stream(_stream_of(stream, dev)):
@@ -238,8 +244,8 @@ _route_workspaces = {}   # (device index, stream handle) -> workspace
 def _route_workspace(dev, handle):
     """The stream's workspace, which every call leaves ready for the next.  A
     captured call gets one of its own, cleared in the graph: its replays may
-    run beside the stream's other calls."""
-    if torch.cuda.is_current_stream_capturing():
+    run beside the stream's other calls.  (The null stream cannot be captured.)"""
+    if handle and torch.cuda.is_current_stream_capturing():
         return torch.zeros(ROUTE_WORKSPACE, dtype=torch.uint8, device=f"cuda:{dev}")
     ws = _route_workspaces.get((dev, handle))
     if ws is None:
@@ -261,7 +267,7 @@ def route(logits, top_k, mask=None, renormalize=False, stream=None):
     experts and 8 choices."""
     logits, mask = _list(logits), _list(mask)
     dev = _training.device(logits)
-    if stream is not None or torch.cuda.current_device() != dev:
+    if stream is not None or _current_device() != dev:
         with torch.cuda.stream(_stream_of(stream, dev)):
             return route(logits, top_k, mask, renormalize)
     handle = _current_stream(dev)
@@ -281,7 +287,7 @@ def route_grad(logits, routing, dweights=None, dloss=None, stream=None):
     scalar; either may be left out."""
     logits, dweights = _list(logits), _list(dweights)
     dev = _training.device(logits)
-    if stream is not None or torch.cuda.current_device() != dev:
+    if stream is not None or _current_device() != dev:
         with torch.cuda.stream(_stream_of(stream, dev)):
             return route_grad(logits, routing, dweights, dloss)
     status, dlogits = _training.route_grad(logits, routing._dtype, routing.indices, routing.share,
