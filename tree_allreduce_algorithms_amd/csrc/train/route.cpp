@@ -30,21 +30,54 @@ ar_status_t check(const void* const* logits, const uint8_t* const* masks, const 
   return AR_SUCCESS;
 }
 
-template <class P> void fill(ar::RankPtrs* to, P const* from, const ar_route_shape_t* s) {
+template <int N, class P> void fill(ar::Pointers<N>* to, P const* from, const ar_route_shape_t* s) {
   std::memset(to, 0, sizeof(*to));
   if (from == nullptr || s->tokens == 0) return;
-  for (int r = 0; r < s->nranks; ++r)
-    to->p[r] = const_cast<void*>(static_cast<const void*>(from[r]));
+  for (int r = 0; r < s->nranks; ++r) to->p[r] = from[r];
 }
 
-template <class A> void fill_shape(A* a, const ar_route_shape_t* s) {
+void fill_shape(ar::RouteShape* a, const ar_route_shape_t* s) {
   a->row_stride = s->row_stride;
   a->tokens = static_cast<uint32_t>(s->tokens);
   a->rows_per_block = 0;
+  a->group = 0;
   a->nranks = s->nranks;
   a->experts = s->experts;
   a->top_k = s->top_k;
   a->renormalize = s->renormalize != 0;
+}
+
+template <int N>
+hipError_t route(const void* const* logits, const uint8_t* const* masks, const ar_route_shape_t* shape,
+                 int32_t* indices, float* weights, int32_t* counts, float* loss, float* share,
+                 void* workspace, hipStream_t stream) {
+  ar::RouteArgs<N> a;
+  fill(&a.logits, logits, shape);
+  fill(&a.masks, masks, shape);
+  fill_shape(&a, shape);
+  a.sums = static_cast<ar::RouteSums*>(workspace);
+  a.indices = indices;
+  a.weights = weights;
+  a.counts = counts;
+  a.loss = loss;
+  a.share = share;
+  return ar::launch_route(a, shape->dtype, stream);
+}
+
+template <int N>
+hipError_t route_grad(const void* const* logits, const uint8_t* const* masks, const ar_route_shape_t* shape,
+                      const int32_t* indices, const float* share, const float* const* dweights,
+                      const float* dloss, void* dlogits, hipStream_t stream) {
+  ar::RouteGradArgs<N> a;
+  fill(&a.logits, logits, shape);
+  fill(&a.masks, masks, shape);
+  fill(&a.dweights, dweights, shape);
+  fill_shape(&a, shape);
+  a.indices = indices;
+  a.share = share;
+  a.dloss = dloss;
+  a.dlogits = dlogits;
+  return ar::launch_route_grad(a, shape->dtype, stream);
 }
 
 }  // namespace
@@ -63,18 +96,10 @@ ar_status_t ar_route(const void* const* logits, const uint8_t* const* masks,
   if (!aligned(indices, 4) || !aligned(weights, 4) || !aligned(counts, 4) || !aligned(loss, 4) ||
       !aligned(share, 4) || !aligned(workspace, 16))
     return AR_ERROR_INVALID_ARGUMENT;
-  ar::RouteArgs a;
-  fill(&a.logits, logits, shape);
-  fill(&a.masks, masks, shape);
-  fill_shape(&a, shape);
-  a.group = 0;
-  a.sums = static_cast<ar::RouteSums*>(workspace);
-  a.indices = indices;
-  a.weights = weights;
-  a.counts = counts;
-  a.loss = loss;
-  a.share = share;
-  return ar::launch_status(ar::enqueue([&] { return ar::launch_route(a, shape->dtype, stream); }));
+  return ar::launch_status(ar::enqueue([&] {
+    return (shape->nranks <= ar::kFewRanks ? route<ar::kFewRanks> : route<AR_MAX_RANKS>)(
+        logits, masks, shape, indices, weights, counts, loss, share, workspace, stream);
+  }));
 }
 
 ar_status_t ar_route_grad(const void* const* logits, const uint8_t* const* masks,
@@ -91,16 +116,10 @@ ar_status_t ar_route_grad(const void* const* logits, const uint8_t* const* masks
   if (dweights != nullptr)
     for (int r = 0; r < shape->nranks; ++r)
       if (dweights[r] == nullptr || !aligned(dweights[r], 4)) return AR_ERROR_INVALID_ARGUMENT;
-  ar::RouteGradArgs a;
-  fill(&a.logits, logits, shape);
-  fill(&a.masks, masks, shape);
-  fill(&a.dweights, dweights, shape);
-  fill_shape(&a, shape);
-  a.indices = indices;
-  a.share = share;
-  a.dloss = dloss;
-  a.dlogits = dlogits;
-  return ar::launch_status(ar::enqueue([&] { return ar::launch_route_grad(a, shape->dtype, stream); }));
+  return ar::launch_status(ar::enqueue([&] {
+    return (shape->nranks <= ar::kFewRanks ? route_grad<ar::kFewRanks> : route_grad<AR_MAX_RANKS>)(
+        logits, masks, shape, indices, share, dweights, dloss, dlogits, stream);
+  }));
 }
 
 }  // extern "C"

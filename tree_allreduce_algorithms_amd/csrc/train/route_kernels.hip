@@ -395,13 +395,13 @@ struct Slices {
 };
 
 // E / (K T^2) of T tokens.
-__device__ __forceinline__ double unit_of(const RouteArgs& a, uint32_t tokens) {
+__device__ __forceinline__ double unit_of(const RouteShape& a, uint32_t tokens) {
   const double n = tokens;
   return n > 0 ? a.experts / (a.top_k * n * n) : 0.0;
 }
 
-template <class T, int LG, int C, int L>
-__global__ __launch_bounds__(kRouteBlock, 2) void route_kernel(RouteArgs a) {
+template <class T, int LG, int C, int L, int RANKS>
+__global__ __launch_bounds__(kRouteBlock, 2) void route_kernel(RouteArgs<RANKS> a) {
   using S = Shape<T, LG, C>;
   constexpr int V = S::V;
   __shared__ uint32_t hist[S::kColumns];
@@ -652,8 +652,8 @@ __global__ __launch_bounds__(kRouteBlock, 2) void route_kernel(RouteArgs a) {
 
 // --- gradient ----------------------------------------------------------------------------
 
-template <class T, int LG, int C, bool RENORMALIZE>
-__global__ __launch_bounds__(kBlock, 4) void route_grad_kernel(RouteGradArgs a) {
+template <class T, int LG, int C, bool RENORMALIZE, int RANKS>
+__global__ __launch_bounds__(kBlock, 4) void route_grad_kernel(RouteGradArgs<RANKS> a) {
   using S = Shape<T, LG, C>;
   constexpr int V = S::V, W = S::W;
   // what the chosen experts' weights add, a row of columns for each row of
@@ -782,7 +782,7 @@ __global__ __launch_bounds__(kBlock, 4) void route_grad_kernel(RouteGradArgs a) 
 // One block of a rank takes rows_per_block tokens, a whole number of the
 // rows that its waves hold at a time; at most `most` blocks in all (or one a
 // rank).
-template <class A> dim3 grid_of(A* a, uint32_t rows, uint32_t most) {
+dim3 grid_of(RouteShape* a, uint32_t rows, uint32_t most) {
   const uint32_t wanted = std::max(1u, (a->tokens + rows - 1) / rows);
   const uint32_t blocks = std::min(wanted, std::max<uint32_t>(1, most / a->nranks));
   const uint32_t each = (wanted + blocks - 1) / blocks;
@@ -795,20 +795,20 @@ hipError_t launch_rows(const void* kernel, dim3 grid, int threads, void* a, hipS
   return hipLaunchKernel(kernel, grid, dim3(threads), args, 0, stream);
 }
 
-template <class T, int LG, int C> hipError_t route_as(RouteArgs a, hipStream_t stream) {
+template <class T, int LG, int C, int RANKS> hipError_t route_as(RouteArgs<RANKS> a, hipStream_t stream) {
   const dim3 grid = grid_of(&a, kRouteWaves * Shape<T, LG, C>::kRows, kRouteBlocks);
   // few blocks are all joined by the last one
   a.group = grid.x * grid.y <= kRouteGroups ? 1 : 16;
-  const void* fn = a.top_k <= 2   ? reinterpret_cast<const void*>(&route_kernel<T, LG, C, 2>)
-                   : a.top_k <= 4 ? reinterpret_cast<const void*>(&route_kernel<T, LG, C, 4>)
-                                  : reinterpret_cast<const void*>(&route_kernel<T, LG, C, 8>);
+  const void* fn = a.top_k <= 2   ? reinterpret_cast<const void*>(&route_kernel<T, LG, C, 2, RANKS>)
+                   : a.top_k <= 4 ? reinterpret_cast<const void*>(&route_kernel<T, LG, C, 4, RANKS>)
+                                  : reinterpret_cast<const void*>(&route_kernel<T, LG, C, 8, RANKS>);
   return launch_rows(fn, grid, kRouteBlock, &a, stream);
 }
 
-template <class T, int LG, int C> hipError_t route_grad_as(RouteGradArgs a, hipStream_t stream) {
+template <class T, int LG, int C, int RANKS> hipError_t route_grad_as(RouteGradArgs<RANKS> a, hipStream_t stream) {
   const dim3 grid = grid_of(&a, kWaves * Shape<T, LG, C>::kRows, 1024);
-  const void* fn = a.renormalize ? reinterpret_cast<const void*>(&route_grad_kernel<T, LG, C, true>)
-                                 : reinterpret_cast<const void*>(&route_grad_kernel<T, LG, C, false>);
+  const void* fn = a.renormalize ? reinterpret_cast<const void*>(&route_grad_kernel<T, LG, C, true, RANKS>)
+                                 : reinterpret_cast<const void*>(&route_grad_kernel<T, LG, C, false, RANKS>);
   return launch_rows(fn, grid, kBlock, &a, stream);
 }
 
@@ -816,26 +816,30 @@ template <class T, int LG, int C> hipError_t route_grad_as(RouteGradArgs a, hipS
 // 16 and 32 lanes.
 #define AR_BY_EXPERTS(call, e, a, dtype, stream)                                          \
   if (dtype == AR_FLOAT32)                                                                \
-    return e <= 32    ? call<float, 3, 1>(a, stream)                                      \
-           : e <= 64  ? call<float, 3, 2>(a, stream)                                      \
-           : e <= 128 ? call<float, 3, 4>(a, stream)                                      \
-           : e <= 256 ? call<float, 3, 8>(a, stream)                                      \
-           : e <= 512 ? call<float, 4, 8>(a, stream)                                      \
-                      : call<float, 5, 8>(a, stream);                                     \
-  return e <= 64    ? call<uint16_t, 3, 1>(a, stream)                                     \
-         : e <= 128 ? call<uint16_t, 3, 2>(a, stream)                                     \
-         : e <= 256 ? call<uint16_t, 3, 4>(a, stream)                                     \
-         : e <= 512 ? call<uint16_t, 4, 4>(a, stream)                                     \
-                    : call<uint16_t, 5, 4>(a, stream)
+    return e <= 32    ? call<float, 3, 1, N>(a, stream)                                      \
+           : e <= 64  ? call<float, 3, 2, N>(a, stream)                                      \
+           : e <= 128 ? call<float, 3, 4, N>(a, stream)                                      \
+           : e <= 256 ? call<float, 3, 8, N>(a, stream)                                      \
+           : e <= 512 ? call<float, 4, 8, N>(a, stream)                                      \
+                      : call<float, 5, 8, N>(a, stream);                                     \
+  return e <= 64    ? call<uint16_t, 3, 1, N>(a, stream)                                     \
+         : e <= 128 ? call<uint16_t, 3, 2, N>(a, stream)                                     \
+         : e <= 256 ? call<uint16_t, 3, 4, N>(a, stream)                                     \
+         : e <= 512 ? call<uint16_t, 4, 4, N>(a, stream)                                     \
+                    : call<uint16_t, 5, 4, N>(a, stream)
 
 }  // namespace
 
-hipError_t launch_route(const RouteArgs& a, ar_dtype_t dtype, hipStream_t stream) {
+template <int N> hipError_t launch_route(const RouteArgs<N>& a, ar_dtype_t dtype, hipStream_t stream) {
   AR_BY_EXPERTS(route_as, a.experts, a, dtype, stream);
 }
-
-hipError_t launch_route_grad(const RouteGradArgs& a, ar_dtype_t dtype, hipStream_t stream) {
+template <int N> hipError_t launch_route_grad(const RouteGradArgs<N>& a, ar_dtype_t dtype, hipStream_t stream) {
   AR_BY_EXPERTS(route_grad_as, a.experts, a, dtype, stream);
 }
+
+template hipError_t launch_route(const RouteArgs<kFewRanks>&, ar_dtype_t, hipStream_t);
+template hipError_t launch_route(const RouteArgs<AR_MAX_RANKS>&, ar_dtype_t, hipStream_t);
+template hipError_t launch_route_grad(const RouteGradArgs<kFewRanks>&, ar_dtype_t, hipStream_t);
+template hipError_t launch_route_grad(const RouteGradArgs<AR_MAX_RANKS>&, ar_dtype_t, hipStream_t);
 
 }  // namespace ar
