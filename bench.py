@@ -113,6 +113,10 @@ KERNEL_FILE = {  # kernel -> the source file that defines it
     "fanout_group_kernel": "copy_kernels.hip", "fanout_kernel": "copy_kernels.hip",
     "alltoall_kernel": "copy_kernels.hip",
     "step_kernel": "step_kernels.hip",
+    "adamw_norm_kernel": "train/adamw_kernels.hip", "adamw_step_kernel": "train/adamw_kernels.hip",
+    "adamw8_step_kernel": "train/adamw_kernels.hip",
+    "adamw_dequantize_kernel": "train/adamw_kernels.hip",
+    "route_kernel": "train/route_kernels.hip", "route_grad_kernel": "train/route_kernels.hip",
 }
 
 
@@ -147,9 +151,9 @@ def _local_includes(code):
 
 def kernel_source_hash(kernel=None, csrc=None):
     """sha256 over the device code a kernel is built from (comments and blank
-    lines removed): its own source file (every .hip file when kernel is None)
-    plus the headers of the same directory that it includes, directly or
-    through one another, in name order."""
+    lines removed): its own source file (every .hip file of the collectives
+    when kernel is None) plus the headers of the same directory that it
+    includes, directly or through one another, in name order."""
     csrc = csrc or os.path.join(ROOT, "tree_allreduce_algorithms_amd", "csrc")
     own = KERNEL_FILE.get(kernel)
     code = {}
@@ -165,6 +169,8 @@ def kernel_source_hash(kernel=None, csrc=None):
     for name in sorted(os.listdir(csrc)):
         if name.endswith(".hip") and (own is None or name == own):
             read(name)
+    if own and os.path.dirname(own):
+        read(own)
     h = hashlib.sha256()
     for name in sorted(code):
         h.update(name.encode() + b"\0" + code[name].encode())

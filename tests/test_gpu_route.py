@@ -185,6 +185,16 @@ def test_tokens_and_ranks(ranks, tokens, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("ranks, tokens, experts", [(8, 9000, 24), (2, 20_001, 200), (64, 300, 17)])
+def test_blocks_of_many_rows(ranks, tokens, experts, dtype):
+    """Enough rows that every block goes round several times, some of them masked."""
+    announce(f"many rows {ranks} {tokens} {experts} {dtype}")
+    rng = np.random.default_rng(tokens)
+    mask = rng.random((ranks, tokens)) >= 0.2
+    check(fill("ruled out", (ranks, tokens, experts), rng), 3, dtype, True, mask=mask)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("share", [0.0, 0.05, 0.5, 1.0])
 def test_masks(share, dtype):
     announce(f"masks {share} {dtype}")
