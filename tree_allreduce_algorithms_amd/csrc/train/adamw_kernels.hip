@@ -351,7 +351,12 @@ template <class T> __device__ __forceinline__ void unstage(const Raw16* from, vo
 }
 
 // The 32-bit step of kPiece elements by a block, through LDS: wave w reads
-// and writes the w-th of the arrays only.
+// and writes the w-th of the arrays only.  Memory binds it; the detour keeps
+// each wave's accesses to one array at a time, in runs of 4 KiB.  Measured,
+// with float32 gradients and copies (30 bytes an element): 300M elements
+// 1,560 us (5.8 TB/s; 1,585 with all arrays in one lane's registers, 1,640
+// with pieces twice as long), 9M in 250 tensors with bfloat16 gradients 38.9 us
+// (46.8 in registers); write-back stores 1,650 us for 300M.
 template <class P, class G, bool COPY, bool KEEP>
 __device__ __forceinline__ void step32_staged(const AdamwStepArgs& a, const AdamwTensor& t, uint64_t begin, float c) {
   __shared__ Raw16 lds[4][kPiece / 4];
@@ -406,7 +411,12 @@ __global__ __launch_bounds__(kBlock) void adamw_step_kernel(AdamwStepArgs a) {
     step32_loose<P, G, COPY>(a, t, begin, c);
 }
 
-// The update from m and v, and their codes.
+// The update from m and v, and their codes.  The 8-bit step's arithmetic
+// (about 60 instructions an element, a third of them in float64) and its bytes
+// take about as long: 300M elements with bfloat16 gradients and copies (16.03
+// bytes each) 785 us, 6.1 TB/s; 6.5M with float32 gradients 18.5 us.  A block
+// of a state per 16 lanes shares the scales' arithmetic over 16 elements a
+// lane; one per wave, four elements a lane, took 2,140 us.
 template <bool TINY, class P, bool COPY, class L>
 __device__ __forceinline__ void finish8(const AdamwStepArgs& a, const AdamwTensor& t, const L& l,
                                         const Quad<P> (&p)[kQuads], const double (&m)[kQuads][4],
@@ -499,7 +509,7 @@ __global__ __launch_bounds__(kBlock, 3) void adamw8_step_kernel(AdamwStepArgs a)
 // --- decoding ---------------------------------------------------------------------------
 
 // One rounding per value: the products are taken in float64 (m's is exact
-// there) and rounded to float32.
+// there) and rounded to float32.  Memory binds it: 300M codes 249 us, 6.0 TB/s.
 template <bool WHOLE, class C>
 __device__ __forceinline__ void decode(const C* codes, const float* scales, uint64_t begin, uint64_t count,
                                        float* out) {

@@ -304,7 +304,8 @@ template <class S, int L> __device__ __forceinline__ void reorder(Choice* c, int
 }
 
 // The same for any row, by top_k searches over all values: exact, NaN never
-// chosen, about three times the work.  Within 2^16 its top is the one above,
+// chosen, about three times the work (of normal logits one row in 2,600 of 256
+// float32 takes it, of bfloat16 none).  Within 2^16 its top is the one above,
 // so that a row's results do not depend on which of the two its wave took.
 template <class T, int LG, int C>
 __device__ __forceinline__ Choice choose_slowly(const float (&x)[Shape<T, LG, C>::V], int top_k) {
@@ -400,6 +401,19 @@ __device__ __forceinline__ double unit_of(const RouteShape& a, uint32_t tokens) 
   return n > 0 ? a.experts / (a.top_k * n * n) : 0.0;
 }
 
+// The forward pass.  Its bytes are few (the logits once, eight bytes a choice)
+// and its VALUs bind it: a row of 256 bfloat16 takes about 94 instructions of
+// a wave, nearly half of them the 8-of-32 lists (a maximum, a minimum or a
+// compare takes 4.3 cycles of a SIMD, an addition, product or xor 2.2 and an
+// exp 8.2), most of the rest keys and exponentials.  Two waves a SIMD fit (200
+// to 240 registers): four of 128 registers spilled and took 46 us where two
+// took 32.4, twice the blocks 39.  The rows' exponentials stay where they were
+// read and are added up per column in registers; the sums of a block's 8
+// waves, of up to 16 blocks and of all are joined by the last to arrive, in
+// three short stages (about 6 us).
+// Measured, 131,072 rows: 256 bfloat16, 8 chosen 30.8 us (2.2 TB/s read; the
+// bytes alone 12), 256 float32 42.9 us (3.1 TB/s; 23); 32,768 rows of 128
+// bfloat16, 2 chosen 11.2 us; one row 3.5 us.
 template <class T, int LG, int C, int L, int RANKS>
 __global__ __launch_bounds__(kRouteBlock, 2) void route_kernel(RouteArgs<RANKS> a) {
   using S = Shape<T, LG, C>;
@@ -445,6 +459,17 @@ __global__ __launch_bounds__(kRouteBlock, 2) void route_kernel(RouteArgs<RANKS> 
   };
   if (begin < end) fetch(begin);
   for (uint32_t first = begin; first < end; first += kRouteWaves * S::kRows) {
+    // a wave that is ahead gives way to the one it shares a SIMD with, which
+    // would otherwise finish alone, at half the rate (32.4 us without, 30.8 with)
+    const uint32_t done = (first - begin) * 4;
+    if (done >= (end - begin) * 3)
+      __builtin_amdgcn_s_setprio(0);
+    else if (done >= (end - begin) * 2)
+      __builtin_amdgcn_s_setprio(1);
+    else if (done >= end - begin)
+      __builtin_amdgcn_s_setprio(2);
+    else
+      __builtin_amdgcn_s_setprio(3);
     const bool token = next_token;
     Chunk raw[C];
 #pragma unroll
@@ -652,6 +677,16 @@ __global__ __launch_bounds__(kRouteBlock, 2) void route_kernel(RouteArgs<RANKS> 
 
 // --- gradient ----------------------------------------------------------------------------
 
+// The gradient.  A row is read again and its softmax taken again, which costs
+// less than keeping it would (8 bytes a row of statistics save two of the
+// reductions, and memory is what binds this kernel); with p and the
+// coefficients c_e = dloss E C_e / (K T^2), per row
+//   dx = p (c - sum p c) + w (dw - sum w dw) at the chosen    (renormalized)
+//   dx = p (d - sum p d), d = c + dw at the chosen            (otherwise)
+// What belongs to the chosen columns alone takes a detour through LDS, one
+// write a choice, instead of a compare of every column with every choice.
+// Measured, 131,072 rows of 256 float32: 42.4 us, 6.3 TB/s of the 268 MB read
+// and written; 32,768 rows of 128 bfloat16, renormalized: 5.5 us.
 template <class T, int LG, int C, bool RENORMALIZE, int RANKS>
 __global__ __launch_bounds__(kBlock, 4) void route_grad_kernel(RouteGradArgs<RANKS> a) {
   using S = Shape<T, LG, C>;
@@ -781,7 +816,8 @@ __global__ __launch_bounds__(kBlock, 4) void route_grad_kernel(RouteGradArgs<RAN
 
 // One block of a rank takes rows_per_block tokens, a whole number of the
 // rows that its waves hold at a time; at most `most` blocks in all (or one a
-// rank).
+// rank).  The gradient has 1,024 (four a CU): 512 took 52 us for the 42 of
+// 131,072 rows of 256 float32, 2,048 the same.
 dim3 grid_of(RouteShape* a, uint32_t rows, uint32_t most) {
   const uint32_t wanted = std::max(1u, (a->tokens + rows - 1) / rows);
   const uint32_t blocks = std::min(wanted, std::max<uint32_t>(1, most / a->nranks));
