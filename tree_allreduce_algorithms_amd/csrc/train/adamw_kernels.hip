@@ -230,8 +230,10 @@ __device__ __forceinline__ float quotient(double x, double d, double inv_d) {
 
 // The roots' arguments come from float32 numbers that the step has anyway,
 // |m| and sqrt(v).  Where a scale is `tiny`, they could be subnormal (which
-// root and reciprocal take as 0) or the scale's reciprocal infinite, and the
-// arguments are taken in float64 instead.
+// root and reciprocal take as 0) or the scale's reciprocal infinite, and where
+// it is `huge` v could be beyond float32's range: there the arguments are
+// taken in float64 instead.
+constexpr double kHugeV = 0x1p127;
 struct ScaleM {
   double a, half;
   float stored, inv;
@@ -246,12 +248,12 @@ struct ScaleM {
     inv = ok ? __builtin_amdgcn_rcpf(s) : 0.0f;
     tiny = ok && s < 1e-30f;
   }
-  template <bool TINY> __device__ __forceinline__ uint32_t code(double m, float m32) const {
+  template <bool FAR> __device__ __forceinline__ uint32_t code(double m, float m32) const {
     const double x = fabs(m);
-    const float t = TINY ? static_cast<float>(tiny ? x * __builtin_amdgcn_rcp(a) : x * inv) : fabsf(m32) * inv;
+    const float t = FAR ? static_cast<float>(tiny ? x * __builtin_amdgcn_rcp(a) : x * inv) : fabsf(m32) * inv;
     const uint32_t j = floor_root(t);
     uint32_t q = j + (x > fma(a, below_border(j), half) ? 1u : 0u);
-    if (TINY) q = min(q, 127u);                   // a subnormal scale may be half of what it should be
+    if (FAR) q = min(q, 127u);                   // a subnormal scale may be half of what it should be
     const uint32_t sign = static_cast<uint32_t>(static_cast<int>(__builtin_bit_cast(uint64_t, m) >> 32) >> 31);
     return (q ^ sign) - sign;
   }
@@ -260,7 +262,7 @@ struct ScaleM {
 struct ScaleV {
   double r, half, zero;
   float stored, inv;
-  bool tiny;
+  bool tiny, huge;
   // `top`: the block's largest v
   __device__ explicit ScaleV(double top) {
     const float s = quotient(sqrt(top), 65025.0, 1.0 / 65025.0);
@@ -271,13 +273,14 @@ struct ScaleV {
     zero = ok ? 0.0 : __builtin_inf();
     inv = ok ? __builtin_amdgcn_rcpf(s) : 0.0f;
     tiny = ok && s < 1e-18f;
+    huge = !(top < kHugeV);
   }
-  template <bool TINY> __device__ __forceinline__ uint32_t code(double v, float root) const {
-    const float t = TINY ? static_cast<float>(__builtin_amdgcn_sqrt(v) * (tiny ? __builtin_amdgcn_rcp(r) : inv)) : root * inv;
+  template <bool FAR> __device__ __forceinline__ uint32_t code(double v, float root) const {
+    const float t = FAR ? static_cast<float>(__builtin_amdgcn_sqrt(v) * (tiny ? __builtin_amdgcn_rcp(r) : inv)) : root * inv;
     const uint32_t j = floor_root(t);
     const double border = fma(r, below_border(j), half);
     uint32_t u = j + (v > border * border ? 1u : 0u);
-    if (TINY) u = min(u, 255u);
+    if (FAR) u = min(u, 255u);
     return max(u, v > zero ? 1u : 0u);
   }
 };
@@ -306,6 +309,12 @@ __device__ __forceinline__ double units(uint8_t code) {
 // subnormal v (a root below 1.1e-19) as 0.
 __device__ __forceinline__ float updated(float p, float m, float root_v, const AdamwStepArgs& a) {
   const float u = m * __builtin_amdgcn_rcpf(root_v + a.eps);
+  return p - fmaf(a.lr_wd, p, a.lr * u);
+}
+
+// The same in float64, for a v beyond float32's range.
+__device__ __forceinline__ float updated_far(float p, double m, double v, const AdamwStepArgs& a) {
+  const float u = static_cast<float>(m / (sqrt(v) + a.eps));
   return p - fmaf(a.lr_wd, p, a.lr * u);
 }
 
@@ -417,7 +426,9 @@ __global__ __launch_bounds__(kBlock) void adamw_step_kernel(AdamwStepArgs a) {
 // bytes each) 785 us, 6.1 TB/s; 6.5M with float32 gradients 18.5 us.  A block
 // of a state per 16 lanes shares the scales' arithmetic over 16 elements a
 // lane; one per wave, four elements a lane, took 2,140 us.
-template <bool TINY, class P, bool COPY, class L>
+// FAR: a block of the wave is tiny or huge, or ends early.  What an element
+// gets does not depend on which of the two forms its wave takes.
+template <bool FAR, class P, bool COPY, class L>
 __device__ __forceinline__ void finish8(const AdamwStepArgs& a, const AdamwTensor& t, const L& l,
                                         const Quad<P> (&p)[kQuads], const double (&m)[kQuads][4],
                                         const double (&v)[kQuads][4], const ScaleM& sm, const ScaleV& sv) {
@@ -429,9 +440,12 @@ __device__ __forceinline__ void finish8(const AdamwStepArgs& a, const AdamwTenso
     for (int i = 0; i < 4; ++i) {
       const float m32 = static_cast<float>(m[q][i]);
       const float root = __builtin_amdgcn_sqrtf(static_cast<float>(v[q][i]));
-      out.e[i] = updated(widen(p[q].e[i]), m32, root, a);
-      nm[i] = sm.template code<TINY>(m[q][i], m32);
-      nv[i] = sv.template code<TINY>(v[q][i], root);
+      if (FAR && v[q][i] >= kHugeV)
+        out.e[i] = updated_far(widen(p[q].e[i]), m[q][i], v[q][i], a);
+      else
+        out.e[i] = updated(widen(p[q].e[i]), m32, root, a);
+      nm[i] = sm.template code<FAR>(m[q][i], m32);
+      nv[i] = sv.template code<FAR>(v[q][i], root);
     }
     l.template store<P>(t.p, q, narrow<P>(out));
     if constexpr (COPY) l.template store<uint16_t>(t.copy, q, narrow<uint16_t>(out));
@@ -480,7 +494,7 @@ __device__ __forceinline__ void step8(const AdamwStepArgs& a, const AdamwTensor&
   if (sum_v != sum_v || am != am) top_m = __builtin_nan("");
   const ScaleM sm(row_max(top_m));
   const ScaleV sv(row_max(top_v));
-  if (!WHOLE || __any(sm.tiny || sv.tiny))
+  if (!WHOLE || __any(sm.tiny || sv.tiny || sv.huge))
     finish8<true, P, COPY>(a, t, l, p, m, v, sm, sv);
   else
     finish8<false, P, COPY>(a, t, l, p, m, v, sm, sv);
