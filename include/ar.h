@@ -412,7 +412,10 @@ ar_status_t ar_adamw_grad_norm(const void* plan, void* device_plan, double max_n
  *   p' = p - lr (weight_decay p + (m' / (1 - beta1^step)) /
  *                                 (sqrt(v' / (1 - beta2^step)) + eps))
  * rounded once to param's type, and to bfloat16 in `copy`.  With 32-bit
- * states in float32, with 8-bit states m' and v' in float64.
+ * states in float32, with 8-bit states m' and v' in float64.  Any eps >= 0 is
+ * taken; with one below about 4e-12 the updates are computed in float64, so
+ * that an element whose v' float32 cannot hold moves as the formula says.
+ * With eps = 0 an element whose m' and v' are both 0 gets 0 / 0, a NaN.
  * AR_ERROR_INVALID_ARGUMENT: a factor that is not finite, lr, eps or
  * weight_decay negative, a beta outside [0, 1), step < 1.
  * AR_ERROR_UNSUPPORTED: `stream` is being captured (a replayed step would

@@ -212,7 +212,9 @@ ar_status_t ar_adamw_step(const void* plan, void* device_plan, const ar_adamw_st
   const double bc1 = 1.0 - std::pow(s->beta1, static_cast<double>(s->step));
   const double bc2 = 1.0 - std::pow(s->beta2, static_cast<double>(s->step));
   a.lr = static_cast<float>(s->lr * std::sqrt(bc2) / bc1);
-  a.eps = static_cast<float>(s->eps * std::sqrt(bc2));
+  a.eps64 = s->eps * std::sqrt(bc2);
+  a.eps = static_cast<float>(a.eps64);
+  a.far = ar::wide_eps(a.eps64);
   a.lr_wd = static_cast<float>(s->lr * s->weight_decay);
   a.b1 = s->beta1;
   a.one_b1 = 1.0 - s->beta1;

@@ -28,6 +28,12 @@ constexpr uint32_t kAdamwMaxTiles = (1u << 22) - 1;
 // 391 and 369.
 constexpr uint64_t kKeepBytes = 320ull << 20;
 
+// An eps (with its bias correction) beside which the float32 root and
+// reciprocal of a step would be wrong: below 2^25 times the roots (1.1e-19)
+// that are taken as 0, or so large that its reciprocal is subnormal, which is
+// taken as 0 too.  Such a step's updates are computed in float64.
+inline bool wide_eps(double eps) { return eps < 4e-12 || eps > 1e37; }
+
 // Blocks of a norm, and how many of them make a group: the sums of a group's
 // blocks, and those of the groups, are added up by one block.
 constexpr uint32_t kMaxNormBlocks = 1024;
@@ -97,6 +103,8 @@ struct AdamwStepArgs {
   double b1, one_b1;          // beta, 1 - beta
   double b2, one_b2;
   double root_b2, root_one_b2;
+  double eps64;               // eps before its rounding
+  int far;                    // wide_eps(eps64)
 };
 
 hipError_t launch_adamw_norm(const AdamwNormArgs& a, ar_dtype_t grad_dtype, hipStream_t stream);

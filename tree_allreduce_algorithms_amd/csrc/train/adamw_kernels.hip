@@ -306,15 +306,17 @@ __device__ __forceinline__ double units(uint8_t code) {
 // u = (m / bc1) / (sqrt(v / bc2) + eps), with the two corrections moved to
 // the factor in front and to eps.  The root and the reciprocal are single
 // instructions, off by one step of the last place each; the root takes a
-// subnormal v (a root below 1.1e-19) as 0.
+// subnormal v (a root below 1.1e-19) as 0, which shows only beside an eps that
+// is hardly larger: see wide_eps().
 __device__ __forceinline__ float updated(float p, float m, float root_v, const AdamwStepArgs& a) {
   const float u = m * __builtin_amdgcn_rcpf(root_v + a.eps);
   return p - fmaf(a.lr_wd, p, a.lr * u);
 }
 
-// The same in float64, for a v beyond float32's range.
+// The same from m and v in float64, for a v beyond float32's range and for a
+// wide_eps().
 __device__ __forceinline__ float updated_far(float p, double m, double v, const AdamwStepArgs& a) {
-  const float u = static_cast<float>(m / (sqrt(v) + a.eps));
+  const float u = static_cast<float>(m / (sqrt(v) + a.eps64));
   return p - fmaf(a.lr_wd, p, a.lr * u);
 }
 
@@ -325,12 +327,20 @@ __device__ __forceinline__ Quad<float> step_quad(const AdamwStepArgs& a, const Q
   const float b1 = static_cast<float>(a.b1), one_b1 = static_cast<float>(a.one_b1);
   const float b2 = static_cast<float>(a.b2), one_b2 = static_cast<float>(a.one_b2);
   Quad<float> out;
+  if (a.far) {                                   // m' and v' before they are rounded
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double x = static_cast<double>(widen(g.e[i])) * c;
+      out.e[i] = updated_far(widen(p.e[i]), fma(a.one_b1, x, a.b1 * m.e[i]),
+                             fma(a.one_b2 * x, x, a.b2 * v.e[i]), a);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float x = widen(g.e[i]) * c;
     m.e[i] = fmaf(b1, m.e[i], one_b1 * x);
     v.e[i] = fmaf(b2, v.e[i], one_b2 * x * x);
-    out.e[i] = updated(widen(p.e[i]), m.e[i], __builtin_amdgcn_sqrtf(v.e[i]), a);
+    if (!a.far) out.e[i] = updated(widen(p.e[i]), m.e[i], __builtin_amdgcn_sqrtf(v.e[i]), a);
   }
   return out;
 }
@@ -426,7 +436,7 @@ __global__ __launch_bounds__(kBlock) void adamw_step_kernel(AdamwStepArgs a) {
 // bytes each) 785 us, 6.1 TB/s; 6.5M with float32 gradients 18.5 us.  A block
 // of a state per 16 lanes shares the scales' arithmetic over 16 elements a
 // lane; one per wave, four elements a lane, took 2,140 us.
-// FAR: a block of the wave is tiny or huge, or ends early.  What an element
+// FAR: a block of the wave is tiny or huge, or ends early, or eps is wide.  What an element
 // gets does not depend on which of the two forms its wave takes.
 template <bool FAR, class P, bool COPY, class L>
 __device__ __forceinline__ void finish8(const AdamwStepArgs& a, const AdamwTensor& t, const L& l,
@@ -440,7 +450,7 @@ __device__ __forceinline__ void finish8(const AdamwStepArgs& a, const AdamwTenso
     for (int i = 0; i < 4; ++i) {
       const float m32 = static_cast<float>(m[q][i]);
       const float root = __builtin_amdgcn_sqrtf(static_cast<float>(v[q][i]));
-      if (FAR && v[q][i] >= kHugeV)
+      if (FAR && (a.far || v[q][i] >= kHugeV))
         out.e[i] = updated_far(widen(p[q].e[i]), m[q][i], v[q][i], a);
       else
         out.e[i] = updated(widen(p[q].e[i]), m32, root, a);
@@ -494,7 +504,7 @@ __device__ __forceinline__ void step8(const AdamwStepArgs& a, const AdamwTensor&
   if (sum_v != sum_v || am != am) top_m = __builtin_nan("");
   const ScaleM sm(row_max(top_m));
   const ScaleV sv(row_max(top_v));
-  if (!WHOLE || __any(sm.tiny || sv.tiny || sv.huge))
+  if (!WHOLE || a.far || __any(sm.tiny || sv.tiny || sv.huge))
     finish8<true, P, COPY>(a, t, l, p, m, v, sm, sv);
   else
     finish8<false, P, COPY>(a, t, l, p, m, v, sm, sv);
