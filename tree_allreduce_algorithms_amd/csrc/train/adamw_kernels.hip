@@ -345,10 +345,20 @@ __device__ __forceinline__ Quad<float> step_quad(const AdamwStepArgs& a, const Q
   return out;
 }
 
-// One array's kPiece elements between memory and LDS, by one wave.
+// One array's kPiece elements between memory and LDS, by one wave, sixteen
+// bytes an access.  The plan lets an array begin at any four elements, so in
+// memory a bfloat16 access is aligned to eight bytes only (the hardware takes
+// it as one access all the same).
 constexpr int kPiece = kBlock * 4;
+template <class T> struct Staged {
+  using type = Raw16;
+};
+template <> struct Staged<uint16_t> {
+  typedef Raw16 type __attribute__((aligned(8)));
+};
 template <class T, bool KEEP> __device__ __forceinline__ void stage(const void* from, uint64_t begin, Raw16* to) {
-  const AR_GLOBAL Raw16* x = (const AR_GLOBAL Raw16*)((const AR_GLOBAL T*)from + begin) + threadIdx.x % kWave;
+  using R = typename Staged<T>::type;
+  const AR_GLOBAL R* x = (const AR_GLOBAL R*)((const AR_GLOBAL T*)from + begin) + threadIdx.x % kWave;
   constexpr int N = kPiece * sizeof(T) / 16 / kWave;
   Raw16 r[N];
 #pragma unroll
@@ -362,7 +372,8 @@ template <class T, bool KEEP> __device__ __forceinline__ void stage(const void* 
   for (int i = 0; i < N; ++i) to[threadIdx.x % kWave + i * kWave] = r[i];
 }
 template <class T> __device__ __forceinline__ void unstage(const Raw16* from, void* to, uint64_t begin) {
-  AR_GLOBAL Raw16* x = (AR_GLOBAL Raw16*)((AR_GLOBAL T*)to + begin) + threadIdx.x % kWave;
+  using R = typename Staged<T>::type;
+  AR_GLOBAL R* x = (AR_GLOBAL R*)((AR_GLOBAL T*)to + begin) + threadIdx.x % kWave;
   constexpr int N = kPiece * sizeof(T) / 16 / kWave;
 #pragma unroll
   for (int i = 0; i < N; ++i)
