@@ -204,8 +204,12 @@ template <class T, int LG, int C> struct Keys {
   static constexpr int kBig = 0x47800000;            // 2^16
   // The order of a logit without the low bits; -infinity is by itself.
   static __device__ __forceinline__ int high(float x) { return order(x, kExact ? 0 : kLow) & ~kLow; }
-  static __device__ __forceinline__ bool big(int high) { return static_cast<uint32_t>(high + kBig) > 2u * kBig; }
+  // In unsigned numbers, which may wrap: high + kBig passes INT_MAX from 6e-5 on.
+  static __host__ __device__ constexpr bool big(int high) { return static_cast<uint32_t>(high) + kBig > 2u * kBig; }
 };
+static_assert(Keys<float, 3, 8>::big(0x7f800000) && Keys<float, 3, 8>::big(-0x7f800000) &&
+                  !Keys<float, 3, 8>::big(0x3f800000) && !Keys<float, 3, 8>::big(-0x47800000),
+              "infinities are big, 1 and -2^16 are not");
 
 // How far the keys have decided a row.
 enum Decided { kDecided, kOrderOpen, kOpen };
