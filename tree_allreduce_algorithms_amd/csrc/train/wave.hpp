@@ -11,21 +11,6 @@ namespace {
 
 constexpr int kWave = 64;
 
-// Maximum over the wave's lanes: row shifts by 1, 2, 4, 8 and the two row
-// broadcasts leave it in lane 63.
-__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-#define AR_DPP_MAX(ctrl) \
-  x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), ctrl, 0xf, 0xf, false)))
-  AR_DPP_MAX(0x111);
-  AR_DPP_MAX(0x112);
-  AR_DPP_MAX(0x114);
-  AR_DPP_MAX(0x118);
-  AR_DPP_MAX(0x142);
-  AR_DPP_MAX(0x143);
-#undef AR_DPP_MAX
-  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), 63));
-}
-
 template <class T> __device__ __forceinline__ T wave_sum(T x) {
 #pragma unroll
   for (int d = kWave / 2; d > 0; d /= 2) x += __shfl_xor(x, d);
@@ -51,6 +36,11 @@ template <int BLOCK> __device__ __forceinline__ double block_sum(double x) {
 // saying so, which settle() does for the wave's own; a release and an acquire
 // of agent scope would also write back and drop the whole L2, which measured
 // about 20 ns a block, one block after another (2,048 blocks: 40 us).
+// This rests on what gfx950 does, not on C++'s memory model, by which a relaxed
+// read need not see what came before the write it reads.  So every access to
+// such values within a launch must be one of these: a plain load or store could
+// stay in an XCD's L2, and no test would have to show it.  (What the last block
+// resets by plain stores is read by later launches only.)
 template <class T> __device__ __forceinline__ T shared_load(const T* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
