@@ -378,8 +378,8 @@ typedef struct {
   int clip;            /* nonzero: use the factor of the last ar_adamw_grad_norm */
 } ar_adamw_step_t;
 
-/* Bytes of a plan for these tensors; 0 on a bad argument (see ar_adamw_plan)
- * or when the host runs out of memory. */
+/* Bytes of a plan for these tensors; 0 for what ar_adamw_plan refuses or when
+ * the host runs out of memory. */
 size_t ar_adamw_plan_bytes(const ar_adamw_tensor_t* tensors, int ntensors, ar_dtype_t param_dtype,
                            ar_dtype_t grad_dtype, int state_bits);
 
@@ -393,16 +393,17 @@ size_t ar_adamw_plan_bytes(const ar_adamw_tensor_t* tensors, int ntensors, ar_dt
  * misaligned pointers, copies of some tensors only or of bfloat16 params,
  * scales missing (8) or given (32), a written range that overlaps any other
  * range; AR_ERROR_UNSUPPORTED for other types or state_bits, or more than
- * 2^24 - 1 tiles of (up to) 4,096 elements of one tensor.  A tensor of count 0 is skipped, its pointers not
- * looked at. */
+ * 2^22 - 1 tiles of (up to) 4,096 elements of one tensor (1.7e10 elements).
+ * A tensor of count 0 is skipped, its pointers not looked at. */
 ar_status_t ar_adamw_plan(const ar_adamw_tensor_t* tensors, int ntensors, ar_dtype_t param_dtype,
                           ar_dtype_t grad_dtype, int state_bits, void* plan, size_t bytes);
 
 /* norm = |grad_scale| sqrt(sum g^2) over all tensors of the plan (products
  * and sums in 64 bits, in an order fixed by the plan), written as float32 to
- * the device address `norm` (may be NULL) and kept in the plan, with the
- * factor c = min(1, max_norm / norm) (1 where norm is NaN) for a following
- * ar_adamw_step with `clip`.  max_norm may be infinite (no clipping). */
+ * the device address `norm` (may be NULL).  The plan keeps the factor
+ * grad_scale min(1, max_norm / norm) (grad_scale where norm is NaN) for the
+ * ar_adamw_step calls with `clip` that follow.  max_norm may be infinite (no
+ * clipping). */
 ar_status_t ar_adamw_grad_norm(const void* plan, void* device_plan, double max_norm,
                                double grad_scale, float* norm, hipStream_t stream);
 
@@ -424,7 +425,8 @@ ar_status_t ar_adamw_step(const void* plan, void* device_plan, const ar_adamw_st
                           hipStream_t stream);
 
 /* The values of `count` 8-bit codes (int8 for m when is_signed, else uint8
- * for v) as float32; code i belongs to scales[i / 256]. */
+ * for v) as float32; code i belongs to scales[i / 256].
+ * AR_ERROR_UNSUPPORTED: more than 4,096 (2^24 - 1) codes (6.9e10). */
 ar_status_t ar_adamw_dequantize(const void* codes, const float* scales, size_t count,
                                 int is_signed, float* out, hipStream_t stream);
 

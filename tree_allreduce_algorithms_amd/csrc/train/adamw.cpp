@@ -121,7 +121,8 @@ extern "C" {
 size_t ar_adamw_plan_bytes(const ar_adamw_tensor_t* tensors, int ntensors, ar_dtype_t param_dtype,
                            ar_dtype_t grad_dtype, int state_bits) {
   if (check_noexcept(tensors, ntensors, param_dtype, grad_dtype, state_bits) != AR_SUCCESS) return 0;
-  return layout_of(tensors, ntensors).bytes;
+  const Layout l = layout_of(tensors, ntensors);
+  return l.tiles > ar::kAdamwMaxTiles ? 0 : l.bytes;
 }
 
 ar_status_t ar_adamw_plan(const ar_adamw_tensor_t* tensors, int ntensors, ar_dtype_t param_dtype,
@@ -129,8 +130,8 @@ ar_status_t ar_adamw_plan(const ar_adamw_tensor_t* tensors, int ntensors, ar_dty
   const ar_status_t st = check_noexcept(tensors, ntensors, param_dtype, grad_dtype, state_bits);
   if (st != AR_SUCCESS) return st;
   const Layout l = layout_of(tensors, ntensors);
-  if (plan == nullptr || bytes < l.bytes || !aligned(plan, 8)) return AR_ERROR_INVALID_ARGUMENT;
   if (l.tiles > ar::kAdamwMaxTiles) return AR_ERROR_UNSUPPORTED;
+  if (plan == nullptr || bytes < l.bytes || !aligned(plan, 8)) return AR_ERROR_INVALID_ARGUMENT;
 
   char* base = static_cast<char*>(plan);
   std::memset(base, 0, l.bytes);
@@ -239,6 +240,7 @@ ar_status_t ar_adamw_dequantize(const void* codes, const float* scales, size_t c
   const uint64_t blocks = (count - 1) / AR_ADAMW_BLOCK + 1;
   if (count > (std::numeric_limits<uintptr_t>::max() - std::max(std::max(c, s), o)) / 4)
     return AR_ERROR_INVALID_ARGUMENT;
+  if ((count - 1) / ar::kAdamwTile + 1 > ar::kAdamwMaxDecodeTiles) return AR_ERROR_UNSUPPORTED;
   const uintptr_t oe = o + count * 4;
   if ((c < oe && o < c + count) || (s < oe && o < s + blocks * 4)) return AR_ERROR_INVALID_ARGUMENT;
   return ar::launch_status(ar::enqueue(

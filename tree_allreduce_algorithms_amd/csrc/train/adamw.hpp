@@ -19,8 +19,10 @@ namespace ar {
 constexpr uint32_t kAdamwMagic = 0x41573031u;
 constexpr uint32_t kAdamwTile = 4096;       // elements of a tile
 
-// At most four blocks a tile; a launch has less than 2^32 threads.
+// A launch has less than 2^32 threads.  A step has up to four blocks of 256 a
+// tile, a decoding one.
 constexpr uint32_t kAdamwMaxTiles = (1u << 22) - 1;
+constexpr uint32_t kAdamwMaxDecodeTiles = (1u << 24) - 1;
 
 // A 32-bit step whose reads come to this much or less goes through the caches
 // for them, a longer one past them.  Norm and step, float32 throughout: 256 MiB

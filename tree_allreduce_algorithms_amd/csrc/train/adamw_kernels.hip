@@ -618,7 +618,6 @@ hipError_t launch_adamw_step(const AdamwStepArgs& a, uint32_t tiles, ar_dtype_t 
 hipError_t launch_adamw_dequantize(const void* codes, const float* scales, uint64_t count,
                                    bool is_signed, float* out, hipStream_t stream) {
   const uint64_t blocks = (count - 1) / kAdamwTile + 1;
-  if (blocks > kAdamwMaxTiles) return hipErrorInvalidValue;          // more codes than memory holds
   int vec = reinterpret_cast<uintptr_t>(codes) % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
   void* args[] = {&codes, &scales, &count, &vec, &out};
   const void* fn = is_signed ? reinterpret_cast<const void*>(&adamw_dequantize_kernel<int8_t>)
