@@ -402,8 +402,8 @@ ar_status_t ar_adamw_plan(const ar_adamw_tensor_t* tensors, int ntensors, ar_dty
  * and sums in 64 bits, in an order fixed by the plan), written as float32 to
  * the device address `norm` (may be NULL).  The plan keeps the factor
  * grad_scale min(1, max_norm / norm) (grad_scale where norm is NaN) for the
- * ar_adamw_step calls with `clip` that follow.  max_norm may be infinite (no
- * clipping). */
+ * ar_adamw_step calls with `clip` that follow; it is NaN before the first
+ * norm.  max_norm may be infinite (no clipping). */
 ar_status_t ar_adamw_grad_norm(const void* plan, void* device_plan, double max_norm,
                                double grad_scale, float* norm, hipStream_t stream);
 

@@ -147,6 +147,8 @@ ar_status_t ar_adamw_plan(const ar_adamw_tensor_t* tensors, int ntensors, ar_dty
   h->sums_at = sums_at();
   h->tensors_at = l.tensors_at;
   h->tiles_at = l.tiles_at;
+  // no norm yet: a step that clips all the same shows it
+  reinterpret_cast<ar::AdamwSums*>(base + h->sums_at)->factor = std::numeric_limits<float>::quiet_NaN();
   AdamwTensor* out = reinterpret_cast<AdamwTensor*>(base + l.tensors_at);
   AdamwTile* tile = reinterpret_cast<AdamwTile*>(base + l.tiles_at);
   const uintptr_t pquad = param_dtype == AR_FLOAT32 ? 16 : 8, gquad = grad_dtype == AR_FLOAT32 ? 16 : 8;

@@ -57,6 +57,17 @@ def _handle(stream, dev):
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _capturing(stream, handle, dev):
+    """Whether `stream` (None: the current one), of this handle, is being
+    captured into a graph.  The null stream cannot be."""
+    if not handle:
+        return False
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(_stream_of(stream, dev)):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _stream_of(stream, dev):
     """`stream` (a torch stream or a raw handle), or the current one of device `dev`."""
     if stream is None:
@@ -103,7 +114,11 @@ class AdamW:
 
     Calls run on the current stream, or on ``stream``; those of one object must
     be ordered.  ``grad_norm`` may be captured into a graph, ``step`` may not
-    (its bias corrections are those of one step).
+    (its bias corrections are those of one step).  Once a bounded norm has been
+    captured, ``step(clip=True)`` is taken without an eager one before it, and
+    it is the caller who replays the graph before each such step: nothing here
+    sees a replay, and without one the step has the factor of the norm before
+    (NaN if there was none).
     """
 
     def __init__(self, params, grads, copies=None, *, state_bits=32, state=None, steps=0,
@@ -140,7 +155,8 @@ class AdamW:
             raise ValueError(f"state must hold {sorted(kinds)}, not {sorted(state)}")
         self.state = {k: _flat(state[k], k, dev, (dt,), ns) for k, (dt, ns) in kinds.items()}
         self.state_bits, self.steps = state_bits, int(steps)
-        self._clip_ready = False
+        self._clip_ready = False      # a bounded norm was enqueued since the last step
+        self._clip_captured = False   # one is in a graph, whose replays are not seen here
         self._args = AdamwStep(0.0, float(betas[0]), float(betas[1]), float(eps),
                                float(weight_decay), float(grad_scale), 0, 0)
         self._grad_scale = float(grad_scale)
@@ -176,19 +192,22 @@ class AdamW:
         if _current_device() != dev:
             with binding._on_device(dev):
                 return self.grad_norm(max_norm, stream)
+        handle = _current_stream(dev) if stream is None else _handle(stream, dev)
         status = self._fn_norm(self._host_ptr, self._device_ptr, _INF if max_norm is None else max_norm,
-                               self._grad_scale, self._norm_ptr,
-                               _current_stream(dev) if stream is None else _handle(stream, dev))
+                               self._grad_scale, self._norm_ptr, handle)
         if status != SUCCESS:
             raise ArError(status, "grad_norm")
-        self._clip_ready = max_norm is not None
+        if max_norm is not None and _capturing(stream, handle, dev):
+            self._clip_captured = True
+        else:
+            self._clip_ready = max_norm is not None
         return self._norm
 
     def step(self, lr, clip=False, stream=None):
         """One step in place.  ``clip=True`` scales the gradients by the factor
         of ``grad_norm(max_norm=...)``, which must have been called since the
-        step before."""
-        if clip and not self._clip_ready:
+        step before, or be part of a graph that has been replayed since."""
+        if clip and not (self._clip_ready or self._clip_captured):
             raise ValueError("step(clip=True) needs grad_norm(max_norm=...) on these gradients first")
         dev = self._dev
         if _current_device() != dev:
