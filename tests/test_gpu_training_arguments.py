@@ -1,0 +1,32 @@
+"""What the training calls refuse and take, beyond the first checks."""
+
+import pytest
+import torch
+
+import tree_allreduce_algorithms_amd as ar
+from test_gpu_route import gpu_ready  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def test_route_grad_checks_the_routing_it_is_given():
+    """A Routing's tensors can be replaced; none that the kernel would misread is taken."""
+    x = [torch.randn(40, 16, device="cuda") for _ in range(2)]
+    one = torch.ones((), device="cuda")
+    want = ar.route_grad(x, ar.route(x, 3), dloss=one)
+    bad = [("share", lambda t: t.bfloat16(), TypeError), ("share", lambda t: t.to(torch.uint8), TypeError),
+           ("share", lambda t: t.double(), TypeError), ("share", lambda t: t[:8], ValueError),
+           ("share", lambda t: torch.stack([t, t], 1)[:, 0], ValueError), ("share", lambda t: t.cpu(), TypeError),
+           ("indices", lambda t: t.long(), TypeError), ("indices", lambda t: t.to(torch.int8), TypeError),
+           ("indices", lambda t: t.float(), TypeError), ("indices", lambda t: t[:1], ValueError),
+           ("indices", lambda t: t[:, :39], ValueError), ("indices", lambda t: t.flatten(), ValueError),
+           ("indices", lambda t: t[..., :2], ValueError), ("indices", lambda t: t[..., :0], ValueError),
+           ("indices", lambda t: t.transpose(0, 1).contiguous().transpose(0, 1), ValueError),
+           ("indices", lambda t: torch.cat([t, t, t], -1), ValueError)]
+    for i, (name, change, error) in enumerate(bad):
+        r = ar.route(x, 3)
+        setattr(r, name, change(getattr(r, name)))
+        with pytest.raises(error):
+            ar.route_grad(x, r, dloss=one)
+            raise AssertionError(f"case {i} was taken")
+    assert torch.equal(ar.route_grad(x, ar.route(x, 3), dloss=one), want)

@@ -189,10 +189,19 @@ PyObject* route_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor* share = indices == nullptr ? nullptr : gpu_tensor(a[3], "share");
   if (share == nullptr) return nullptr;
   const int64_t tokens = static_cast<int64_t>(s.tokens);
-  if (indices->size(0) != s.nranks || indices->size(1) != tokens || share->numel() != s.experts ||
-      indices->device() != first->device() || !THPDtype_Check(a[1]) ||
+  // a Routing's tensors are plain attributes: what the kernel reads is checked here
+  if (indices->dim() != 3 || indices->size(0) != s.nranks || indices->size(1) != tokens ||
+      share->numel() != s.experts || indices->device() != first->device() ||
+      share->device() != first->device() || !THPDtype_Check(a[1]) ||
       reinterpret_cast<THPDtype*>(a[1])->scalar_type != first->scalar_type())
     return fail(PyExc_ValueError, "these are not the logits of this routing");
+  if (indices->scalar_type() != at::kInt || share->scalar_type() != at::kFloat)
+    return fail(PyExc_TypeError, "need int32 indices and a float32 share, not %s and %s",
+                c10::toString(indices->scalar_type()), c10::toString(share->scalar_type()));
+  if (!indices->is_contiguous() || !share->is_contiguous())
+    return fail(PyExc_ValueError, "indices and share must be contiguous");
+  if (indices->size(2) < 1 || indices->size(2) > AR_MAX_TOP_K || indices->size(2) > s.experts)
+    return fail(PyExc_ValueError, "indices must hold 1 to %d choices a token", AR_MAX_TOP_K);
   s.top_k = static_cast<int>(indices->size(2));
   s.renormalize = PyObject_IsTrue(a[5]);
   bool masked, weighted;
