@@ -1,5 +1,6 @@
 """What the training calls refuse and take, beyond the first checks."""
 
+import numpy as np
 import pytest
 import torch
 
@@ -30,3 +31,17 @@ def test_route_grad_checks_the_routing_it_is_given():
             ar.route_grad(x, r, dloss=one)
             raise AssertionError(f"case {i} was taken")
     assert torch.equal(ar.route_grad(x, ar.route(x, 3), dloss=one), want)
+
+
+def test_a_renormalize_without_a_truth_value():
+    """The object's own error, before anything is enqueued."""
+    x = [torch.randn(4, 16, device="cuda")]
+    r = ar.route(x, 2)
+    r._renormalize = np.zeros(2)
+    for call in (lambda: ar.route(x, 2, renormalize=np.zeros(2)), lambda: ar.route_grad(x, r)):
+        ar.debug_fail_launch(1)
+        try:
+            with pytest.raises(ValueError, match="truth value"):
+                call()
+        finally:
+            ar.debug_fail_launch(0)

@@ -161,7 +161,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   bool masked;
   if (!check_ranks(a[2], "mask", at::kBool, {tokens}, *first, s.nranks, &masks, &masked)) return nullptr;
   s.top_k = static_cast<int>(k);
-  s.renormalize = PyObject_IsTrue(a[3]);
+  if ((s.renormalize = PyObject_IsTrue(a[3])) < 0) return nullptr;
   const at::Tensor indices = empty({s.nranks, tokens, k}, at::kInt);
   const at::Tensor weights = empty({s.nranks, tokens, k}, at::kFloat);
   const at::Tensor counts = empty({s.nranks, s.experts}, at::kInt);
@@ -203,7 +203,7 @@ PyObject* route_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (indices->size(2) < 1 || indices->size(2) > AR_MAX_TOP_K || indices->size(2) > s.experts)
     return fail(PyExc_ValueError, "indices must hold 1 to %d choices a token", AR_MAX_TOP_K);
   s.top_k = static_cast<int>(indices->size(2));
-  s.renormalize = PyObject_IsTrue(a[5]);
+  if ((s.renormalize = PyObject_IsTrue(a[5])) < 0) return nullptr;
   bool masked, weighted;
   if (!check_ranks(a[4], "mask", at::kBool, {tokens}, *first, s.nranks, &masks, &masked) ||
       !check_ranks(a[6], "dweights", at::kFloat, {tokens, s.top_k}, *first, s.nranks, &dweights, &weighted))
