@@ -45,3 +45,20 @@ def test_a_renormalize_without_a_truth_value():
                 call()
         finally:
             ar.debug_fail_launch(0)
+
+
+def test_strides_that_say_nothing_may_differ():
+    """Single tokens cut out of matrices of several widths, and one expert."""
+    wide = [torch.randn(5, n, device="cuda") for n in (16, 24, 40)]
+    x = [t[2:3, :16] for t in wide]
+    a, b = ar.route(x, 4), ar.route([t.clone() for t in x], 4)
+    one = torch.ones((), device="cuda")
+    assert torch.equal(a.indices, b.indices) and torch.equal(a.weights, b.weights) and torch.equal(a.loss, b.loss)
+    assert torch.equal(ar.route_grad(x, a, dloss=one), ar.route_grad([t.clone() for t in x], b, dloss=one))
+    empty = [t[:0, :16] for t in wide]
+    assert ar.route(empty, 4).indices.shape == (3, 0, 4)
+    single = [torch.randn(6, 1, device="cuda"), torch.randn(1, 6, device="cuda").t()]
+    assert not ar.route(single, 1).indices.any()
+    for bad in ([t[:, :16] for t in wide], [wide[0][:1], wide[0].t()[:1, :1].expand(1, 16)]):
+        with pytest.raises(ValueError):
+            ar.route(bad, 4)

@@ -43,7 +43,8 @@ Py_ssize_t list_size(PyObject* list, const char* what) {
 }
 
 // The ranks' logits: GPU tensors [tokens, experts] of one type, shape and
-// strides, experts next to each other.
+// strides, experts next to each other.  A stride along one element or none
+// says nothing and may be any.
 const at::Tensor* check_logits(PyObject* list, Ranks* at, ar_route_shape_t* s) {
   const Py_ssize_t n = list_size(list, "logits");
   if (n < 0) return nullptr;
@@ -65,7 +66,8 @@ const at::Tensor* check_logits(PyObject* list, Ranks* at, ar_route_shape_t* s) {
     if (t == nullptr) return nullptr;
     if (t->scalar_type() != type || t->device() != first->device())
       return fail(PyExc_TypeError, "logits must share type and device");
-    if (t->sizes() != first->sizes() || t->strides() != first->strides())
+    if (t->sizes() != first->sizes() || (tokens > 1 && t->stride(0) != row) ||
+        (tokens > 0 && experts > 1 && t->stride(1) != 1))
       return fail(PyExc_ValueError, "logits must share shape and strides");
     at->p[i] = t->const_data_ptr();
   }
