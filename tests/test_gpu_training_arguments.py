@@ -62,3 +62,22 @@ def test_strides_that_say_nothing_may_differ():
     for bad in ([t[:, :16] for t in wide], [wide[0][:1], wide[0].t()[:1, :1].expand(1, 16)]):
         with pytest.raises(ValueError):
             ar.route(bad, 4)
+
+
+def test_a_step_shows_in_a_backward_pass_that_saved_the_parameter():
+    w = torch.ones(1000, device="cuda", requires_grad=True)
+    copy = torch.zeros(1000, device="cuda", dtype=torch.bfloat16)
+    opt = ar.AdamW([w], [torch.ones(1000, device="cuda")], [copy])
+    y = (w * w).sum()
+    versions = w._version, copy._version
+    opt.grad_norm(max_norm=1.0)
+    assert (w._version, copy._version) == versions
+    with pytest.raises(ar.ArError):
+        opt.step(-1.0)
+    assert (w._version, copy._version) == versions
+    opt.step(1e-3, clip=True)
+    assert w._version > versions[0] and copy._version > versions[1]
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward()
+    (w * w).sum().backward()
+    assert torch.equal(w.grad, 2 * w.detach())

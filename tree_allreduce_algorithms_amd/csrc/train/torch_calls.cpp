@@ -253,6 +253,22 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// written(list): tells autograd that these tensors were written in place (their
+// version counters; tensors made in inference mode have none).
+PyObject* written(PyObject*, PyObject* list) {
+  HANDLE_TH_ERRORS
+  const Py_ssize_t n = list_size(list, "tensors");
+  if (n < 0) return nullptr;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    PyObject* o = PyList_GET_ITEM(list, i);
+    if (!THPVariable_Check(o)) return fail(PyExc_TypeError, "tensors must be tensors");
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  }
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
 template <class F> PyCFunction as_function(F f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)); }
 
 PyMethodDef methods[] = {
@@ -260,6 +276,7 @@ PyMethodDef methods[] = {
     {"route", as_function(route), METH_FASTCALL, nullptr},
     {"route_grad", as_function(route_grad), METH_FASTCALL, nullptr},
     {"dequantize", as_function(dequantize), METH_FASTCALL, nullptr},
+    {"written", written, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_training", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

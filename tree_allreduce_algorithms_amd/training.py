@@ -161,6 +161,8 @@ class AdamW:
                                float(weight_decay), float(grad_scale), 0, 0)
         self._grad_scale = float(grad_scale)
 
+        self._written = [t for ts in (self.params, self.copies or []) for t in ts]
+
         # a row of ar_adamw_tensor_t per tensor
         none = [0] * len(params)
         columns = [[t.data_ptr() for t in ts] if ts else none
@@ -204,7 +206,8 @@ class AdamW:
         return self._norm
 
     def step(self, lr, clip=False, stream=None):
-        """One step in place.  ``clip=True`` scales the gradients by the factor
+        """One step in place: params, copies and states are overwritten, and
+        autograd notices it for params and copies.  ``clip=True`` scales the gradients by the factor
         of ``grad_norm(max_norm=...)``, which must have been called since the
         step before, or be part of a graph that has been replayed since."""
         if clip and not (self._clip_ready or self._clip_captured):
@@ -221,6 +224,9 @@ class AdamW:
             raise ArError(status, "step")
         self.steps += 1
         self._clip_ready = False
+        # a backward pass that saved one of these before the step must not
+        # take the new values for the old
+        _training.written(self._written)
 
 
 def dequantize(codes, scales, stream=None):
