@@ -1,0 +1,91 @@
+"""Training calls on named streams: what they were given may be dropped after
+the call."""
+
+import pytest
+import torch
+
+import tree_allreduce_algorithms_amd as ar
+from test_gpu_route import gpu_ready  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+SLEEP = 100_000_000      # cycles, some 50 ms
+
+
+def busy_stream():
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(SLEEP)
+    return side
+
+
+def blocks(tensors):
+    return {t.data_ptr() for t in tensors}
+
+
+def fill(like, value):
+    """New tensors of these sizes, written at once on the current stream; their addresses."""
+    return blocks([torch.full_like(t, value) for t in like for _ in range(2)])
+
+
+def test_inputs_of_the_router_may_be_dropped():
+    sizes = [torch.empty(3001, 64, device="cuda"), torch.empty(3001, 4, device="cuda")]
+    logits = [torch.randn(3001, 64, device="cuda") for _ in range(2)]
+    mask = [torch.rand(3001, device="cuda") < 0.9 for _ in range(2)]
+    dw = [torch.randn(3001, 4, device="cuda") for _ in range(2)]
+    one = torch.ones((), device="cuda")
+    want = ar.route(logits, 4, mask=mask)
+    wants = [want.indices, want.weights, want.counts, want.loss, ar.route_grad(logits, want, dw, one)]
+    side = busy_stream()
+    r = ar.route(logits, 4, mask=mask, stream=side)
+    dx = ar.route_grad(logits, r, dw, one, stream=side)
+    got = [r.indices, r.weights, r.counts, r.loss, dx]
+    used = blocks(logits + dw)
+    del logits, mask, dw, r, want
+    assert not used & fill(sizes, float("nan"))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, wants))
+
+
+def test_codes_and_scales_may_be_dropped():
+    codes = torch.randint(-127, 128, (100_000,), device="cuda", dtype=torch.int8)
+    scales = torch.rand(391, device="cuda")
+    want = ar.dequantize(codes, scales)
+    like = [torch.empty_like(codes)]
+    side = busy_stream()
+    out = ar.dequantize(codes, scales, stream=side)
+    used = blocks([codes])
+    del codes, scales
+    assert not used & fill(like, 3)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_an_optimizer_may_be_dropped(bits):
+    """The gradients, the states and the plan; the parameters are read afterwards."""
+    g = torch.randn(300_001, device="cuda")
+    p, q = torch.ones(300_001, device="cuda"), torch.ones(300_001, device="cuda")
+    ar.AdamW([q], [g], state_bits=bits).step(1e-3)
+    opt = ar.AdamW([p], [g], state_bits=bits)
+    like = [torch.empty_like(g), torch.empty_like(opt._device)]
+    side = busy_stream()
+    opt.grad_norm(stream=side)
+    opt.step(1e-3, stream=side)
+    used = blocks([g, opt._device, *opt.state["exp_avg"]])
+    del opt, g
+    assert not used & fill(like, 0)
+    torch.cuda.synchronize()
+    assert torch.equal(p, q)
+
+
+def test_a_raw_handle_is_left_to_the_caller():
+    """No event may be recorded on a stream that could be gone by then."""
+    stream = torch.cuda.Stream()
+    x = [torch.randn(100, 16, device="cuda")]
+    torch.cuda.synchronize()
+    for s in (stream.cuda_stream, torch.cuda.ExternalStream(stream.cuda_stream)):
+        r = ar.route(x, 2, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(r.indices, ar.route(x, 2).indices)

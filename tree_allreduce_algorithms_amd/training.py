@@ -5,6 +5,13 @@ Argument marshalling only, as in ``binding``: the work is done by libar.so's
 HIP kernels, on the current stream unless a call names another.  The calls
 that take lists of tensors or allocate their results go through _training.so,
 which is built with the library.
+
+Where a call names a torch stream, the allocator is told that the tensors it
+was given are in use there, so that they may be dropped after the call; what
+it returns belongs to that stream.  Another library's stream (a raw handle or
+a torch.cuda.ExternalStream) may be gone when a tensor is freed, so there the
+caller keeps the tensors until the work is done.  Ordering the streams is the
+caller's, as with every call of torch.
 """
 
 import ctypes
@@ -73,6 +80,16 @@ def _stream_of(stream, dev):
     if stream is None:
         return torch.cuda.current_stream(dev)
     return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=dev)
+
+
+def _in_use(stream, *groups):
+    """Tells the allocator that these tensors (lists of them, None for none) are
+    in use on `stream`, a call's argument (see above)."""
+    if not isinstance(stream, torch.cuda.Stream) or isinstance(stream, torch.cuda.ExternalStream):
+        return
+    for group in groups:
+        for t in group or ():
+            t.record_stream(stream)
 
 
 def _flat(tensors, what, dev, dtypes, sizes):
@@ -183,7 +200,15 @@ class AdamW:
         self._host_ptr, self._device_ptr = ctypes.addressof(self._host), self._device.data_ptr()
         self._norm_ptr = self._norm.data_ptr()
         self._step_args = ctypes.byref(self._args)
+        self._streams = set()     # named streams that the tensors are known to be in use on
         self._fn_norm, self._fn_step = lib().ar_adamw_grad_norm, lib().ar_adamw_step
+
+    def _on(self, stream, handle):
+        # once a stream: the allocator remembers it for as long as a tensor lives
+        if handle not in self._streams:
+            self._streams.add(handle)
+            _in_use(stream, self.params, self.grads, self.copies, *self.state.values(),
+                    (self._device, self._norm))
 
     def grad_norm(self, max_norm=None, stream=None):
         """The 2-norm over all gradients (times ``grad_scale``), a float32 GPU
@@ -199,6 +224,8 @@ class AdamW:
                                self._grad_scale, self._norm_ptr, handle)
         if status != SUCCESS:
             raise ArError(status, "grad_norm")
+        if stream is not None:
+            self._on(stream, handle)
         if max_norm is not None and _capturing(stream, handle, dev):
             self._clip_captured = True
         else:
@@ -218,10 +245,12 @@ class AdamW:
                 return self.step(lr, clip, stream)
         args = self._args
         args.lr, args.step, args.clip = lr, self.steps + 1, 1 if clip else 0
-        status = self._fn_step(self._host_ptr, self._device_ptr, self._step_args,
-                               _current_stream(dev) if stream is None else _handle(stream, dev))
+        handle = _current_stream(dev) if stream is None else _handle(stream, dev)
+        status = self._fn_step(self._host_ptr, self._device_ptr, self._step_args, handle)
         if status != SUCCESS:
             raise ArError(status, "step")
+        if stream is not None:
+            self._on(stream, handle)
         self.steps += 1
         self._clip_ready = False
         # a backward pass that saved one of these before the step must not
@@ -239,7 +268,9 @@ def dequantize(codes, scales, stream=None):
         # the result belongs to that stream: its memory is not handed out
         # again before the kernel there has run
         with torch.cuda.stream(_stream_of(stream, dev)):
-            return dequantize(codes, scales)
+            out = dequantize(codes, scales)
+        _in_use(stream, (codes, scales))
+        return out
     status, out = _training.dequantize(codes, scales, _current_stream(dev))
     if status != SUCCESS:
         raise ArError(status, "dequantize")
@@ -294,7 +325,9 @@ def route(logits, top_k, mask=None, renormalize=False, stream=None):
     dev = _training.device(logits)
     if stream is not None or _current_device() != dev:
         with torch.cuda.stream(_stream_of(stream, dev)):
-            return route(logits, top_k, mask, renormalize)
+            routing = route(logits, top_k, mask, renormalize)
+        _in_use(stream, logits, mask)
+        return routing
     handle = _current_stream(dev)
     workspace = _route_workspace(dev, handle)
     status, *outputs = _training.route(logits, top_k, mask, renormalize, workspace.data_ptr(), handle)
@@ -314,7 +347,10 @@ def route_grad(logits, routing, dweights=None, dloss=None, stream=None):
     dev = _training.device(logits)
     if stream is not None or _current_device() != dev:
         with torch.cuda.stream(_stream_of(stream, dev)):
-            return route_grad(logits, routing, dweights, dloss)
+            dlogits = route_grad(logits, routing, dweights, dloss)
+        _in_use(stream, logits, routing._mask, dweights, () if dloss is None else (dloss,),
+                (routing.indices, routing.share))
+        return dlogits
     status, dlogits = _training.route_grad(logits, routing._dtype, routing.indices, routing.share,
                                            routing._mask, routing._renormalize, dweights, dloss,
                                            _current_stream(dev))
