@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import tree_allreduce_algorithms_amd as ar
+from tree_allreduce_algorithms_amd import training
 from test_gpu_route import gpu_ready  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -89,3 +90,21 @@ def test_a_raw_handle_is_left_to_the_caller():
         r = ar.route(x, 2, stream=s)
         torch.cuda.synchronize()
         assert torch.equal(r.indices, ar.route(x, 2).indices)
+
+
+def test_external_streams_keep_no_workspace():
+    """A handle that the runtime gives out again must not find another stream's sums."""
+    x = [torch.randn(2000, 64, device="cuda") for _ in range(3)]
+    want = ar.route(x, 4)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    before = dict(training._route_workspaces)
+    for s in (stream.cuda_stream, torch.cuda.ExternalStream(stream.cuda_stream)):
+        got = [ar.route(x, 4, stream=s) for _ in range(4)]
+        torch.cuda.synchronize()
+        for r in got:
+            assert torch.equal(r.indices, want.indices) and torch.equal(r.counts, want.counts)
+            assert torch.equal(r.weights, want.weights) and torch.equal(r.loss, want.loss)
+    assert training._route_workspaces.keys() == before.keys()
+    ar.route(x, 4, stream=stream)
+    assert (0, stream.cuda_stream) in training._route_workspaces

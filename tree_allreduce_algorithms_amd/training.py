@@ -298,15 +298,19 @@ _route_workspaces = {}   # (device index, stream handle) -> workspace
 
 
 def _route_workspace(dev, handle):
-    """The stream's workspace, which every call leaves ready for the next.  A
-    captured call gets one of its own, cleared in the graph: its replays may
-    run beside the stream's other calls.  (The null stream cannot be captured.)"""
+    """The current stream's workspace, which every call leaves ready for the
+    next: one for each of torch's own streams, which last as long as the
+    process.  Other calls get one of their own, cleared on the stream: captured
+    ones, whose replays may run beside the stream's other calls (the null
+    stream cannot be captured), and those on another library's stream, whose
+    handle may come back as that of a new stream beside the old one's work."""
     if handle and torch.cuda.is_current_stream_capturing():
         return torch.zeros(ROUTE_WORKSPACE, dtype=torch.uint8, device=f"cuda:{dev}")
     ws = _route_workspaces.get((dev, handle))
     if ws is None:
         ws = torch.zeros(ROUTE_WORKSPACE, dtype=torch.uint8, device=f"cuda:{dev}")
-        _route_workspaces[dev, handle] = ws
+        if not handle or torch.cuda.current_stream(dev).stream_id != handle:   # an external stream's id is its handle
+            _route_workspaces[dev, handle] = ws
     return ws
 
 
