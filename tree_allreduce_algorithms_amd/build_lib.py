@@ -5,9 +5,12 @@ Usage: ``python -m tree_allreduce_algorithms_amd.build_lib`` (or call
 ``build()``).  hipcc cross-compiles for gfx950 without a GPU present.  Each
 source compiles to its own object in parallel (the kernel files instantiate
 many dtype x op x unroll variants), then one hipcc call links the library and
-one compiler call the module that calls it.
+one compiler call the module that calls it.  Both are put in place together,
+when both are whole.  Without torch, which the collectives do without, the
+library is built alone, and says so.
 """
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -52,22 +55,39 @@ def sources():
     return [os.path.join(CSRC, s) for s in SOURCES]
 
 
-def module_command(out):
-    """The compiler call that builds the module, from torch's own headers and libraries."""
-    from torch.utils import cpp_extension
+def has_torch():
+    return importlib.util.find_spec("torch") is not None
+
+
+def host_compiler():
+    """CXX, the system's compiler, or the one that comes with hipcc."""
     cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
-    if not cxx:
-        raise RuntimeError("no host C++ compiler (g++) found")
+    return cxx or os.path.join(os.path.dirname(os.path.realpath(hipcc())), "amdclang++")
+
+
+def module_command(out, libdir):
+    """The compiler call that builds the module, from torch's own headers and
+    libraries and the libar.so in `libdir`."""
+    from torch.utils import cpp_extension
     includes = [INCLUDE, *cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
-    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+    return [host_compiler(), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
             *[a for i in includes for a in ("-isystem", i)],
-            os.path.join(CSRC, "train", "torch_calls.cpp"), "-o", out, "-L", PKG, "-lar",
+            os.path.join(CSRC, "train", "torch_calls.cpp"), "-o", out, "-L", libdir, "-lar",
             "-Wl,-rpath,$ORIGIN", *[f"-L{p}" for p in cpp_extension.library_paths()],
             "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
+def _run(what, cmd, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"{what} failed ({proc.returncode}):\n{proc.stdout}\n{proc.stderr}")
+
+
 def build(verbose=False, jobs=None):
-    """Compile every source into libar.so next to this file; returns its path."""
+    """Compile every source into libar.so and _training.so next to this file;
+    returns the library's path.  Where anything fails, both stay as they were."""
     cc = hipcc()
     jobs = jobs or min(len(SOURCES), os.cpu_count() or 1, 8)
     with tempfile.TemporaryDirectory(prefix="ar_build_") as tmpdir:
@@ -91,17 +111,21 @@ def build(verbose=False, jobs=None):
                 print(out, file=sys.stderr)
         if failures:
             raise RuntimeError("hipcc failed:\n" + "\n".join(failures))
-        tmp = LIB + ".tmp"
-        cmd = [cc, *LINK_FLAGS, *objs, "-o", tmp]
-        proc = subprocess.run(cmd, capture_output=True, text=True)
-        if proc.returncode != 0:
-            raise RuntimeError(f"link failed ({proc.returncode}):\n{proc.stdout}\n{proc.stderr}")
-    os.replace(tmp, LIB)
-    tmp = MODULE + ".tmp"
-    proc = subprocess.run(module_command(tmp), capture_output=True, text=True)
-    if proc.returncode != 0:
-        raise RuntimeError(f"module failed ({proc.returncode}):\n{proc.stdout}\n{proc.stderr}")
-    os.replace(tmp, MODULE)
+        built = os.path.join(tmpdir, os.path.basename(LIB))
+        _run("link", [cc, *LINK_FLAGS, *objs, "-o", built], verbose)
+        targets = [(built, LIB)]
+        if has_torch():
+            module = os.path.join(tmpdir, os.path.basename(MODULE))
+            _run("module", module_command(module, tmpdir), verbose)
+            targets.append((module, MODULE))
+        else:
+            print(f"torch is not installed: {os.path.basename(MODULE)} (the training calls) is not built",
+                  file=sys.stderr)
+        # into this folder first, so that the last step renames within one file system
+        for made, target in targets:
+            shutil.copy2(made, target + ".tmp")
+        for _, target in targets:
+            os.replace(target + ".tmp", target)
     return LIB
 
 
