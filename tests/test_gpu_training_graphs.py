@@ -63,3 +63,33 @@ def test_a_captured_norm_without_a_bound_is_none_to_clip_by():
     graph.replay()
     with pytest.raises(ValueError, match="clip"):
         a.step(1e-3, clip=True)
+
+
+def test_replays_of_the_router_run_beside_eager_calls():
+    """Replays on one stream while eager calls run on another: each has sums of its own."""
+    logits = [torch.randn(4000, 64, device="cuda") for _ in range(4)]
+    dw = [torch.randn(4000, 4, device="cuda") for _ in range(4)]
+    one = torch.ones((), device="cuda")
+
+    def both():
+        r = ar.route(logits, 4, renormalize=True)
+        return r.indices, r.weights, r.counts, r.loss, ar.route_grad(logits, r, dw, one)
+
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        replayed = both()
+    side = torch.cuda.Stream()
+    for k in range(6):
+        for t in logits:
+            t.normal_()
+        want = both()
+        torch.cuda.synchronize()
+        for _ in range(10):
+            with torch.cuda.stream(side):
+                graph.replay()
+            eager = both()
+        torch.cuda.synchronize()
+        for a, b, c in zip(replayed, eager, want):
+            assert torch.equal(a, c) and torch.equal(b, c), k
