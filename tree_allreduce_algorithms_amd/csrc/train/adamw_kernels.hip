@@ -525,8 +525,11 @@ __device__ __forceinline__ void step8(const AdamwStepArgs& a, const AdamwTensor&
   }
 }
 
+// Three waves a SIMD, though registers allow four: 300M elements in eight
+// tensors that begin off the cache lines 842 us against 882 (float32 params,
+// bfloat16 gradients and copies), that begin on them 767 to 776 either way.
 template <class P, class G, bool COPY>
-__global__ __launch_bounds__(kBlock, 3) void adamw8_step_kernel(AdamwStepArgs a) {
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(3, 3))) void adamw8_step_kernel(AdamwStepArgs a) {
   // from the end, where the norm has just been, and where the last tile's
   // elements one by one would keep the rest waiting (6.5M elements: 25.1 us
   // in order, 22.5 from the end; 300M 803 and 798)
