@@ -56,3 +56,18 @@ def test_only_streams_that_last_keep_a_workspace(monkeypatch):
     capturing = True
     assert training._route_workspace(0, 0x7F01) is not training._route_workspaces[0, 0x7F01]
     assert training._route_workspace(0, 0) is training._route_workspaces[0, 0]
+
+
+def test_an_optimizer_records_a_torch_stream_once_also_after_its_raw_handle(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", External)
+    opt = training.AdamW.__new__(training.AdamW)
+    opt.params, opt.grads, opt.copies, opt.state = [Tensor()], [Tensor()], None, {"exp_avg": [Tensor()]}
+    opt._device, opt._norm, opt._streams = Tensor(), Tensor(), set()
+    tensors = [*opt.params, *opt.grads, *opt.state["exp_avg"], opt._device, opt._norm]
+    opt._on(77, 77)
+    assert not any(t.streams for t in tensors)
+    side = Stream("side")
+    for _ in range(3):
+        opt._on(side, 77)
+    assert all(t.streams == [side] for t in tensors)

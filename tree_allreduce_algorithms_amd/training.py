@@ -84,12 +84,13 @@ def _stream_of(stream, dev):
 
 def _in_use(stream, *groups):
     """Tells the allocator that these tensors (lists of them, None for none) are
-    in use on `stream`, a call's argument (see above)."""
+    in use on `stream`, a call's argument (see above); whether it was told."""
     if not isinstance(stream, torch.cuda.Stream) or isinstance(stream, torch.cuda.ExternalStream):
-        return
+        return False
     for group in groups:
         for t in group or ():
             t.record_stream(stream)
+    return True
 
 
 def _flat(tensors, what, dev, dtypes, sizes):
@@ -205,10 +206,10 @@ class AdamW:
 
     def _on(self, stream, handle):
         # once a stream: the allocator remembers it for as long as a tensor lives
-        if handle not in self._streams:
+        if handle not in self._streams and \
+                _in_use(stream, self.params, self.grads, self.copies, *self.state.values(),
+                        (self._device, self._norm)):
             self._streams.add(handle)
-            _in_use(stream, self.params, self.grads, self.copies, *self.state.values(),
-                    (self._device, self._norm))
 
     def grad_norm(self, max_norm=None, stream=None):
         """The 2-norm over all gradients (times ``grad_scale``), a float32 GPU
