@@ -328,8 +328,9 @@ int ar_version(void);
  *
  * AdamW over many tensors at once (the update of the shards that a
  * ReduceScatter leaves with their owners, before the AllGather of the result)
- * and the router of a mixture of experts (what decides the AllToAll's
- * exchange).  As above: device pointers, the caller's stream, argument errors
+ * and the router of a mixture of experts (which experts a token goes to, and
+ * how many tokens go to each; no call here exchanges tokens by such counts,
+ * ar_alltoall swaps equal blocks).  As above: device pointers, the caller's stream, argument errors
  * reported before anything is enqueued, no allocation, no synchronisation;
  * ar_debug_fail_launch counts these launches too.  None of these calls
  * touches the byte counters or the choice of implementation.
@@ -415,7 +416,9 @@ ar_status_t ar_adamw_grad_norm(const void* plan, void* device_plan, double max_n
  * rounded once to param's type, and to bfloat16 in `copy`.  With 32-bit
  * states in float32, with 8-bit states m' and v' in float64.  Any eps >= 0 is
  * taken; with one below about 4e-12 the updates are computed in float64, so
- * that an element whose v' float32 cannot hold moves as the formula says.
+ * that an element whose v' float32 cannot hold moves as the formula says;
+ * otherwise in float32, with a root and a reciprocal that are off by up to one
+ * step of its last place.
  * With eps = 0 an element whose m' and v' are both 0 gets 0 / 0, a NaN.
  * AR_ERROR_INVALID_ARGUMENT: a factor that is not finite, lr, eps or
  * weight_decay negative, a beta outside [0, 1), step < 1.
@@ -466,7 +469,9 @@ typedef struct {
  * is 0, or with every logit -infinity, is no token: index -1, weight 0,
  * nothing counted.  A token with a NaN or +infinite logit has NaN for every
  * weight and makes loss NaN; a NaN is never chosen.  p and weights are
- * computed in float32; the sums S are added up in float32 over the tokens of
+ * computed in float32, with exponentials and reciprocals that are off by up to
+ * one step of its last place (what is below its normal numbers may become 0);
+ * the sums S are added up in float32 over the tokens of
  * a block, in float64 over some blocks and in fixed point (2^-32) beyond, in
  * ways that depend on the shape alone.  Outputs are written whole. */
 ar_status_t ar_route(const void* const* logits, const uint8_t* const* masks,
@@ -476,10 +481,11 @@ ar_status_t ar_route(const void* const* logits, const uint8_t* const* masks,
 
 /* Gradient of sum(dweights * weights) + dloss * loss with respect to the
  * logits, the counts held fixed: dlogits [nranks][tokens][experts],
- * contiguous, of the logits' type (one rounding).  logits, masks and shape
- * are the forward call's, indices and share its outputs; dweights (NULL: 0)
- * holds one pointer a rank to [tokens][top_k] float32, dloss (NULL: 0) a
- * float32 on the device.  0 for a token that is none. */
+ * contiguous, of the logits' type (one rounding), computed in float32 as
+ * ar_route's weights are.  logits, masks and shape are the forward call's,
+ * indices and share its outputs; dweights (NULL: 0) holds one pointer a rank
+ * to [tokens][top_k] float32, dloss (NULL: 0) a float32 on the device.  0 for
+ * a token that is none. */
 ar_status_t ar_route_grad(const void* const* logits, const uint8_t* const* masks,
                           const ar_route_shape_t* shape, const int32_t* indices,
                           const float* share, const float* const* dweights, const float* dloss,

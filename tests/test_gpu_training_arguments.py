@@ -81,3 +81,18 @@ def test_a_step_shows_in_a_backward_pass_that_saved_the_parameter():
         y.backward()
     (w * w).sum().backward()
     assert torch.equal(w.grad, 2 * w.detach())
+
+
+def test_a_graphs_logits_take_the_gradient_by_hand():
+    """Autograd records nothing of the router; its gradient is handed on."""
+    w = torch.randn(32, 16, device="cuda", requires_grad=True)
+    x = [torch.randn(50, 32, device="cuda") for _ in range(2)]
+    logits = [t @ w for t in x]
+    r = ar.route(logits, 2)
+    assert r.weights.grad_fn is None and r.loss.grad_fn is None
+    dx = ar.route_grad(logits, r, dloss=torch.ones((), device="cuda"))
+    torch.autograd.backward(logits, list(dx))
+    want = sum(t.double().t() @ d.double() for t, d in zip(x, dx))
+    # 100 products a sum, each rounded, in any order
+    bound = 101 * 2.0 ** -24 * sum(t.double().abs().t() @ d.double().abs() for t, d in zip(x, dx))
+    assert ((w.grad.double() - want).abs() <= bound).all()

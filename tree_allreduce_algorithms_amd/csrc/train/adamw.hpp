@@ -25,9 +25,9 @@ constexpr uint32_t kAdamwMaxTiles = (1u << 22) - 1;
 constexpr uint32_t kAdamwMaxDecodeTiles = (1u << 24) - 1;
 
 // A 32-bit step whose reads come to this much or less goes through the caches
-// for them, a longer one past them.  Norm and step, float32 throughout: 256 MiB
-// 83 us through and 97 past, 320 MiB 103 and 122, 400 MiB 154 and 145, 1 GiB
-// 391 and 369.
+// for them, a longer one past them.  Norm and step back to back, float32
+// throughout: 256 MiB 83 us through and 97 past, 320 MiB 103 and 122, 400 MiB
+// 154 and 145, 1 GiB 391 and 369.
 constexpr uint64_t kKeepBytes = 320ull << 20;
 
 // An eps (with its bias correction) beside which the float32 root and

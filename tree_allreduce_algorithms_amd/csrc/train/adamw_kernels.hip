@@ -5,6 +5,10 @@
 // once, by one lane, so HBM bandwidth is what should bound them.  Work is cut
 // into tiles of kAdamwTile elements of one tensor (the plan's table), one
 // quarter for each of the block's four waves, sixteen elements a lane.
+//
+// Times in this file are medians of a kernel trace unless they say otherwise;
+// pairs that compare two forms were taken together, on one card, when the one
+// was chosen.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -44,8 +48,10 @@ template <> struct Raw<uint8_t> {
 
 // Which elements of a tensor a lane has: kQuads runs of four, `step` apart.
 // WHOLE: all of the wave's elements exist, and the tensor's pointers allow
-// quads.  Only the last wave of a tensor goes element by element, or those of
-// arrays that are aligned to their elements only.
+// quads.  Only the last wave of a tensor goes element by element, or all of
+// them where one of its arrays is aligned to its elements only: 300M in eight
+// shards of an odd count take 1.4 to 1.5 times as long (norm of float32, 32-bit
+// steps) to 2.2 times (norm of bfloat16, 8-bit steps).
 template <bool WHOLE> struct Lanes {
   uint64_t first, count;
   uint32_t step;
@@ -136,9 +142,10 @@ __device__ __forceinline__ void add_squares(const AdamwTensor& t, uint64_t begin
 // are decided on what it scales.  Every block leaves a partial sum; the last
 // block of each group adds up the group's, the last group the groups', each
 // in their order, so a norm is one launch and its bits do not depend on which
-// block comes last.  1,024 blocks in groups of 32 measured 175 us for 300M
-// float32 (6.9 TB/s) and 87 us for 300M bfloat16; 2,048 in groups of 64 175
-// and 97, 512 in groups of 16 167 and 130.
+// block comes last.  300M float32 take 170 to 176 us (6.8-7.1 TB/s), 300M
+// bfloat16 94 us (6.4 TB/s).  Of 1,024 blocks in groups of 32, 2,048 in groups
+// of 64 and 512 in groups of 16 the first were best for both together: 175
+// and 87 us back to back, against 175 and 97, and 167 and 130.
 template <class G> __global__ __launch_bounds__(kBlock) void adamw_norm_kernel(AdamwNormArgs a) {
   const AdamwTensor* tensors = reinterpret_cast<const AdamwTensor*>(a.plan + a.tensors_at);
   const AdamwTile* tiles = reinterpret_cast<const AdamwTile*>(a.plan + a.tiles_at);
@@ -384,9 +391,10 @@ template <class T> __device__ __forceinline__ void unstage(const Raw16* from, vo
 // and writes the w-th of the arrays only.  Memory binds it; the detour keeps
 // each wave's accesses to one array at a time, in runs of 4 KiB.  Measured,
 // with float32 gradients and copies (30 bytes an element): 300M elements
-// 1,560 us (5.8 TB/s; 1,585 with all arrays in one lane's registers, 1,640
-// with pieces twice as long), 9M in 250 tensors with bfloat16 gradients 38.9 us
-// (46.8 in registers); write-back stores 1,650 us for 300M.
+// 1,555 to 1,575 us (5.7-5.8 TB/s), 9M in 250 tensors with bfloat16 gradients
+// 40.8 us.  When it was chosen: 1,560 us against 1,585 with all arrays in one
+// lane's registers, 1,640 with pieces twice as long and 1,650 with write-back
+// stores; 38.9 us against 46.8 in registers.
 template <class P, class G, bool COPY, bool KEEP>
 __device__ __forceinline__ void step32_staged(const AdamwStepArgs& a, const AdamwTensor& t, uint64_t begin, float c) {
   __shared__ Raw16 lds[4][kPiece / 4];
@@ -444,11 +452,12 @@ __global__ __launch_bounds__(kBlock) void adamw_step_kernel(AdamwStepArgs a) {
 // The update from m and v, and their codes.  The 8-bit step's arithmetic
 // (about 60 instructions an element, a third of them in float64) and its bytes
 // take about as long: 300M elements with bfloat16 gradients and copies (16.03
-// bytes each) 785 us, 6.1 TB/s; 6.5M with float32 gradients 18.5 us.  A block
+// bytes each) 776 us, 6.2 TB/s; 6.5M with float32 gradients 22.6 us.  A block
 // of a state per 16 lanes shares the scales' arithmetic over 16 elements a
 // lane; one per wave, four elements a lane, took 2,140 us.
-// FAR: a block of the wave is tiny or huge, or ends early, or eps is wide.  What an element
-// gets does not depend on which of the two forms its wave takes.
+// FAR: a block of the wave is tiny or huge, or ends early, or eps is wide.
+// What an element gets does not depend on which of the two forms its wave
+// takes.
 template <bool FAR, class P, bool COPY, class L>
 __device__ __forceinline__ void finish8(const AdamwStepArgs& a, const AdamwTensor& t, const L& l,
                                         const Quad<P> (&p)[kQuads], const double (&m)[kQuads][4],
@@ -526,13 +535,14 @@ __device__ __forceinline__ void step8(const AdamwStepArgs& a, const AdamwTensor&
 }
 
 // Three waves a SIMD, though registers allow four: 300M elements in eight
-// tensors that begin off the cache lines 842 us against 882 (float32 params,
-// bfloat16 gradients and copies), that begin on them 767 to 776 either way.
+// tensors that begin off the cache lines 842 to 852 us against 882, back to
+// back (float32 params, bfloat16 gradients and copies), that begin on them 767
+// to 776 either way.
 template <class P, class G, bool COPY>
 __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(3, 3))) void adamw8_step_kernel(AdamwStepArgs a) {
   // from the end, where the norm has just been, and where the last tile's
   // elements one by one would keep the rest waiting (6.5M elements: 25.1 us
-  // in order, 22.5 from the end; 300M 803 and 798)
+  // in order, 22.5 from the end; 300M 803 and 798; as the step was then)
   const AdamwTile tile = reinterpret_cast<const AdamwTile*>(a.plan + a.tiles_at)[gridDim.x - 1 - blockIdx.x];
   const AdamwTensor t = reinterpret_cast<const AdamwTensor*>(a.plan + a.tensors_at)[tile.tensor];
   const float c = a.clip ? reinterpret_cast<const AdamwSums*>(a.plan + a.sums_at)->factor : a.factor;
@@ -547,7 +557,8 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(3, 3))) 
 // --- decoding ---------------------------------------------------------------------------
 
 // One rounding per value: the products are taken in float64 (m's is exact
-// there) and rounded to float32.  Memory binds it: 300M codes 249 us, 6.0 TB/s.
+// there) and rounded to float32.  Memory binds it: 300M codes of m 264 us (5.7
+// TB/s), of v 288 us (5.2 TB/s).
 template <bool WHOLE, class C>
 __device__ __forceinline__ void decode(const C* codes, const float* scales, uint64_t begin, uint64_t count,
                                        float* out) {

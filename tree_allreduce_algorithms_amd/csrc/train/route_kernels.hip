@@ -6,6 +6,15 @@
 // row's maximum and sums then take three steps across lanes, shared by 8
 // rows, where a wave a row would take six for each.  Rows are read in
 // 16-byte accesses whatever their alignment.
+//
+// Exponentials and reciprocals are single instructions, off by one step of the
+// last place each: a weight's error is then a few roundings of float32, most of
+// them the exponent's, 3 |x - top| half steps.  A full-precision exponential is
+// several instructions more a value, in a kernel that instructions bind.
+//
+// Times in this file are medians of a kernel trace unless they say otherwise;
+// pairs that compare two forms were taken together, back to back, when the one
+// was chosen.
 #include "device_common.hpp"
 #include "train/route.hpp"
 #include "train/wave.hpp"
@@ -308,9 +317,14 @@ template <class S, int L> __device__ __forceinline__ void reorder(Choice* c, int
 }
 
 // The same for any row, by top_k searches over all values: exact, NaN never
-// chosen, about three times the work (of normal logits one row in 2,600 of 256
-// float32 takes it, of bfloat16 none).  Within 2^16 its top is the one above,
-// so that a row's results do not depend on which of the two its wave took.
+// chosen, about three times the work, and a wave takes it for all its rows if
+// one of them is open.  Of normal bfloat16 logits none is.  Of float32 ones
+// with eight of 256 chosen one row in 2,600 is; but with two chosen, where the
+// list ends with the choice, every row whose two best lie in one lane: 10 to
+// 12 % of the rows of 32 to 256 experts and 42 % of 8, which are 57 to 99 % of
+// the waves (131,072 rows of 256 take 40.8 us back to back for two chosen, 35.3
+// for four).  Within 2^16 its top is the one above, so that a row's results do
+// not depend on which of the two its wave took.
 template <class T, int LG, int C>
 __device__ __forceinline__ Choice choose_slowly(const float (&x)[Shape<T, LG, C>::V], int top_k) {
   using S = Shape<T, LG, C>;
@@ -415,9 +429,9 @@ __device__ __forceinline__ double unit_of(const RouteShape& a, uint32_t tokens) 
 // read and are added up per column in registers; the sums of a block's 8
 // waves, of up to 16 blocks and of all are joined by the last to arrive, in
 // three short stages (about 6 us).
-// Measured, 131,072 rows: 256 bfloat16, 8 chosen 30.8 us (2.2 TB/s read; the
-// bytes alone 12), 256 float32 42.9 us (3.1 TB/s; 23); 32,768 rows of 128
-// bfloat16, 2 chosen 11.2 us; one row 3.5 us.
+// Measured, 131,072 rows: 256 bfloat16, 8 chosen 32.7 us (2.1 TB/s read; the
+// bytes alone 12; 31 back to back), 256 float32 45.6 us (2.9 TB/s; 23; 42 back
+// to back); 32,768 rows of 128 bfloat16, 2 chosen 12 us; one row 3.8 us.
 template <class T, int LG, int C, int L, int RANKS>
 __global__ __launch_bounds__(kRouteBlock, 2) void route_kernel(RouteArgs<RANKS> a) {
   using S = Shape<T, LG, C>;
@@ -689,8 +703,9 @@ __global__ __launch_bounds__(kRouteBlock, 2) void route_kernel(RouteArgs<RANKS> 
 //   dx = p (d - sum p d), d = c + dw at the chosen            (otherwise)
 // What belongs to the chosen columns alone takes a detour through LDS, one
 // write a choice, instead of a compare of every column with every choice.
-// Measured, 131,072 rows of 256 float32: 42.4 us, 6.3 TB/s of the 268 MB read
-// and written; 32,768 rows of 128 bfloat16, renormalized: 5.5 us.
+// Measured, 131,072 rows of 256 float32: 42.9 us, 6.3 TB/s of the 268 MB read
+// and written; of 256 bfloat16 24 us back to back (5.6 TB/s); 32,768 rows of
+// 128 bfloat16, renormalized: 5.8 us.
 template <class T, int LG, int C, bool RENORMALIZE, int RANKS>
 __global__ __launch_bounds__(kBlock, 4) void route_grad_kernel(RouteGradArgs<RANKS> a) {
   using S = Shape<T, LG, C>;

@@ -325,7 +325,11 @@ def route(logits, top_k, mask=None, renormalize=False, stream=None):
     ``logits`` lists one [tokens, experts] tensor a rank (float32 or bfloat16;
     rows may be strided); ``mask`` optionally lists one boolean [tokens] tensor
     a rank, False for what is no token.  Returns a ``Routing``.  Up to 1,024
-    experts and 8 choices."""
+    experts and 8 choices.
+
+    Autograd records nothing: the outputs have no ``grad_fn``, whatever the
+    logits have.  Where a graph made the logits, hand it their gradient:
+    ``torch.autograd.backward(logits, list(route_grad(logits, r, ...)))``."""
     logits, mask = _list(logits), _list(mask)
     dev = _training.device(logits)
     if stream is not None or _current_device() != dev:
