@@ -491,6 +491,157 @@ ar_status_t ar_route_grad(const void* const* logits, const uint8_t* const* masks
                           const float* share, const float* const* dweights, const float* dloss,
                           void* dlogits, hipStream_t stream);
 
+/* ---- the experts' products ------------------------------------------------------
+ *
+ * What follows ar_route: the pairs (token, choice) in order by expert, matrix
+ * products grouped by expert, the weighted sum back to the tokens, and the
+ * gradients of all of it.  Pair p = token * top_k + choice.  Rows are the pairs
+ * in order: by expert, within an expert by p, those without an expert behind
+ * all others.  The counts stay on the GPU, no call waits for them.  Matrices
+ * are bfloat16, products are added up in float32 and rounded once.  What the
+ * device arrays `order`, `position` and `offsets` hold is bounds-checked by the
+ * kernels (a row or token out of range is none).
+ */
+
+/* Device memory that ar_expert_order needs for so many pairs and experts, in
+ * bytes (16-byte aligned, any content); 0 for none. */
+size_t ar_expert_order_workspace(size_t pairs, int experts);
+
+/* The order of `pairs` choices (indices as ar_route writes them; a number
+ * outside [0, experts) is no expert), stable:
+ *   order    [pairs]        the pairs, -1 behind the last that has an expert
+ *   position [pairs]        the row of each pair, -1 for none
+ *   offsets  [experts + 1]  the row where each expert's pairs begin; the last is
+ *            the number of pairs that have an expert
+ * experts <= AR_MAX_EXPERTS, pairs < 2^31. */
+ar_status_t ar_expert_order(const int32_t* indices, size_t pairs, int experts, int32_t* order,
+                            int32_t* position, int32_t* offsets, void* workspace,
+                            hipStream_t stream);
+
+/* Operands of the products below.  Strides count elements.  `order` NULL: x has
+ * a row for each pair, in order; else x has a row for each token (x_rows of
+ * them), and the row of pair p is that of token p / top_k. */
+typedef struct {
+  const void* x;               /* [x_rows][in], rows x_stride apart */
+  size_t x_rows;
+  size_t x_stride;
+  const int32_t* order;
+  int top_k;
+  const int32_t* offsets;
+  size_t pairs;                /* < 2^31 */
+  int experts;
+  size_t in;
+  size_t out;
+  ar_dtype_t dtype;            /* AR_BFLOAT16 */
+} ar_expert_rows_t;
+
+/* y [pairs][out] (contiguous): y_i = x_i W_e for the rows i of expert e, 0 for
+ * rows without an expert.  Element (k, n) of W_e lies at weight + e *
+ * expert_stride + k * in_stride + n * out_stride; one of in_stride and
+ * out_stride is 1 and the other at least the size along the first.  With the
+ * two sizes and strides exchanged this is also the gradient with respect to x's
+ * rows.  AR_ERROR_UNSUPPORTED: another dtype, or 2^23 tiles of 128 x 128 or
+ * more. */
+ar_status_t ar_expert_matmul(const ar_expert_rows_t* rows, const void* weight,
+                             size_t expert_stride, size_t in_stride, size_t out_stride, void* y,
+                             hipStream_t stream);
+
+/* dw [experts][in][out] (contiguous, AR_FLOAT32 or AR_BFLOAT16): dw_e = the sum
+ * over the rows i of expert e of x_i^T dy_i, 0 for an expert without rows.  dy
+ * has a row of `out` elements for each pair in order, dy_stride apart. */
+ar_status_t ar_expert_weight_grad(const ar_expert_rows_t* rows, const void* dy, size_t dy_stride,
+                                  void* dw, ar_dtype_t dw_dtype, hipStream_t stream);
+
+/* out [tokens][size] (contiguous): out_t = the sum over the choices k of token t
+ * that have a row of weights[t][k] * y_row, in the order of k (weights NULL: 1).
+ * y has `pairs` rows, y_stride apart; position is [tokens][top_k]. */
+ar_status_t ar_expert_combine(const void* y, size_t y_stride, size_t pairs, size_t size,
+                              ar_dtype_t dtype, const int32_t* position, const float* weights,
+                              size_t tokens, int top_k, void* out, hipStream_t stream);
+
+/* Gradient of ar_expert_combine: dy [pairs][size] (contiguous, bfloat16), dy_row
+ * = weights[t][k] * dout_t, 0 for rows behind offsets[experts]; dweights
+ * [tokens][top_k] float32, dout_t . y_row, 0 for a pair without a row. */
+ar_status_t ar_expert_combine_grad(const void* dout, size_t dout_stride, const void* y,
+                                   size_t y_stride, size_t pairs, size_t size, ar_dtype_t dtype,
+                                   const int32_t* position, const int32_t* offsets, int experts,
+                                   const float* weights, size_t tokens, int top_k, void* dy,
+                                   float* dweights, hipStream_t stream);
+
+/* ---- Muon ------------------------------------------------------------------------
+ *
+ * The step of an optimiser for matrices, beside ar_adamw_*: the momentum is
+ * orthogonalised (its singular values brought near 1) before it is applied.
+ */
+
+/* One tensor of a Muon plan: `count` matrices of rows x cols, contiguous, one
+ * behind the other.
+ *   param     AR_FLOAT32 or AR_BFLOAT16, updated in place
+ *   grad      AR_FLOAT32 or AR_BFLOAT16, only read
+ *   copy      bfloat16 working copy of a float32 param, rewritten by every step;
+ *             NULL for none (all tensors of a plan or none)
+ *   momentum  float32, updated in place */
+typedef struct {
+  void* param;
+  const void* grad;
+  void* copy;
+  float* momentum;
+  size_t count;
+  size_t rows;
+  size_t cols;
+} ar_muon_tensor_t;
+
+/* Hyperparameters of one step. */
+typedef struct {
+  double lr;
+  double momentum;
+  double eps;            /* added to the norm */
+  double weight_decay;
+  double grad_scale;     /* the gradients' factor, e.g. 1/N for a mean over N ranks */
+  double match_rms;      /* 0: s = sqrt(max(1, rows / cols)); else s = match_rms sqrt(max(rows, cols)) */
+  int nesterov;
+  int ns_steps;          /* 1 to 32 */
+} ar_muon_step_t;
+
+/* Bytes of a plan for these tensors; 0 for what ar_muon_plan refuses or when
+ * the host runs out of memory. */
+size_t ar_muon_plan_bytes(const ar_muon_tensor_t* tensors, int ntensors, ar_dtype_t param_dtype,
+                          ar_dtype_t grad_dtype);
+
+/* Writes the plan of these tensors into `plan` (host memory of
+ * ar_muon_plan_bytes bytes).  The caller copies all of it to device memory
+ * (256-byte aligned) and passes both to ar_muon_step; the device copy also holds
+ * the norms, so steps on one plan must be ordered on one stream (or by events).
+ * Everything is checked here: AR_ERROR_INVALID_ARGUMENT for NULL or misaligned
+ * pointers, copies of some tensors only or of bfloat16 params, a written range
+ * that overlaps any other range; AR_ERROR_UNSUPPORTED for other types, a matrix
+ * whose sides, each rounded up to a multiple of 128, multiply to more than 2^30
+ * or of which one exceeds 4,194,240, or more than 2^22 - 1 tiles (of 64 x 64 at
+ * least) in all.  A tensor without elements is skipped. */
+ar_status_t ar_muon_plan(const ar_muon_tensor_t* tensors, int ntensors, ar_dtype_t param_dtype,
+                         ar_dtype_t grad_dtype, void* plan, size_t bytes);
+
+/* Bytes of device memory (256-byte aligned, any content) that a step on this
+ * plan works in: about 8 an element and 8 for each of the shorter sides'
+ * squares. */
+size_t ar_muon_workspace(const void* plan);
+
+/* One step in place, per matrix, with G = grad_scale g:
+ *   m' = momentum m + G;   u = G + momentum m' (nesterov) or m'
+ *   X = u / (|u| + eps);   ns_steps times: A = X X^T, X = a X + (b A + c A A) X
+ *   p' = p - lr (weight_decay p + s X)
+ * with (a, b, c) = (3.4445, -4.7750, 2.0315), |u| the root of the sum of squares
+ * and X X^T taken over the longer side.  m' and p' are computed in float32 (p'
+ * rounded once to param's type, and to bfloat16 in `copy`), |u| in float64; X, A
+ * and the polynomial are held in 22 bits and multiplied with float32 sums.  A
+ * matrix with a NaN or an infinity in u gets NaN throughout; one of zeros is
+ * not moved but by its decay.
+ * AR_ERROR_INVALID_ARGUMENT: a value that is not finite, lr, eps, weight_decay
+ * or match_rms negative, momentum outside [0, 1), ns_steps out of range.
+ * May be captured into a graph (a replay repeats the step with these values). */
+ar_status_t ar_muon_step(const void* plan, void* device_plan, void* workspace,
+                         const ar_muon_step_t* args, hipStream_t stream);
+
 /* ---- testing ---------------------------------------------------------------- */
 
 /* For callers' tests of their AR_ERROR_HIP handling (the error path of the

@@ -1,6 +1,6 @@
 """MI355X-native ring / tree collectives over N rank buffers on one GPU, with
-the AdamW step that updates a rank's shard between them and the router that
-sends tokens to experts.
+the AdamW step that updates a rank's shard between them, the Muon step for
+matrices, the router that sends tokens to experts and the experts' products.
 
 The operators live in a C-ABI shared library (``libar.so``: HIP kernels for
 gfx950 plus the C ABI declared in ``include/ar.h``); this package is a thin
@@ -39,13 +39,19 @@ from .binding import (  # noqa: F401
     tree_allreduce,
 )
 
-_TRAINING = ("AdamW", "Routing", "dequantize", "route", "route_grad")
+# these need torch, which the collectives' raw calls do without
+_TRAINING = {name: module for module, names in {
+    "training": ("AdamW", "Routing", "dequantize", "route", "route_grad"),
+    "experts": ("ExpertOrder", "expert_combine", "expert_combine_grad", "expert_matmul", "expert_order",
+                "expert_weight_grad"),
+    "muon": ("Muon",),
+}.items() for name in names}
 
 
 def __getattr__(name):
-    # these need torch, which the collectives' raw calls do without
     if name in _TRAINING:
-        from . import training
-        globals().update({n: getattr(training, n) for n in _TRAINING})
+        import importlib
+        module = importlib.import_module("." + _TRAINING[name], __name__)
+        globals().update({n: getattr(module, n) for n, m in _TRAINING.items() if m == _TRAINING[name]})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

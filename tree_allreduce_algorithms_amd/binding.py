@@ -44,6 +44,27 @@ class RouteShape(ctypes.Structure):
                 ("renormalize", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
+class ExpertRows(ctypes.Structure):
+    """ar_expert_rows_t."""
+    _fields_ = [("x", ctypes.c_void_p), ("x_rows", ctypes.c_size_t), ("x_stride", ctypes.c_size_t),
+                ("order", ctypes.c_void_p), ("top_k", ctypes.c_int), ("offsets", ctypes.c_void_p),
+                ("pairs", ctypes.c_size_t), ("experts", ctypes.c_int), ("inputs", ctypes.c_size_t),
+                ("outputs", ctypes.c_size_t), ("dtype", ctypes.c_int)]
+
+
+class MuonTensor(ctypes.Structure):
+    """ar_muon_tensor_t."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("param", "grad", "copy", "momentum")] + \
+               [(f, ctypes.c_size_t) for f in ("count", "rows", "cols")]
+
+
+class MuonStep(ctypes.Structure):
+    """ar_muon_step_t."""
+    _fields_ = [(f, ctypes.c_double) for f in ("lr", "momentum", "eps", "weight_decay", "grad_scale",
+                                               "match_rms")] + \
+               [("nesterov", ctypes.c_int), ("ns_steps", ctypes.c_int)]
+
+
 # name -> (restype, argtypes), in the order include/ar.h declares them
 SIGNATURES = {
     "ar_ring_allreduce": (_I, [_PP, _I, _SZ, _I, _I, _VP]),
@@ -81,6 +102,17 @@ SIGNATURES = {
     "ar_adamw_dequantize": (_I, [_VP, _VP, _SZ, _I, _VP, _VP]),
     "ar_route": (_I, [_VP, _VP, ctypes.POINTER(RouteShape)] + [_VP] * 7),
     "ar_route_grad": (_I, [_VP, _VP, ctypes.POINTER(RouteShape)] + [_VP] * 6),
+    "ar_expert_order_workspace": (_SZ, [_SZ, _I]),
+    "ar_expert_order": (_I, [_VP, _SZ, _I] + [_VP] * 5),
+    "ar_expert_matmul": (_I, [ctypes.POINTER(ExpertRows), _VP, _SZ, _SZ, _SZ, _VP, _VP]),
+    "ar_expert_weight_grad": (_I, [ctypes.POINTER(ExpertRows), _VP, _SZ, _VP, _I, _VP]),
+    "ar_expert_combine": (_I, [_VP, _SZ, _SZ, _SZ, _I, _VP, _VP, _SZ, _I, _VP, _VP]),
+    "ar_expert_combine_grad": (_I, [_VP, _SZ, _VP, _SZ, _SZ, _SZ, _I, _VP, _VP, _I, _VP, _SZ, _I,
+                                    _VP, _VP, _VP]),
+    "ar_muon_plan_bytes": (_SZ, [ctypes.POINTER(MuonTensor), _I, _I, _I]),
+    "ar_muon_plan": (_I, [ctypes.POINTER(MuonTensor), _I, _I, _I, _VP, _SZ]),
+    "ar_muon_workspace": (_SZ, [_VP]),
+    "ar_muon_step": (_I, [_VP, _VP, _VP, ctypes.POINTER(MuonStep), _VP]),
     "ar_debug_fail_launch": (_I, [_I]),
 }
 

@@ -27,7 +27,8 @@ MODULE = os.path.join(PKG, "_training.so")
 
 SOURCES = ["api.cpp", "plan.cpp", "ring_kernels.hip", "copy_kernels.hip", "tree_kernels.hip",
            "step_kernels.hip", "train/adamw.cpp", "train/adamw_kernels.hip", "train/route.cpp",
-           "train/route_kernels.hip"]
+           "train/route_kernels.hip", "train/experts.cpp", "train/experts_kernels.hip",
+           "train/expert_products.hip", "train/muon.cpp", "train/muon_kernels.hip"]
 
 COMPILE_FLAGS = [
     "--offload-arch=gfx950",

@@ -1,0 +1,85 @@
+// The experts' products: what the host hands to the kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "ar.h"
+
+namespace ar {
+
+// Pairs of a block of the order's kernels, and the most blocks: longer lists
+// give every block more, since each block reads all blocks' counts.
+constexpr uint32_t kOrderWaves = 16;
+constexpr uint32_t kOrderBlockPairs = 4096;
+constexpr uint32_t kOrderBlocks = 64;
+
+inline uint32_t order_blocks(uint64_t pairs) {
+  const uint64_t n = (pairs + kOrderBlockPairs - 1) / kOrderBlockPairs;
+  return n < 1 ? 1 : n > kOrderBlocks ? kOrderBlocks : static_cast<uint32_t>(n);
+}
+
+struct OrderArgs {
+  const int32_t* indices;
+  uint32_t pairs, block_pairs, blocks;
+  int32_t experts;
+  int32_t* order;
+  int32_t* position;
+  int32_t* offsets;
+  uint32_t* counts;       // [blocks][experts], more than one block
+};
+hipError_t launch_expert_order(const OrderArgs& a, hipStream_t stream);
+
+// Products by expert.  `line` is the distance of a weight's lines: of its rows
+// (in) where the columns (out) are contiguous, of its columns otherwise.
+struct ProductArgs {
+  const void* x;
+  const void* w;
+  void* y;
+  const int32_t* order;    // null: x's rows are the pairs in order
+  const int32_t* offsets;
+  uint64_t x_stride, w_expert, w_line;
+  uint32_t x_rows, pairs, in, out, tiles_n;
+  int32_t experts, top_k;
+  uint32_t vec;            // four outputs may be stored at once
+};
+// Blocks of a launch; one has less than 2^32 threads of at most 512 a block.
+constexpr uint64_t kMaxProductBlocks = (1u << 23) - 1;
+uint64_t expert_product_blocks(uint64_t pairs, int experts, uint64_t out);
+uint64_t expert_weight_grad_blocks(int experts, uint64_t in, uint64_t out);
+
+// Bytes that 32-bit offsets reach from one base (see tile.hpp).
+constexpr uint64_t kProductReach = 0x80000000ull;
+
+hipError_t launch_expert_product(const ProductArgs& a, bool out_contiguous, bool direct, hipStream_t stream);
+
+struct WeightGradArgs {
+  const void* x;
+  const void* dy;
+  void* dw;
+  const int32_t* order;
+  const int32_t* offsets;
+  uint64_t x_stride, dy_stride;
+  uint32_t x_rows, pairs, in, out, tiles_m, tiles_n;
+  int32_t experts, top_k;
+  uint32_t vec;
+};
+hipError_t launch_expert_weight_grad(const WeightGradArgs& a, ar_dtype_t dw_dtype, bool direct, hipStream_t stream);
+
+struct CombineArgs {
+  const void* y;
+  const void* dout;          // gradient only
+  const int32_t* position;
+  const int32_t* offsets;    // gradient only
+  const float* weights;
+  void* out;                 // the tokens' sums, or dy
+  float* dweights;
+  uint64_t y_stride, dout_stride;
+  uint32_t tokens, pairs, size;
+  int32_t experts, top_k;
+};
+hipError_t launch_expert_combine(const CombineArgs& a, hipStream_t stream);
+hipError_t launch_expert_combine_grad(const CombineArgs& a, hipStream_t stream);
+
+}  // namespace ar

@@ -1,0 +1,274 @@
+// The order of (token, choice) pairs by expert, and the sums over a token's
+// pairs with their gradient (gfx950).
+#include "train/experts.hpp"
+
+#include "train/wave.hpp"
+
+namespace ar {
+namespace {
+
+constexpr int kOrderThreads = kOrderWaves * kWave;
+constexpr uint32_t kNone = 0xffffffffu;
+
+// The expert of a pair, kNone for what is no expert's number.
+__device__ __forceinline__ uint32_t expert_of(const OrderArgs& a, uint32_t p) {
+  const uint32_t e = static_cast<uint32_t>(a.indices[p]);
+  return e < static_cast<uint32_t>(a.experts) ? e : kNone;
+}
+
+// The wave's part of the block's pairs.
+__device__ __forceinline__ void span_of(const OrderArgs& a, uint32_t wave, uint32_t* begin, uint32_t* end) {
+  const uint32_t first = blockIdx.x * a.block_pairs;
+  const uint32_t last = a.pairs - first < a.block_pairs ? a.pairs : first + a.block_pairs;
+  const uint32_t each = a.block_pairs / kOrderWaves;
+  *begin = min(first + wave * each, last);
+  *end = min(*begin + each, last);
+}
+
+__device__ __forceinline__ void count_pairs(const OrderArgs& a, uint32_t* mine, uint32_t begin, uint32_t end) {
+  const uint32_t lane = threadIdx.x % kWave;
+  for (uint32_t p = begin + lane; p < end; p += kWave) {
+    const uint32_t e = expert_of(a, p);
+    if (e != kNone) atomicAdd(mine + e, 1u);
+  }
+}
+
+// A block's pairs of each expert, for lists of more than one block.
+__global__ __launch_bounds__(kOrderThreads) void order_count(OrderArgs a) {
+  extern __shared__ uint32_t counts[];
+  for (int e = threadIdx.x; e < a.experts; e += kOrderThreads) counts[e] = 0;
+  __syncthreads();
+  uint32_t begin, end;
+  span_of(a, threadIdx.x / kWave, &begin, &end);
+  count_pairs(a, counts, begin, end);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += kOrderThreads)
+    a.counts[static_cast<size_t>(blockIdx.x) * a.experts + e] = counts[e];
+}
+
+// A stable counting sort.  Every wave takes its pairs in their order, 64 at a
+// time; a pair's row is its expert's beginning, plus the expert's pairs of the
+// blocks and waves before, plus those of the wave's lower lanes (found by
+// comparing the number's bits across the lanes).
+__global__ __launch_bounds__(kOrderThreads) void order_place(OrderArgs a) {
+  extern __shared__ uint32_t next[];       // [waves][experts]
+  __shared__ uint32_t part[kOrderWaves];
+  const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int experts = a.experts;
+  for (int i = threadIdx.x; i < experts * static_cast<int>(kOrderWaves); i += kOrderThreads) next[i] = 0;
+  __syncthreads();
+  uint32_t begin, end;
+  span_of(a, wave, &begin, &end);
+  uint32_t* mine = next + wave * experts;
+  count_pairs(a, mine, begin, end);
+  __syncthreads();
+
+  // thread e has expert e (at most 1,024 of both): its pairs in all blocks, and
+  // in those before this one
+  const int e = threadIdx.x;
+  uint32_t all = 0, before = 0;
+  if (e < experts) {
+    if (a.blocks == 1) {
+      for (uint32_t w = 0; w < kOrderWaves; ++w) all += next[w * experts + e];
+    } else {
+      for (uint32_t b = 0; b < a.blocks; ++b) {
+        const uint32_t n = a.counts[static_cast<size_t>(b) * experts + e];
+        all += n;
+        before += b < blockIdx.x ? n : 0;
+      }
+    }
+  }
+  // where each expert begins: a scan over the threads
+  uint32_t sum = all;
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) {
+    const uint32_t up = __shfl_up(sum, d);
+    if (static_cast<int>(lane) >= d) sum += up;
+  }
+  if (lane == kWave - 1) part[wave] = sum;
+  __syncthreads();
+  uint32_t live = 0, lower = 0;
+  for (uint32_t w = 0; w < kOrderWaves; ++w) {
+    lower += w < wave ? part[w] : 0;
+    live += part[w];
+  }
+  sum += lower;
+  if (e < experts) {
+    uint32_t at = sum - all + before;
+    for (uint32_t w = 0; w < kOrderWaves; ++w) {
+      const uint32_t n = next[w * experts + e];
+      next[w * experts + e] = at;
+      at += n;
+    }
+    if (blockIdx.x == 0) {
+      a.offsets[e + 1] = static_cast<int32_t>(sum);
+      if (e == 0) a.offsets[0] = 0;
+    }
+  }
+  __syncthreads();
+
+  for (uint32_t p0 = begin; p0 < end; p0 += kWave) {
+    const uint32_t p = p0 + lane;
+    const uint32_t key = p < end ? expert_of(a, p) : kNone;
+    uint64_t same = __ballot(key != kNone);
+#pragma unroll
+    for (int bit = 0; bit < 10; ++bit) {
+      const uint64_t ones = __ballot((key >> bit) & 1);
+      same &= (key >> bit) & 1 ? ones : ~ones;
+    }
+    if (p < end) {
+      int32_t row = -1;
+      if (key != kNone) {
+        const uint32_t rank = __popcll(same & ((1ull << lane) - 1));
+        row = static_cast<int32_t>(mine[key] + rank);
+        a.order[row] = static_cast<int32_t>(p);
+      }
+      a.position[p] = row;
+    }
+    // every lane has read before the first of each group counts on, and reads
+    // what was counted in the next round
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (key != kNone && (same & ((1ull << lane) - 1)) == 0) mine[key] += __popcll(same);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  // behind the last pair that has an expert
+  for (uint32_t i = live + blockIdx.x * kOrderThreads + threadIdx.x; i < a.pairs; i += a.blocks * kOrderThreads)
+    a.order[i] = -1;
+}
+
+// --- sums over a token's pairs ------------------------------------------------------
+
+// Eight bfloat16 at any element's address.
+struct __attribute__((packed, aligned(2))) Eight {
+  uint16_t v[8];
+};
+
+__device__ __forceinline__ float to_float(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+
+// Round to nearest, ties to even; NaN stays NaN.
+__device__ __forceinline__ uint16_t to_bf16(float f) {
+  const uint32_t u = __float_as_uint(f);
+  if ((u & 0x7fffffffu) > 0x7f800000u) return static_cast<uint16_t>(u >> 16 | 0x40);
+  return static_cast<uint16_t>((u + 0x7fffu + (u >> 16 & 1)) >> 16);
+}
+
+// The `n` (1 to 8) elements at p, zeros behind them.
+__device__ __forceinline__ Eight read(const uint16_t* p, uint32_t n) {
+  Eight r = {};
+  if (n == 8) return *reinterpret_cast<const Eight*>(p);
+#pragma unroll
+  for (uint32_t i = 0; i < 8; ++i)
+    if (i < n) r.v[i] = p[i];
+  return r;
+}
+__device__ __forceinline__ void write(uint16_t* p, const Eight& x, uint32_t n) {
+  if (n == 8) {
+    *reinterpret_cast<Eight*>(p) = x;
+    return;
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < 8; ++i)
+    if (i < n) p[i] = x.v[i];
+}
+
+constexpr int kSumThreads = 256;
+
+// out_t = sum over the choices k that have an expert of w_tk y_row(t,k), added
+// up in float32 in the order of k.  A thread has eight columns of a token; a
+// block has `lanes` of a token's threads, so whole tokens where they are short.
+__global__ __launch_bounds__(kSumThreads) void combine(CombineArgs a, uint32_t lanes) {
+  const uint32_t per_block = kSumThreads / lanes, in_block = threadIdx.x / lanes;
+  const uint64_t c = (static_cast<uint64_t>(blockIdx.y) * lanes + threadIdx.x % lanes) * 8;
+  if (in_block >= per_block || c >= a.size) return;
+  const uint32_t n = min(8u, a.size - static_cast<uint32_t>(c));
+  const uint16_t* y = static_cast<const uint16_t*>(a.y) + c;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + c;
+  for (uint64_t t = static_cast<uint64_t>(blockIdx.x) * per_block + in_block; t < a.tokens;
+       t += static_cast<uint64_t>(gridDim.x) * per_block) {
+    const uint64_t first = t * a.top_k;
+    float sum[8] = {};
+    for (int k = 0; k < a.top_k; ++k) {
+      const uint32_t row = static_cast<uint32_t>(a.position[first + k]);
+      if (row >= a.pairs) continue;
+      const float w = a.weights == nullptr ? 1.0f : a.weights[first + k];
+      const Eight r = read(y + row * a.y_stride, n);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w, to_float(r.v[i]), sum[i]);
+    }
+    Eight o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o.v[i] = to_bf16(sum[i]);
+    write(out + t * a.size, o, n);
+  }
+}
+
+// dy_i = w_p dout_t and dw_p = dout_t . y_i, i the row of pair p of token t; a
+// wave has a token.  Rows that belong to no pair become 0.
+__global__ __launch_bounds__(kSumThreads) void combine_grad(CombineArgs a) {
+  constexpr uint32_t kWaves = kSumThreads / kWave;
+  const uint32_t lane = threadIdx.x % kWave;
+  const uint32_t id = blockIdx.x * kWaves + threadIdx.x / kWave, waves = gridDim.x * kWaves;
+  const uint16_t* y = static_cast<const uint16_t*>(a.y);
+  uint16_t* dy = static_cast<uint16_t*>(a.out);
+  for (uint32_t t = id; t < a.tokens; t += waves) {
+    const uint16_t* dout = static_cast<const uint16_t*>(a.dout) + t * a.dout_stride;
+    const uint64_t first = static_cast<uint64_t>(t) * a.top_k;
+    for (int k = 0; k < a.top_k; ++k) {
+      const uint32_t row = static_cast<uint32_t>(a.position[first + k]);
+      float dot = 0.0f;
+      if (row < a.pairs) {
+        const float w = a.weights[first + k];
+        for (uint32_t c = lane * 8; c < a.size; c += kWave * 8) {
+          const uint32_t n = min(8u, a.size - c);
+          const Eight d = read(dout + c, n), r = read(y + row * a.y_stride + c, n);
+          Eight o;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x = to_float(d.v[i]);
+            dot = __builtin_fmaf(x, to_float(r.v[i]), dot);
+            o.v[i] = to_bf16(w * x);
+          }
+          write(dy + static_cast<uint64_t>(row) * a.size + c, o, n);
+        }
+        dot = wave_sum(dot);
+      }
+      if (lane == 0) a.dweights[first + k] = dot;
+    }
+  }
+  const uint32_t live = min(static_cast<uint32_t>(max(a.offsets[a.experts], 0)), a.pairs);
+  const Eight zero = {};
+  for (uint32_t row = live + id; row < a.pairs; row += waves)
+    for (uint32_t c = lane * 8; c < a.size; c += kWave * 8)
+      write(dy + static_cast<uint64_t>(row) * a.size + c, zero, min(8u, a.size - c));
+}
+
+}  // namespace
+
+hipError_t launch_expert_order(const OrderArgs& a, hipStream_t stream) {
+  const size_t row = static_cast<size_t>(a.experts) * sizeof(uint32_t);
+  if (a.blocks > 1) {
+    order_count<<<a.blocks, kOrderThreads, row, stream>>>(a);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  order_place<<<a.blocks, kOrderThreads, row * kOrderWaves, stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_combine(const CombineArgs& a, hipStream_t stream) {
+  const uint32_t per = (a.size - 1) / 8 + 1, lanes = per < kSumThreads ? per : kSumThreads;
+  const uint32_t tokens = kSumThreads / lanes, blocks = (a.tokens - 1) / tokens + 1;
+  const dim3 grid(blocks < 65536 ? blocks : 65536, (per - 1) / lanes + 1);
+  combine<<<grid, kSumThreads, 0, stream>>>(a, lanes);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_combine_grad(const CombineArgs& a, hipStream_t stream) {
+  const uint32_t per = kSumThreads / kWave;
+  const uint32_t rows = a.tokens > a.pairs / 2 ? a.tokens : a.pairs / 2;
+  const uint32_t blocks = (rows + per - 1) / per;
+  combine_grad<<<blocks < 8192 ? (blocks ? blocks : 1) : 8192, kSumThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace ar

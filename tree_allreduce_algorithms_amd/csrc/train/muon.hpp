@@ -1,0 +1,95 @@
+// Muon plans: what the host lays out and the kernels read.
+//
+// A plan is one image, identical in host and device memory:
+//   MuonHead      sizes and types (the host reads them)
+//   matrices      one MuonMatrix per matrix
+//   chunks        one MuonChunk per unit of element-wise work
+//   squares       one MuonTile per tile of X X^T on or above the diagonal
+//   tiles         one MuonTile per tile of X
+//   norms         MuonNorm per matrix (device only), then a double per chunk
+// All offsets are from the image's start.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "ar.h"
+
+namespace ar {
+
+constexpr uint32_t kMuonMagic = 0x4d553031u;
+constexpr uint32_t kMuonChunk = 8192;         // elements of a chunk of a matrix
+constexpr uint64_t kMuonMaxTiles = (1u << 22) - 1;
+// elements of one padded matrix: 32-bit offsets reach 2^31 bytes of 16 bits
+constexpr uint64_t kMuonMaxElements = 1ull << 30;
+constexpr int kMuonMaxSteps = 32;
+
+struct MuonHead {
+  uint32_t magic;
+  uint32_t matrices;
+  uint32_t chunks;
+  uint32_t squares;
+  uint32_t tiles;
+  uint32_t side;             // of a tile: 64 or 128
+  int32_t param_dtype;
+  int32_t grad_dtype;
+  uint64_t bytes;
+  uint64_t workspace;        // bytes
+  uint64_t matrices_at, chunks_at, squares_at, tiles_at, norms_at, sums_at;
+  int32_t has_copy;
+  uint32_t pad;
+};
+
+struct MuonMatrix {
+  void* p;
+  const void* g;
+  void* copy;
+  float* m;
+  uint64_t x[2], gram, poly;       // in the workspace; the small parts lie behind the large
+  uint64_t x_plane, gram_plane;    // bytes of a plane
+  uint32_t rows, cols;
+  uint32_t height, width;          // of X: the shorter and the longer side, padded to whole tiles
+  uint32_t tall;                   // X is the transposed matrix
+  uint32_t vec;                    // four elements of a row may be accessed at once
+  uint32_t first_chunk, chunks;
+  float by_shape, by_size;         // sqrt(max(1, rows / cols)), sqrt(max(rows, cols))
+  uint32_t pad[2];
+};
+
+struct MuonChunk {
+  uint32_t matrix, index;
+};
+
+struct MuonTile {
+  uint32_t matrix;
+  uint16_t m, n;
+};
+
+struct MuonNorm {
+  uint32_t arrived;          // chunks that have left their sum; 0 between calls
+  uint32_t pad;
+  double inverse;            // 1 / (|u| + eps)
+  uint32_t rest[12];
+};
+
+struct MuonStepArgs {
+  char* plan;
+  char* workspace;
+  uint64_t matrices_at, chunks_at, squares_at, tiles_at, norms_at, sums_at;
+  float momentum, grad_scale, lr, lr_wd;
+  double eps;
+  float rms;                 // 0: scaled by shape
+  int nesterov, last;        // last: the final product updates the parameters
+  int from;                  // which of the two X is read
+};
+
+hipError_t launch_muon_momentum(const MuonStepArgs& a, uint32_t chunks, ar_dtype_t grad_dtype, hipStream_t stream);
+hipError_t launch_muon_start(const MuonStepArgs& a, uint32_t tiles, uint32_t side, ar_dtype_t grad_dtype,
+                             hipStream_t stream);
+hipError_t launch_muon_gram(const MuonStepArgs& a, uint32_t squares, uint32_t side, hipStream_t stream);
+hipError_t launch_muon_poly(const MuonStepArgs& a, uint32_t squares, uint32_t side, hipStream_t stream);
+hipError_t launch_muon_apply(const MuonStepArgs& a, uint32_t tiles, uint32_t side, ar_dtype_t param_dtype, bool copy,
+                             hipStream_t stream);
+
+}  // namespace ar

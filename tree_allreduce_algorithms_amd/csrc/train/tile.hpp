@@ -1,0 +1,145 @@
+// A block's tile of a matrix product by matrix instructions (gfx950), shared by
+// the experts' products and the Muon step.
+//
+// D[m][n] = sum_k A[m][k] B[k][n] for BM x BN of D, k in steps of 64.  A step
+// of each operand lies in LDS as 16-byte chunks (8 elements) of lines:
+//   k-major   a line is one row m (or column n): 64 consecutive k
+//   r-major   a line is one k: BM (or BN) consecutive rows (columns)
+// so either order of an operand in memory is staged as it is.  A wave reads a
+// k-major fragment by 16-byte loads and an r-major one by the transposing
+// loads, which give a lane four k of one row.  Chunks are permuted within a
+// line by the line's number, so that the lanes of one access meet different
+// banks.
+//
+// Steps are double-buffered: the loads of step k + 1 are under way while step k
+// is multiplied; one barrier a step.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace ar {
+namespace {
+
+constexpr int kStep = 64;      // k of a step
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+
+__device__ __forceinline__ f32x4 multiply(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 multiply(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+typedef __attribute__((address_space(3))) char lds_char;
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_char*)p));
+}
+
+// One operand's step in LDS: R rows (or columns) times 64 k.
+template <int R, bool RMAJOR> struct Staged {
+  static constexpr int kLines = RMAJOR ? kStep : R;
+  static constexpr int kPerLine = (RMAJOR ? R : kStep) / 8;     // chunks
+  static constexpr int kChunks = R * kStep / 8;
+  static constexpr int kBytes = R * kStep * 2;
+
+  // where chunk `c` of a line lies among the line's chunks
+  static __device__ __forceinline__ int place(int line, int c) {
+    if (RMAJOR) return c ^ ((2 * (line & 3) + (kPerLine >= 16 ? line & 8 : 0)) & (kPerLine - 1));
+    return c ^ (line & 7);
+  }
+
+  // the lane's 8 k (8 (lane / 16) and on, of 32 from k0) of row r0 + lane % 16
+  template <class V> static __device__ __forceinline__ V fragment(const char* step, int r0, int k0, int lane) {
+    if (!RMAJOR) {
+      const int line = r0 + lane % 16, c = k0 / 8 + lane / 16;
+      return *reinterpret_cast<const V*>(step + (line * kPerLine + place(line, c)) * 16);
+    } else {
+      // of each 16 lanes, four lie along a line and four lines are read; lane l
+      // gets row l of the four k
+      const int l = lane % 16, line = k0 + 8 * (lane / 16) + l / 4;
+      const int c = (r0 + l % 4 * 4) / 8, half = l & 1;
+      union {
+        V v;
+        s16x4 part[2];
+      } u;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const char* at = step + ((line + 4 * i) * kPerLine + place(line + 4 * i, c)) * 16 + half * 8;
+        u.part[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)(at));
+      }
+      return u.v;
+    }
+  }
+};
+
+// The loads of operands whose rows allow 16-byte accesses: straight to LDS,
+// 1 KB a wave, past the registers.  `limit` bytes from `base` may be read; an
+// offset of kNowhere gives zeros.
+constexpr uint32_t kNowhere = 0xfffffff0u;
+constexpr uint32_t kReach = 0x80000000u;      // bytes that one base can reach
+
+struct Source {
+  u32x4 words;
+  __device__ __forceinline__ explicit Source(const void* base) {
+    const uint64_t p = reinterpret_cast<uintptr_t>(base);
+    words[0] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p));
+    words[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p >> 32) & 0xffffu);
+    words[2] = kReach;
+    words[3] = 0x00020000u;
+  }
+};
+
+// 16 bytes a lane from `offset` of the source to lds + 16 lane; lds is uniform.
+// Written as asm because the compiler takes every later LDS read for a reader
+// of this load's target and would wait for all of them; settled() waits.
+__device__ __forceinline__ void load_to_lds(const Source& s, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               ::"s"(lds), "v"(offset), "s"(s.words)
+               : "memory");
+}
+
+// Waits until all of the wave's loads to LDS have arrived and its own LDS reads
+// are done.
+__device__ __forceinline__ void settled() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+
+// Multiplies one step: acc[i][j] holds rows 16 i, columns 16 j of the wave's
+// part, D[n][m] in a lane: m = lane % 16, n = 4 (lane / 16) + element.
+// `planes` bytes lie between the planes of a value that is held as the sum of
+// two; their products without that of the two small parts are added up.
+template <int TM, int TN, class V, int P, class A, class B>
+__device__ __forceinline__ void multiply_step(const char* a, const char* b, int m0, int n0, int lane,
+                                              f32x4 (&acc)[TM][TN]) {
+#pragma unroll
+  for (int k0 = 0; k0 < kStep; k0 += 32) {
+    V fa[P][TM], fb[P][TN];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) fa[p][i] = A::template fragment<V>(a + p * A::kBytes, m0 + 16 * i, k0, lane);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) fb[p][j] = B::template fragment<V>(b + p * B::kBytes, n0 + 16 * j, k0, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        if (P == 2) {
+          acc[i][j] = multiply(fb[P - 1][j], fa[0][i], acc[i][j]);
+          acc[i][j] = multiply(fb[0][j], fa[P - 1][i], acc[i][j]);
+        }
+        acc[i][j] = multiply(fb[0][j], fa[0][i], acc[i][j]);
+      }
+  }
+}
+
+}  // namespace
+}  // namespace ar

@@ -253,6 +253,242 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// --- the experts' products ---------------------------------------------------------
+
+// A contiguous int32 tensor on a GPU, of `count` elements where that is not negative.
+const at::Tensor* int32_tensor(PyObject* o, const char* what, int64_t count) {
+  const at::Tensor* t = gpu_tensor(o, what);
+  if (t == nullptr) return nullptr;
+  if (t->scalar_type() != at::kInt) return fail(PyExc_TypeError, "%s must be int32, not %s", what, c10::toString(t->scalar_type()));
+  if (!t->is_contiguous()) return fail(PyExc_ValueError, "%s must be contiguous", what);
+  if (count >= 0 && t->numel() != count)
+    return fail(PyExc_ValueError, "%s must hold %lld numbers, not %lld", what, static_cast<long long>(count),
+                static_cast<long long>(t->numel()));
+  return t;
+}
+
+// A bfloat16 matrix whose rows lie apart, each contiguous; `rows` and `cols` where
+// they are not negative.
+const at::Tensor* matrix(PyObject* o, const char* what, int64_t rows, int64_t cols, size_t* stride) {
+  const at::Tensor* t = gpu_tensor(o, what);
+  if (t == nullptr) return nullptr;
+  if (t->scalar_type() != at::kBFloat16)
+    return fail(PyExc_TypeError, "%s must be bfloat16, not %s", what, c10::toString(t->scalar_type()));
+  if (t->dim() != 2 || t->size(1) < 1) return fail(PyExc_ValueError, "%s must be a matrix with columns", what);
+  if ((rows >= 0 && t->size(0) != rows) || (cols >= 0 && t->size(1) != cols))
+    return fail(PyExc_ValueError, "%s must be [%lld, %lld], not [%lld, %lld]", what,
+                static_cast<long long>(rows >= 0 ? rows : t->size(0)), static_cast<long long>(cols >= 0 ? cols : t->size(1)),
+                static_cast<long long>(t->size(0)), static_cast<long long>(t->size(1)));
+  if (t->size(0) > 0 && ((t->size(1) > 1 && t->stride(1) != 1) || (t->size(0) > 1 && t->stride(0) < t->size(1))))
+    return fail(PyExc_ValueError, "a row of %s must lie next to each other, rows apart", what);
+  *stride = static_cast<size_t>(t->size(0) > 1 ? t->stride(0) : t->size(1));
+  return t;
+}
+
+// What expert_order found: (order, position, offsets, top_k).
+struct Order {
+  const at::Tensor *order, *position, *offsets;
+  int64_t pairs, tokens;
+  int experts, top_k;
+};
+
+bool check_order(PyObject* const* a, Order* o) {
+  const long k = PyLong_AsLong(a[3]);
+  if (k == -1 && PyErr_Occurred()) return false;
+  if ((o->order = int32_tensor(a[0], "order", -1)) == nullptr) return false;
+  o->pairs = o->order->numel();
+  if ((o->position = int32_tensor(a[1], "position", o->pairs)) == nullptr ||
+      (o->offsets = int32_tensor(a[2], "offsets", -1)) == nullptr)
+    return false;
+  if (k < 1 || k > INT32_MAX || o->pairs % k != 0 || o->offsets->numel() < 2 ||
+      o->offsets->numel() > AR_MAX_EXPERTS + 1 || o->position->device() != o->order->device() ||
+      o->offsets->device() != o->order->device()) {
+    fail(PyExc_ValueError, "this is not the order of top_k choices a token");
+    return false;
+  }
+  o->top_k = static_cast<int>(k);
+  o->tokens = o->pairs / k;
+  o->experts = static_cast<int>(o->offsets->numel() - 1);
+  return true;
+}
+
+bool same_device(const Order& o, std::initializer_list<const at::Tensor*> tensors) {
+  for (const at::Tensor* t : tensors)
+    if (t->device() != o.order->device()) {
+      fail(PyExc_ValueError, "all tensors must be on the order's device");
+      return false;
+    }
+  return true;
+}
+
+ar_expert_rows_t rows_of(const Order& o, const at::Tensor& x, size_t stride, bool gather, int64_t out) {
+  ar_expert_rows_t r;
+  r.x = x.const_data_ptr();
+  r.x_rows = static_cast<size_t>(x.size(0));
+  r.x_stride = stride;
+  r.order = gather ? static_cast<const int32_t*>(o.order->const_data_ptr()) : nullptr;
+  r.top_k = o.top_k;
+  r.offsets = static_cast<const int32_t*>(o.offsets->const_data_ptr());
+  r.pairs = static_cast<size_t>(o.pairs);
+  r.experts = o.experts;
+  r.in = static_cast<size_t>(x.size(1));
+  r.out = static_cast<size_t>(out);
+  r.dtype = AR_BFLOAT16;
+  return r;
+}
+
+// expert_order(indices, experts, stream) -> (status, order, position, offsets)
+PyObject* expert_order(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!arguments(n, 3)) return nullptr;
+  const at::Tensor* indices = int32_tensor(a[0], "indices", -1);
+  if (indices == nullptr) return nullptr;
+  const long experts = PyLong_AsLong(a[1]);
+  if (experts == -1 && PyErr_Occurred()) return nullptr;
+  if (experts < 1 || experts > AR_MAX_EXPERTS)
+    return fail(PyExc_ValueError, "experts must be 1 to %d, not %ld", AR_MAX_EXPERTS, experts);
+  if (indices->dim() < 1 || indices->size(-1) < 1)
+    return fail(PyExc_ValueError, "indices must be [..., top_k]");
+  const int64_t pairs = indices->numel();
+  const at::Tensor order = empty({pairs}, at::kInt), position = empty(indices->sizes(), at::kInt);
+  const at::Tensor offsets = empty({experts + 1}, at::kInt);
+  const size_t bytes = ar_expert_order_workspace(static_cast<size_t>(pairs), static_cast<int>(experts));
+  at::Tensor workspace;
+  if (bytes != 0) workspace = empty({static_cast<int64_t>(bytes)}, at::kByte);
+  const ar_status_t status = ar_expert_order(
+      static_cast<const int32_t*>(indices->const_data_ptr()), static_cast<size_t>(pairs), static_cast<int>(experts),
+      static_cast<int32_t*>(order.data_ptr()), static_cast<int32_t*>(position.data_ptr()),
+      static_cast<int32_t*>(offsets.data_ptr()), bytes != 0 ? workspace.data_ptr() : nullptr, stream_of(a[2]));
+  return result(status, {&order, &position, &offsets});
+  END_HANDLE_TH_ERRORS
+}
+
+// expert_matmul(x, weight, order, position, offsets, top_k, gather, stream) -> (status, y)
+PyObject* expert_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!arguments(n, 8)) return nullptr;
+  Order o;
+  if (!check_order(a + 2, &o)) return nullptr;
+  const int gather = PyObject_IsTrue(a[6]);
+  if (gather < 0) return nullptr;
+  size_t stride;
+  const at::Tensor* x = matrix(a[0], "x", gather ? o.tokens : o.pairs, -1, &stride);
+  if (x == nullptr) return nullptr;
+  const at::Tensor* w = gpu_tensor(a[1], "weight");
+  if (w == nullptr) return nullptr;
+  if (w->scalar_type() != at::kBFloat16)
+    return fail(PyExc_TypeError, "weight must be bfloat16, not %s", c10::toString(w->scalar_type()));
+  if (w->dim() != 3 || w->size(0) != o.experts || w->size(1) != x->size(1) || w->size(2) < 1)
+    return fail(PyExc_ValueError, "weight must be [%d experts, %lld, size]", o.experts,
+                static_cast<long long>(x->size(1)));
+  const int64_t in = w->size(1), out = w->size(2), si = w->stride(1), so = w->stride(2);
+  if (!((out == 1 || so == 1) && (in == 1 || si >= out)) && !((in == 1 || si == 1) && (out == 1 || so >= in)))
+    return fail(PyExc_ValueError, "an expert's rows or its columns must lie next to each other");
+  if (!same_device(o, {x, w})) return nullptr;
+  const ar_expert_rows_t rows = rows_of(o, *x, stride, gather, out);
+  const at::Tensor y = empty({o.pairs, out}, at::kBFloat16);
+  const ar_status_t status = ar_expert_matmul(&rows, w->const_data_ptr(), static_cast<size_t>(w->stride(0)),
+                                              static_cast<size_t>(si), static_cast<size_t>(so), y.data_ptr(),
+                                              stream_of(a[7]));
+  return result(status, {&y});
+  END_HANDLE_TH_ERRORS
+}
+
+// expert_weight_grad(x, dy, order, position, offsets, top_k, gather, wide, out, stream) -> (status, dw)
+PyObject* expert_weight_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!arguments(n, 10)) return nullptr;
+  Order o;
+  if (!check_order(a + 2, &o)) return nullptr;
+  const int gather = PyObject_IsTrue(a[6]), wide = PyObject_IsTrue(a[7]);
+  if (gather < 0 || wide < 0) return nullptr;
+  size_t stride, dy_stride;
+  const at::Tensor* x = matrix(a[0], "x", gather ? o.tokens : o.pairs, -1, &stride);
+  const at::Tensor* dy = x == nullptr ? nullptr : matrix(a[1], "dy", o.pairs, -1, &dy_stride);
+  if (dy == nullptr || !same_device(o, {x, dy})) return nullptr;
+  at::Tensor dw;
+  if (a[8] != Py_None) {
+    const at::Tensor* out = gpu_tensor(a[8], "out");
+    if (out == nullptr) return nullptr;
+    if (out->scalar_type() != at::kFloat && out->scalar_type() != at::kBFloat16)
+      return fail(PyExc_TypeError, "out must be float32 or bfloat16, not %s", c10::toString(out->scalar_type()));
+    if (out->dim() != 3 || out->size(0) != o.experts || out->size(1) != x->size(1) || out->size(2) != dy->size(1) ||
+        !out->is_contiguous())
+      return fail(PyExc_ValueError, "out must be contiguous, [%d, %lld, %lld]", o.experts,
+                  static_cast<long long>(x->size(1)), static_cast<long long>(dy->size(1)));
+    if (!same_device(o, {out})) return nullptr;
+    dw = *out;
+  } else {
+    dw = empty({o.experts, x->size(1), dy->size(1)}, wide ? at::kFloat : at::kBFloat16);
+  }
+  const ar_expert_rows_t rows = rows_of(o, *x, stride, gather, dy->size(1));
+  const ar_status_t status = ar_expert_weight_grad(&rows, dy->const_data_ptr(), dy_stride, dw.data_ptr(),
+                                                   dw.scalar_type() == at::kFloat ? AR_FLOAT32 : AR_BFLOAT16,
+                                                   stream_of(a[9]));
+  if (a[8] != Py_None && status == AR_SUCCESS && !dw.is_inference()) dw.unsafeGetTensorImpl()->bump_version();
+  return result(status, {&dw});
+  END_HANDLE_TH_ERRORS
+}
+
+// The weights of a token's choices, contiguous float32; false on an error.
+bool check_weights(PyObject* p, const Order& o, const float** at) {
+  const at::Tensor* t = gpu_tensor(p, "weights");
+  if (t == nullptr) return false;
+  if (t->scalar_type() != at::kFloat) {
+    fail(PyExc_TypeError, "weights must be float32, not %s", c10::toString(t->scalar_type()));
+    return false;
+  }
+  if (t->numel() != o.pairs || !t->is_contiguous()) {
+    fail(PyExc_ValueError, "weights must be contiguous, one for each of the %lld pairs", static_cast<long long>(o.pairs));
+    return false;
+  }
+  *at = static_cast<const float*>(t->const_data_ptr());
+  return same_device(o, {t});
+}
+
+// expert_combine(y, order, position, offsets, top_k, weights, stream) -> (status, out)
+PyObject* expert_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!arguments(n, 7)) return nullptr;
+  Order o;
+  if (!check_order(a + 1, &o)) return nullptr;
+  size_t stride;
+  const at::Tensor* y = matrix(a[0], "y", o.pairs, -1, &stride);
+  if (y == nullptr || !same_device(o, {y})) return nullptr;
+  const float* weights = nullptr;
+  if (a[5] != Py_None && !check_weights(a[5], o, &weights)) return nullptr;
+  const at::Tensor out = empty({o.tokens, y->size(1)}, at::kBFloat16);
+  const ar_status_t status = ar_expert_combine(
+      y->const_data_ptr(), stride, static_cast<size_t>(o.pairs), static_cast<size_t>(y->size(1)), AR_BFLOAT16,
+      static_cast<const int32_t*>(o.position->const_data_ptr()), weights, static_cast<size_t>(o.tokens), o.top_k,
+      out.data_ptr(), stream_of(a[6]));
+  return result(status, {&out});
+  END_HANDLE_TH_ERRORS
+}
+
+// expert_combine_grad(dout, y, order, position, offsets, top_k, weights, stream) -> (status, dy, dweights)
+PyObject* expert_combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!arguments(n, 8)) return nullptr;
+  Order o;
+  if (!check_order(a + 2, &o)) return nullptr;
+  size_t dout_stride, y_stride;
+  const at::Tensor* y = matrix(a[1], "y", o.pairs, -1, &y_stride);
+  const at::Tensor* dout = y == nullptr ? nullptr : matrix(a[0], "dout", o.tokens, y->size(1), &dout_stride);
+  if (dout == nullptr || !same_device(o, {y, dout})) return nullptr;
+  const float* weights = nullptr;
+  if (!check_weights(a[6], o, &weights)) return nullptr;
+  const at::Tensor dy = empty({o.pairs, y->size(1)}, at::kBFloat16);
+  const at::Tensor dweights = empty({o.tokens, o.top_k}, at::kFloat);
+  const ar_status_t status = ar_expert_combine_grad(
+      dout->const_data_ptr(), dout_stride, y->const_data_ptr(), y_stride, static_cast<size_t>(o.pairs),
+      static_cast<size_t>(y->size(1)), AR_BFLOAT16, static_cast<const int32_t*>(o.position->const_data_ptr()),
+      static_cast<const int32_t*>(o.offsets->const_data_ptr()), o.experts, weights, static_cast<size_t>(o.tokens),
+      o.top_k, dy.data_ptr(), static_cast<float*>(dweights.data_ptr()), stream_of(a[7]));
+  return result(status, {&dy, &dweights});
+  END_HANDLE_TH_ERRORS
+}
+
 // written(list): tells autograd that these tensors were written in place (their
 // version counters; tensors made in inference mode have none).
 PyObject* written(PyObject*, PyObject* list) {
@@ -276,6 +512,11 @@ PyMethodDef methods[] = {
     {"route", as_function(route), METH_FASTCALL, nullptr},
     {"route_grad", as_function(route_grad), METH_FASTCALL, nullptr},
     {"dequantize", as_function(dequantize), METH_FASTCALL, nullptr},
+    {"expert_order", as_function(expert_order), METH_FASTCALL, nullptr},
+    {"expert_matmul", as_function(expert_matmul), METH_FASTCALL, nullptr},
+    {"expert_weight_grad", as_function(expert_weight_grad), METH_FASTCALL, nullptr},
+    {"expert_combine", as_function(expert_combine), METH_FASTCALL, nullptr},
+    {"expert_combine_grad", as_function(expert_combine_grad), METH_FASTCALL, nullptr},
     {"written", written, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
