@@ -540,8 +540,8 @@ typedef struct {
  * expert_stride + k * in_stride + n * out_stride; one of in_stride and
  * out_stride is 1 and the other at least the size along the first.  With the
  * two sizes and strides exchanged this is also the gradient with respect to x's
- * rows.  AR_ERROR_UNSUPPORTED: another dtype, or 2^23 tiles of 128 x 128 or
- * more. */
+ * rows.  AR_ERROR_UNSUPPORTED: another dtype, or 2^23 tiles (of 16 x 64 to 128 x 256)
+ * or more. */
 ar_status_t ar_expert_matmul(const ar_expert_rows_t* rows, const void* weight,
                              size_t expert_stride, size_t in_stride, size_t out_stride, void* y,
                              hipStream_t stream);

@@ -163,33 +163,59 @@ def plan(ts, pd=F32, gd=F32):
 
 
 def head(image):
-    """The image's head: eight 32-bit words, then 64-bit sizes and offsets."""
-    small = (ctypes.c_uint32 * 8).from_buffer(image)
-    large = (ctypes.c_uint64 * 8).from_buffer(image, 32)
-    return dict(zip(("matrices", "chunks", "squares", "tiles", "side"), small[1:6])), \
-        dict(zip(("bytes", "workspace", "matrices_at", "chunks_at", "squares_at", "tiles_at"), large[:6]))
+    """The image's head: eleven 32-bit words, then 64-bit sizes and offsets."""
+    small = (ctypes.c_uint32 * 11).from_buffer(image)
+    large = (ctypes.c_uint64 * 9).from_buffer(image, 48)
+    return dict(zip(("matrices", "chunks", "squares", "polys", "tiles", "side", "square_side"), small[1:])), \
+        dict(zip(("bytes", "workspace", "matrices_at", "chunks_at", "squares_at", "polys_at", "tiles_at"), large))
 
 
 @pytest.mark.parametrize("shapes", [[(1, 1, 1)], [(3, 61, 100)], [(2, 0, 5), (1, 100, 61), (0, 4, 4)],
-                                    [(40, 300, 500)], [(1, 8192, 4096), (2, 129, 127)], [(1, 1, 4_000_000)]])
+                                    [(40, 300, 500)], [(1, 8192, 4096), (2, 129, 127)], [(1, 1, 4_000_000)], [(6, 1024, 1024), (3, 64, 512)]])
 def test_plan_covers_every_matrix_once(shapes):
     status, image = plan(tensors(shapes))
     assert status == OK
     small, large = head(image)
     live = [(r, c) for n, r, c in shapes for _ in range(n if r and c else 0)]
-    side = small["side"]
-    assert side in (64, 128) and small["matrices"] == len(live)
+    side, square = small["side"], small["square_side"]
+    assert side in (64, 128) and side % square == 0 and square in (64, 128) and small["matrices"] == len(live)
     read = lambda where, n: (ctypes.c_uint32 * (2 * n)).from_buffer(image, large[where])  # noqa: E731
     chunks = read("chunks_at", small["chunks"])
     assert [(chunks[2 * i], chunks[2 * i + 1]) for i in range(small["chunks"])] == \
         [(i, j) for i, (r, c) in enumerate(live) for j in range(-(-r * c // 8192))]
-    unpack = lambda where, n: [(w[2 * i], w[2 * i + 1] & 0xFFFF, w[2 * i + 1] >> 16)  # noqa: E731
-                               for w in [read(where, n)] for i in range(n)]
+
+    def unpack(where, n, steps):
+        """The tiles of a table, each once; its parts cover its steps."""
+        words = (ctypes.c_uint32 * (8 * n)).from_buffer(image, large[where])
+        parts = {}
+        for i in range(n):
+            matrix, at, first, count, part, of, slot, counter = words[8 * i:8 * i + 8]
+            if matrix != 2 ** 32 - 1:
+                parts.setdefault((matrix, at & 0xFFFF, at >> 16), []).append((part, of, first, count, slot, counter))
+        for (matrix, _, _), p in parts.items():
+            p.sort()
+            assert [q[0] for q in p] == list(range(p[0][1])) and all(q[1] == len(p) <= 8 for q in p)
+            assert [q[2] for q in p] == [sum(r[3] for r in p[:i]) for i in range(len(p))]
+            assert sum(q[3] for q in p) == steps(matrix) and len({q[4:] for q in p}) == 1 and min(q[3] for q in p) > 0
+        split = [p[0] for p in parts.values() if len(p) > 1]
+        assert len({q[5] for q in split}) == len(split)               # a counter each, and sums apart
+        taken = [s for q in split for s in range(q[4], q[4] + q[1])]
+        assert len(set(taken)) == len(taken)
+        return list(parts)
+
     size = [tuple(-(-s // side) for s in (min(m), max(m))) for m in live]
-    assert sorted(unpack("tiles_at", small["tiles"])) == \
+    short = lambda i: size[i][0] * side // 32  # noqa: E731
+    assert sorted(unpack("tiles_at", small["tiles"], short)) == \
         [(i, a, b) for i, (h, w) in enumerate(size) for a in range(h) for b in range(w)]
-    assert sorted(unpack("squares_at", small["squares"])) == \
-        [(i, a, b) for i, (h, _) in enumerate(size) for a in range(h) for b in range(a, h)]
+    assert sorted(unpack("squares_at", small["squares"], lambda i: size[i][1] * side // 32)) == \
+        sorted(unpack("polys_at", small["polys"], short)) == \
+        [(i, a, b) for i, (h, _) in enumerate(size) for a in range(h * side // square) for b in range(a, h * side // square)]
+    # no XCD (entries 8 apart) has much more to do than another
+    if len(live) > 1:
+        for where, n in (("tiles_at", small["tiles"]), ("squares_at", small["squares"]), ("polys_at", small["polys"])):
+            words = list((ctypes.c_uint32 * (8 * n)).from_buffer(image, large[where]))
+            of = [sum(w != 2 ** 32 - 1 for w in words[8 * x::64]) for x in range(8)]
+            assert max(of) * 8 == n and (len(set(size)) > 1 or min(of) >= max(of) - 32)
     assert large["workspace"] >= sum(8 * h * w * side ** 2 + 8 * h * h * side ** 2 for h, w in size)
     assert ar.lib().ar_muon_workspace(image) == large["workspace"]
 

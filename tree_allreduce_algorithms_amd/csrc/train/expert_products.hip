@@ -8,8 +8,12 @@
 namespace ar {
 namespace {
 
+// Eight elements of 16 bits, four of 32, at any element's address.
 struct __attribute__((packed, aligned(2))) Chunk {
   u32x4 v;
+};
+struct __attribute__((packed, aligned(4))) Four {
+  f32x4 v;
 };
 
 __device__ __forceinline__ uint32_t clamped(int32_t x, uint32_t lo, uint32_t hi) {
@@ -39,53 +43,61 @@ __device__ __forceinline__ uint32_t two_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, t);
 }
 
-constexpr int kTileM = 128, kTileN = 128, kWavesM = 2, kWavesN = 2;
-constexpr int kThreads = kWavesM * kWavesN * kWave;
-constexpr int kPartM = kTileM / kWavesM / 16, kPartN = kTileN / kWavesN / 16;
+// Rows and columns of a block's tile, its waves along each, the k of a step, the
+// waves on a SIMD and the steps in LDS.
+template <int M_, int N_, int WAVES_M, int WAVES_N, int STEP_, int PER_SIMD, int STAGES_> struct Tile {
+  static constexpr int M = M_, N = N_, STEP = STEP_, kPerSimd = PER_SIMD, STAGES = STAGES_;
+  static constexpr int kThreads = WAVES_M * WAVES_N * kWave;
+  static constexpr int kPartM = M / WAVES_M, kPartN = N / WAVES_N;      // of a wave
+  static constexpr int kM = kPartM / 16, kN = kPartN / 16;
+  static __device__ __forceinline__ int row0(int wave) { return wave / WAVES_N * kPartM; }
+  static __device__ __forceinline__ int column0(int wave) { return wave % WAVES_N * kPartN; }
+};
+// Two blocks of eight waves on a CU.  131,072 x 1,024 by k = 2,048: 1,099 TFLOP/s;
+// 128 x 128 976; 256 x 256 1,120, but an expert's last rows fill 128 more often.
+// Weights come from HBM, each expert's for a few tiles only, so products keep two
+// steps under way: 131,072 pairs of 128 experts 695 us instead of 712, 8,192 of 64
+// 75 instead of 79.
+using Large = Tile<128, 256, 2, 4, 32, 4, 3>;
+using LargeGrad = Tile<128, 256, 2, 4, 32, 4, 2>;
+using Middle = Tile<128, 128, 2, 2, 64, 2, 2>;
+using Small = Tile<64, 128, 2, 2, 64, 3, 2>;
+
+__device__ __forceinline__ uint32_t token_of(const TokenOf& t, uint32_t pair) {
+  if (t.top_k == 1) return pair;
+  return t.reciprocal != 0 ? __umulhi(pair, t.reciprocal) : pair / t.top_k;
+}
+
+constexpr uint32_t kXcds = 8;
 
 // Blocks come to the XCDs in turn; of `n` tiles in order each XCD gets
 // neighbours, which share operands in its L2.
 __device__ __forceinline__ uint32_t near_tile(uint32_t block, uint32_t n) {
-  constexpr uint32_t kXcds = 8;
   const uint32_t x = block % kXcds;
   return x * (n / kXcds) + min(x, n % kXcds) + block / kXcds;
 }
 
 // --- products ----------------------------------------------------------------------
 
-// The expert and the row tile of unit `id`, when the experts' pairs (and those
-// without one, as a last group) are cut into tiles of kTileM rows; `total` of
-// them.  Every lane has some neighbouring groups.
-struct Unit {
-  int expert;
-  uint32_t lo, hi;      // rows of the tile
+// A block's part: rows [m0, hi) of expert e, columns from n0.
+struct Part {
+  int e;
+  uint32_t m0, hi, n0;
 };
 
-__device__ __forceinline__ uint32_t tiles_of(const ProductArgs& a, int e) {
-  uint32_t lo, hi;
-  rows_of(a.offsets, a.experts, e, a.pairs, &lo, &hi);
-  return (hi - lo + kTileM - 1) / kTileM;
-}
-
-// y_i = x_t(i) W_e(i) for the rows of an expert; 0 for rows without one.
-//
-// A block has kTileM rows of one expert and kTileN columns.  The grid is cut
-// for any distribution of the pairs (the counts stay on the GPU): each block
-// finds its tile from the experts' beginnings, and blocks past the last end.
-template <bool BR, bool DIRECT>
-__global__ __launch_bounds__(kThreads, 2) void expert_product(ProductArgs a) {
-  using SA = Staged<kTileM, false>;
-  using SB = Staged<kTileN, BR>;
-  constexpr int kStage = SA::kBytes + SB::kBytes;
-  constexpr int kLoadsA = SA::kChunks / kThreads, kLoadsB = SB::kChunks / kThreads;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
-  const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-
-  // the tile
-  const int groups = a.experts + 1, each = (groups + kWave - 1) / kWave;
+// Cuts the experts' pairs (and those without one, as a last group) into tiles of
+// M rows and gives the block its one; false for blocks past the last.  Every
+// lane counts some neighbouring groups.
+template <int M, int N> __device__ __forceinline__ bool part_of(const ProductArgs& a, Part* part) {
+  const int lane = threadIdx.x % kWave, groups = a.experts + 1, each = (groups + kWave - 1) / kWave;
+  const auto tiles = [&](int e) {
+    uint32_t lo, hi;
+    rows_of(a.offsets, a.experts, e, a.pairs, &lo, &hi);
+    return (hi - lo + M - 1) / M;
+  };
   uint32_t mine = 0;
   for (int i = 0; i < each; ++i)
-    if (lane * each + i < groups) mine += tiles_of(a, lane * each + i);
+    if (lane * each + i < groups) mine += tiles(lane * each + i);
   uint32_t upto = mine;
 #pragma unroll
   for (int d = 1; d < kWave; d *= 2) {
@@ -93,213 +105,365 @@ __global__ __launch_bounds__(kThreads, 2) void expert_product(ProductArgs a) {
     if (lane >= d) upto += up;
   }
   const uint64_t total = static_cast<uint64_t>(__shfl(upto, kWave - 1)) * a.tiles_n;
-  if (blockIdx.x >= total) return;
-  const uint32_t tile = near_tile(blockIdx.x, static_cast<uint32_t>(total));
-  const uint32_t unit = tile / a.tiles_n, n0 = tile % a.tiles_n * kTileN;
+  if (blockIdx.x >= total) return false;
+  const uint32_t tile = near_tile(blockIdx.x, static_cast<uint32_t>(total)), unit = tile / a.tiles_n;
   const int owner = __popcll(__ballot(upto <= unit));
   uint32_t rest = unit - __shfl(upto - mine, owner);
   int e = owner * each;
-  for (uint32_t n; rest >= (n = tiles_of(a, e)); ++e) rest -= n;
-  e = __builtin_amdgcn_readfirstlane(e);
+  for (uint32_t n; rest >= (n = tiles(e)); ++e) rest -= n;
   uint32_t lo, hi;
   rows_of(a.offsets, a.experts, e, a.pairs, &lo, &hi);
-  const uint32_t m0 = __builtin_amdgcn_readfirstlane(lo + rest * kTileM);
-  hi = __builtin_amdgcn_readfirstlane(hi);
+  part->e = __builtin_amdgcn_readfirstlane(e);
+  part->m0 = __builtin_amdgcn_readfirstlane(lo + rest * M);
+  part->hi = __builtin_amdgcn_readfirstlane(hi);
+  part->n0 = tile % a.tiles_n * N;
+  return true;
+}
 
-  f32x4 acc[kPartM][kPartN];
-#pragma unroll
-  for (auto& row : acc)
-#pragma unroll
-    for (auto& x : row) x = f32x4{0, 0, 0, 0};
-
-  const int steps = e < a.experts ? static_cast<int>((a.in + kStep - 1) / kStep) : 0;
-  const int wave_m = wave / kWavesN * (kTileM / kWavesM), wave_n = wave % kWavesN * (kTileN / kWavesN);
-  const uint16_t* x = static_cast<const uint16_t*>(a.x);
-  const uint16_t* w = static_cast<const uint16_t*>(a.w) + (e < a.experts ? e * a.w_expert : 0);
-
-  // the thread's chunks of a step: the rows of x that they come from, kNowhere for none
-  uint32_t row[kLoadsA], at[kLoadsA], col[kLoadsB], line[kLoadsB];
-#pragma unroll
-  for (int j = 0; j < kLoadsA; ++j) {
-    const int slot = j * kThreads + tid, l = slot / SA::kPerLine;
-    const uint32_t r = m0 + l;
-    row[j] = kNowhere;
-    at[j] = SA::place(l, slot % SA::kPerLine) * 8;
-    if (steps > 0 && r < hi) {
-      uint32_t t = r;
-      if (a.order != nullptr) t = static_cast<uint32_t>(a.order[r]) / static_cast<uint32_t>(a.top_k);
-      if (t < a.x_rows) row[j] = t;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kLoadsB; ++j) {
-    const int slot = j * kThreads + tid, l = slot / SB::kPerLine;
-    line[j] = l;
-    col[j] = SB::place(l, slot % SB::kPerLine) * 8;
-  }
-  // elements of a chunk that lie in the operands
-  const auto left_a = [&](int j, uint32_t k) {
-    return row[j] == kNowhere || k + at[j] >= a.in ? 0 : static_cast<int>(min(a.in - k - at[j], 8u));
-  };
-  const auto left_b = [&](int j, uint32_t k) {
-    const uint32_t kk = BR ? k + line[j] : k + col[j], n = BR ? n0 + col[j] : n0 + line[j];
-    if (kk >= a.in || n >= a.out) return 0;
-    return static_cast<int>(min(BR ? a.out - n : a.in - kk, 8u));
-  };
-
-  if (DIRECT) {
-    const Source from_x(x), from_w(w);
-    const uint32_t base = lds_address(lds) + wave * (kWave * 16);
-    const uint32_t x_bytes = static_cast<uint32_t>(a.x_stride) * 2, w_bytes = static_cast<uint32_t>(a.w_line) * 2;
-    const auto issue = [&](int step) {
-      const uint32_t to = base + (step & 1) * kStage, k = step * kStep;
-#pragma unroll
-      for (int j = 0; j < kLoadsA; ++j)
-        load_to_lds(from_x, left_a(j, k) ? row[j] * x_bytes + (k + at[j]) * 2 : kNowhere,
-                    __builtin_amdgcn_readfirstlane(to + j * kThreads * 16));
-#pragma unroll
-      for (int j = 0; j < kLoadsB; ++j)
-        load_to_lds(from_w,
-                    left_b(j, k) ? (BR ? (k + line[j]) * w_bytes + (n0 + col[j]) * 2
-                                       : (n0 + line[j]) * w_bytes + (k + col[j]) * 2)
-                                 : kNowhere,
-                    __builtin_amdgcn_readfirstlane(to + SA::kBytes + j * kThreads * 16));
-    };
-    if (steps > 0) issue(0);
-    for (int s = 0; s < steps; ++s) {
-      settled();
-      __builtin_amdgcn_s_barrier();
-      if (s + 1 < steps) issue(s + 1);
-      const char* stage = lds + (s & 1) * kStage;
-      multiply_step<kPartM, kPartN, bf16x8, 1, SA, SB>(stage, stage + SA::kBytes, wave_m, wave_n, lane, acc);
-    }
+// Up to 16 bytes of a row from column n on (of `size`), PAST the caches or not.
+template <bool PAST>
+__device__ __forceinline__ void write_values(uint16_t* row, uint32_t n, uint32_t size, f32x4 lo, f32x4 hi) {
+  const u32x4 r = {two_bf16(lo[0], lo[1]), two_bf16(lo[2], lo[3]), two_bf16(hi[0], hi[1]), two_bf16(hi[2], hi[3])};
+  if (n + 8 <= size) {
+    if (PAST)
+      __builtin_nontemporal_store(r, &reinterpret_cast<Chunk*>(row + n)->v);
+    else
+      reinterpret_cast<Chunk*>(row + n)->v = r;
   } else {
-    u32x4 ra[kLoadsA], rb[kLoadsB];
-    const auto load = [&](int step) {
-      const uint32_t k = step * kStep;
 #pragma unroll
-      for (int j = 0; j < kLoadsA; ++j) ra[j] = read_elements(x + row[j] * a.x_stride + k + at[j], left_a(j, k));
-#pragma unroll
-      for (int j = 0; j < kLoadsB; ++j)
-        rb[j] = read_elements(BR ? w + (k + line[j]) * a.w_line + n0 + col[j] : w + (n0 + line[j]) * a.w_line + k + col[j],
-                              left_b(j, k));
-    };
-    if (steps > 0) load(0);
-    for (int s = 0; s < steps; ++s) {
-      char* stage = lds + (s & 1) * kStage;
-#pragma unroll
-      for (int j = 0; j < kLoadsA; ++j) *reinterpret_cast<u32x4*>(stage + (j * kThreads + tid) * 16) = ra[j];
-#pragma unroll
-      for (int j = 0; j < kLoadsB; ++j)
-        *reinterpret_cast<u32x4*>(stage + SA::kBytes + (j * kThreads + tid) * 16) = rb[j];
-      __syncthreads();
-      if (s + 1 < steps) load(s + 1);
-      multiply_step<kPartM, kPartN, bf16x8, 1, SA, SB>(stage, stage + SA::kBytes, wave_m, wave_n, lane, acc);
-    }
+    for (int q = 0; q < 8; ++q)
+      if (n + q < size) row[n + q] = static_cast<uint16_t>(r[q / 2] >> (16 * (q % 2)));
   }
+}
+template <bool PAST>
+__device__ __forceinline__ void write_values(float* row, uint32_t n, uint32_t size, f32x4 v) {
+  if (n + 4 <= size) {
+    if (PAST)
+      __builtin_nontemporal_store(v, &reinterpret_cast<Four*>(row + n)->v);
+    else
+      reinterpret_cast<Four*>(row + n)->v = v;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (n + q < size) row[n + q] = v[q];
+  }
+}
 
+// Stores a wave's part, kM x kN fragments from row m0 and column n0 on, of a
+// matrix of `rows` x `size`.  Each 16 rows go through LDS (the wave's own
+// kTurnBytes), so that neighbouring lanes store neighbouring pieces: whole cache
+// lines at a time, which the caches need not hold (PAST).  The weights' gradient
+// of 8,192 pairs of 64 experts, 1,024 x 2,048: 205 us with each lane storing what
+// it has, 150 so, 124 past the caches.
+constexpr int kTurnPitch = 64 + 4;
+constexpr int kTurnBytes = 16 * kTurnPitch * sizeof(float);
+
+template <bool PAST, int TM, int TN, class OUT>
+__device__ __forceinline__ void write_part(const f32x4 (&acc)[TM][TN], float* turn, OUT* to, uint32_t m0, uint32_t rows,
+                                           uint32_t n0, uint32_t size, int lane) {
+  constexpr int kEach = 16 / sizeof(OUT), kLanes = 64 / kEach;      // values a lane, lanes a row
 #pragma unroll
-  for (int i = 0; i < kPartM; ++i) {
-    const uint32_t r = m0 + wave_m + 16 * i + lane % 16;
-    if (r >= hi) continue;
-    uint16_t* y = static_cast<uint16_t*>(a.y) + static_cast<uint64_t>(r) * a.out;
+  for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < kPartN; ++j) {
-      const uint32_t n = n0 + wave_n + 16 * j + 4 * (lane / 16);
-      if (n >= a.out) continue;
-      const uint2 v = {two_bf16(acc[i][j][0], acc[i][j][1]), two_bf16(acc[i][j][2], acc[i][j][3])};
-      if (a.vec) {
-        *reinterpret_cast<uint2*>(y + n) = v;
-      } else {
-        const uint32_t part[4] = {v.x & 0xffff, v.x >> 16, v.y & 0xffff, v.y >> 16};
+    for (int group = 0; group < TN / 4; ++group) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (n + q < a.out) y[n + q] = static_cast<uint16_t>(part[q]);
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<f32x4*>(turn + lane % 16 * kTurnPitch + 16 * (lane / 16) + 4 * j) = acc[i][4 * group + j];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int r0 = 0; r0 < 16; r0 += kWave / kLanes) {
+        const int r = r0 + lane / kLanes, c = lane % kLanes * kEach;
+        const uint32_t m = m0 + 16 * i + r, n = n0 + 64 * group + c;
+        const f32x4* v = reinterpret_cast<const f32x4*>(turn + r * kTurnPitch + c);
+        if (m < rows && n < size) {
+          OUT* row = to + static_cast<uint64_t>(m) * size;
+          if constexpr (sizeof(OUT) == 2)
+            write_values<PAST>(row, n, size, v[0], v[1]);
+          else
+            write_values<PAST>(row, n, size, v[0]);
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
+// A thread's chunks of the steps of a product: where they come from in x and in
+// the expert's matrix, and how much of each lies in them.  Chunk j of thread t is
+// slot j * T::kThreads + t of the step.
+template <class T, class SA, class SB, bool BR> struct Operands {
+  static constexpr int kA = SA::kChunks / T::kThreads, kB = SB::kChunks / T::kThreads;
+  uint32_t row[kA], at[kA];       // kNowhere for no row; first k of a step
+  uint32_t line[kB], first[kB];   // line of a step, first element along it
+  uint32_t n0;
+
+  __device__ __forceinline__ Operands(const ProductArgs& a, const Part& p, int thread) : n0(p.n0) {
+#pragma unroll
+    for (int j = 0; j < kA; ++j) {
+      const int slot = j * T::kThreads + thread, l = slot / SA::kPerLine;
+      const uint32_t r = p.m0 + l;
+      row[j] = kNowhere;
+      at[j] = SA::place(l, slot % SA::kPerLine) * 8;
+      if (p.e < a.experts && r < p.hi) {
+        const uint32_t t = a.order == nullptr ? r : token_of(a.token, static_cast<uint32_t>(a.order[r]));
+        if (t < a.x_rows) row[j] = t;
       }
     }
+#pragma unroll
+    for (int j = 0; j < kB; ++j) {
+      const int slot = j * T::kThreads + thread;
+      line[j] = slot / SB::kPerLine;
+      first[j] = SB::place(line[j], slot % SB::kPerLine) * 8;
+    }
   }
+  // elements of chunk j, from k on, that lie in the operand
+  __device__ __forceinline__ int left_a(const ProductArgs& a, int j, uint32_t k) const {
+    return row[j] == kNowhere || k + at[j] >= a.in ? 0 : static_cast<int>(min(a.in - k - at[j], 8u));
+  }
+  __device__ __forceinline__ int left_b(const ProductArgs& a, int j, uint32_t k) const {
+    const uint32_t kk = k + (BR ? line[j] : first[j]), n = n0 + (BR ? first[j] : line[j]);
+    if (kk >= a.in || n >= a.out) return 0;
+    return static_cast<int>(min(BR ? a.out - n : a.in - kk, 8u));
+  }
+  // straight to LDS: `to` is the wave's first chunk of the step, the waves' chunks
+  // of one j follow one another
+  __device__ __forceinline__ void issue(const ProductArgs& a, const Source& x, const Source& w, int step,
+                                        char* to) const {
+    const uint32_t k = step * T::STEP, lds = lds_address(to);
+    const uint32_t x_bytes = static_cast<uint32_t>(a.x_stride) * 2, w_bytes = static_cast<uint32_t>(a.w_line) * 2;
+#pragma unroll
+    for (int j = 0; j < kA; ++j)
+      load_to_lds(x, left_a(a, j, k) ? row[j] * x_bytes + (k + at[j]) * 2 : kNowhere,
+                  __builtin_amdgcn_readfirstlane(lds + j * T::kThreads * 16));
+#pragma unroll
+    for (int j = 0; j < kB; ++j) {
+      const uint32_t at_line = BR ? k + line[j] : n0 + line[j], along = BR ? n0 + first[j] : k + first[j];
+      load_to_lds(w, left_b(a, j, k) ? at_line * w_bytes + along * 2 : kNowhere,
+                  __builtin_amdgcn_readfirstlane(lds + SA::kBytes + j * T::kThreads * 16));
+    }
+  }
+  // through registers
+  struct Held {
+    u32x4 a[kA], b[kB];
+  };
+  __device__ __forceinline__ void load(const ProductArgs& a, const uint16_t* w, int step, Held* h) const {
+    const uint32_t k = step * T::STEP;
+    const uint16_t* x = static_cast<const uint16_t*>(a.x);
+#pragma unroll
+    for (int j = 0; j < kA; ++j) h->a[j] = read_elements(x + row[j] * a.x_stride + k + at[j], left_a(a, j, k));
+#pragma unroll
+    for (int j = 0; j < kB; ++j) {
+      const uint64_t at_line = BR ? k + line[j] : n0 + line[j];
+      h->b[j] = read_elements(w + at_line * a.w_line + (BR ? n0 : k) + first[j], left_b(a, j, k));
+    }
+  }
+  __device__ __forceinline__ void put(const Held& h, char* stage, int thread) const {
+#pragma unroll
+    for (int j = 0; j < kA; ++j) *reinterpret_cast<u32x4*>(stage + (j * T::kThreads + thread) * 16) = h.a[j];
+#pragma unroll
+    for (int j = 0; j < kB; ++j)
+      *reinterpret_cast<u32x4*>(stage + SA::kBytes + (j * T::kThreads + thread) * 16) = h.b[j];
+  }
+};
+
+// y_i = x_t(i) W_e(i) for the rows of an expert; 0 for rows without one.
+//
+// A block has T::M rows of one expert and T::N columns.  The grid is cut for any
+// distribution of the pairs (the counts stay on the GPU): each block finds its
+// tile from the experts' beginnings, and blocks past the last end.  BR: the
+// columns of W are contiguous.  DIRECT: all rows are in 16-byte pieces, which go
+// straight to LDS; otherwise they go through registers, element by element only
+// at their ends.
+template <class T, bool BR, bool DIRECT, bool PAST>
+__global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_product(ProductArgs a) {
+  using SA = Staged<T::M, false, T::STEP, false>;
+  using SB = Staged<T::N, BR, T::STEP, true>;
+  constexpr int kStage = SA::kBytes + SB::kBytes;
+  __shared__ __attribute__((aligned(1024))) char lds[T::STAGES * kStage];
+  const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  Part p;
+  if (!part_of<T::M, T::N>(a, &p)) return;
+  f32x4 acc[T::kM][T::kN];
+  clear(acc);
+  const int steps = p.e < a.experts ? static_cast<int>((a.in + T::STEP - 1) / T::STEP) : 0;
+  const uint16_t* w = static_cast<const uint16_t*>(a.w) + (p.e < a.experts ? p.e * a.w_expert : 0);
+  const Operands<T, SA, SB, BR> from(a, p, tid);
+  char* const mine = lds + wave * (kWave * 16);
+  if (DIRECT) {
+    const Source sx(a.x), sw(w);
+    constexpr int kAhead = T::STAGES - 1, kLoads = from.kA + from.kB;
+    if (steps > 0)
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) from.issue(a, sx, sw, s, mine + s * kStage);
+    for (int s = 0; s < steps; ++s) {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kAhead - 1) * kLoads) : "memory");
+      __builtin_amdgcn_s_barrier();
+      from.issue(a, sx, sw, s + kAhead, mine + (s + kAhead) % T::STAGES * kStage);
+      const char* stage = lds + s % T::STAGES * kStage;
+      multiply_step<T::kM, T::kN, bf16x8, 1, T::STEP, SA, SB>(stage, stage + SA::kBytes, T::row0(wave),
+                                                              T::column0(wave), lane, acc);
+    }
+    settled();
+  } else {
+    typename Operands<T, SA, SB, BR>::Held held;
+    if (steps > 0) from.load(a, w, 0, &held);
+    for (int s = 0; s < steps; ++s) {
+      char* stage = lds + (s & 1) * kStage;
+      from.put(held, stage, tid);
+      __syncthreads();
+      if (s + 1 < steps) from.load(a, w, s + 1, &held);
+      multiply_step<T::kM, T::kN, bf16x8, 1, T::STEP, SA, SB>(stage, stage + SA::kBytes, T::row0(wave),
+                                                              T::column0(wave), lane, acc);
+    }
+  }
+  __syncthreads();
+  static_assert(T::kThreads / kWave * kTurnBytes <= T::STAGES * kStage);
+  write_part<PAST>(acc, reinterpret_cast<float*>(lds + wave * kTurnBytes), static_cast<uint16_t*>(a.y), p.m0 + T::row0(wave),
+             p.hi, p.n0 + T::column0(wave), a.out, lane);
+}
+
+// The same for few rows: 16 of them and 64 columns a block, whose waves share the
+// k out among themselves, each with steps of its own in LDS and no barrier, and
+// add up their sums in the waves' order at the end.  What binds is the reading of
+// the weights; a block has 40 KB of them under way.
+using Thin = Tile<16, 64, 1, 1, 64, 2, 2>;
+constexpr int kThinWaves = 4, kThinThreads = kThinWaves * kWave;
+
+template <bool BR, bool DIRECT>
+__global__ __launch_bounds__(kThinThreads, 2) void expert_product_thin(ProductArgs a) {
+  using T = Thin;
+  using SA = Staged<T::M, false, T::STEP, false>;
+  using SB = Staged<T::N, BR, T::STEP, true>;
+  constexpr int kStage = SA::kBytes + SB::kBytes;
+  constexpr int kLoads = SA::kChunks / kWave + SB::kChunks / kWave;
+  __shared__ __attribute__((aligned(1024))) char lds[kThinWaves * 2 * kStage];
+  const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  Part p;
+  if (!part_of<T::M, T::N>(a, &p)) return;
+  f32x4 acc[1][T::kN];
+  clear(acc);
+  const int steps = p.e < a.experts ? static_cast<int>((a.in + T::STEP - 1) / T::STEP) : 0;
+  const uint16_t* w = static_cast<const uint16_t*>(a.w) + (p.e < a.experts ? p.e * a.w_expert : 0);
+  const Operands<T, SA, SB, BR> from(a, p, lane);
+  char* const mine = lds + wave * (2 * kStage);
+  if (DIRECT) {
+    const Source sx(a.x), sw(w);
+    if (wave < steps) from.issue(a, sx, sw, wave, mine);
+    int buffer = 0;
+    for (int s = wave; s < steps; s += kThinWaves, buffer ^= 1) {
+      // the other buffer's reads are done; this one's loads are the older ones
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (s + kThinWaves < steps) {
+        from.issue(a, sx, sw, s + kThinWaves, mine + (buffer ^ 1) * kStage);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+      } else {
+        settled();
+      }
+      const char* stage = mine + buffer * kStage;
+      multiply_step<1, T::kN, bf16x8, 1, T::STEP, SA, SB>(stage, stage + SA::kBytes, 0, 0, lane, acc);
+    }
+  } else {
+    typename Operands<T, SA, SB, BR>::Held held;
+    if (wave < steps) from.load(a, w, wave, &held);
+    for (int s = wave; s < steps; s += kThinWaves) {
+      from.put(held, mine, lane);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (s + kThinWaves < steps) from.load(a, w, s + kThinWaves, &held);
+      multiply_step<1, T::kN, bf16x8, 1, T::STEP, SA, SB>(mine, mine + SA::kBytes, 0, 0, lane, acc);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+  }
+  // every wave's sums where its steps were: four lanes' worth of columns a row
+  f32x4(*sums)[T::kN][kWave] = reinterpret_cast<f32x4(*)[T::kN][kWave]>(lds);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < T::kN; ++j) sums[wave][j][lane] = acc[0][j];
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int j = 0; j < T::kN; ++j) {
+    acc[0][j] = sums[0][j][lane];
+#pragma unroll
+    for (int v = 1; v < kThinWaves; ++v) acc[0][j] += sums[v][j][lane];
+  }
+  write_part<false>(acc, reinterpret_cast<float*>(lds + 2 * kThinWaves * kStage - kTurnBytes), static_cast<uint16_t*>(a.y), p.m0,
+             p.hi, p.n0, a.out, lane);
 }
 
 // --- the weights' gradient ------------------------------------------------------------
 
 // dW_e = sum over the rows i of expert e of x_t(i)^T dy_i: a block has a tile of
-// one expert's matrix and goes over the expert's rows, 64 at a time.  An expert
-// without rows gets zeros.
-template <bool WIDE, bool DIRECT>
-__global__ __launch_bounds__(kThreads, 2) void expert_weight_grad(WeightGradArgs a) {
-  using SA = Staged<kTileM, true>;
-  using SB = Staged<kTileN, true>;
+// one expert's matrix and goes over the expert's rows, a step's at a time.  An
+// expert without rows gets zeros.
+//
+// A tile costs what its expert has rows, so every XCD gets a part of each
+// expert's tiles (neighbours, of the same rows of dW).
+template <class T, class OUT, bool DIRECT, bool PAST>
+__global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(WeightGradArgs a) {
+  using SA = Staged<T::M, true, T::STEP, false>;
+  using SB = Staged<T::N, true, T::STEP, true>;
   constexpr int kStage = SA::kBytes + SB::kBytes;
-  constexpr int kLoadsA = SA::kChunks / kThreads, kLoadsB = SB::kChunks / kThreads;
+  constexpr int kA = SA::kChunks / T::kThreads, kB = SB::kChunks / T::kThreads;
   __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const uint32_t tile = near_tile(blockIdx.x, gridDim.x), of_expert = a.tiles_m * a.tiles_n;
-  const int e = tile / of_expert;
-  const uint32_t m0 = tile % of_expert / a.tiles_n * kTileM, n0 = tile % a.tiles_n * kTileN;
+  const uint32_t turn = blockIdx.x / kXcds, e = turn / a.tiles_xcd;
+  const uint32_t tile = (blockIdx.x + e) % kXcds * a.tiles_xcd + turn % a.tiles_xcd;
+  if (tile >= a.tiles) return;
+  const uint32_t m0 = tile / a.tiles_n * T::M, n0 = tile % a.tiles_n * T::N;
   uint32_t lo, hi;
   rows_of(a.offsets, a.experts, e, a.pairs, &lo, &hi);
   lo = __builtin_amdgcn_readfirstlane(lo);
   hi = __builtin_amdgcn_readfirstlane(hi);
-  const int steps = static_cast<int>((hi - lo + kStep - 1) / kStep);
+  const int steps = static_cast<int>((hi - lo + T::STEP - 1) / T::STEP);
+  f32x4 acc[T::kM][T::kN];
+  clear(acc);
 
-  f32x4 acc[kPartM][kPartN];
+  uint32_t line_a[kA], col_a[kA], line_b[kB], col_b[kB];
 #pragma unroll
-  for (auto& row : acc)
-#pragma unroll
-    for (auto& x : row) x = f32x4{0, 0, 0, 0};
-
-  const int wave_m = wave / kWavesN * (kTileM / kWavesM), wave_n = wave % kWavesN * (kTileN / kWavesN);
-  const uint16_t* x = static_cast<const uint16_t*>(a.x);
-  const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
-  uint32_t line_a[kLoadsA], col_a[kLoadsA], line_b[kLoadsB], col_b[kLoadsB], token[kLoadsA];
-#pragma unroll
-  for (int j = 0; j < kLoadsA; ++j) {
-    const int slot = j * kThreads + tid;
+  for (int j = 0; j < kA; ++j) {
+    const int slot = j * T::kThreads + tid;
     line_a[j] = slot / SA::kPerLine;
     col_a[j] = m0 + SA::place(line_a[j], slot % SA::kPerLine) * 8;
   }
 #pragma unroll
-  for (int j = 0; j < kLoadsB; ++j) {
-    const int slot = j * kThreads + tid;
+  for (int j = 0; j < kB; ++j) {
+    const int slot = j * T::kThreads + tid;
     line_b[j] = slot / SB::kPerLine;
     col_b[j] = n0 + SB::place(line_b[j], slot % SB::kPerLine) * 8;
   }
-  // the rows of x of a step's lines, found one step before their loads are issued
+  // the pairs of a step's lines are read one step before they are used, so that
+  // the waits for the steps cover these reads too
+  uint32_t pair[kA];
   const auto find = [&](int step) {
 #pragma unroll
-    for (int j = 0; j < kLoadsA; ++j) {
-      const uint32_t r = lo + step * kStep + line_a[j];
-      token[j] = kNowhere;
-      if (r < hi) {
-        uint32_t t = r;
-        if (a.order != nullptr) t = static_cast<uint32_t>(a.order[r]) / static_cast<uint32_t>(a.top_k);
-        if (t < a.x_rows) token[j] = t;
-      }
+    for (int j = 0; j < kA; ++j) {
+      const uint32_t r = lo + step * T::STEP + line_a[j];
+      pair[j] = r >= hi ? kNowhere : a.order == nullptr ? r : static_cast<uint32_t>(a.order[r]);
     }
   };
-  const auto left_a = [&](int j) {
-    return token[j] == kNowhere || col_a[j] >= a.in ? 0 : static_cast<int>(min(a.in - col_a[j], 8u));
+  const auto row_of_x = [&](int j) {
+    if (pair[j] == kNowhere || col_a[j] >= a.in) return kNowhere;
+    const uint32_t t = a.order == nullptr ? pair[j] : token_of(a.token, pair[j]);
+    return t < a.x_rows ? t : kNowhere;
   };
-  const auto left_b = [&](int j, uint32_t r) {
-    return r >= hi || col_b[j] >= a.out ? 0 : static_cast<int>(min(a.out - col_b[j], 8u));
-  };
-
   if (steps > 0) find(0);
+  const uint16_t* dy = static_cast<const uint16_t*>(a.dy) + lo * a.dy_stride;
   if (DIRECT) {
-    const Source from_x(x), from_y(dy + lo * a.dy_stride);
+    const Source sx(a.x), sy(dy);
     const uint32_t base = lds_address(lds) + wave * (kWave * 16);
     const uint32_t x_bytes = static_cast<uint32_t>(a.x_stride) * 2, y_bytes = static_cast<uint32_t>(a.dy_stride) * 2;
     const auto issue = [&](int step) {
       const uint32_t to = base + (step & 1) * kStage;
 #pragma unroll
-      for (int j = 0; j < kLoadsA; ++j)
-        load_to_lds(from_x, left_a(j) ? token[j] * x_bytes + col_a[j] * 2 : kNowhere,
-                    __builtin_amdgcn_readfirstlane(to + j * kThreads * 16));
+      for (int j = 0; j < kA; ++j) {
+        const uint32_t r = row_of_x(j);
+        load_to_lds(sx, r != kNowhere ? r * x_bytes + col_a[j] * 2 : kNowhere,
+                    __builtin_amdgcn_readfirstlane(to + j * T::kThreads * 16));
+      }
 #pragma unroll
-      for (int j = 0; j < kLoadsB; ++j) {
-        const uint32_t r = step * kStep + line_b[j];
-        load_to_lds(from_y, left_b(j, lo + r) ? r * y_bytes + col_b[j] * 2 : kNowhere,
-                    __builtin_amdgcn_readfirstlane(to + SA::kBytes + j * kThreads * 16));
+      for (int j = 0; j < kB; ++j) {
+        const uint32_t r = step * T::STEP + line_b[j];
+        load_to_lds(sy, lo + r < hi && col_b[j] < a.out ? r * y_bytes + col_b[j] * 2 : kNowhere,
+                    __builtin_amdgcn_readfirstlane(to + SA::kBytes + j * T::kThreads * 16));
       }
     };
     if (steps > 0) issue(0);
@@ -310,17 +474,23 @@ __global__ __launch_bounds__(kThreads, 2) void expert_weight_grad(WeightGradArgs
       if (s + 1 < steps) issue(s + 1);
       if (s + 2 < steps) find(s + 2);
       const char* stage = lds + (s & 1) * kStage;
-      multiply_step<kPartM, kPartN, bf16x8, 1, SA, SB>(stage, stage + SA::kBytes, wave_m, wave_n, lane, acc);
+      multiply_step<T::kM, T::kN, bf16x8, 1, T::STEP, SA, SB>(stage, stage + SA::kBytes, T::row0(wave),
+                                                              T::column0(wave), lane, acc);
     }
   } else {
-    u32x4 ra[kLoadsA], rb[kLoadsB];
+    const uint16_t* x = static_cast<const uint16_t*>(a.x);
+    u32x4 ra[kA], rb[kB];
     const auto load = [&](int step) {
 #pragma unroll
-      for (int j = 0; j < kLoadsA; ++j) ra[j] = read_elements(x + token[j] * a.x_stride + col_a[j], left_a(j));
+      for (int j = 0; j < kA; ++j) {
+        const uint32_t r = row_of_x(j);
+        ra[j] = read_elements(x + r * a.x_stride + col_a[j], r != kNowhere ? static_cast<int>(min(a.in - col_a[j], 8u)) : 0);
+      }
 #pragma unroll
-      for (int j = 0; j < kLoadsB; ++j) {
-        const uint32_t r = lo + step * kStep + line_b[j];
-        rb[j] = read_elements(dy + r * a.dy_stride + col_b[j], left_b(j, r));
+      for (int j = 0; j < kB; ++j) {
+        const uint32_t r = step * T::STEP + line_b[j];
+        rb[j] = read_elements(dy + r * a.dy_stride + col_b[j],
+                              lo + r < hi && col_b[j] < a.out ? static_cast<int>(min(a.out - col_b[j], 8u)) : 0);
       }
     };
     if (steps > 0) load(0);
@@ -328,85 +498,109 @@ __global__ __launch_bounds__(kThreads, 2) void expert_weight_grad(WeightGradArgs
     for (int s = 0; s < steps; ++s) {
       char* stage = lds + (s & 1) * kStage;
 #pragma unroll
-      for (int j = 0; j < kLoadsA; ++j) *reinterpret_cast<u32x4*>(stage + (j * kThreads + tid) * 16) = ra[j];
+      for (int j = 0; j < kA; ++j) *reinterpret_cast<u32x4*>(stage + (j * T::kThreads + tid) * 16) = ra[j];
 #pragma unroll
-      for (int j = 0; j < kLoadsB; ++j)
-        *reinterpret_cast<u32x4*>(stage + SA::kBytes + (j * kThreads + tid) * 16) = rb[j];
+      for (int j = 0; j < kB; ++j)
+        *reinterpret_cast<u32x4*>(stage + SA::kBytes + (j * T::kThreads + tid) * 16) = rb[j];
       __syncthreads();
       if (s + 1 < steps) load(s + 1);
       if (s + 2 < steps) find(s + 2);
-      multiply_step<kPartM, kPartN, bf16x8, 1, SA, SB>(stage, stage + SA::kBytes, wave_m, wave_n, lane, acc);
+      multiply_step<T::kM, T::kN, bf16x8, 1, T::STEP, SA, SB>(stage, stage + SA::kBytes, T::row0(wave),
+                                                              T::column0(wave), lane, acc);
     }
   }
+  __syncthreads();
+  static_assert(T::kThreads / kWave * kTurnBytes <= 2 * kStage);
+  write_part<PAST>(acc, reinterpret_cast<float*>(lds + wave * kTurnBytes),
+             static_cast<OUT*>(a.dw) + static_cast<uint64_t>(e) * a.in * a.out, m0 + T::row0(wave), a.in,
+             n0 + T::column0(wave), a.out, lane);
+}
 
-#pragma unroll
-  for (int i = 0; i < kPartM; ++i) {
-    const uint32_t m = m0 + wave_m + 16 * i + lane % 16;
-    if (m >= a.in) continue;
-    const uint64_t first = (static_cast<uint64_t>(e) * a.in + m) * a.out;
-#pragma unroll
-    for (int j = 0; j < kPartN; ++j) {
-      const uint32_t n = n0 + wave_n + 16 * j + 4 * (lane / 16);
-      if (n >= a.out) continue;
-      if (WIDE) {
-        float* to = static_cast<float*>(a.dw) + first + n;
-        if (a.vec) {
-          *reinterpret_cast<f32x4*>(to) = acc[i][j];
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (n + q < a.out) to[q] = acc[i][j][q];
-        }
-      } else {
-        uint16_t* to = static_cast<uint16_t*>(a.dw) + first + n;
-        const uint2 v = {two_bf16(acc[i][j][0], acc[i][j][1]), two_bf16(acc[i][j][2], acc[i][j][3])};
-        if (a.vec) {
-          *reinterpret_cast<uint2*>(to) = v;
-        } else {
-          const uint32_t part[4] = {v.x & 0xffff, v.x >> 16, v.y & 0xffff, v.y >> 16};
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (n + q < a.out) to[q] = static_cast<uint16_t>(part[q]);
-        }
-      }
-    }
-  }
+template <class T> uint64_t tiles_n(uint64_t out) { return (out + T::N - 1) / T::N; }
+
+// Tiles for any distribution of the pairs: whole ones, and a part of one for
+// every group that has pairs.
+template <class T> uint64_t product_blocks(uint64_t pairs, int experts, uint64_t out) {
+  const uint64_t groups = static_cast<uint64_t>(experts) + 1;
+  return (pairs / T::M + (groups < pairs ? groups : pairs)) * tiles_n<T>(out);
+}
+template <class T> uint64_t weight_grad_tiles(uint64_t in, uint64_t out) {
+  return (in + T::M - 1) / T::M * tiles_n<T>(out);
+}
+
+// Which tiles a product has, by the rows of an expert if all have as many.
+enum class Rows { kFew, kSome, kMany };
+Rows rows_of_product(uint64_t pairs, int experts, uint64_t out, bool direct) {
+  const uint64_t each = pairs / (static_cast<uint64_t>(experts) < pairs ? experts : pairs);
+  if (each <= 16) return Rows::kFew;
+  return each <= 64 || out <= 128 || !direct ? Rows::kSome : Rows::kMany;
+}
+
+// Results of this size and more are stored past the caches: they would push out
+// what the product reads.
+constexpr uint64_t kPastBytes = 32ull << 20;
+bool past_caches(uint64_t bytes) { return bytes >= kPastBytes; }
+
+template <class T, bool BR, bool DIRECT> void launch_product(ProductArgs a, hipStream_t stream) {
+  a.tiles_n = static_cast<uint32_t>(tiles_n<T>(a.out));
+  const dim3 grid(static_cast<uint32_t>(product_blocks<T>(a.pairs, a.experts, a.out)));
+  if constexpr (T::M == Thin::M)
+    expert_product_thin<BR, DIRECT><<<grid, kThinThreads, 0, stream>>>(a);
+  else
+    (past_caches(a.pairs * static_cast<uint64_t>(a.out) * 2) ? expert_product<T, BR, DIRECT, true>
+                                                             : expert_product<T, BR, DIRECT, false>)
+        <<<grid, T::kThreads, 0, stream>>>(a);
+}
+
+template <class T, class OUT, bool DIRECT> void launch_weight_grad(WeightGradArgs a, hipStream_t stream) {
+  a.tiles_n = static_cast<uint32_t>(tiles_n<T>(a.out));
+  a.tiles = static_cast<uint32_t>(weight_grad_tiles<T>(a.in, a.out));
+  a.tiles_xcd = (a.tiles - 1) / kXcds + 1;
+  const uint64_t bytes = static_cast<uint64_t>(a.experts) * a.in * a.out * sizeof(OUT);
+  (past_caches(bytes) ? expert_weight_grad<T, OUT, DIRECT, true> : expert_weight_grad<T, OUT, DIRECT, false>)
+      <<<a.experts * a.tiles_xcd * kXcds, T::kThreads, 0, stream>>>(a);
 }
 
 }  // namespace
 
-// Tiles for any distribution of the pairs: whole ones, and a part of one for
-// every group that has pairs.
-uint64_t expert_product_blocks(uint64_t pairs, int experts, uint64_t out) {
-  const uint64_t groups = static_cast<uint64_t>(experts) + 1;
-  return (pairs / kTileM + (groups < pairs ? groups : pairs)) * ((out + kTileN - 1) / kTileN);
+uint64_t expert_product_blocks(uint64_t pairs, int experts, uint64_t out, bool direct) {
+  switch (rows_of_product(pairs, experts, out, direct)) {
+    case Rows::kFew: return product_blocks<Thin>(pairs, experts, out);
+    case Rows::kSome: return product_blocks<Small>(pairs, experts, out);
+    default: return product_blocks<Large>(pairs, experts, out);
+  }
 }
 
-uint64_t expert_weight_grad_blocks(int experts, uint64_t in, uint64_t out) {
-  return experts * ((in + kTileM - 1) / kTileM) * ((out + kTileN - 1) / kTileN);
+uint64_t expert_weight_grad_blocks(int experts, uint64_t in, uint64_t out, bool direct) {
+  const uint64_t tiles = direct ? weight_grad_tiles<Large>(in, out) : weight_grad_tiles<Middle>(in, out);
+  return experts * ((tiles - 1) / kXcds + 1) * kXcds;
 }
 
-hipError_t launch_expert_product(const ProductArgs& args, bool out_contiguous, bool direct, hipStream_t stream) {
-  ProductArgs a = args;
-  a.tiles_n = (a.out + kTileN - 1) / kTileN;
-  const dim3 grid(static_cast<uint32_t>(expert_product_blocks(a.pairs, a.experts, a.out)));
-  if (out_contiguous)
-    (direct ? expert_product<true, true> : expert_product<true, false>)<<<grid, kThreads, 0, stream>>>(a);
-  else
-    (direct ? expert_product<false, true> : expert_product<false, false>)<<<grid, kThreads, 0, stream>>>(a);
+hipError_t launch_expert_product(const ProductArgs& a, bool out_contiguous, bool direct, hipStream_t stream) {
+  switch (rows_of_product(a.pairs, a.experts, a.out, direct)) {
+    case Rows::kFew:
+      if (direct)
+        (out_contiguous ? launch_product<Thin, true, true> : launch_product<Thin, false, true>)(a, stream);
+      else
+        (out_contiguous ? launch_product<Thin, true, false> : launch_product<Thin, false, false>)(a, stream);
+      break;
+    case Rows::kSome:
+      if (direct)
+        (out_contiguous ? launch_product<Small, true, true> : launch_product<Small, false, true>)(a, stream);
+      else
+        (out_contiguous ? launch_product<Small, true, false> : launch_product<Small, false, false>)(a, stream);
+      break;
+    case Rows::kMany:
+      (out_contiguous ? launch_product<Large, true, true> : launch_product<Large, false, true>)(a, stream);
+  }
   return hipGetLastError();
 }
 
-hipError_t launch_expert_weight_grad(const WeightGradArgs& args, ar_dtype_t dw_dtype, bool direct,
-                                     hipStream_t stream) {
-  WeightGradArgs a = args;
-  a.tiles_m = (a.in + kTileM - 1) / kTileM;
-  a.tiles_n = (a.out + kTileN - 1) / kTileN;
-  const dim3 grid(static_cast<uint32_t>(expert_weight_grad_blocks(a.experts, a.in, a.out)));
+hipError_t launch_expert_weight_grad(const WeightGradArgs& a, ar_dtype_t dw_dtype, bool direct, hipStream_t stream) {
   if (dw_dtype == AR_FLOAT32)
-    (direct ? expert_weight_grad<true, true> : expert_weight_grad<true, false>)<<<grid, kThreads, 0, stream>>>(a);
+    (direct ? launch_weight_grad<LargeGrad, float, true> : launch_weight_grad<Middle, float, false>)(a, stream);
   else
-    (direct ? expert_weight_grad<false, true> : expert_weight_grad<false, false>)<<<grid, kThreads, 0, stream>>>(a);
+    (direct ? launch_weight_grad<LargeGrad, uint16_t, true> : launch_weight_grad<Middle, uint16_t, false>)(a, stream);
   return hipGetLastError();
 }
 

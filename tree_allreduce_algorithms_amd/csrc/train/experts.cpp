@@ -112,15 +112,18 @@ ar_status_t ar_expert_matmul(const ar_expert_rows_t* r, const void* weight, size
     return AR_ERROR_INVALID_ARGUMENT;
   if (r->pairs == 0) return AR_SUCCESS;
   if (y == nullptr || !aligned(y, 2) || !fits(y, r->pairs, r->out, r->out, 2)) return AR_ERROR_INVALID_ARGUMENT;
-  if (ar::expert_product_blocks(r->pairs, r->experts, r->out) > ar::kMaxProductBlocks) return AR_ERROR_UNSUPPORTED;
+  const uint64_t x_stride = r->x_rows > 1 ? r->x_stride : r->in, w_expert = r->experts > 1 ? expert_stride : 0;
+  const bool direct = wide(r->x, r->x_rows, x_stride, r->in) && wide(weight, lines, line, length) && w_expert % 8 == 0;
+  if (ar::expert_product_blocks(r->pairs, r->experts, r->out, direct) > ar::kMaxProductBlocks)
+    return AR_ERROR_UNSUPPORTED;
   ar::ProductArgs a;
   a.x = r->x;
   a.w = weight;
   a.y = y;
   a.order = r->order;
   a.offsets = r->offsets;
-  a.x_stride = r->x_rows > 1 ? r->x_stride : r->in;
-  a.w_expert = r->experts > 1 ? expert_stride : 0;
+  a.x_stride = x_stride;
+  a.w_expert = w_expert;
   a.w_line = line;
   a.x_rows = static_cast<uint32_t>(r->x_rows);
   a.pairs = static_cast<uint32_t>(r->pairs);
@@ -128,10 +131,7 @@ ar_status_t ar_expert_matmul(const ar_expert_rows_t* r, const void* weight, size
   a.out = static_cast<uint32_t>(r->out);
   a.tiles_n = 0;
   a.experts = r->experts;
-  a.top_k = r->top_k;
-  a.vec = r->out % 4 == 0 && aligned(y, 8);
-  const bool direct = wide(r->x, r->x_rows, a.x_stride, r->in) && wide(weight, lines, line, length) &&
-                      a.w_expert % 8 == 0;
+  a.token = ar::token_of(r->pairs, r->order != nullptr ? r->top_k : 1);
   return ar::launch_status(ar::enqueue([&] { return ar::launch_expert_product(a, by_out, direct, stream); }));
 }
 
@@ -153,24 +153,25 @@ ar_status_t ar_expert_weight_grad(const ar_expert_rows_t* r, const void* dy, siz
       !apart(dw, bytes, dy, r->pairs, dy_stride, r->out, 2) || !apart(dw, bytes, r->offsets, 1, 0, r->experts + 1, 4) ||
       !apart(dw, bytes, r->order, 1, 0, r->pairs, 4))
     return AR_ERROR_INVALID_ARGUMENT;
-  if (ar::expert_weight_grad_blocks(r->experts, r->in, r->out) > ar::kMaxProductBlocks) return AR_ERROR_UNSUPPORTED;
+  const uint64_t x_stride = r->x_rows > 1 ? r->x_stride : r->in, y_stride = r->pairs > 1 ? dy_stride : r->out;
+  const bool direct = wide(r->x, r->x_rows, x_stride, r->in) && wide(dy, r->pairs, y_stride, r->out);
+  if (ar::expert_weight_grad_blocks(r->experts, r->in, r->out, direct) > ar::kMaxProductBlocks)
+    return AR_ERROR_UNSUPPORTED;
   ar::WeightGradArgs a;
   a.x = r->x;
   a.dy = dy;
   a.dw = dw;
   a.order = r->order;
   a.offsets = r->offsets;
-  a.x_stride = r->x_rows > 1 ? r->x_stride : r->in;
-  a.dy_stride = r->pairs > 1 ? dy_stride : r->out;
+  a.x_stride = x_stride;
+  a.dy_stride = y_stride;
   a.x_rows = static_cast<uint32_t>(r->x_rows);
   a.pairs = static_cast<uint32_t>(r->pairs);
   a.in = static_cast<uint32_t>(r->in);
   a.out = static_cast<uint32_t>(r->out);
-  a.tiles_m = a.tiles_n = 0;
+  a.tiles_n = a.tiles = a.tiles_xcd = 0;
   a.experts = r->experts;
-  a.top_k = r->top_k;
-  a.vec = r->out % 4 == 0 && aligned(dw, 4 * size);
-  const bool direct = wide(r->x, r->x_rows, a.x_stride, r->in) && wide(dy, r->pairs, a.dy_stride, r->out);
+  a.token = ar::token_of(r->pairs, r->order != nullptr ? r->top_k : 1);
   return ar::launch_status(
       ar::enqueue([&] { return ar::launch_expert_weight_grad(a, dw_dtype, direct, stream); }));
 }

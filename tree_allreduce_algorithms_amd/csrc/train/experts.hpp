@@ -31,6 +31,16 @@ struct OrderArgs {
 };
 hipError_t launch_expert_order(const OrderArgs& a, hipStream_t stream);
 
+// The token of a pair, pair / top_k: by a product with `reciprocal` = ceil(2^32 /
+// top_k) where pairs * top_k <= 2^32 makes that exact, else (0) by a division.
+struct TokenOf {
+  uint32_t top_k, reciprocal;
+};
+inline TokenOf token_of(uint64_t pairs, uint32_t top_k) {
+  const uint64_t two32 = 1ull << 32;
+  return {top_k, top_k > 1 && pairs * top_k <= two32 ? static_cast<uint32_t>((two32 + top_k - 1) / top_k) : 0};
+}
+
 // Products by expert.  `line` is the distance of a weight's lines: of its rows
 // (in) where the columns (out) are contiguous, of its columns otherwise.
 struct ProductArgs {
@@ -41,13 +51,14 @@ struct ProductArgs {
   const int32_t* offsets;
   uint64_t x_stride, w_expert, w_line;
   uint32_t x_rows, pairs, in, out, tiles_n;
-  int32_t experts, top_k;
-  uint32_t vec;            // four outputs may be stored at once
+  int32_t experts;
+  TokenOf token;
 };
+
 // Blocks of a launch; one has less than 2^32 threads of at most 512 a block.
 constexpr uint64_t kMaxProductBlocks = (1u << 23) - 1;
-uint64_t expert_product_blocks(uint64_t pairs, int experts, uint64_t out);
-uint64_t expert_weight_grad_blocks(int experts, uint64_t in, uint64_t out);
+uint64_t expert_product_blocks(uint64_t pairs, int experts, uint64_t out, bool direct);
+uint64_t expert_weight_grad_blocks(int experts, uint64_t in, uint64_t out, bool direct);
 
 // Bytes that 32-bit offsets reach from one base (see tile.hpp).
 constexpr uint64_t kProductReach = 0x80000000ull;
@@ -61,9 +72,10 @@ struct WeightGradArgs {
   const int32_t* order;
   const int32_t* offsets;
   uint64_t x_stride, dy_stride;
-  uint32_t x_rows, pairs, in, out, tiles_m, tiles_n;
-  int32_t experts, top_k;
-  uint32_t vec;
+  uint32_t x_rows, pairs, in, out, tiles_n;
+  uint32_t tiles, tiles_xcd;    // of an expert; an XCD's of these
+  int32_t experts;
+  TokenOf token;
 };
 hipError_t launch_expert_weight_grad(const WeightGradArgs& a, ar_dtype_t dw_dtype, bool direct, hipStream_t stream);
 

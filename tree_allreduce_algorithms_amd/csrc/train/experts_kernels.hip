@@ -71,10 +71,16 @@ __global__ __launch_bounds__(kOrderThreads) void order_place(OrderArgs a) {
     if (a.blocks == 1) {
       for (uint32_t w = 0; w < kOrderWaves; ++w) all += next[w * experts + e];
     } else {
-      for (uint32_t b = 0; b < a.blocks; ++b) {
-        const uint32_t n = a.counts[static_cast<size_t>(b) * experts + e];
-        all += n;
-        before += b < blockIdx.x ? n : 0;
+      for (uint32_t b = 0; b < a.blocks; b += 8) {
+        uint32_t n[8];
+#pragma unroll
+        for (uint32_t q = 0; q < 8; ++q)
+          n[q] = b + q < a.blocks ? a.counts[static_cast<size_t>(b + q) * experts + e] : 0;
+#pragma unroll
+        for (uint32_t q = 0; q < 8; ++q) {
+          all += n[q];
+          before += b + q < blockIdx.x ? n[q] : 0;
+        }
       }
     }
   }
@@ -152,10 +158,10 @@ __device__ __forceinline__ uint16_t to_bf16(float f) {
   return static_cast<uint16_t>((u + 0x7fffu + (u >> 16 & 1)) >> 16);
 }
 
-// The `n` (1 to 8) elements at p, zeros behind them.
+// The `n` (up to 8) elements at p, zeros behind them.
 __device__ __forceinline__ Eight read(const uint16_t* p, uint32_t n) {
-  Eight r = {};
   if (n == 8) return *reinterpret_cast<const Eight*>(p);
+  Eight r = {};
 #pragma unroll
   for (uint32_t i = 0; i < 8; ++i)
     if (i < n) r.v[i] = p[i];
@@ -187,13 +193,23 @@ __global__ __launch_bounds__(kSumThreads) void combine(CombineArgs a, uint32_t l
        t += static_cast<uint64_t>(gridDim.x) * per_block) {
     const uint64_t first = t * a.top_k;
     float sum[8] = {};
-    for (int k = 0; k < a.top_k; ++k) {
-      const uint32_t row = static_cast<uint32_t>(a.position[first + k]);
-      if (row >= a.pairs) continue;
-      const float w = a.weights == nullptr ? 1.0f : a.weights[first + k];
-      const Eight r = read(y + row * a.y_stride, n);
+    // four choices' rows under way at a time
+    for (int k = 0; k < a.top_k; k += 4) {
+      uint32_t row[4];
+      float w[4];
+      Eight r[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w, to_float(r.v[i]), sum[i]);
+      for (int q = 0; q < 4; ++q) {
+        row[q] = k + q < a.top_k ? static_cast<uint32_t>(a.position[first + k + q]) : kNone;
+        w[q] = a.weights == nullptr || k + q >= a.top_k ? 1.0f : a.weights[first + k + q];
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) r[q] = read(y + row[q] * a.y_stride, row[q] < a.pairs ? n : 0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (row[q] < a.pairs)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w[q], to_float(r[q].v[i]), sum[i]);
     }
     Eight o;
 #pragma unroll
@@ -203,42 +219,46 @@ __global__ __launch_bounds__(kSumThreads) void combine(CombineArgs a, uint32_t l
 }
 
 // dy_i = w_p dout_t and dw_p = dout_t . y_i, i the row of pair p of token t; a
-// wave has a token.  Rows that belong to no pair become 0.
+// wave has a pair, a block neighbours, whose token is mostly the same.  Rows that
+// belong to no pair become 0.
 __global__ __launch_bounds__(kSumThreads) void combine_grad(CombineArgs a) {
-  constexpr uint32_t kWaves = kSumThreads / kWave;
+  constexpr uint32_t kWaves = kSumThreads / kWave, kRound = kWave * 8;
   const uint32_t lane = threadIdx.x % kWave;
   const uint32_t id = blockIdx.x * kWaves + threadIdx.x / kWave, waves = gridDim.x * kWaves;
-  const uint16_t* y = static_cast<const uint16_t*>(a.y);
   uint16_t* dy = static_cast<uint16_t*>(a.out);
-  for (uint32_t t = id; t < a.tokens; t += waves) {
-    const uint16_t* dout = static_cast<const uint16_t*>(a.dout) + t * a.dout_stride;
-    const uint64_t first = static_cast<uint64_t>(t) * a.top_k;
-    for (int k = 0; k < a.top_k; ++k) {
-      const uint32_t row = static_cast<uint32_t>(a.position[first + k]);
-      float dot = 0.0f;
-      if (row < a.pairs) {
-        const float w = a.weights[first + k];
-        for (uint32_t c = lane * 8; c < a.size; c += kWave * 8) {
-          const uint32_t n = min(8u, a.size - c);
-          const Eight d = read(dout + c, n), r = read(y + row * a.y_stride + c, n);
+  const uint32_t pairs = a.tokens * a.top_k;
+  for (uint32_t p = id; p < pairs; p += waves) {
+    const uint32_t row = static_cast<uint32_t>(a.position[p]);
+    float dot = 0.0f;
+    if (row < a.pairs) {
+      const uint16_t* dout = static_cast<const uint16_t*>(a.dout) + p / a.top_k * a.dout_stride;
+      const uint16_t* y = static_cast<const uint16_t*>(a.y) + row * a.y_stride;
+      uint16_t* to = dy + static_cast<uint64_t>(row) * a.size;
+      const float w = a.weights[p];
+      for (uint32_t c = lane * 8; c < a.size; c += 2 * kRound) {
+        const uint32_t n = min(8u, a.size - c), m = c + kRound < a.size ? min(8u, a.size - c - kRound) : 0;
+        const Eight d[2] = {read(dout + c, n), read(dout + c + kRound, m)};
+        const Eight r[2] = {read(y + c, n), read(y + c + kRound, m)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           Eight o;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float x = to_float(d.v[i]);
-            dot = __builtin_fmaf(x, to_float(r.v[i]), dot);
+            const float x = to_float(d[h].v[i]);
+            dot = __builtin_fmaf(x, to_float(r[h].v[i]), dot);
             o.v[i] = to_bf16(w * x);
           }
-          write(dy + static_cast<uint64_t>(row) * a.size + c, o, n);
+          write(to + c + h * kRound, o, h == 0 ? n : m);
         }
-        dot = wave_sum(dot);
       }
-      if (lane == 0) a.dweights[first + k] = dot;
+      dot = wave_sum(dot);
     }
+    if (lane == 0) a.dweights[p] = dot;
   }
   const uint32_t live = min(static_cast<uint32_t>(max(a.offsets[a.experts], 0)), a.pairs);
   const Eight zero = {};
   for (uint32_t row = live + id; row < a.pairs; row += waves)
-    for (uint32_t c = lane * 8; c < a.size; c += kWave * 8)
+    for (uint32_t c = lane * 8; c < a.size; c += kRound)
       write(dy + static_cast<uint64_t>(row) * a.size + c, zero, min(8u, a.size - c));
 }
 
@@ -265,9 +285,9 @@ hipError_t launch_expert_combine(const CombineArgs& a, hipStream_t stream) {
 
 hipError_t launch_expert_combine_grad(const CombineArgs& a, hipStream_t stream) {
   const uint32_t per = kSumThreads / kWave;
-  const uint32_t rows = a.tokens > a.pairs / 2 ? a.tokens : a.pairs / 2;
-  const uint32_t blocks = (rows + per - 1) / per;
-  combine_grad<<<blocks < 8192 ? (blocks ? blocks : 1) : 8192, kSumThreads, 0, stream>>>(a);
+  const uint32_t pairs = a.tokens * static_cast<uint32_t>(a.top_k), rows = pairs > a.pairs ? pairs : a.pairs;
+  const uint32_t blocks = (rows - 1) / per + 1;
+  combine_grad<<<blocks < 65536 ? blocks : 65536, kSumThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -21,16 +21,12 @@ namespace {
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kScale = 4096.0f, kUnscale = 1.0f / 4096.0f;
 
-typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
-
 __device__ __forceinline__ const MuonMatrix& matrix_of(const MuonStepArgs& a, uint32_t i) {
   return reinterpret_cast<const MuonMatrix*>(a.plan + a.matrices_at)[i];
 }
 __device__ __forceinline__ MuonNorm* norm_of(const MuonStepArgs& a, uint32_t i) {
   return reinterpret_cast<MuonNorm*>(a.plan + a.norms_at) + i;
 }
-
-template <class T> __device__ __forceinline__ float load(const T* p) { return static_cast<float>(*p); }
 
 // A value times kScale as the sum of two float16.
 __device__ __forceinline__ void split(float v, _Float16* large, _Float16* small) {
@@ -42,23 +38,58 @@ __device__ __forceinline__ void split(float v, _Float16* large, _Float16* small)
 
 constexpr int kElementThreads = 256;
 
+// N elements from p on; `vec`: p allows them at once.
+template <int N, class T> __device__ __forceinline__ void read(const T* p, bool vec, int n, float (&v)[N]) {
+  typedef __attribute__((ext_vector_type(4))) T Four;
+  if (vec && n >= N) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const Four f = *reinterpret_cast<const Four*>(p + i);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[i + q] = static_cast<float>(f[q]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i < n ? static_cast<float>(p[i]) : 0.0f;
+  }
+}
+
 // m' = mu m + s g, and the norm of u = s g + mu m' (nesterov) or m': squares and
-// their sums in float64, joined in the chunks' order by a matrix's last block.
+// their sums in float64, joined in the chunks' order by a matrix's last block.  A
+// thread has four times eight elements.
 template <class G> __global__ __launch_bounds__(kElementThreads) void muon_momentum(MuonStepArgs a) {
+  constexpr int kEach = 8;
   const MuonChunk c = reinterpret_cast<const MuonChunk*>(a.plan + a.chunks_at)[blockIdx.x];
   const MuonMatrix& x = matrix_of(a, c.matrix);
   const uint64_t count = static_cast<uint64_t>(x.rows) * x.cols;
   const uint64_t first = static_cast<uint64_t>(c.index) * kMuonChunk;
-  const uint32_t n = static_cast<uint32_t>(min(count - first, static_cast<uint64_t>(kMuonChunk)));
+  const int n = static_cast<int>(min(count - first, static_cast<uint64_t>(kMuonChunk)));
   const G* g = static_cast<const G*>(x.g) + first;
   float* m = x.m + first;
+  const bool flat = x.flat != 0;
   double sum = 0;
-  for (uint32_t i = threadIdx.x; i < n; i += kElementThreads) {
-    const float s = a.grad_scale * load(g + i);
-    const float next = __builtin_fmaf(a.momentum, m[i], s);
-    m[i] = next;
-    const double u = a.nesterov ? __builtin_fmaf(a.momentum, next, s) : next;
-    sum += u * u;
+#pragma unroll
+  for (int r = 0; r < static_cast<int>(kMuonChunk); r += kElementThreads * kEach) {
+    const int i = r + threadIdx.x * kEach;
+    if (i >= n) break;
+    float s[kEach], v[kEach];
+    read(g + i, flat, n - i, s);
+    read(m + i, flat, n - i, v);
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) {
+      s[q] *= a.grad_scale;
+      v[q] = __builtin_fmaf(a.momentum, v[q], s[q]);
+      const double u = a.nesterov ? __builtin_fmaf(a.momentum, v[q], s[q]) : v[q];
+      sum += u * u;
+    }
+    if (flat && i + kEach <= n) {
+#pragma unroll
+      for (int q = 0; q < kEach; q += 4) *reinterpret_cast<f32x4*>(m + i + q) = f32x4{v[q], v[q + 1], v[q + 2], v[q + 3]};
+    } else {
+#pragma unroll
+      for (int q = 0; q < kEach; ++q)
+        if (i + q < n) m[i + q] = v[q];
+    }
   }
   sum = block_sum<kElementThreads>(sum);
   double* sums = reinterpret_cast<double*>(a.plan + a.sums_at) + x.first_chunk;
@@ -74,44 +105,59 @@ template <class G> __global__ __launch_bounds__(kElementThreads) void muon_momen
   }
 }
 
-// X = u / (|u| + eps) in two parts, transposed where the matrix is taller than
-// wide, zeros around it.  A block has a tile of SIDE x SIDE of X.
-template <int SIDE, class G> __global__ __launch_bounds__(kElementThreads) void muon_start(MuonStepArgs a) {
-  __shared__ float turned[SIDE][SIDE + 1];
-  const MuonTile t = reinterpret_cast<const MuonTile*>(a.plan + a.tiles_at)[blockIdx.x];
-  const MuonMatrix& x = matrix_of(a, t.matrix);
-  const double scale = norm_of(a, t.matrix)->inverse * kScale;   // float32 would lose the far norms
-  const G* g = static_cast<const G*>(x.g);
-  const uint32_t m0 = t.m * SIDE, n0 = t.n * SIDE;          // of X
-  const uint32_t r0 = x.tall ? n0 : m0, c0 = x.tall ? m0 : n0;
-  for (uint32_t i = threadIdx.x; i < SIDE * SIDE; i += kElementThreads) {
-    const uint32_t r = r0 + i / SIDE, c = c0 + i % SIDE;
-    float v = 0.0f;
-    if (r < x.rows && c < x.cols) {
-      const uint64_t at = static_cast<uint64_t>(r) * x.cols + c;
-      v = x.m[at];
-      if (a.nesterov) v = __builtin_fmaf(a.momentum, v, a.grad_scale * load(g + at));
-      v = static_cast<float>(v * scale);
-    }
-    turned[i / SIDE][i % SIDE] = v;
-  }
-  __syncthreads();
-  _Float16* to = reinterpret_cast<_Float16*>(a.workspace + x.x[0]);
-  const uint64_t plane = x.x_plane / sizeof(_Float16);
-  for (uint32_t i = threadIdx.x * 4; i < SIDE * SIDE; i += kElementThreads * 4) {
-    const uint32_t m = i / SIDE, n = i % SIDE;
-    f16x4 large, small;
+// Values of a row, times kScale, in two parts; `at` is a multiple of 8.
+template <int N> __device__ __forceinline__ void store(_Float16* to, uint64_t plane, uint64_t at, const float (&v)[N]) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+  for (int h = 0; h < N; h += 8) {
+    f16x8 large, small;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
       _Float16 l, s;
-      split(x.tall ? turned[n + q][m] : turned[m][n + q], &l, &s);
+      split(v[h + q], &l, &s);
       large[q] = l;
       small[q] = s;
     }
-    const uint64_t at = static_cast<uint64_t>(m0 + m) * x.width + n0 + n;
-    *reinterpret_cast<f16x4*>(to + at) = large;
-    *reinterpret_cast<f16x4*>(to + plane + at) = small;
+    *reinterpret_cast<f16x8*>(to + at + h) = large;
+    *reinterpret_cast<f16x8*>(to + plane + at + h) = small;
   }
+}
+
+// X = u / (|u| + eps) in two parts, transposed where the matrix is taller than
+// wide, zeros around it.  A block has 64 x 64 of X, a thread 16 of a row.
+template <int SIDE, class G> __global__ __launch_bounds__(kElementThreads) void muon_start(MuonStepArgs a) {
+  constexpr uint32_t kPart = 64, kParts = SIDE / kPart;
+  __shared__ float turned[kPart][kPart + 1];
+  const MuonTile t = reinterpret_cast<const MuonTile*>(a.plan + a.tiles_at)[blockIdx.x];
+  if (t.matrix == kMuonNoMatrix) return;
+  const MuonMatrix& x = matrix_of(a, t.matrix);
+  const double scale = norm_of(a, t.matrix)->inverse * kScale;   // float32 would lose the far norms
+  const uint32_t m0 = t.m * SIDE + blockIdx.y / kParts * kPart, n0 = t.n * SIDE + blockIdx.y % kParts * kPart;   // of X
+  const uint32_t line = threadIdx.x / 4, piece = threadIdx.x % 4 * 16;
+  const uint32_t r = (x.tall ? n0 : m0) + line, c = (x.tall ? m0 : n0) + piece;
+  float v[16] = {};
+  if (r < x.rows && c < x.cols) {
+    const uint64_t at = static_cast<uint64_t>(r) * x.cols + c;
+    const int n = static_cast<int>(min(x.cols - c, 16u));
+    const bool vec = x.flat != 0 && x.cols % 4 == 0;
+    read(x.m + at, vec, n, v);
+    if (a.nesterov) {
+      float s[16];
+      read(static_cast<const G*>(x.g) + at, vec, n, s);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) v[q] = __builtin_fmaf(a.momentum, v[q], a.grad_scale * s[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < 16; ++q) v[q] = static_cast<float>(v[q] * scale);
+  }
+  if (x.tall) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) turned[line][piece + q] = v[q];
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 16; ++q) v[q] = turned[piece + q][line];
+  }
+  store(reinterpret_cast<_Float16*>(a.workspace + x.x[0]), x.x_plane / sizeof(_Float16),
+        static_cast<uint64_t>(m0 + line) * x.width + n0 + piece, v);
 }
 
 // --- products -------------------------------------------------------------------------
@@ -119,177 +165,277 @@ template <int SIDE, class G> __global__ __launch_bounds__(kElementThreads) void 
 // The tile of D = A B: A [..][k] with `k` contiguous from row m0 on, B the same
 // from its row n0 on (BR false) or [k][..] from its column n0 on.  All are padded
 // to whole tiles, so nothing is checked.
-template <int SIDE, int WM, int WN, bool BR> struct Product {
-  using SA = Staged<SIDE, false>;
-  using SB = Staged<SIDE, BR>;
-  static constexpr int kThreads = WM * WN * kWave;
+constexpr int kProductThreads = 256;
+
+// Two blocks of 128 x 128 with steps of 32 on a CU: 1,390 TFLOP/s of matrix
+// instructions for 131,072 x 1,024 by k = 2,048, against 1,213 of one block of
+// eight waves with steps of 64, and 1,299-1,324 of 256 x 128 and 128 x 256.
+template <int SIDE, bool BR> struct Product {
+  static constexpr int kStep = kMuonStep;
+  using SA = Staged<SIDE, false, kStep, false>;
+  using SB = Staged<SIDE, BR, kStep, true>;
+  static constexpr int kWavesM = SIDE == 128 ? 2 : 4, kWavesN = SIDE == 128 ? 2 : 1;
+  static constexpr int kThreads = kWavesM * kWavesN * kWave;
+  static_assert(kThreads == kProductThreads);
   static constexpr int kStage = 2 * (SA::kBytes + SB::kBytes);
-  static constexpr int kBytes = 2 * kStage;
-  static constexpr int kM = SIDE / WM / 16, kN = SIDE / WN / 16;
+  static constexpr int kStages = SIDE == 128 ? 2 : 4, kAhead = kStages - 1;
+  static constexpr int kBytes = kStages * kStage;
+  static constexpr int kM = SIDE / kWavesM / 16, kN = SIDE / kWavesN / 16;
 
   f32x4 acc[kM][kN];
   int m, n, lane;              // of the wave's part; of the thread
 
   __device__ __forceinline__ void run(char* lds, const char* a, uint64_t a_plane, uint32_t a_line, uint32_t m0,
-                                      const char* b, uint64_t b_plane, uint32_t b_line, uint32_t n0, uint32_t k) {
+                                      const char* b, uint64_t b_plane, uint32_t b_line, uint32_t n0,
+                                      uint32_t first, uint32_t steps) {
     constexpr int kLoadsA = SA::kChunks / kThreads, kLoadsB = SB::kChunks / kThreads;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     lane = tid % kWave;
-    m = wave / WN * (SIDE / WM);
-    n = wave % WN * (SIDE / WN);
-#pragma unroll
-    for (auto& row : acc)
-#pragma unroll
-      for (auto& v : row) v = f32x4{0, 0, 0, 0};
+    m = wave / kWavesN * (SIDE / kWavesM);
+    n = wave % kWavesN * (SIDE / kWavesN);
+    clear(acc);
     const Source from_a[2] = {Source(a), Source(a + a_plane)}, from_b[2] = {Source(b), Source(b + b_plane)};
     uint32_t at_a[kLoadsA], at_b[kLoadsB];
 #pragma unroll
     for (int j = 0; j < kLoadsA; ++j) {
       const int slot = j * kThreads + tid, l = slot / SA::kPerLine;
-      at_a[j] = ((m0 + l) * a_line + SA::place(l, slot % SA::kPerLine) * 8) * 2;
+      at_a[j] = ((m0 + l) * a_line + SA::place(l, slot % SA::kPerLine) * 8) * 2 + first * kStep * 2;
     }
 #pragma unroll
     for (int j = 0; j < kLoadsB; ++j) {
       const int slot = j * kThreads + tid, l = slot / SB::kPerLine, c = SB::place(l, slot % SB::kPerLine) * 8;
-      at_b[j] = BR ? (l * b_line + n0 + c) * 2 : ((n0 + l) * b_line + c) * 2;
+      at_b[j] = BR ? ((first * kStep + l) * b_line + n0 + c) * 2 : ((n0 + l) * b_line + first * kStep + c) * 2;
     }
     const uint32_t next_a = kStep * 2, next_b = BR ? kStep * b_line * 2 : kStep * 2;
     const uint32_t base = lds_address(lds) + wave * (kWave * 16);
+    // (past the last step nothing is read, but as many loads are counted)
     const auto issue = [&](uint32_t step) {
-      const uint32_t to = base + (step & 1) * kStage;
+      const uint32_t to = base + step % kStages * kStage;
+      const bool more = step < steps;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
 #pragma unroll
         for (int j = 0; j < kLoadsA; ++j)
-          load_to_lds(from_a[p], at_a[j] + step * next_a,
+          load_to_lds(from_a[p], more ? at_a[j] + step * next_a : kNowhere,
                       __builtin_amdgcn_readfirstlane(to + p * SA::kBytes + j * kThreads * 16));
 #pragma unroll
         for (int j = 0; j < kLoadsB; ++j)
-          load_to_lds(from_b[p], at_b[j] + step * next_b,
+          load_to_lds(from_b[p], more ? at_b[j] + step * next_b : kNowhere,
                       __builtin_amdgcn_readfirstlane(to + 2 * SA::kBytes + p * SB::kBytes + j * kThreads * 16));
       }
     };
-    const uint32_t steps = k / kStep;
-    issue(0);
+#pragma unroll
+    for (uint32_t s = 0; s < kAhead; ++s) issue(s);
     for (uint32_t s = 0; s < steps; ++s) {
-      settled();
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kAhead - 1) * 2 * (kLoadsA + kLoadsB)) : "memory");
       __builtin_amdgcn_s_barrier();
-      if (s + 1 < steps) issue(s + 1);
-      const char* stage = lds + (s & 1) * kStage;
-      multiply_step<kM, kN, f16x8, 2, SA, SB>(stage, stage + 2 * SA::kBytes, m, n, lane, acc);
+      issue(s + kAhead);
+      const char* stage = lds + s % kStages * kStage;
+      multiply_step<kM, kN, f16x8, 2, kStep, SA, SB>(stage, stage + 2 * SA::kBytes, m, n, lane, acc);
+    }
+    settled();
+  }
+
+  // Joins the parts of a tile; true in the block that has the whole.  The sums
+  // pass through memory as wave.hpp says, eight bytes at a time.
+  __device__ __forceinline__ bool join(const MuonStepArgs& a, const MuonTile& t) {
+    if (t.parts == 1) return true;
+    constexpr uint32_t kPairs = SIDE * SIDE / 2;
+    uint64_t* parts = reinterpret_cast<uint64_t*>(a.workspace + a.parts_at) + static_cast<uint64_t>(t.slot) * kPairs;
+    union Pair {
+      uint64_t word;
+      float v[2];
+    };
+    uint64_t* mine = parts + t.part * kPairs + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kM; ++i)
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          Pair p;
+          p.v[0] = acc[i][j][2 * h];
+          p.v[1] = acc[i][j][2 * h + 1];
+          shared_store(mine + ((i * kN + j) * 2 + h) * kThreads, p.word);
+        }
+    uint32_t* arrived = reinterpret_cast<uint32_t*>(a.plan + a.arrived_at) + t.counter;
+    if (!last_to_arrive(arrived, t.parts)) return false;
+    if (threadIdx.x == 0) *arrived = 0;
+    clear(acc);
+    for (uint32_t part = 0; part < t.parts; ++part) {
+      const uint64_t* from = parts + part * kPairs + threadIdx.x;
+      Pair p[kM][kN][2];
+#pragma unroll
+      for (int i = 0; i < kM; ++i)
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) p[i][j][h].word = shared_load(from + ((i * kN + j) * 2 + h) * kThreads);
+#pragma unroll
+      for (int i = 0; i < kM; ++i)
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[i][j][q] += p[i][j][q / 2].v[q % 2];
+    }
+    return true;
+  }
+
+  // The tile in LDS, so that neighbouring lanes can take neighbouring values of a
+  // row: a row m of it, or TURNED a column n, has SIDE float32 in pieces of four
+  // that are permuted by the row, against bank conflicts of the writes.
+  template <bool TURNED> static __device__ __forceinline__ int place(int r, int c) {
+    return r * SIDE + (c ^ (TURNED ? r / 16 % 4 * 16 : r % 16 * 4));
+  }
+  template <bool TURNED> __device__ __forceinline__ void put(float* tile) const {
+    static_assert(SIDE * SIDE * sizeof(float) <= kBytes);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kM; ++i)
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const int r = m + 16 * i + lane % 16, c = n + j / 4 * 64 + 16 * (lane / 16) + 4 * (j % 4);
+        if (TURNED) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tile[place<true>(c + q, r)] = acc[i][j][q];
+        } else {
+          *reinterpret_cast<f32x4*>(tile + place<false>(r, c)) = acc[i][j];
+        }
+      }
+    __syncthreads();
+  }
+  // Calls f(row, first column, values) for N of a row at a time.
+  template <bool TURNED, int N, class F> static __device__ __forceinline__ void rows(const float* tile, F&& f) {
+#pragma unroll 2
+    for (int i = threadIdx.x * N; i < SIDE * SIDE; i += kThreads * N) {
+      const int r = i / SIDE, c = i % SIDE;
+      float v[N];
+#pragma unroll
+      for (int h = 0; h < N; h += 4) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(tile + place<TURNED>(r, c + h));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[h + q] = x[q];
+      }
+      f(r, c, v);
     }
   }
 };
 
-template <int SIDE> struct Shape {
-  static constexpr int kWavesM = 2, kWavesN = SIDE == 128 ? 4 : 2;
-  static constexpr int kThreads = kWavesM * kWavesN * kWave;
-  // blocks on a CU by their LDS: 128 KB or 64
-  static constexpr int kWavesPerSimd = 2;
-};
-
-// Four values of a row in two parts.
-__device__ __forceinline__ void store(_Float16* to, uint64_t plane, uint64_t at, f32x4 v, f16x4* large, f16x4* small) {
+// The values of a tile of X X^T, or of the polynomial, from row m0 and column n0 on.
+template <class P, bool POLY, bool TURNED>
+__device__ __forceinline__ void store_square(const MuonStepArgs& a, const MuonMatrix& x, const float* tile, uint32_t m0,
+                                             uint32_t n0) {
+  const uint64_t plane = x.gram_plane / sizeof(_Float16);
+  _Float16* to = reinterpret_cast<_Float16*>(a.workspace + (POLY ? x.poly : x.gram));
+  const _Float16* gram = reinterpret_cast<const _Float16*>(a.workspace + x.gram);
+  P::template rows<TURNED, 8>(tile, [&](uint32_t r, uint32_t c, float (&v)[8]) {
+    const uint64_t at = static_cast<uint64_t>(m0 + r) * x.height + n0 + c;
+    f16x8 gl, gs;
+    if (POLY) {
+      gl = *reinterpret_cast<const f16x8*>(gram + at);
+      gs = *reinterpret_cast<const f16x8*>(gram + plane + at);
+    }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    _Float16 l, s;
-    split(v[q], &l, &s);
-    (*large)[q] = l;
-    (*small)[q] = s;
-  }
-  *reinterpret_cast<f16x4*>(to + at) = *large;
-  *reinterpret_cast<f16x4*>(to + plane + at) = *small;
+    for (int q = 0; q < 8; ++q) {
+      v[q] *= kUnscale;
+      if (POLY) {
+        const float g = static_cast<float>(gl[q]) + static_cast<float>(gs[q]);
+        v[q] = __builtin_fmaf(kC, v[q], kB * g) + (m0 + r == n0 + c + q ? kA * kScale : 0.0f);
+      }
+    }
+    store(to, plane, at, v);
+  });
 }
 
 // POLY false: gram = X X^T.  POLY true: poly = a I + b gram + c gram gram.  Both are
 // symmetric: tiles above the diagonal are stored a second time, transposed.
 template <int SIDE, bool POLY>
-__global__ __launch_bounds__(Shape<SIDE>::kThreads, Shape<SIDE>::kWavesPerSimd) void muon_square(MuonStepArgs a) {
-  using P = Product<SIDE, Shape<SIDE>::kWavesM, Shape<SIDE>::kWavesN, false>;
+__global__ __launch_bounds__(kProductThreads, 2) void muon_square(MuonStepArgs a) {
+  using P = Product<SIDE, false>;
   __shared__ __attribute__((aligned(1024))) char lds[P::kBytes];
-  const MuonTile t = reinterpret_cast<const MuonTile*>(a.plan + a.squares_at)[blockIdx.x];
+  const MuonTile t = reinterpret_cast<const MuonTile*>(a.plan + (POLY ? a.polys_at : a.squares_at))[blockIdx.x];
+  if (t.matrix == kMuonNoMatrix) return;
   const MuonMatrix& x = matrix_of(a, t.matrix);
-  const uint32_t m0 = t.m * SIDE, n0 = t.n * SIDE, side = x.height;
+  const uint32_t m0 = t.m * SIDE, n0 = t.n * SIDE;
   const char* from = a.workspace + (POLY ? x.gram : x.x[a.from]);
   const uint64_t from_plane = POLY ? x.gram_plane : x.x_plane;
-  const uint32_t k = POLY ? x.height : x.width;
+  const uint32_t line = POLY ? x.height : x.width;
   P p;
-  p.run(lds, from, from_plane, k, m0, from, from_plane, k, n0, k);
-
-  const uint64_t plane = x.gram_plane / sizeof(_Float16);
-  _Float16* to = reinterpret_cast<_Float16*>(a.workspace + (POLY ? x.poly : x.gram));
-  const _Float16* gram = reinterpret_cast<const _Float16*>(a.workspace + x.gram);
-#pragma unroll
-  for (int i = 0; i < P::kM; ++i)
-#pragma unroll
-    for (int j = 0; j < P::kN; ++j) {
-      const uint32_t m = m0 + p.m + 16 * i + p.lane % 16, n = n0 + p.n + 16 * j + 4 * (p.lane / 16);
-      const uint64_t at = static_cast<uint64_t>(m) * side + n;
-      f32x4 v = p.acc[i][j] * kUnscale;
-      if (POLY) {
-        const f16x4 gl = *reinterpret_cast<const f16x4*>(gram + at);
-        const f16x4 gs = *reinterpret_cast<const f16x4*>(gram + plane + at);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float g = static_cast<float>(gl[q]) + static_cast<float>(gs[q]);
-          v[q] = __builtin_fmaf(kC, v[q], kB * g) + (m == n + q ? kA * kScale : 0.0f);
-        }
-      }
-      f16x4 large, small;
-      store(to, plane, at, v, &large, &small);
-      if (t.m != t.n) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint64_t mirror = static_cast<uint64_t>(n + q) * side + m;
-          to[mirror] = large[q];
-          to[plane + mirror] = small[q];
-        }
-      }
-    }
+  p.run(lds, from, from_plane, line, m0, from, from_plane, line, n0, t.first, t.steps);
+  if (!p.join(a, t)) return;
+  float* tile = reinterpret_cast<float*>(lds);
+  p.template put<false>(tile);
+  store_square<P, POLY, false>(a, x, tile, m0, n0);
+  if (t.m == t.n) return;
+  p.template put<true>(tile);
+  store_square<P, POLY, true>(a, x, tile, n0, m0);
 }
 
-// p' = (1 - lr wd) p - lr s x
-template <class T, bool COPY>
-__device__ __forceinline__ void update(const MuonMatrix& x, uint64_t at, float lr, float lr_wd, float v) {
-  T* p = static_cast<T*>(x.p) + at;
-  const float old = static_cast<float>(*p);
-  const float next = old - __builtin_fmaf(lr, v, lr_wd * old);
-  *p = static_cast<T>(next);
-  if (COPY) static_cast<__bf16*>(x.copy)[at] = static_cast<__bf16>(next);
+// p' = (1 - lr wd) p - lr s x for N consecutive elements
+template <int N, class T, bool COPY>
+__device__ __forceinline__ void update(const MuonMatrix& x, uint64_t at, float lr, float lr_wd, const float* v) {
+  typedef __attribute__((ext_vector_type(N))) T Values;
+  typedef __attribute__((ext_vector_type(N))) __bf16 Copies;
+  Values* p = reinterpret_cast<Values*>(static_cast<T*>(x.p) + at);
+  Values old = *p;
+  Copies copy;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const float o = static_cast<float>(old[q]), next = o - __builtin_fmaf(lr, v[q], lr_wd * o);
+    old[q] = static_cast<T>(next);
+    copy[q] = static_cast<__bf16>(next);
+  }
+  *p = old;
+  if (COPY) *reinterpret_cast<Copies*>(static_cast<__bf16*>(x.copy) + at) = copy;
+}
+
+template <class P, class T, bool COPY, bool TURNED>
+__device__ __forceinline__ void update_tile(const MuonStepArgs& a, const MuonMatrix& x, const float* tile, uint32_t r0,
+                                            uint32_t c0) {
+  const float lr = a.lr * (a.rms != 0.0f ? a.rms * x.by_size : x.by_shape) * (kUnscale * kUnscale);
+  P::template rows<TURNED, 4>(tile, [&](uint32_t r, uint32_t c, float (&v)[4]) {
+    if (r0 + r >= x.rows || c0 + c >= x.cols) return;
+    const uint64_t at = static_cast<uint64_t>(r0 + r) * x.cols + c0 + c;
+    if (x.vec) {
+      update<4, T, COPY>(x, at, lr, a.lr_wd, v);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (c0 + c + q < x.cols) update<1, T, COPY>(x, at + q, lr, a.lr_wd, v + q);
+    }
+  });
 }
 
 // X' = poly X; the last one updates the parameters instead.
 template <int SIDE, class T, bool COPY>
-__global__ __launch_bounds__(Shape<SIDE>::kThreads, Shape<SIDE>::kWavesPerSimd) void muon_apply(MuonStepArgs a) {
-  using P = Product<SIDE, Shape<SIDE>::kWavesM, Shape<SIDE>::kWavesN, true>;
+__global__ __launch_bounds__(kProductThreads, 2) void muon_apply(MuonStepArgs a) {
+  using P = Product<SIDE, true>;
   __shared__ __attribute__((aligned(1024))) char lds[P::kBytes];
   const MuonTile t = reinterpret_cast<const MuonTile*>(a.plan + a.tiles_at)[blockIdx.x];
+  if (t.matrix == kMuonNoMatrix) return;
   const MuonMatrix& x = matrix_of(a, t.matrix);
   const uint32_t m0 = t.m * SIDE, n0 = t.n * SIDE;
   P p;
   p.run(lds, a.workspace + x.poly, x.gram_plane, x.height, m0, a.workspace + x.x[a.from], x.x_plane, x.width, n0,
-        x.height);
-
-  const float lr = a.lr * (a.rms != 0.0f ? a.rms * x.by_size : x.by_shape) * (kUnscale * kUnscale);
+        t.first, t.steps);
+  if (!p.join(a, t)) return;
+  float* tile = reinterpret_cast<float*>(lds);
+  if (a.last && x.tall) {
+    p.template put<true>(tile);
+    update_tile<P, T, COPY, true>(a, x, tile, n0, m0);
+    return;
+  }
+  p.template put<false>(tile);
+  if (a.last) {
+    update_tile<P, T, COPY, false>(a, x, tile, m0, n0);
+    return;
+  }
   _Float16* to = reinterpret_cast<_Float16*>(a.workspace + x.x[1 - a.from]);
+  P::template rows<false, 8>(tile, [&](uint32_t r, uint32_t c, float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < P::kM; ++i)
-#pragma unroll
-    for (int j = 0; j < P::kN; ++j) {
-      const uint32_t m = m0 + p.m + 16 * i + p.lane % 16, n = n0 + p.n + 16 * j + 4 * (p.lane / 16);
-      if (!a.last) {
-        f16x4 large, small;
-        store(to, x.x_plane / sizeof(_Float16), static_cast<uint64_t>(m) * x.width + n, p.acc[i][j] * kUnscale, &large,
-              &small);
-        continue;
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t r = x.tall ? n + q : m, c = x.tall ? m : n + q;
-        if (r < x.rows && c < x.cols)
-          update<T, COPY>(x, static_cast<uint64_t>(r) * x.cols + c, lr, a.lr_wd, p.acc[i][j][q]);
-      }
-    }
+    for (int q = 0; q < 8; ++q) v[q] *= kUnscale;
+    store(to, x.x_plane / sizeof(_Float16), static_cast<uint64_t>(m0 + r) * x.width + n0 + c, v);
+  });
 }
 
 }  // namespace
@@ -301,7 +447,7 @@ hipError_t launch_muon_momentum(const MuonStepArgs& a, uint32_t chunks, ar_dtype
 
 template <int SIDE>
 static hipError_t start(const MuonStepArgs& a, uint32_t tiles, ar_dtype_t grad_dtype, hipStream_t stream) {
-  (grad_dtype == AR_FLOAT32 ? muon_start<SIDE, float> : muon_start<SIDE, __bf16>)<<<tiles, kElementThreads, 0, stream>>>(a);
+  (grad_dtype == AR_FLOAT32 ? muon_start<SIDE, float> : muon_start<SIDE, __bf16>)<<<dim3(tiles, (SIDE / 64) * (SIDE / 64)), kElementThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -312,17 +458,17 @@ hipError_t launch_muon_start(const MuonStepArgs& a, uint32_t tiles, uint32_t sid
 
 hipError_t launch_muon_gram(const MuonStepArgs& a, uint32_t squares, uint32_t side, hipStream_t stream) {
   if (side == 128)
-    muon_square<128, false><<<squares, Shape<128>::kThreads, 0, stream>>>(a);
+    muon_square<128, false><<<squares, kProductThreads, 0, stream>>>(a);
   else
-    muon_square<64, false><<<squares, Shape<64>::kThreads, 0, stream>>>(a);
+    muon_square<64, false><<<squares, kProductThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 hipError_t launch_muon_poly(const MuonStepArgs& a, uint32_t squares, uint32_t side, hipStream_t stream) {
   if (side == 128)
-    muon_square<128, true><<<squares, Shape<128>::kThreads, 0, stream>>>(a);
+    muon_square<128, true><<<squares, kProductThreads, 0, stream>>>(a);
   else
-    muon_square<64, true><<<squares, Shape<64>::kThreads, 0, stream>>>(a);
+    muon_square<64, true><<<squares, kProductThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -331,7 +477,7 @@ static hipError_t apply(const MuonStepArgs& a, uint32_t tiles, ar_dtype_t param_
   const auto kernel = param_dtype == AR_BFLOAT16 ? muon_apply<SIDE, __bf16, false>
                       : copy                     ? muon_apply<SIDE, float, true>
                                                  : muon_apply<SIDE, float, false>;
-  kernel<<<tiles, Shape<SIDE>::kThreads, 0, stream>>>(a);
+  kernel<<<tiles, kProductThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

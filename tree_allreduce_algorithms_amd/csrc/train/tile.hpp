@@ -1,10 +1,10 @@
 // A block's tile of a matrix product by matrix instructions (gfx950), shared by
 // the experts' products and the Muon step.
 //
-// D[m][n] = sum_k A[m][k] B[k][n] for BM x BN of D, k in steps of 64.  A step
-// of each operand lies in LDS as 16-byte chunks (8 elements) of lines:
-//   k-major   a line is one row m (or column n): 64 consecutive k
-//   r-major   a line is one k: BM (or BN) consecutive rows (columns)
+// D[m][n] = sum_k A[m][k] B[k][n], k in steps.  A step of each operand lies in
+// LDS as 16-byte chunks (8 elements) of lines:
+//   k-major   a line is one row m (or column n): the step's k, consecutive
+//   r-major   a line is one k: consecutive rows (columns) of the tile
 // so either order of an operand in memory is staged as it is.  A wave reads a
 // k-major fragment by 16-byte loads and an r-major one by the transposing
 // loads, which give a lane four k of one row.  Chunks are permuted within a
@@ -12,7 +12,15 @@
 // banks.
 //
 // Steps are double-buffered: the loads of step k + 1 are under way while step k
-// is multiplied; one barrier a step.
+// is multiplied; one barrier a step.  More stages measured slower (8192^3: 1,276
+// TFLOP/s with four half steps against 1,310 with two whole ones): it is not the
+// loads' latency that binds but what L2 and LDS move, so tiles are as wide as
+// the registers of two blocks on a CU allow.
+//
+// B's columns are dealt to the fragments so that a lane holds 16 consecutive
+// ones in four fragments (`turned`): 32 bytes of bfloat16, with its neighbours a
+// whole cache line of a row.  Fragments in order, 8 bytes a lane, took 629 us
+// instead of 580 for 131,072 x 2,048 by k = 1,024, and 275 instead of 233 by 256.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -21,8 +29,6 @@
 
 namespace ar {
 namespace {
-
-constexpr int kStep = 64;      // k of a step
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
@@ -43,38 +49,48 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_char*)p));
 }
 
-// One operand's step in LDS: R rows (or columns) times 64 k.
-template <int R, bool RMAJOR> struct Staged {
-  static constexpr int kLines = RMAJOR ? kStep : R;
-  static constexpr int kPerLine = (RMAJOR ? R : kStep) / 8;     // chunks
-  static constexpr int kChunks = R * kStep / 8;
-  static constexpr int kBytes = R * kStep * 2;
+// One operand's step in LDS: R rows (or columns) times STEP k.
+template <int R, bool RMAJOR, int STEP, bool TURNED> struct Staged {
+  static constexpr int kLines = RMAJOR ? STEP : R;
+  static constexpr int kPerLine = (RMAJOR ? R : STEP) / 8;     // chunks
+  static constexpr int kChunks = R * STEP / 8;
+  static constexpr int kBytes = R * STEP * 2;
+  static_assert(STEP == 32 || STEP == 64, "bank permutations are for these");
+  static_assert(!TURNED || R % 64 == 0, "columns are dealt in groups of 64");
 
-  // where chunk `c` of a line lies among the line's chunks
+  // Where chunk `c` of a line lies among the line's chunks.  One access reads
+  // 16 bytes of 8 lines (k-major) or 8 bytes at four places of four lines
+  // (r-major) at a time, which 256 bytes of banks take at once if they differ.
   static __device__ __forceinline__ int place(int line, int c) {
-    if (RMAJOR) return c ^ ((2 * (line & 3) + (kPerLine >= 16 ? line & 8 : 0)) & (kPerLine - 1));
-    return c ^ (line & 7);
+    if (RMAJOR) {
+      if (TURNED) return c ^ (kPerLine >= 16 ? (line & 1) | (line & 2) << 2 : line >> 1 & 1);
+      return c ^ ((2 * (line & 3) + (kPerLine >= 16 ? line & 8 : 0)) & (kPerLine - 1));
+    }
+    if (STEP == 64) return c ^ (TURNED ? (line & 3) | (line >> 2 & 4) : line & 7);
+    return c ^ (TURNED ? (line >> 1 & 1) | (line >> 3 & 2) : line >> 1 & 3);
   }
 
-  // the lane's 8 k (8 (lane / 16) and on, of 32 from k0) of row r0 + lane % 16
-  template <class V> static __device__ __forceinline__ V fragment(const char* step, int r0, int k0, int lane) {
+  // The lane's 8 k (8 (lane / 16) and on, of 32 from k0) of a row: row r0 + 16 j
+  // + lane % 16, or turned, row r0 + 64 (j / 4) + 16 i + 4 (j % 4) + q of lane %
+  // 16 = 4 i + q.
+  template <class V>
+  static __device__ __forceinline__ V fragment(const char* step, int r0, int j, int k0, int lane) {
+    const int l = lane % 16, first = TURNED ? r0 + j / 4 * 64 + j % 4 * 4 : r0 + j * 16;
     if (!RMAJOR) {
-      const int line = r0 + lane % 16, c = k0 / 8 + lane / 16;
+      const int line = first + (TURNED ? l / 4 * 16 + l % 4 : l), c = k0 / 8 + lane / 16;
       return *reinterpret_cast<const V*>(step + (line * kPerLine + place(line, c)) * 16);
     } else {
       // of each 16 lanes, four lie along a line and four lines are read; lane l
       // gets row l of the four k
-      const int l = lane % 16, line = k0 + 8 * (lane / 16) + l / 4;
-      const int c = (r0 + l % 4 * 4) / 8, half = l & 1;
+      const int line = k0 + 8 * (lane / 16) + l / 4, row = first + l % 4 * (TURNED ? 16 : 4);
       union {
         V v;
         s16x4 part[2];
       } u;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const char* at = step + ((line + 4 * i) * kPerLine + place(line + 4 * i, c)) * 16 + half * 8;
-        u.part[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s16x4*)(at));
+        const char* at = step + ((line + 4 * i) * kPerLine + place(line + 4 * i, row / 8)) * 16 + row % 8 * 2;
+        u.part[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at));
       }
       return u.v;
     }
@@ -111,22 +127,23 @@ __device__ __forceinline__ void load_to_lds(const Source& s, uint32_t offset, ui
 // are done.
 __device__ __forceinline__ void settled() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
 
-// Multiplies one step: acc[i][j] holds rows 16 i, columns 16 j of the wave's
-// part, D[n][m] in a lane: m = lane % 16, n = 4 (lane / 16) + element.
-// `planes` bytes lie between the planes of a value that is held as the sum of
-// two; their products without that of the two small parts are added up.
-template <int TM, int TN, class V, int P, class A, class B>
+// Multiplies one step: acc[i][j] holds rows 16 i and the columns of fragment j of
+// the wave's part, D[n][m] in a lane: row lane % 16, columns 4 (lane / 16) +
+// element of the fragment, so turned, columns 64 (j / 4) + 16 (lane / 16) + 4 (j
+// % 4) + element.  With P = 2 a value is the sum of two planes, kBytes apart;
+// their products without that of the two small parts are added up.
+template <int TM, int TN, class V, int P, int STEP, class A, class B>
 __device__ __forceinline__ void multiply_step(const char* a, const char* b, int m0, int n0, int lane,
                                               f32x4 (&acc)[TM][TN]) {
 #pragma unroll
-  for (int k0 = 0; k0 < kStep; k0 += 32) {
+  for (int k0 = 0; k0 < STEP; k0 += 32) {
     V fa[P][TM], fb[P][TN];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
 #pragma unroll
-      for (int i = 0; i < TM; ++i) fa[p][i] = A::template fragment<V>(a + p * A::kBytes, m0 + 16 * i, k0, lane);
+      for (int i = 0; i < TM; ++i) fa[p][i] = A::template fragment<V>(a + p * A::kBytes, m0, i, k0, lane);
 #pragma unroll
-      for (int j = 0; j < TN; ++j) fb[p][j] = B::template fragment<V>(b + p * B::kBytes, n0 + 16 * j, k0, lane);
+      for (int j = 0; j < TN; ++j) fb[p][j] = B::template fragment<V>(b + p * B::kBytes, n0, j, k0, lane);
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -139,6 +156,13 @@ __device__ __forceinline__ void multiply_step(const char* a, const char* b, int 
         acc[i][j] = multiply(fb[0][j], fa[0][i], acc[i][j]);
       }
   }
+}
+
+template <int TM, int TN> __device__ __forceinline__ void clear(f32x4 (&acc)[TM][TN]) {
+#pragma unroll
+  for (auto& row : acc)
+#pragma unroll
+    for (auto& x : row) x = f32x4{0, 0, 0, 0};
 }
 
 }  // namespace
