@@ -37,6 +37,35 @@ __device__ __forceinline__ u32x4 read_elements(const uint16_t* p, int n) {
   return r;
 }
 
+// The chunk of elements e to e + 7 of a line of `length`, in two steps, so that
+// many loads can be under way without a branch between them: a chunk over the
+// line's end is read from its last 8 elements, and shifted into place when the
+// values have come.  Lines of less than 8 are read element by element.
+__device__ __forceinline__ u32x4 fetch(const uint16_t* line, uint32_t e, uint32_t length) {
+  if (length < 8) return read_elements(line + e, e < length ? static_cast<int>(length - e) : 0);
+  return reinterpret_cast<const Chunk*>(line + min(e, length - 8))->v;
+}
+// `ends`: whether a chunk of the step may lie over its line's end.
+__device__ __forceinline__ u32x4 in_place(u32x4 v, bool valid, bool ends, uint32_t e, uint32_t length) {
+  if (ends && length >= 8) {
+    const uint32_t over = e + 8 > length ? min(e + 8 - length, 8u) : 0;      // elements past the end
+    uint64_t lo = v[0] | static_cast<uint64_t>(v[1]) << 32, hi = v[2] | static_cast<uint64_t>(v[3]) << 32;
+    if (over & 4) {
+      lo = hi;
+      hi = 0;
+    }
+    const uint32_t bits = over % 4 * 16;
+    if (bits != 0) {
+      lo = lo >> bits | hi << (64 - bits);
+      hi >>= bits;
+    }
+    if (over == 8) lo = hi = 0;
+    v = u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+              static_cast<uint32_t>(hi >> 32)};
+  }
+  return valid ? v : u32x4{0, 0, 0, 0};
+}
+
 __device__ __forceinline__ uint32_t two_bf16(float a, float b) {
   typedef __attribute__((ext_vector_type(2))) __bf16 two;
   two t = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
@@ -249,19 +278,26 @@ template <class T, class SA, class SB, bool BR> struct Operands {
     const uint32_t k = step * T::STEP;
     const uint16_t* x = static_cast<const uint16_t*>(a.x);
 #pragma unroll
-    for (int j = 0; j < kA; ++j) h->a[j] = read_elements(x + row[j] * a.x_stride + k + at[j], left_a(a, j, k));
+    for (int j = 0; j < kA; ++j) h->a[j] = fetch(x + (row[j] == kNowhere ? 0 : row[j]) * a.x_stride, k + at[j], a.in);
 #pragma unroll
     for (int j = 0; j < kB; ++j) {
-      const uint64_t at_line = BR ? k + line[j] : n0 + line[j];
-      h->b[j] = read_elements(w + at_line * a.w_line + (BR ? n0 : k) + first[j], left_b(a, j, k));
+      const uint32_t l = (BR ? k : n0) + line[j], lines = BR ? a.in : a.out;
+      h->b[j] = fetch(w + (l < lines ? l : 0) * a.w_line, (BR ? n0 : k) + first[j], BR ? a.out : a.in);
     }
   }
-  __device__ __forceinline__ void put(const Held& h, char* stage, int thread) const {
+  __device__ __forceinline__ void put(const ProductArgs& a, const Held& h, int step, char* stage, int thread) const {
+    const uint32_t k = step * T::STEP;
+    const bool end_k = k + T::STEP > a.in, end_n = n0 + T::N > a.out;
 #pragma unroll
-    for (int j = 0; j < kA; ++j) *reinterpret_cast<u32x4*>(stage + (j * T::kThreads + thread) * 16) = h.a[j];
+    for (int j = 0; j < kA; ++j)
+      *reinterpret_cast<u32x4*>(stage + (j * T::kThreads + thread) * 16) =
+          in_place(h.a[j], row[j] != kNowhere, end_k, k + at[j], a.in);
 #pragma unroll
-    for (int j = 0; j < kB; ++j)
-      *reinterpret_cast<u32x4*>(stage + SA::kBytes + (j * T::kThreads + thread) * 16) = h.b[j];
+    for (int j = 0; j < kB; ++j) {
+      const uint32_t l = (BR ? k : n0) + line[j], lines = BR ? a.in : a.out;
+      *reinterpret_cast<u32x4*>(stage + SA::kBytes + (j * T::kThreads + thread) * 16) =
+          in_place(h.b[j], l < lines, BR ? end_n : end_k, (BR ? n0 : k) + first[j], BR ? a.out : a.in);
+    }
   }
 };
 
@@ -284,7 +320,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_product(Produ
   if (!part_of<T::M, T::N>(a, &p)) return;
   f32x4 acc[T::kM][T::kN];
   clear(acc);
-  const int steps = p.e < a.experts ? static_cast<int>((a.in + T::STEP - 1) / T::STEP) : 0;
+  const int steps = p.e < a.experts && a.x_rows > 0 ? static_cast<int>((a.in + T::STEP - 1) / T::STEP) : 0;
   const uint16_t* w = static_cast<const uint16_t*>(a.w) + (p.e < a.experts ? p.e * a.w_expert : 0);
   const Operands<T, SA, SB, BR> from(a, p, tid);
   char* const mine = lds + wave * (kWave * 16);
@@ -308,7 +344,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_product(Produ
     if (steps > 0) from.load(a, w, 0, &held);
     for (int s = 0; s < steps; ++s) {
       char* stage = lds + (s & 1) * kStage;
-      from.put(held, stage, tid);
+      from.put(a, held, s, stage, tid);
       __syncthreads();
       if (s + 1 < steps) from.load(a, w, s + 1, &held);
       multiply_step<T::kM, T::kN, bf16x8, 1, T::STEP, SA, SB>(stage, stage + SA::kBytes, T::row0(wave),
@@ -341,7 +377,7 @@ __global__ __launch_bounds__(kThinThreads, 2) void expert_product_thin(ProductAr
   if (!part_of<T::M, T::N>(a, &p)) return;
   f32x4 acc[1][T::kN];
   clear(acc);
-  const int steps = p.e < a.experts ? static_cast<int>((a.in + T::STEP - 1) / T::STEP) : 0;
+  const int steps = p.e < a.experts && a.x_rows > 0 ? static_cast<int>((a.in + T::STEP - 1) / T::STEP) : 0;
   const uint16_t* w = static_cast<const uint16_t*>(a.w) + (p.e < a.experts ? p.e * a.w_expert : 0);
   const Operands<T, SA, SB, BR> from(a, p, lane);
   char* const mine = lds + wave * (2 * kStage);
@@ -365,7 +401,7 @@ __global__ __launch_bounds__(kThinThreads, 2) void expert_product_thin(ProductAr
     typename Operands<T, SA, SB, BR>::Held held;
     if (wave < steps) from.load(a, w, wave, &held);
     for (int s = wave; s < steps; s += kThinWaves) {
-      from.put(held, mine, lane);
+      from.put(a, held, s, mine, lane);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       if (s + kThinWaves < steps) from.load(a, w, s + kThinWaves, &held);
       multiply_step<1, T::kN, bf16x8, 1, T::STEP, SA, SB>(mine, mine + SA::kBytes, 0, 0, lane, acc);
@@ -413,7 +449,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(W
   rows_of(a.offsets, a.experts, e, a.pairs, &lo, &hi);
   lo = __builtin_amdgcn_readfirstlane(lo);
   hi = __builtin_amdgcn_readfirstlane(hi);
-  const int steps = static_cast<int>((hi - lo + T::STEP - 1) / T::STEP);
+  const int steps = a.x_rows > 0 ? static_cast<int>((hi - lo + T::STEP - 1) / T::STEP) : 0;
   f32x4 acc[T::kM][T::kN];
   clear(acc);
 
@@ -480,17 +516,19 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(W
   } else {
     const uint16_t* x = static_cast<const uint16_t*>(a.x);
     u32x4 ra[kA], rb[kB];
+    bool found[kA];
+    const bool end_m = m0 + T::M > a.in, end_n = n0 + T::N > a.out;
     const auto load = [&](int step) {
 #pragma unroll
       for (int j = 0; j < kA; ++j) {
         const uint32_t r = row_of_x(j);
-        ra[j] = read_elements(x + r * a.x_stride + col_a[j], r != kNowhere ? static_cast<int>(min(a.in - col_a[j], 8u)) : 0);
+        found[j] = r != kNowhere;
+        ra[j] = fetch(x + (found[j] ? r : 0) * a.x_stride, col_a[j], a.in);
       }
 #pragma unroll
       for (int j = 0; j < kB; ++j) {
         const uint32_t r = step * T::STEP + line_b[j];
-        rb[j] = read_elements(dy + r * a.dy_stride + col_b[j],
-                              lo + r < hi && col_b[j] < a.out ? static_cast<int>(min(a.out - col_b[j], 8u)) : 0);
+        rb[j] = fetch(dy + (lo + r < hi ? r : 0) * a.dy_stride, col_b[j], a.out);
       }
     };
     if (steps > 0) load(0);
@@ -498,10 +536,13 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(W
     for (int s = 0; s < steps; ++s) {
       char* stage = lds + (s & 1) * kStage;
 #pragma unroll
-      for (int j = 0; j < kA; ++j) *reinterpret_cast<u32x4*>(stage + (j * T::kThreads + tid) * 16) = ra[j];
+      for (int j = 0; j < kA; ++j)
+        *reinterpret_cast<u32x4*>(stage + (j * T::kThreads + tid) * 16) =
+            in_place(ra[j], found[j], end_m, col_a[j], a.in);
 #pragma unroll
       for (int j = 0; j < kB; ++j)
-        *reinterpret_cast<u32x4*>(stage + SA::kBytes + (j * T::kThreads + tid) * 16) = rb[j];
+        *reinterpret_cast<u32x4*>(stage + SA::kBytes + (j * T::kThreads + tid) * 16) =
+            in_place(rb[j], lo + s * T::STEP + line_b[j] < hi, end_n, col_b[j], a.out);
       __syncthreads();
       if (s + 1 < steps) load(s + 1);
       if (s + 2 < steps) find(s + 2);
@@ -533,13 +574,17 @@ enum class Rows { kFew, kSome, kMany };
 Rows rows_of_product(uint64_t pairs, int experts, uint64_t out, bool direct) {
   const uint64_t each = pairs / (static_cast<uint64_t>(experts) < pairs ? experts : pairs);
   if (each <= 16) return Rows::kFew;
-  return each <= 64 || out <= 128 || !direct ? Rows::kSome : Rows::kMany;
+  return each <= (direct ? 64 : 128) || (out <= 128 && direct) ? Rows::kSome : Rows::kMany;
 }
 
-// Results of this size and more are stored past the caches: they would push out
-// what the product reads.
+// Results of this size and more are stored past the caches, since they would push
+// out what the product reads, if their rows are whole cache lines: parts of lines
+// have to meet in a cache (61 matrices of 1,000 x 776 float32: 109 us past the
+// caches, 73 through them).
 constexpr uint64_t kPastBytes = 32ull << 20;
-bool past_caches(uint64_t bytes) { return bytes >= kPastBytes; }
+bool past_caches(const void* to, uint64_t rows, uint64_t row_bytes) {
+  return rows * row_bytes >= kPastBytes && (reinterpret_cast<uintptr_t>(to) | row_bytes) % 128 == 0;
+}
 
 template <class T, bool BR, bool DIRECT> void launch_product(ProductArgs a, hipStream_t stream) {
   a.tiles_n = static_cast<uint32_t>(tiles_n<T>(a.out));
@@ -547,7 +592,7 @@ template <class T, bool BR, bool DIRECT> void launch_product(ProductArgs a, hipS
   if constexpr (T::M == Thin::M)
     expert_product_thin<BR, DIRECT><<<grid, kThinThreads, 0, stream>>>(a);
   else
-    (past_caches(a.pairs * static_cast<uint64_t>(a.out) * 2) ? expert_product<T, BR, DIRECT, true>
+    (past_caches(a.y, a.pairs, static_cast<uint64_t>(a.out) * 2) ? expert_product<T, BR, DIRECT, true>
                                                              : expert_product<T, BR, DIRECT, false>)
         <<<grid, T::kThreads, 0, stream>>>(a);
 }
@@ -556,8 +601,7 @@ template <class T, class OUT, bool DIRECT> void launch_weight_grad(WeightGradArg
   a.tiles_n = static_cast<uint32_t>(tiles_n<T>(a.out));
   a.tiles = static_cast<uint32_t>(weight_grad_tiles<T>(a.in, a.out));
   a.tiles_xcd = (a.tiles - 1) / kXcds + 1;
-  const uint64_t bytes = static_cast<uint64_t>(a.experts) * a.in * a.out * sizeof(OUT);
-  (past_caches(bytes) ? expert_weight_grad<T, OUT, DIRECT, true> : expert_weight_grad<T, OUT, DIRECT, false>)
+  (past_caches(a.dw, static_cast<uint64_t>(a.experts) * a.in, a.out * sizeof(OUT)) ? expert_weight_grad<T, OUT, DIRECT, true> : expert_weight_grad<T, OUT, DIRECT, false>)
       <<<a.experts * a.tiles_xcd * kXcds, T::kThreads, 0, stream>>>(a);
 }
 
@@ -567,7 +611,7 @@ uint64_t expert_product_blocks(uint64_t pairs, int experts, uint64_t out, bool d
   switch (rows_of_product(pairs, experts, out, direct)) {
     case Rows::kFew: return product_blocks<Thin>(pairs, experts, out);
     case Rows::kSome: return product_blocks<Small>(pairs, experts, out);
-    default: return product_blocks<Large>(pairs, experts, out);
+    default: return direct ? product_blocks<Large>(pairs, experts, out) : product_blocks<Middle>(pairs, experts, out);
   }
 }
 
@@ -591,7 +635,10 @@ hipError_t launch_expert_product(const ProductArgs& a, bool out_contiguous, bool
         (out_contiguous ? launch_product<Small, true, false> : launch_product<Small, false, false>)(a, stream);
       break;
     case Rows::kMany:
-      (out_contiguous ? launch_product<Large, true, true> : launch_product<Large, false, true>)(a, stream);
+      if (direct)
+        (out_contiguous ? launch_product<Large, true, true> : launch_product<Large, false, true>)(a, stream);
+      else
+        (out_contiguous ? launch_product<Middle, true, false> : launch_product<Middle, false, false>)(a, stream);
   }
   return hipGetLastError();
 }
