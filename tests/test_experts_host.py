@@ -163,7 +163,7 @@ def plan(ts, pd=F32, gd=F32):
 
 
 def head(image):
-    """The image's head: eleven 32-bit words, then 64-bit sizes and offsets."""
+    """The image's head: twelve 32-bit words, then 64-bit sizes and offsets."""
     small = (ctypes.c_uint32 * 11).from_buffer(image)
     large = (ctypes.c_uint64 * 9).from_buffer(image, 48)
     return dict(zip(("matrices", "chunks", "squares", "polys", "tiles", "side", "square_side"), small[1:])), \

@@ -88,6 +88,11 @@ template <int M_, int N_, int WAVES_M, int WAVES_N, int STEP_, int PER_SIMD, int
 // steps under way: 131,072 pairs of 128 experts 695 us instead of 712, 8,192 of 64
 // 75 instead of 79.
 using Large = Tile<128, 256, 2, 4, 32, 4, 3>;
+// One block of 256 x 256 moves less through L2 and LDS, which tells where rows
+// fill it and the weights' columns are read along k: 131,072 pairs of 128 experts
+// 723 us instead of 764, of 8 experts 548 instead of 620.  (With rows of k 672
+// against 675 and 490 against 508, but 159 against 148 for k = 1,024.)
+using Huge = Tile<256, 256, 2, 4, 64, 2, 2>;
 using LargeGrad = Tile<128, 256, 2, 4, 32, 4, 2>;
 using Middle = Tile<128, 128, 2, 2, 64, 2, 2>;
 using Small = Tile<64, 128, 2, 2, 64, 3, 2>;
@@ -95,6 +100,17 @@ using Small = Tile<64, 128, 2, 2, 64, 3, 2>;
 __device__ __forceinline__ uint32_t token_of(const TokenOf& t, uint32_t pair) {
   if (t.top_k == 1) return pair;
   return t.reciprocal != 0 ? __umulhi(pair, t.reciprocal) : pair / t.top_k;
+}
+
+// What lies at an address that is the same in all lanes, by a scalar load.
+__device__ __forceinline__ uint32_t scalar(const int32_t* p) {
+  typedef const __attribute__((address_space(4))) int32_t* Constant;
+  const uint64_t at = reinterpret_cast<uintptr_t>(p);
+  // (the builtin gives an int, whose sign must not reach the upper half)
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32));
+  const uint64_t uniform = static_cast<uint64_t>(hi) << 32 | lo;
+  return static_cast<uint32_t>(*reinterpret_cast<Constant>(uniform));
 }
 
 constexpr uint32_t kXcds = 8;
@@ -197,7 +213,7 @@ __device__ __forceinline__ void write_part(const f32x4 (&acc)[TM][TN], float* tu
     for (int group = 0; group < TN / 4; ++group) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<f32x4*>(turn + lane % 16 * kTurnPitch + 16 * (lane / 16) + 4 * j) = acc[i][4 * group + j];
+        *reinterpret_cast<f32x4*>(turn + lane % 16 * kTurnPitch + column(j, lane / 16)) = acc[i][4 * group + j];
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
       for (int r0 = 0; r0 < 16; r0 += kWave / kLanes) {
@@ -439,7 +455,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(W
   using SB = Staged<T::N, true, T::STEP, true>;
   constexpr int kStage = SA::kBytes + SB::kBytes;
   constexpr int kA = SA::kChunks / T::kThreads, kB = SB::kChunks / T::kThreads;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
+  __shared__ __attribute__((aligned(1024))) char lds[T::STAGES * kStage];
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const uint32_t turn = blockIdx.x / kXcds, e = turn / a.tiles_xcd;
   const uint32_t tile = (blockIdx.x + e) % kXcds * a.tiles_xcd + turn % a.tiles_xcd;
@@ -466,33 +482,37 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(W
     line_b[j] = slot / SB::kPerLine;
     col_b[j] = n0 + SB::place(line_b[j], slot % SB::kPerLine) * 8;
   }
-  // the pairs of a step's lines are read one step before they are used, so that
-  // the waits for the steps cover these reads too
-  uint32_t pair[kA];
-  const auto find = [&](int step) {
-#pragma unroll
-    for (int j = 0; j < kA; ++j) {
-      const uint32_t r = lo + step * T::STEP + line_a[j];
-      pair[j] = r >= hi ? kNowhere : a.order == nullptr ? r : static_cast<uint32_t>(a.order[r]);
-    }
-  };
-  const auto row_of_x = [&](int j) {
-    if (pair[j] == kNowhere || col_a[j] >= a.in) return kNowhere;
-    const uint32_t t = a.order == nullptr ? pair[j] : token_of(a.token, pair[j]);
-    return t < a.x_rows ? t : kNowhere;
-  };
-  if (steps > 0) find(0);
   const uint16_t* dy = static_cast<const uint16_t*>(a.dy) + lo * a.dy_stride;
   if (DIRECT) {
     const Source sx(a.x), sy(dy);
     const uint32_t base = lds_address(lds) + wave * (kWave * 16);
     const uint32_t x_bytes = static_cast<uint32_t>(a.x_stride) * 2, y_bytes = static_cast<uint32_t>(a.dy_stride) * 2;
+    constexpr int kAhead = T::STAGES - 1, kOfWave = kWave / SA::kPerLine;
+    // The pairs of a step: a wave's chunks j are of kOfWave lines.  They are read
+    // one step before they are used, by scalar loads, which the waits for the
+    // steps' loads do not count.
+    uint32_t pair[kA][kOfWave];
+    const auto find = [&](int step) {
+#pragma unroll
+      for (int j = 0; j < kA; ++j)
+#pragma unroll
+        for (int i = 0; i < kOfWave; ++i) {
+          const uint32_t r = lo + step * T::STEP + (j * T::kThreads + wave * kWave) / SA::kPerLine + i;
+          pair[j][i] = a.order == nullptr ? r : scalar(a.order + min(r, hi - 1));
+        }
+    };
     const auto issue = [&](int step) {
-      const uint32_t to = base + (step & 1) * kStage;
+      const uint32_t to = base + step % T::STAGES * kStage;
 #pragma unroll
       for (int j = 0; j < kA; ++j) {
-        const uint32_t r = row_of_x(j);
-        load_to_lds(sx, r != kNowhere ? r * x_bytes + col_a[j] * 2 : kNowhere,
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < kOfWave; ++i) {
+          const uint32_t of = a.order == nullptr ? pair[j][i] : token_of(a.token, pair[j][i]);
+          t = lane / SA::kPerLine == i ? of : t;
+        }
+        const bool in = lo + step * T::STEP + line_a[j] < hi && col_a[j] < a.in && t < a.x_rows;
+        load_to_lds(sx, in ? t * x_bytes + col_a[j] * 2 : kNowhere,
                     __builtin_amdgcn_readfirstlane(to + j * T::kThreads * 16));
       }
 #pragma unroll
@@ -502,18 +522,40 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(W
                     __builtin_amdgcn_readfirstlane(to + SA::kBytes + j * T::kThreads * 16));
       }
     };
-    if (steps > 0) issue(0);
-    if (steps > 1) find(1);
+    if (steps > 0) {
+      find(0);
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        issue(s);
+        find(s + 1);
+      }
+    }
     for (int s = 0; s < steps; ++s) {
-      settled();
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kAhead - 1) * (kA + kB)) : "memory");
       __builtin_amdgcn_s_barrier();
-      if (s + 1 < steps) issue(s + 1);
-      if (s + 2 < steps) find(s + 2);
-      const char* stage = lds + (s & 1) * kStage;
+      issue(s + kAhead);
+      find(s + kAhead + 1);
+      const char* stage = lds + s % T::STAGES * kStage;
       multiply_step<T::kM, T::kN, bf16x8, 1, T::STEP, SA, SB>(stage, stage + SA::kBytes, T::row0(wave),
                                                               T::column0(wave), lane, acc);
     }
+    settled();
   } else {
+    // the pairs of a step's lines are read one step before they are used, so that
+    // the waits for the steps cover these reads too
+    uint32_t pair[kA];
+    const auto find = [&](int step) {
+  #pragma unroll
+      for (int j = 0; j < kA; ++j) {
+        const uint32_t r = lo + step * T::STEP + line_a[j];
+        pair[j] = r >= hi ? kNowhere : a.order == nullptr ? r : static_cast<uint32_t>(a.order[r]);
+      }
+    };
+    const auto row_of_x = [&](int j) {
+      if (pair[j] == kNowhere || col_a[j] >= a.in) return kNowhere;
+      const uint32_t t = a.order == nullptr ? pair[j] : token_of(a.token, pair[j]);
+      return t < a.x_rows ? t : kNowhere;
+    };
     const uint16_t* x = static_cast<const uint16_t*>(a.x);
     u32x4 ra[kA], rb[kB];
     bool found[kA];
@@ -531,7 +573,10 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(W
         rb[j] = fetch(dy + (lo + r < hi ? r : 0) * a.dy_stride, col_b[j], a.out);
       }
     };
-    if (steps > 0) load(0);
+    if (steps > 0) {
+      find(0);
+      load(0);
+    }
     if (steps > 1) find(1);
     for (int s = 0; s < steps; ++s) {
       char* stage = lds + (s & 1) * kStage;
@@ -551,7 +596,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(W
     }
   }
   __syncthreads();
-  static_assert(T::kThreads / kWave * kTurnBytes <= 2 * kStage);
+  static_assert(T::kThreads / kWave * kTurnBytes <= T::STAGES * kStage);
   write_part<PAST>(acc, reinterpret_cast<float*>(lds + wave * kTurnBytes),
              static_cast<OUT*>(a.dw) + static_cast<uint64_t>(e) * a.in * a.out, m0 + T::row0(wave), a.in,
              n0 + T::column0(wave), a.out, lane);
@@ -570,11 +615,12 @@ template <class T> uint64_t weight_grad_tiles(uint64_t in, uint64_t out) {
 }
 
 // Which tiles a product has, by the rows of an expert if all have as many.
-enum class Rows { kFew, kSome, kMany };
-Rows rows_of_product(uint64_t pairs, int experts, uint64_t out, bool direct) {
+enum class Rows { kFew, kSome, kMany, kMost };
+Rows rows_of_product(uint64_t pairs, int experts, uint64_t out, bool by_out, bool direct) {
   const uint64_t each = pairs / (static_cast<uint64_t>(experts) < pairs ? experts : pairs);
   if (each <= 16) return Rows::kFew;
-  return each <= (direct ? 64 : 128) || (out <= 128 && direct) ? Rows::kSome : Rows::kMany;
+  if (each <= (direct ? 64 : 128) || (out <= 128 && direct)) return Rows::kSome;
+  return each >= 1024 && direct && !by_out ? Rows::kMost : Rows::kMany;
 }
 
 // Results of this size and more are stored past the caches, since they would push
@@ -607,10 +653,11 @@ template <class T, class OUT, bool DIRECT> void launch_weight_grad(WeightGradArg
 
 }  // namespace
 
-uint64_t expert_product_blocks(uint64_t pairs, int experts, uint64_t out, bool direct) {
-  switch (rows_of_product(pairs, experts, out, direct)) {
+uint64_t expert_product_blocks(uint64_t pairs, int experts, uint64_t out, bool by_out, bool direct) {
+  switch (rows_of_product(pairs, experts, out, by_out, direct)) {
     case Rows::kFew: return product_blocks<Thin>(pairs, experts, out);
     case Rows::kSome: return product_blocks<Small>(pairs, experts, out);
+    case Rows::kMost: return product_blocks<Huge>(pairs, experts, out);
     default: return direct ? product_blocks<Large>(pairs, experts, out) : product_blocks<Middle>(pairs, experts, out);
   }
 }
@@ -621,7 +668,7 @@ uint64_t expert_weight_grad_blocks(int experts, uint64_t in, uint64_t out, bool 
 }
 
 hipError_t launch_expert_product(const ProductArgs& a, bool out_contiguous, bool direct, hipStream_t stream) {
-  switch (rows_of_product(a.pairs, a.experts, a.out, direct)) {
+  switch (rows_of_product(a.pairs, a.experts, a.out, out_contiguous, direct)) {
     case Rows::kFew:
       if (direct)
         (out_contiguous ? launch_product<Thin, true, true> : launch_product<Thin, false, true>)(a, stream);
@@ -639,6 +686,9 @@ hipError_t launch_expert_product(const ProductArgs& a, bool out_contiguous, bool
         (out_contiguous ? launch_product<Large, true, true> : launch_product<Large, false, true>)(a, stream);
       else
         (out_contiguous ? launch_product<Middle, true, false> : launch_product<Middle, false, false>)(a, stream);
+      break;
+    case Rows::kMost:
+      launch_product<Huge, false, true>(a, stream);
   }
   return hipGetLastError();
 }

@@ -114,7 +114,7 @@ ar_status_t ar_expert_matmul(const ar_expert_rows_t* r, const void* weight, size
   if (y == nullptr || !aligned(y, 2) || !fits(y, r->pairs, r->out, r->out, 2)) return AR_ERROR_INVALID_ARGUMENT;
   const uint64_t x_stride = r->x_rows > 1 ? r->x_stride : r->in, w_expert = r->experts > 1 ? expert_stride : 0;
   const bool direct = wide(r->x, r->x_rows, x_stride, r->in) && wide(weight, lines, line, length) && w_expert % 8 == 0;
-  if (ar::expert_product_blocks(r->pairs, r->experts, r->out, direct) > ar::kMaxProductBlocks)
+  if (ar::expert_product_blocks(r->pairs, r->experts, r->out, by_out, direct) > ar::kMaxProductBlocks)
     return AR_ERROR_UNSUPPORTED;
   ar::ProductArgs a;
   a.x = r->x;

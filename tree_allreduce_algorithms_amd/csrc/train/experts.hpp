@@ -57,7 +57,7 @@ struct ProductArgs {
 
 // Blocks of a launch; one has less than 2^32 threads of at most 512 a block.
 constexpr uint64_t kMaxProductBlocks = (1u << 23) - 1;
-uint64_t expert_product_blocks(uint64_t pairs, int experts, uint64_t out, bool direct);
+uint64_t expert_product_blocks(uint64_t pairs, int experts, uint64_t out, bool by_out, bool direct);
 uint64_t expert_weight_grad_blocks(int experts, uint64_t in, uint64_t out, bool direct);
 
 // Bytes that 32-bit offsets reach from one base (see tile.hpp).

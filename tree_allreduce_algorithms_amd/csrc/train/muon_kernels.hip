@@ -28,6 +28,8 @@ __device__ __forceinline__ MuonNorm* norm_of(const MuonStepArgs& a, uint32_t i) 
   return reinterpret_cast<MuonNorm*>(a.plan + a.norms_at) + i;
 }
 
+typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
+
 // A value times kScale as the sum of two float16.
 __device__ __forceinline__ void split(float v, _Float16* large, _Float16* small) {
   *large = static_cast<_Float16>(v);
@@ -294,7 +296,7 @@ template <int SIDE, bool BR> struct Product {
     for (int i = 0; i < kM; ++i)
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
-        const int r = m + 16 * i + lane % 16, c = n + j / 4 * 64 + 16 * (lane / 16) + 4 * (j % 4);
+        const int r = m + 16 * i + lane % 16, c = n + column(j, lane / 16);
         if (TURNED) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) tile[place<true>(c + q, r)] = acc[i][j][q];
@@ -438,7 +440,225 @@ __global__ __launch_bounds__(kProductThreads, 2) void muon_apply(MuonStepArgs a)
   });
 }
 
+// --- small matrices -----------------------------------------------------------------
+
+// A whole step of a matrix of up to MOST x MOST in one block, X and X X^T in LDS:
+// fifteen products whose launches would take longer than they do.
+//
+// Both are [line][k] in 16-byte chunks, permuted by the line; a product reads X's
+// lines along k, or across it by transposing loads.
+template <int MOST> struct Whole {
+  static constexpr int kThreads = MOST == 128 ? 1024 : 256, kWaves = kThreads / kWave;
+  static_assert(kWaves == (MOST / 32) * (MOST / 32));     // a wave has 32 x 32 of a result
+
+  static __device__ __forceinline__ int place(int line, int k) { return line * MOST + ((k / 8 ^ (line & 7)) * 8 | k % 8); }
+
+  // 8 k of row r0 + lane % 16, from lines or across them
+  template <bool ACROSS> static __device__ __forceinline__ f16x8 fragment(const _Float16* x, int r0, int k0, int lane) {
+    const int l = lane % 16;
+    if (!ACROSS) return *reinterpret_cast<const f16x8*>(x + place(r0 + l, k0 + 8 * (lane / 16)));
+    union {
+      f16x8 v;
+      s16x4 part[2];
+    } u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const _Float16* at = x + place(k0 + 8 * (lane / 16) + 4 * i + l / 4, r0 + l % 4 * 4);
+      u.part[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at));
+    }
+    return u.v;
+  }
+
+  // The wave's part of a result of rows x columns.
+  struct Part {
+    bool any;
+    int m, n;
+    __device__ __forceinline__ Part(int rows, int columns) {
+      const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wide = columns / 32;
+      m = wave / wide * 32;
+      n = wave % wide * 32;
+      any = m < rows;
+    }
+  };
+
+  // This part of A B^T (or A B where ACROSS), k in steps of 32.
+  template <bool ACROSS>
+  static __device__ __forceinline__ void product(const _Float16* a, const _Float16* b, const Part& part, int k,
+                                                 f32x4 (&acc)[2][2]) {
+    const int lane = threadIdx.x % kWave;
+    clear(acc);
+    if (!part.any) return;
+    for (int k0 = 0; k0 < k; k0 += 32) {
+      f16x8 fa[2][2], fb[2][2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          fa[p][i] = fragment<false>(a + p * (MOST * MOST), part.m + 16 * i, k0, lane);
+          fb[p][i] = fragment<ACROSS>(b + p * (MOST * MOST), part.n + 16 * i, k0, lane);
+        }
+      // large by large, and large by small either way
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][j] = multiply(fb[t == 0][j], fa[t == 1][i], acc[i][j]);
+    }
+  }
+
+  // Calls f(row, first column, values) for what product() left in the thread.
+  template <class F>
+  static __device__ __forceinline__ void each(const Part& part, const f32x4 (&acc)[2][2], F&& f) {
+    const int lane = threadIdx.x % kWave;
+    if (!part.any) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) f(part.m + 16 * i + lane % 16, part.n + 16 * j + 4 * (lane / 16), acc[i][j]);
+  }
+
+  static __device__ __forceinline__ void keep(_Float16* to, int r, int c, float v) {
+    split(v, to + place(r, c), to + MOST * MOST + place(r, c));
+  }
+  // Four of a row from a fourth column on.
+  static __device__ __forceinline__ void keep(_Float16* to, int r, int c, f32x4 v) {
+    f16x4 large, small;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      _Float16 l, s;
+      split(v[q], &l, &s);
+      large[q] = l;
+      small[q] = s;
+    }
+    *reinterpret_cast<f16x4*>(to + place(r, c)) = large;
+    *reinterpret_cast<f16x4*>(to + MOST * MOST + place(r, c)) = small;
+  }
+};
+
+template <int MOST, class T, class G, bool COPY>
+__global__ __launch_bounds__(Whole<MOST>::kThreads, 4) void muon_whole(MuonStepArgs a) {
+  using W = Whole<MOST>;
+  __shared__ __attribute__((aligned(16))) _Float16 held[4 * MOST * MOST];
+  _Float16 *x = held, *gram = held + 2 * MOST * MOST;
+  const MuonMatrix& matrix = matrix_of(a, blockIdx.x);
+  const int rows = matrix.rows, cols = matrix.cols, tall = matrix.tall, count = rows * cols;
+  const int height = (min(rows, cols) + 31) / 32 * 32, width = (max(rows, cols) + 31) / 32 * 32;
+  const G* g = static_cast<const G*>(matrix.g);
+
+  // Momentum and norm, as muon_momentum.  A thread's elements are read at once
+  // and stay in registers until X is made of them.
+  constexpr int kEach = MOST * MOST / W::kThreads;
+  float u[kEach];
+  {
+    float s[kEach], m[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = threadIdx.x + e * W::kThreads;
+      s[e] = i < count ? static_cast<float>(g[i]) : 0.0f;
+      m[e] = i < count ? matrix.m[i] : 0.0f;
+    }
+    for (int i = threadIdx.x; i < 4 * MOST * MOST / 8; i += W::kThreads)
+      *reinterpret_cast<f16x8*>(held + 8 * i) = f16x8{0, 0, 0, 0, 0, 0, 0, 0};      // around X
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = threadIdx.x + e * W::kThreads;
+      s[e] *= a.grad_scale;
+      m[e] = __builtin_fmaf(a.momentum, m[e], s[e]);
+      u[e] = a.nesterov ? __builtin_fmaf(a.momentum, m[e], s[e]) : m[e];
+      if (i < count) matrix.m[i] = m[e];
+    }
+  }
+  double sum = 0;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) sum += static_cast<double>(u[e]) * u[e];
+  const double scale = 1.0 / (sqrt(block_sum<W::kThreads>(sum)) + a.eps) * kScale;
+  int r = threadIdx.x / cols, c = threadIdx.x % cols;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    if (r < rows) W::keep(x, tall ? c : r, tall ? r : c, static_cast<float>(u[e] * scale));
+    r += W::kThreads / cols;
+    c += W::kThreads % cols;
+    if (c >= cols) {
+      c -= cols;
+      ++r;
+    }
+  }
+  __syncthreads();
+
+  const typename W::Part square(height, height), wide(height, width);
+  f32x4 acc[2][2];
+  const float lr = a.lr * (a.rms != 0.0f ? a.rms * matrix.by_size : matrix.by_shape) * (kUnscale * kUnscale);
+  for (int step = 0; step < a.steps; ++step) {
+    W::template product<false>(x, x, square, width, acc);
+    W::each(square, acc, [&](int r, int c, f32x4 v) { W::keep(gram, r, c, v * kUnscale); });
+    __syncthreads();
+    W::template product<false>(gram, gram, square, height, acc);
+    __syncthreads();
+    // the polynomial in the place of X X^T
+    W::each(square, acc, [&](int r, int c, f32x4 v) {
+      const f16x4 large = *reinterpret_cast<const f16x4*>(gram + W::place(r, c));
+      const f16x4 small = *reinterpret_cast<const f16x4*>(gram + MOST * MOST + W::place(r, c));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float old = static_cast<float>(large[q]) + static_cast<float>(small[q]);
+        v[q] = __builtin_fmaf(kC, v[q] * kUnscale, kB * old) + (r == c + q ? kA * kScale : 0.0f);
+      }
+      W::keep(gram, r, c, v);
+    });
+    __syncthreads();
+    W::template product<true>(gram, x, wide, height, acc);
+    if (step + 1 == a.steps) break;
+    __syncthreads();
+    W::each(wide, acc, [&](int r, int c, f32x4 v) { W::keep(x, r, c, v * kUnscale); });
+    __syncthreads();
+  }
+  if (!wide.any) return;
+  // p' = (1 - lr wd) p - lr s x; all of a thread's are read at once
+  T* p = static_cast<T*>(matrix.p);
+  float old[2][2][4];
+  int at[2][2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int lane = threadIdx.x % kWave, m = wide.m + 16 * i + lane % 16, n = wide.n + 16 * j + 4 * (lane / 16) + q;
+        const int row = tall ? n : m, col = tall ? m : n;
+        at[i][j][q] = row < rows && col < cols ? row * cols + col : -1;
+        old[i][j][q] = at[i][j][q] >= 0 ? static_cast<float>(p[at[i][j][q]]) : 0.0f;
+      }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (at[i][j][q] < 0) continue;
+        const float o = old[i][j][q], next = o - __builtin_fmaf(lr, acc[i][j][q], a.lr_wd * o);
+        p[at[i][j][q]] = static_cast<T>(next);
+        if (COPY) static_cast<__bf16*>(matrix.copy)[at[i][j][q]] = static_cast<__bf16>(next);
+      }
+}
+
 }  // namespace
+
+template <int MOST, class G>
+static hipError_t whole(const MuonStepArgs& a, uint32_t matrices, ar_dtype_t param_dtype, bool copy, hipStream_t stream) {
+  const auto kernel = param_dtype == AR_BFLOAT16 ? muon_whole<MOST, __bf16, G, false>
+                      : copy                     ? muon_whole<MOST, float, G, true>
+                                                 : muon_whole<MOST, float, G, false>;
+  kernel<<<matrices, Whole<MOST>::kThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_muon_whole(const MuonStepArgs& a, uint32_t matrices, uint32_t side, ar_dtype_t param_dtype,
+                             ar_dtype_t grad_dtype, bool copy, hipStream_t stream) {
+  const bool wide = grad_dtype == AR_FLOAT32;
+  return (side == 128 ? (wide ? whole<128, float> : whole<128, __bf16>)
+                      : (wide ? whole<64, float> : whole<64, __bf16>))(a, matrices, param_dtype, copy, stream);
+}
 
 hipError_t launch_muon_momentum(const MuonStepArgs& a, uint32_t chunks, ar_dtype_t grad_dtype, hipStream_t stream) {
   (grad_dtype == AR_FLOAT32 ? muon_momentum<float> : muon_momentum<__bf16>)<<<chunks, kElementThreads, 0, stream>>>(a);

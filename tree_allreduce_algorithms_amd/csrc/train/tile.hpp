@@ -18,9 +18,8 @@
 // the registers of two blocks on a CU allow.
 //
 // B's columns are dealt to the fragments so that a lane holds 16 consecutive
-// ones in four fragments (`turned`): 32 bytes of bfloat16, with its neighbours a
-// whole cache line of a row.  Fragments in order, 8 bytes a lane, took 629 us
-// instead of 580 for 131,072 x 2,048 by k = 1,024, and 275 instead of 233 by 256.
+// ones in four fragments (`turned`), four of each, and so that the lanes of a
+// transposing load meet all banks: see column().
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -49,6 +48,12 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_char*)p));
 }
 
+// The first of the four columns that place i of a turned fragment j has: the 16
+// from 64 (j / 4) + 16 i on are dealt to four fragments, at each place in another
+// order, so that half of an access' 8-byte pieces are first halves of chunks and
+// half are second ones (in one order for all, 32 % of LDS' cycles were conflicts).
+__device__ __forceinline__ constexpr int column(int j, int i) { return j / 4 * 64 + 16 * i + (j + i) % 4 * 4; }
+
 // One operand's step in LDS: R rows (or columns) times STEP k.
 template <int R, bool RMAJOR, int STEP, bool TURNED> struct Staged {
   static constexpr int kLines = RMAJOR ? STEP : R;
@@ -58,31 +63,31 @@ template <int R, bool RMAJOR, int STEP, bool TURNED> struct Staged {
   static_assert(STEP == 32 || STEP == 64, "bank permutations are for these");
   static_assert(!TURNED || R % 64 == 0, "columns are dealt in groups of 64");
 
-  // Where chunk `c` of a line lies among the line's chunks.  One access reads
-  // 16 bytes of 8 lines (k-major) or 8 bytes at four places of four lines
-  // (r-major) at a time, which 256 bytes of banks take at once if they differ.
+  // Where chunk `c` of a line lies among the line's chunks.  An access reads 16
+  // bytes of 8 lines at a time (k-major), or 8 bytes at four places of each of
+  // eight lines (r-major; four from each of two that are 8 apart), which lie in
+  // different banks so.
   static __device__ __forceinline__ int place(int line, int c) {
     if (RMAJOR) {
-      if (TURNED) return c ^ (kPerLine >= 16 ? (line & 1) | (line & 2) << 2 : line >> 1 & 1);
+      if (TURNED) return c ^ (kPerLine >= 16 ? (line & 1) | (line & 2) << 2 | (line >> 2 & 2) : (line >> 1 & 1) | (line >> 2 & 2));
       return c ^ ((2 * (line & 3) + (kPerLine >= 16 ? line & 8 : 0)) & (kPerLine - 1));
     }
     if (STEP == 64) return c ^ (TURNED ? (line & 3) | (line >> 2 & 4) : line & 7);
     return c ^ (TURNED ? (line >> 1 & 1) | (line >> 3 & 2) : line >> 1 & 3);
   }
 
-  // The lane's 8 k (8 (lane / 16) and on, of 32 from k0) of a row: row r0 + 16 j
-  // + lane % 16, or turned, row r0 + 64 (j / 4) + 16 i + 4 (j % 4) + q of lane %
-  // 16 = 4 i + q.
+  // The lane's 8 k (8 (lane / 16) and on, of 32 from k0) of a row of fragment j:
+  // row r0 + 16 j + lane % 16, or turned, r0 + column(j, i) + q of lane % 16 = 4 i + q.
   template <class V>
   static __device__ __forceinline__ V fragment(const char* step, int r0, int j, int k0, int lane) {
-    const int l = lane % 16, first = TURNED ? r0 + j / 4 * 64 + j % 4 * 4 : r0 + j * 16;
+    const int l = lane % 16;
     if (!RMAJOR) {
-      const int line = first + (TURNED ? l / 4 * 16 + l % 4 : l), c = k0 / 8 + lane / 16;
+      const int line = r0 + (TURNED ? column(j, l / 4) + l % 4 : j * 16 + l), c = k0 / 8 + lane / 16;
       return *reinterpret_cast<const V*>(step + (line * kPerLine + place(line, c)) * 16);
     } else {
       // of each 16 lanes, four lie along a line and four lines are read; lane l
       // gets row l of the four k
-      const int line = k0 + 8 * (lane / 16) + l / 4, row = first + l % 4 * (TURNED ? 16 : 4);
+      const int line = k0 + 8 * (lane / 16) + l / 4, row = r0 + (TURNED ? column(j, l % 4) : j * 16 + l % 4 * 4);
       union {
         V v;
         s16x4 part[2];
@@ -129,8 +134,7 @@ __device__ __forceinline__ void settled() { asm volatile("s_waitcnt vmcnt(0) lgk
 
 // Multiplies one step: acc[i][j] holds rows 16 i and the columns of fragment j of
 // the wave's part, D[n][m] in a lane: row lane % 16, columns 4 (lane / 16) +
-// element of the fragment, so turned, columns 64 (j / 4) + 16 (lane / 16) + 4 (j
-// % 4) + element.  With P = 2 a value is the sum of two planes, kBytes apart;
+// element of the fragment, so turned, column(j, lane / 16) + element.  With P = 2 a value is the sum of two planes, kBytes apart;
 // their products without that of the two small parts are added up.
 template <int TM, int TN, class V, int P, int STEP, class A, class B>
 __device__ __forceinline__ void multiply_step(const char* a, const char* b, int m0, int n0, int lane,
