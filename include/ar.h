@@ -546,11 +546,18 @@ ar_status_t ar_expert_matmul(const ar_expert_rows_t* rows, const void* weight,
                              size_t expert_stride, size_t in_stride, size_t out_stride, void* y,
                              hipStream_t stream);
 
+/* Device memory that ar_expert_weight_grad needs for these sizes, in bytes
+ * (16-byte aligned, any content); 0 for none. */
+size_t ar_expert_weight_grad_workspace(size_t pairs, int experts, size_t in, size_t out);
+
 /* dw [experts][in][out] (contiguous, AR_FLOAT32 or AR_BFLOAT16): dw_e = the sum
  * over the rows i of expert e of x_i^T dy_i, 0 for an expert without rows.  dy
- * has a row of `out` elements for each pair in order, dy_stride apart. */
+ * has a row of `out` elements for each pair in order, dy_stride apart.  The
+ * rows of an expert are added up in an order that the sizes alone decide.
+ * AR_ERROR_INVALID_ARGUMENT also where dw meets what is read. */
 ar_status_t ar_expert_weight_grad(const ar_expert_rows_t* rows, const void* dy, size_t dy_stride,
-                                  void* dw, ar_dtype_t dw_dtype, hipStream_t stream);
+                                  void* dw, ar_dtype_t dw_dtype, void* workspace,
+                                  hipStream_t stream);
 
 /* out [tokens][size] (contiguous): out_t = the sum over the choices k of token t
  * that have a row of weights[t][k] * y_row, in the order of k (weights NULL: 1).

@@ -106,7 +106,18 @@ def test_matmul_arguments(change, more, want):
 ])
 def test_weight_grad_arguments(change, dy, stride, dw, dtype, want):
     assert launched(lambda: ar.lib().ar_expert_weight_grad(ctypes.byref(rows(**change)), dy, stride, dw, dtype,
-                                                           None)) == want
+                                                           None, None)) == want
+
+
+def test_weight_grad_workspace():
+    """Only few tiles with many rows share them, and then need memory."""
+    size = ar.lib().ar_expert_weight_grad_workspace
+    assert size(200, 8, 64, 96) == size(0, 1, 64, 96) == size(2 ** 20, 128, 2048, 1024) == 0
+    assert size(2 ** 20, 1, 64, 96) == 16 * 4 * 64 * 96 and size(1024, 1, 64, 96) == 4 * 4 * 64 * 96 and size(1024, 2, 64, 96) == 0
+    assert size(2 ** 31 - 1, 1, 2 ** 31 - 1, 2 ** 31 - 1) == size(100, 0, 64, 96) == size(100, 8, 0, 96) == 0
+    for workspace, want in ((None, INVALID), (at(5) + 8, INVALID), (at(5), HIP)):
+        assert launched(lambda: ar.lib().ar_expert_weight_grad(
+            ctypes.byref(rows(pairs=1024, experts=1, x_rows=512)), at(3), 96, at(4), F32, workspace, None)) == want
 
 
 def combine(**change):

@@ -230,6 +230,16 @@ def test_weight_grad(tokens, k, experts, n_in, n_out, kind, gather, dtype):
         near(dw[e], xs @ d, xs.abs() @ d.abs(), max(1, hi - lo), f"dw {e}", stored=dtype == BF16)
 
 
+@pytest.mark.parametrize("tokens,k,experts,n_in,n_out,kind", [
+    (5000, 1, 1, 64, 96, "even"), (3001, 2, 2, 130, 264, "skewed"), (2000, 3, 4, 61, 77, "masked"), (8000, 1, 5, 64, 64, "skewed"), (4000, 1, 3, 40, 8, "one"),
+])
+def test_weight_grad_of_shared_rows(tokens, k, experts, n_in, n_out, kind):
+    """Few tiles: several blocks share an expert's rows."""
+    assert ar.lib().ar_expert_weight_grad_workspace(tokens * k, experts, n_in, n_out) > 0
+    for gather, dtype in ((True, F32), (False, BF16), (True, BF16)):
+        test_weight_grad(tokens, k, experts, n_in, n_out, kind, gather, dtype)
+
+
 def test_weight_grad_into_a_tensor():
     rng = np.random.default_rng(5)
     idx = choices(100, 2, 6, "even", 3)

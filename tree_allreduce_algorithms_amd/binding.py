@@ -105,7 +105,8 @@ SIGNATURES = {
     "ar_expert_order_workspace": (_SZ, [_SZ, _I]),
     "ar_expert_order": (_I, [_VP, _SZ, _I] + [_VP] * 5),
     "ar_expert_matmul": (_I, [ctypes.POINTER(ExpertRows), _VP, _SZ, _SZ, _SZ, _VP, _VP]),
-    "ar_expert_weight_grad": (_I, [ctypes.POINTER(ExpertRows), _VP, _SZ, _VP, _I, _VP]),
+    "ar_expert_weight_grad_workspace": (_SZ, [_SZ, _I, _SZ, _SZ]),
+    "ar_expert_weight_grad": (_I, [ctypes.POINTER(ExpertRows), _VP, _SZ, _VP, _I, _VP, _VP]),
     "ar_expert_combine": (_I, [_VP, _SZ, _SZ, _SZ, _I, _VP, _VP, _SZ, _I, _VP, _VP]),
     "ar_expert_combine_grad": (_I, [_VP, _SZ, _VP, _SZ, _SZ, _SZ, _I, _VP, _VP, _I, _VP, _SZ, _I,
                                     _VP, _VP, _VP]),

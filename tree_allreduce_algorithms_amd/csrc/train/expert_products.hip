@@ -2,6 +2,8 @@
 // (gfx950).
 #include "train/experts.hpp"
 
+#include <algorithm>
+
 #include "train/tile.hpp"
 #include "train/wave.hpp"
 
@@ -445,7 +447,8 @@ __global__ __launch_bounds__(kThinThreads, 2) void expert_product_thin(ProductAr
 
 // dW_e = sum over the rows i of expert e of x_t(i)^T dy_i: a block has a tile of
 // one expert's matrix and goes over the expert's rows, a step's at a time.  An
-// expert without rows gets zeros.
+// expert without rows gets zeros.  With `parts` the rows are shared among so many
+// blocks (blockIdx.y), whose sums, a matrix each, add_parts() joins.
 //
 // A tile costs what its expert has rows, so every XCD gets a part of each
 // expert's tiles (neighbours, of the same rows of dW).
@@ -463,6 +466,12 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(W
   const uint32_t m0 = tile / a.tiles_n * T::M, n0 = tile % a.tiles_n * T::N;
   uint32_t lo, hi;
   rows_of(a.offsets, a.experts, e, a.pairs, &lo, &hi);
+  if (a.parts > 1) {
+    const uint32_t all = (hi - lo + T::STEP - 1) / T::STEP;
+    const uint32_t begin = all * blockIdx.y / a.parts, end = all * (blockIdx.y + 1) / a.parts;
+    hi = min(hi, lo + end * T::STEP);
+    lo = min(hi, lo + begin * T::STEP);
+  }
   lo = __builtin_amdgcn_readfirstlane(lo);
   hi = __builtin_amdgcn_readfirstlane(hi);
   const int steps = a.x_rows > 0 ? static_cast<int>((hi - lo + T::STEP - 1) / T::STEP) : 0;
@@ -598,8 +607,36 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(W
   __syncthreads();
   static_assert(T::kThreads / kWave * kTurnBytes <= T::STAGES * kStage);
   write_part<PAST>(acc, reinterpret_cast<float*>(lds + wave * kTurnBytes),
-             static_cast<OUT*>(a.dw) + static_cast<uint64_t>(e) * a.in * a.out, m0 + T::row0(wave), a.in,
+             static_cast<OUT*>(a.dw) + (static_cast<uint64_t>(blockIdx.y) * a.experts + e) * a.in * a.out, m0 + T::row0(wave), a.in,
              n0 + T::column0(wave), a.out, lane);
+}
+
+// The sum of `parts` arrays of n elements, one behind the other, in their order.
+constexpr int kAddThreads = 256;
+template <class OUT>
+__global__ __launch_bounds__(kAddThreads) void add_parts(const float* from, OUT* to, uint64_t n, uint32_t parts) {
+  const uint64_t i = (static_cast<uint64_t>(blockIdx.x) * kAddThreads + threadIdx.x) * 4;
+  if (i >= n) return;
+  if (i + 4 <= n) {
+    f32x4 sum = {0, 0, 0, 0};
+    for (uint32_t p = 0; p < parts; ++p) sum += reinterpret_cast<const Four*>(from + p * n + i)->v;
+    if constexpr (sizeof(OUT) == 4) {
+      reinterpret_cast<Four*>(to + i)->v = sum;
+    } else {
+      const uint32_t w[2] = {two_bf16(sum[0], sum[1]), two_bf16(sum[2], sum[3])};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) to[i + q] = static_cast<OUT>(w[q / 2] >> (16 * (q % 2)));
+    }
+    return;
+  }
+  for (uint64_t j = i; j < n; ++j) {
+    float sum = 0;
+    for (uint32_t p = 0; p < parts; ++p) sum += from[p * n + j];
+    if constexpr (sizeof(OUT) == 4)
+      to[j] = sum;
+    else
+      to[j] = static_cast<OUT>(two_bf16(sum, 0.0f));
+  }
 }
 
 template <class T> uint64_t tiles_n(uint64_t out) { return (out + T::N - 1) / T::N; }
@@ -614,12 +651,18 @@ template <class T> uint64_t weight_grad_tiles(uint64_t in, uint64_t out) {
   return (in + T::M - 1) / T::M * tiles_n<T>(out);
 }
 
+// So many wide tiles give every CU one.  With fewer, smaller ones are faster: 2,048
+// pairs of 8 experts, 1,024 x 1,024, 14 us in 64 x 128 and 21 in 128 x 256, 8,192
+// pairs 33 either way.
+constexpr uint64_t kFull = 256;
+
 // Which tiles a product has, by the rows of an expert if all have as many.
 enum class Rows { kFew, kSome, kMany, kMost };
 Rows rows_of_product(uint64_t pairs, int experts, uint64_t out, bool by_out, bool direct) {
   const uint64_t each = pairs / (static_cast<uint64_t>(experts) < pairs ? experts : pairs);
   if (each <= 16) return Rows::kFew;
-  if (each <= (direct ? 64 : 128) || (out <= 128 && direct)) return Rows::kSome;
+  if (each <= (direct ? 64 : 128) || (out <= 128 && direct) || pairs / 128 * ((out + 255) / 256) < kFull)
+    return Rows::kSome;
   return each >= 1024 && direct && !by_out ? Rows::kMost : Rows::kMany;
 }
 
@@ -643,12 +686,27 @@ template <class T, bool BR, bool DIRECT> void launch_product(ProductArgs a, hipS
         <<<grid, T::kThreads, 0, stream>>>(a);
 }
 
-template <class T, class OUT, bool DIRECT> void launch_weight_grad(WeightGradArgs a, hipStream_t stream) {
+template <class T, class OUT, bool DIRECT>
+hipError_t launch_weight_grad(WeightGradArgs a, void* workspace, hipStream_t stream) {
   a.tiles_n = static_cast<uint32_t>(tiles_n<T>(a.out));
   a.tiles = static_cast<uint32_t>(weight_grad_tiles<T>(a.in, a.out));
   a.tiles_xcd = (a.tiles - 1) / kXcds + 1;
-  (past_caches(a.dw, static_cast<uint64_t>(a.experts) * a.in, a.out * sizeof(OUT)) ? expert_weight_grad<T, OUT, DIRECT, true> : expert_weight_grad<T, OUT, DIRECT, false>)
-      <<<a.experts * a.tiles_xcd * kXcds, T::kThreads, 0, stream>>>(a);
+  const dim3 grid(a.experts * a.tiles_xcd * kXcds, a.parts);
+  if (a.parts == 1) {
+    (past_caches(a.dw, static_cast<uint64_t>(a.experts) * a.in, a.out * sizeof(OUT)) ? expert_weight_grad<T, OUT, DIRECT, true>
+                                                                                     : expert_weight_grad<T, OUT, DIRECT, false>)
+        <<<grid, T::kThreads, 0, stream>>>(a);
+    return hipGetLastError();
+  }
+  OUT* to = static_cast<OUT*>(a.dw);
+  a.dw = workspace;
+  expert_weight_grad<T, float, DIRECT, false><<<grid, T::kThreads, 0, stream>>>(a);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const uint64_t n = static_cast<uint64_t>(a.experts) * a.in * a.out;
+  add_parts<OUT><<<static_cast<uint32_t>((n + kAddThreads * 4 - 1) / (kAddThreads * 4)), kAddThreads, 0, stream>>>(
+      static_cast<const float*>(workspace), to, n, a.parts);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -663,8 +721,19 @@ uint64_t expert_product_blocks(uint64_t pairs, int experts, uint64_t out, bool b
 }
 
 uint64_t expert_weight_grad_blocks(int experts, uint64_t in, uint64_t out, bool direct) {
-  const uint64_t tiles = direct ? weight_grad_tiles<Large>(in, out) : weight_grad_tiles<Middle>(in, out);
+  const uint64_t tiles = direct ? weight_grad_tiles<LargeGrad>(in, out) : weight_grad_tiles<Middle>(in, out);
   return experts * ((tiles - 1) / kXcds + 1) * kXcds;
+}
+
+// Where the tiles leave places on the CUs free and have many rows to go over, the
+// rows are shared: 16,384 pairs of 4 experts, 256 x 512, 28 us instead of 123; but
+// two parts are no faster than one (8,192 pairs of 8 experts, 1,024 x 1,024, 53 us
+// against 48).  A part has at least 256 rows if all experts have as many.
+uint32_t expert_weight_grad_parts(uint64_t pairs, int experts, uint64_t in, uint64_t out) {
+  constexpr uint64_t kPlaces = 512, kMost = 16, kRows = 256;
+  const uint64_t tiles = experts * weight_grad_tiles<LargeGrad>(in, out);
+  const uint64_t parts = std::min({kMost, kPlaces / tiles, pairs / experts / kRows});
+  return parts > 2 ? static_cast<uint32_t>(parts) : 1;
 }
 
 hipError_t launch_expert_product(const ProductArgs& a, bool out_contiguous, bool direct, hipStream_t stream) {
@@ -693,12 +762,13 @@ hipError_t launch_expert_product(const ProductArgs& a, bool out_contiguous, bool
   return hipGetLastError();
 }
 
-hipError_t launch_expert_weight_grad(const WeightGradArgs& a, ar_dtype_t dw_dtype, bool direct, hipStream_t stream) {
+hipError_t launch_expert_weight_grad(const WeightGradArgs& a, ar_dtype_t dw_dtype, bool direct, void* workspace,
+                                     hipStream_t stream) {
   if (dw_dtype == AR_FLOAT32)
-    (direct ? launch_weight_grad<LargeGrad, float, true> : launch_weight_grad<Middle, float, false>)(a, stream);
-  else
-    (direct ? launch_weight_grad<LargeGrad, uint16_t, true> : launch_weight_grad<Middle, uint16_t, false>)(a, stream);
-  return hipGetLastError();
+    return (direct ? launch_weight_grad<LargeGrad, float, true> : launch_weight_grad<Middle, float, false>)(a, workspace,
+                                                                                                            stream);
+  return (direct ? launch_weight_grad<LargeGrad, uint16_t, true> : launch_weight_grad<Middle, uint16_t, false>)(
+      a, workspace, stream);
 }
 
 }  // namespace ar

@@ -135,8 +135,15 @@ ar_status_t ar_expert_matmul(const ar_expert_rows_t* r, const void* weight, size
   return ar::launch_status(ar::enqueue([&] { return ar::launch_expert_product(a, by_out, direct, stream); }));
 }
 
+size_t ar_expert_weight_grad_workspace(size_t pairs, int experts, size_t in, size_t out) {
+  if (experts < 1 || experts > AR_MAX_EXPERTS || in < 1 || out < 1 || in > kMost || out > kMost || pairs > kMost) return 0;
+  const uint32_t parts = ar::expert_weight_grad_parts(pairs, experts, in, out);
+  // (with parts there are at most 256 tiles of 128 x 256 float32)
+  return parts > 1 ? parts * sizeof(float) * experts * in * out : 0;
+}
+
 ar_status_t ar_expert_weight_grad(const ar_expert_rows_t* r, const void* dy, size_t dy_stride, void* dw,
-                                  ar_dtype_t dw_dtype, hipStream_t stream) {
+                                  ar_dtype_t dw_dtype, void* workspace, hipStream_t stream) {
   const ar_status_t st = check(r);
   if (st != AR_SUCCESS) return st;
   if (dw_dtype != AR_FLOAT32 && dw_dtype != AR_BFLOAT16) return AR_ERROR_UNSUPPORTED;
@@ -157,6 +164,8 @@ ar_status_t ar_expert_weight_grad(const ar_expert_rows_t* r, const void* dy, siz
   const bool direct = wide(r->x, r->x_rows, x_stride, r->in) && wide(dy, r->pairs, y_stride, r->out);
   if (ar::expert_weight_grad_blocks(r->experts, r->in, r->out, direct) > ar::kMaxProductBlocks)
     return AR_ERROR_UNSUPPORTED;
+  const uint32_t parts = ar::expert_weight_grad_parts(r->pairs, r->experts, r->in, r->out);
+  if (parts > 1 && (workspace == nullptr || !aligned(workspace, 16))) return AR_ERROR_INVALID_ARGUMENT;
   ar::WeightGradArgs a;
   a.x = r->x;
   a.dy = dy;
@@ -170,10 +179,11 @@ ar_status_t ar_expert_weight_grad(const ar_expert_rows_t* r, const void* dy, siz
   a.in = static_cast<uint32_t>(r->in);
   a.out = static_cast<uint32_t>(r->out);
   a.tiles_n = a.tiles = a.tiles_xcd = 0;
+  a.parts = parts;
   a.experts = r->experts;
   a.token = ar::token_of(r->pairs, r->order != nullptr ? r->top_k : 1);
   return ar::launch_status(
-      ar::enqueue([&] { return ar::launch_expert_weight_grad(a, dw_dtype, direct, stream); }));
+      ar::enqueue([&] { return ar::launch_expert_weight_grad(a, dw_dtype, direct, workspace, stream); }));
 }
 
 ar_status_t ar_expert_combine(const void* y, size_t y_stride, size_t pairs, size_t size, ar_dtype_t dtype,

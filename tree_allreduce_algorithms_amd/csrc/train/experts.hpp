@@ -74,10 +74,14 @@ struct WeightGradArgs {
   uint64_t x_stride, dy_stride;
   uint32_t x_rows, pairs, in, out, tiles_n;
   uint32_t tiles, tiles_xcd;    // of an expert; an XCD's of these
+  uint32_t parts;               // blocks that share a tile's rows
   int32_t experts;
   TokenOf token;
 };
-hipError_t launch_expert_weight_grad(const WeightGradArgs& a, ar_dtype_t dw_dtype, bool direct, hipStream_t stream);
+uint32_t expert_weight_grad_parts(uint64_t pairs, int experts, uint64_t in, uint64_t out);
+// `workspace`: with more than one part, that many float32 arrays of dw's size.
+hipError_t launch_expert_weight_grad(const WeightGradArgs& a, ar_dtype_t dw_dtype, bool direct, void* workspace,
+                                     hipStream_t stream);
 
 struct CombineArgs {
   const void* y;

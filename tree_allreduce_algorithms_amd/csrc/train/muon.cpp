@@ -20,7 +20,9 @@ using ar::MuonTile;
 
 constexpr uint64_t kMost = std::numeric_limits<uintptr_t>::max();
 
-// Tiles are 128 wide from so many of X, and of X X^T, on: fewer leave CUs idle.
+// Tiles are 128 wide from so many of X, and of X X^T, on: fewer leave CUs idle (one
+// of 2,048 x 2,048, 136 squares: 866 us in 64, 924 in 128; four of 1,024 x 1,024 with
+// two of 4,096 x 1,024, 216 squares: 1,170 and 1,050).
 constexpr uint64_t kWideTiles = 256, kWideSquares = 160;
 
 // Where every matrix has at most so many rows and columns, each goes a block in
@@ -145,11 +147,14 @@ Counts count_with(const ar_muon_tensor_t* t, int n, uint64_t side) {
 
 enum class Kind { kSquares, kPolys, kTiles };
 
-// Blocks that run at a time: two of 128 x 128 on a CU, five of 64 x 64.
-uint64_t places(uint32_t) { return 512; }
+// Blocks that run at a time, two on a CU.
+constexpr uint64_t kPlaces = 512;
 
 // A tile's k is split into at most so many parts (one block adds all of them up),
-// none of less steps than kLeast but of a whole tile.
+// none of less than kLeast steps: joining them takes as long as about ten.  One of
+// 4,096 x 4,096: 4,063 us, 4,372 without parts, whose 528 squares would be two
+// rounds; 16 of 256 x 4,096 561 and 609.  With parts of 8 steps 64 of 512 x 512 took
+// 1,092 us instead of 907.
 constexpr uint32_t kMostParts = 8, kLeast = 32;
 
 // The parts of the tiles that are left when all places have had the same number
@@ -203,14 +208,14 @@ Table deal(const ar_muon_tensor_t* t, int n, uint32_t pad, uint32_t side, Kind k
                    [&](uint32_t a, uint32_t b) { return steps_of[shape_of[a]] > steps_of[shape_of[b]]; });
 
   // whole tiles up to a multiple of the places, parts of the others
-  uint64_t whole = total - total % places(side), seen = 0;
+  uint64_t whole = total - total % kPlaces, seen = 0;
   std::vector<Rest> rest;
   for (uint32_t k : matrices) {
     const uint64_t tiles = order[shape_of[k]].size();
     if (seen + tiles > whole) rest.push_back({steps_of[shape_of[k]], seen + tiles - std::max(seen, whole)});
     seen += tiles;
   }
-  const uint32_t each = steps_each(rest, places(side));
+  const uint32_t each = steps_each(rest, kPlaces);
   // groups small enough for the XCDs' loads to come out even
   const uint32_t most = static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(32, total / (4 * ar::kMuonXcds))));
   std::vector<Group> groups;

@@ -167,18 +167,22 @@ template <int SIDE, class G> __global__ __launch_bounds__(kElementThreads) void 
 // The tile of D = A B: A [..][k] with `k` contiguous from row m0 on, B the same
 // from its row n0 on (BR false) or [k][..] from its column n0 on.  All are padded
 // to whole tiles, so nothing is checked.
-constexpr int kProductThreads = 256;
+template <int SIDE> constexpr int kProductThreads = SIDE == 128 ? 512 : 256;
+template <int SIDE> constexpr int kPerSimd = SIDE == 128 ? 4 : 2;
 
 // Two blocks of 128 x 128 with steps of 32 on a CU: 1,390 TFLOP/s of matrix
-// instructions for 131,072 x 1,024 by k = 2,048, against 1,213 of one block of
-// eight waves with steps of 64, and 1,299-1,324 of 256 x 128 and 128 x 256.
+// instructions for 131,072 x 1,024 by k = 2,048, against 1,213 of one block with
+// steps of 64, and 1,299-1,324 of 256 x 128 and 128 x 256.  Eight waves a block:
+// with four, steps of matrices of 512 to 1,024 rows take 3 to 8 % longer, those of
+// 4,096 rows 1 % less.  64 x 64 is for few tiles, one or two on a CU: three steps
+// under way (one of 1,024 x 1,024 220 us, 289 with one).
 template <int SIDE, bool BR> struct Product {
   static constexpr int kStep = kMuonStep;
   using SA = Staged<SIDE, false, kStep, false>;
   using SB = Staged<SIDE, BR, kStep, true>;
-  static constexpr int kWavesM = SIDE == 128 ? 2 : 4, kWavesN = SIDE == 128 ? 2 : 1;
+  static constexpr int kWavesM = 4, kWavesN = SIDE / 64;
   static constexpr int kThreads = kWavesM * kWavesN * kWave;
-  static_assert(kThreads == kProductThreads);
+  static_assert(kThreads == kProductThreads<SIDE>);
   static constexpr int kStage = 2 * (SA::kBytes + SB::kBytes);
   static constexpr int kStages = SIDE == 128 ? 2 : 4, kAhead = kStages - 1;
   static constexpr int kBytes = kStages * kStage;
@@ -352,7 +356,7 @@ __device__ __forceinline__ void store_square(const MuonStepArgs& a, const MuonMa
 // POLY false: gram = X X^T.  POLY true: poly = a I + b gram + c gram gram.  Both are
 // symmetric: tiles above the diagonal are stored a second time, transposed.
 template <int SIDE, bool POLY>
-__global__ __launch_bounds__(kProductThreads, 2) void muon_square(MuonStepArgs a) {
+__global__ __launch_bounds__(kProductThreads<SIDE>, kPerSimd<SIDE>) void muon_square(MuonStepArgs a) {
   using P = Product<SIDE, false>;
   __shared__ __attribute__((aligned(1024))) char lds[P::kBytes];
   const MuonTile t = reinterpret_cast<const MuonTile*>(a.plan + (POLY ? a.polys_at : a.squares_at))[blockIdx.x];
@@ -410,7 +414,7 @@ __device__ __forceinline__ void update_tile(const MuonStepArgs& a, const MuonMat
 
 // X' = poly X; the last one updates the parameters instead.
 template <int SIDE, class T, bool COPY>
-__global__ __launch_bounds__(kProductThreads, 2) void muon_apply(MuonStepArgs a) {
+__global__ __launch_bounds__(kProductThreads<SIDE>, kPerSimd<SIDE>) void muon_apply(MuonStepArgs a) {
   using P = Product<SIDE, true>;
   __shared__ __attribute__((aligned(1024))) char lds[P::kBytes];
   const MuonTile t = reinterpret_cast<const MuonTile*>(a.plan + a.tiles_at)[blockIdx.x];
@@ -678,17 +682,17 @@ hipError_t launch_muon_start(const MuonStepArgs& a, uint32_t tiles, uint32_t sid
 
 hipError_t launch_muon_gram(const MuonStepArgs& a, uint32_t squares, uint32_t side, hipStream_t stream) {
   if (side == 128)
-    muon_square<128, false><<<squares, kProductThreads, 0, stream>>>(a);
+    muon_square<128, false><<<squares, kProductThreads<128>, 0, stream>>>(a);
   else
-    muon_square<64, false><<<squares, kProductThreads, 0, stream>>>(a);
+    muon_square<64, false><<<squares, kProductThreads<64>, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 hipError_t launch_muon_poly(const MuonStepArgs& a, uint32_t squares, uint32_t side, hipStream_t stream) {
   if (side == 128)
-    muon_square<128, true><<<squares, kProductThreads, 0, stream>>>(a);
+    muon_square<128, true><<<squares, kProductThreads<128>, 0, stream>>>(a);
   else
-    muon_square<64, true><<<squares, kProductThreads, 0, stream>>>(a);
+    muon_square<64, true><<<squares, kProductThreads<64>, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -697,7 +701,7 @@ static hipError_t apply(const MuonStepArgs& a, uint32_t tiles, ar_dtype_t param_
   const auto kernel = param_dtype == AR_BFLOAT16 ? muon_apply<SIDE, __bf16, false>
                       : copy                     ? muon_apply<SIDE, float, true>
                                                  : muon_apply<SIDE, float, false>;
-  kernel<<<tiles, kProductThreads, 0, stream>>>(a);
+  kernel<<<tiles, kProductThreads<SIDE>, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -422,9 +422,12 @@ PyObject* expert_weight_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     dw = empty({o.experts, x->size(1), dy->size(1)}, wide ? at::kFloat : at::kBFloat16);
   }
   const ar_expert_rows_t rows = rows_of(o, *x, stride, gather, dy->size(1));
+  const size_t bytes = ar_expert_weight_grad_workspace(rows.pairs, rows.experts, rows.in, rows.out);
+  at::Tensor workspace;
+  if (bytes != 0) workspace = empty({static_cast<int64_t>(bytes)}, at::kByte);
   const ar_status_t status = ar_expert_weight_grad(&rows, dy->const_data_ptr(), dy_stride, dw.data_ptr(),
                                                    dw.scalar_type() == at::kFloat ? AR_FLOAT32 : AR_BFLOAT16,
-                                                   stream_of(a[9]));
+                                                   bytes != 0 ? workspace.data_ptr() : nullptr, stream_of(a[9]));
   if (a[8] != Py_None && status == AR_SUCCESS && !dw.is_inference()) dw.unsafeGetTensorImpl()->bump_version();
   return result(status, {&dw});
   END_HANDLE_TH_ERRORS
