@@ -285,36 +285,114 @@ const at::Tensor* matrix(PyObject* o, const char* what, int64_t rows, int64_t co
   return t;
 }
 
-// What expert_order found: (order, position, offsets, top_k).
+// What the experts' calls need of Python: torch's current device and stream (of
+// a device), the classes of an order and of a library error, attributes' names.
+struct Hooks {
+  PyObject *device, *stream, *order_class, *error_class;
+  PyObject *order, *position, *offsets, *top_k;
+} hooks;
+
+// hooks(current device, current stream, ExpertOrder, ArError)
+PyObject* set_hooks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arguments(n, 4)) return nullptr;
+  for (Py_ssize_t i = 0; i < 4; ++i) Py_INCREF(a[i]);
+  hooks = {a[0], a[1], a[2], a[3], PyUnicode_InternFromString("order"), PyUnicode_InternFromString("position"),
+           PyUnicode_InternFromString("offsets"), PyUnicode_InternFromString("top_k")};
+  Py_RETURN_NONE;
+}
+
+// The device of the calls' first tensor, if it is the current one, and its current
+// stream.  Otherwise false, with an error, or without one where another device is
+// current: the caller has to change to it (and gets None).
+bool on_current(PyObject* first, const char* what, hipStream_t* stream) {
+  const at::Tensor* t = gpu_tensor(first, what);
+  if (t == nullptr) return false;
+  PyObject* current = PyObject_CallNoArgs(hooks.device);
+  if (current == nullptr) return false;
+  const long device = PyLong_AsLong(current);
+  PyObject* handle = device == t->get_device() ? PyObject_CallOneArg(hooks.stream, current) : nullptr;
+  Py_DECREF(current);
+  if (handle == nullptr) return false;
+  *stream = stream_of(handle);
+  Py_DECREF(handle);
+  return !PyErr_Occurred();
+}
+
+PyObject* elsewhere() {
+  if (PyErr_Occurred()) return nullptr;
+  Py_RETURN_NONE;
+}
+
+// The tensor, or an ArError.
+PyObject* checked(ar_status_t status, const char* call, const at::Tensor& t) {
+  if (status == AR_SUCCESS) return THPVariable_Wrap(t);
+  PyObject* error = PyObject_CallFunction(hooks.error_class, "is", static_cast<int>(status), call);
+  if (error != nullptr) PyErr_SetObject(hooks.error_class, error);
+  Py_XDECREF(error);
+  return nullptr;
+}
+PyObject* checked(ar_status_t status, const char* call, std::initializer_list<const at::Tensor*> tensors) {
+  PyObject* out = checked(status, call, **tensors.begin());
+  if (out == nullptr) return nullptr;
+  PyObject* tuple = PyTuple_New(static_cast<Py_ssize_t>(tensors.size()));
+  if (tuple == nullptr) {
+    Py_DECREF(out);
+    return nullptr;
+  }
+  PyTuple_SET_ITEM(tuple, 0, out);
+  for (size_t i = 1; i < tensors.size(); ++i)
+    PyTuple_SET_ITEM(tuple, static_cast<Py_ssize_t>(i), THPVariable_Wrap(**(tensors.begin() + i)));
+  return tuple;
+}
+
+// What expert_order found.  Its attributes are plain, so what the kernels read is
+// checked; their tensors are held for the call.
 struct Order {
-  const at::Tensor *order, *position, *offsets;
+  at::Tensor order, position, offsets;
   int64_t pairs, tokens;
   int experts, top_k;
 };
 
-bool check_order(PyObject* const* a, Order* o) {
-  const long k = PyLong_AsLong(a[3]);
-  if (k == -1 && PyErr_Occurred()) return false;
-  if ((o->order = int32_tensor(a[0], "order", -1)) == nullptr) return false;
-  o->pairs = o->order->numel();
-  if ((o->position = int32_tensor(a[1], "position", o->pairs)) == nullptr ||
-      (o->offsets = int32_tensor(a[2], "offsets", -1)) == nullptr)
+// An attribute that is a contiguous int32 tensor of `count` elements (any if negative).
+bool attribute(PyObject* from, PyObject* name, const char* what, int64_t count, at::Tensor* to) {
+  PyObject* o = PyObject_GetAttr(from, name);
+  if (o == nullptr) return false;
+  const at::Tensor* t = int32_tensor(o, what, count);
+  if (t != nullptr) *to = *t;
+  Py_DECREF(o);
+  return t != nullptr;
+}
+
+bool check_order(PyObject* from, Order* o) {
+  if (!PyObject_TypeCheck(from, reinterpret_cast<PyTypeObject*>(hooks.order_class))) {
+    fail(PyExc_TypeError, "order must be what expert_order returned");
     return false;
-  if (k < 1 || k > INT32_MAX || o->pairs % k != 0 || o->offsets->numel() < 2 ||
-      o->offsets->numel() > AR_MAX_EXPERTS + 1 || o->position->device() != o->order->device() ||
-      o->offsets->device() != o->order->device()) {
+  }
+  PyObject* number = PyObject_GetAttr(from, hooks.top_k);
+  if (number == nullptr) return false;
+  const long k = PyLong_AsLong(number);
+  Py_DECREF(number);
+  if (k == -1 && PyErr_Occurred()) return false;
+  if (!attribute(from, hooks.order, "order", -1, &o->order)) return false;
+  o->pairs = o->order.numel();
+  if (!attribute(from, hooks.position, "position", o->pairs, &o->position) ||
+      !attribute(from, hooks.offsets, "offsets", -1, &o->offsets))
+    return false;
+  if (k < 1 || k > INT32_MAX || o->pairs % k != 0 || o->offsets.numel() < 2 ||
+      o->offsets.numel() > AR_MAX_EXPERTS + 1 || o->position.device() != o->order.device() ||
+      o->offsets.device() != o->order.device()) {
     fail(PyExc_ValueError, "this is not the order of top_k choices a token");
     return false;
   }
   o->top_k = static_cast<int>(k);
   o->tokens = o->pairs / k;
-  o->experts = static_cast<int>(o->offsets->numel() - 1);
+  o->experts = static_cast<int>(o->offsets.numel() - 1);
   return true;
 }
 
 bool same_device(const Order& o, std::initializer_list<const at::Tensor*> tensors) {
   for (const at::Tensor* t : tensors)
-    if (t->device() != o.order->device()) {
+    if (t->device() != o.order.device()) {
       fail(PyExc_ValueError, "all tensors must be on the order's device");
       return false;
     }
@@ -326,9 +404,9 @@ ar_expert_rows_t rows_of(const Order& o, const at::Tensor& x, size_t stride, boo
   r.x = x.const_data_ptr();
   r.x_rows = static_cast<size_t>(x.size(0));
   r.x_stride = stride;
-  r.order = gather ? static_cast<const int32_t*>(o.order->const_data_ptr()) : nullptr;
+  r.order = gather ? static_cast<const int32_t*>(o.order.const_data_ptr()) : nullptr;
   r.top_k = o.top_k;
-  r.offsets = static_cast<const int32_t*>(o.offsets->const_data_ptr());
+  r.offsets = static_cast<const int32_t*>(o.offsets.const_data_ptr());
   r.pairs = static_cast<size_t>(o.pairs);
   r.experts = o.experts;
   r.in = static_cast<size_t>(x.size(1));
@@ -337,10 +415,14 @@ ar_expert_rows_t rows_of(const Order& o, const at::Tensor& x, size_t stride, boo
   return r;
 }
 
-// expert_order(indices, experts, stream) -> (status, order, position, offsets)
+// The calls below return None where another device than their tensors' is current.
+
+// expert_order(indices, experts) -> (order, position, offsets)
 PyObject* expert_order(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!arguments(n, 3)) return nullptr;
+  if (!arguments(n, 2)) return nullptr;
+  hipStream_t stream;
+  if (!on_current(a[0], "indices", &stream)) return elsewhere();
   const at::Tensor* indices = int32_tensor(a[0], "indices", -1);
   if (indices == nullptr) return nullptr;
   const long experts = PyLong_AsLong(a[1]);
@@ -358,18 +440,20 @@ PyObject* expert_order(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const ar_status_t status = ar_expert_order(
       static_cast<const int32_t*>(indices->const_data_ptr()), static_cast<size_t>(pairs), static_cast<int>(experts),
       static_cast<int32_t*>(order.data_ptr()), static_cast<int32_t*>(position.data_ptr()),
-      static_cast<int32_t*>(offsets.data_ptr()), bytes != 0 ? workspace.data_ptr() : nullptr, stream_of(a[2]));
-  return result(status, {&order, &position, &offsets});
+      static_cast<int32_t*>(offsets.data_ptr()), bytes != 0 ? workspace.data_ptr() : nullptr, stream);
+  return checked(status, "expert_order", {&order, &position, &offsets});
   END_HANDLE_TH_ERRORS
 }
 
-// expert_matmul(x, weight, order, position, offsets, top_k, gather, stream) -> (status, y)
+// expert_matmul(x, weight, order, gather) -> y
 PyObject* expert_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!arguments(n, 8)) return nullptr;
+  if (!arguments(n, 4)) return nullptr;
   Order o;
-  if (!check_order(a + 2, &o)) return nullptr;
-  const int gather = PyObject_IsTrue(a[6]);
+  hipStream_t stream;
+  if (!check_order(a[2], &o)) return nullptr;
+  if (!on_current(a[0], "x", &stream)) return elsewhere();
+  const int gather = PyObject_IsTrue(a[3]);
   if (gather < 0) return nullptr;
   size_t stride;
   const at::Tensor* x = matrix(a[0], "x", gather ? o.tokens : o.pairs, -1, &stride);
@@ -389,26 +473,28 @@ PyObject* expert_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor y = empty({o.pairs, out}, at::kBFloat16);
   const ar_status_t status = ar_expert_matmul(&rows, w->const_data_ptr(), static_cast<size_t>(w->stride(0)),
                                               static_cast<size_t>(si), static_cast<size_t>(so), y.data_ptr(),
-                                              stream_of(a[7]));
-  return result(status, {&y});
+                                              stream);
+  return checked(status, "expert_matmul", y);
   END_HANDLE_TH_ERRORS
 }
 
-// expert_weight_grad(x, dy, order, position, offsets, top_k, gather, wide, out, stream) -> (status, dw)
+// expert_weight_grad(x, dy, order, gather, wide, out) -> dw
 PyObject* expert_weight_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!arguments(n, 10)) return nullptr;
+  if (!arguments(n, 6)) return nullptr;
   Order o;
-  if (!check_order(a + 2, &o)) return nullptr;
-  const int gather = PyObject_IsTrue(a[6]), wide = PyObject_IsTrue(a[7]);
+  hipStream_t stream;
+  if (!check_order(a[2], &o)) return nullptr;
+  if (!on_current(a[0], "x", &stream)) return elsewhere();
+  const int gather = PyObject_IsTrue(a[3]), wide = PyObject_IsTrue(a[4]);
   if (gather < 0 || wide < 0) return nullptr;
   size_t stride, dy_stride;
   const at::Tensor* x = matrix(a[0], "x", gather ? o.tokens : o.pairs, -1, &stride);
   const at::Tensor* dy = x == nullptr ? nullptr : matrix(a[1], "dy", o.pairs, -1, &dy_stride);
   if (dy == nullptr || !same_device(o, {x, dy})) return nullptr;
   at::Tensor dw;
-  if (a[8] != Py_None) {
-    const at::Tensor* out = gpu_tensor(a[8], "out");
+  if (a[5] != Py_None) {
+    const at::Tensor* out = gpu_tensor(a[5], "out");
     if (out == nullptr) return nullptr;
     if (out->scalar_type() != at::kFloat && out->scalar_type() != at::kBFloat16)
       return fail(PyExc_TypeError, "out must be float32 or bfloat16, not %s", c10::toString(out->scalar_type()));
@@ -427,9 +513,9 @@ PyObject* expert_weight_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (bytes != 0) workspace = empty({static_cast<int64_t>(bytes)}, at::kByte);
   const ar_status_t status = ar_expert_weight_grad(&rows, dy->const_data_ptr(), dy_stride, dw.data_ptr(),
                                                    dw.scalar_type() == at::kFloat ? AR_FLOAT32 : AR_BFLOAT16,
-                                                   bytes != 0 ? workspace.data_ptr() : nullptr, stream_of(a[9]));
-  if (a[8] != Py_None && status == AR_SUCCESS && !dw.is_inference()) dw.unsafeGetTensorImpl()->bump_version();
-  return result(status, {&dw});
+                                                   bytes != 0 ? workspace.data_ptr() : nullptr, stream);
+  if (a[5] != Py_None && status == AR_SUCCESS && !dw.is_inference()) dw.unsafeGetTensorImpl()->bump_version();
+  return checked(status, "expert_weight_grad", dw);
   END_HANDLE_TH_ERRORS
 }
 
@@ -449,46 +535,50 @@ bool check_weights(PyObject* p, const Order& o, const float** at) {
   return same_device(o, {t});
 }
 
-// expert_combine(y, order, position, offsets, top_k, weights, stream) -> (status, out)
+// expert_combine(y, order, weights) -> out
 PyObject* expert_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!arguments(n, 7)) return nullptr;
+  if (!arguments(n, 3)) return nullptr;
   Order o;
-  if (!check_order(a + 1, &o)) return nullptr;
+  hipStream_t stream;
+  if (!check_order(a[1], &o)) return nullptr;
+  if (!on_current(a[0], "y", &stream)) return elsewhere();
   size_t stride;
   const at::Tensor* y = matrix(a[0], "y", o.pairs, -1, &stride);
   if (y == nullptr || !same_device(o, {y})) return nullptr;
   const float* weights = nullptr;
-  if (a[5] != Py_None && !check_weights(a[5], o, &weights)) return nullptr;
+  if (a[2] != Py_None && !check_weights(a[2], o, &weights)) return nullptr;
   const at::Tensor out = empty({o.tokens, y->size(1)}, at::kBFloat16);
   const ar_status_t status = ar_expert_combine(
       y->const_data_ptr(), stride, static_cast<size_t>(o.pairs), static_cast<size_t>(y->size(1)), AR_BFLOAT16,
-      static_cast<const int32_t*>(o.position->const_data_ptr()), weights, static_cast<size_t>(o.tokens), o.top_k,
-      out.data_ptr(), stream_of(a[6]));
-  return result(status, {&out});
+      static_cast<const int32_t*>(o.position.const_data_ptr()), weights, static_cast<size_t>(o.tokens), o.top_k,
+      out.data_ptr(), stream);
+  return checked(status, "expert_combine", out);
   END_HANDLE_TH_ERRORS
 }
 
-// expert_combine_grad(dout, y, order, position, offsets, top_k, weights, stream) -> (status, dy, dweights)
+// expert_combine_grad(dout, y, order, weights) -> (dy, dweights)
 PyObject* expert_combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!arguments(n, 8)) return nullptr;
+  if (!arguments(n, 4)) return nullptr;
   Order o;
-  if (!check_order(a + 2, &o)) return nullptr;
+  hipStream_t stream;
+  if (!check_order(a[2], &o)) return nullptr;
+  if (!on_current(a[0], "dout", &stream)) return elsewhere();
   size_t dout_stride, y_stride;
   const at::Tensor* y = matrix(a[1], "y", o.pairs, -1, &y_stride);
   const at::Tensor* dout = y == nullptr ? nullptr : matrix(a[0], "dout", o.tokens, y->size(1), &dout_stride);
   if (dout == nullptr || !same_device(o, {y, dout})) return nullptr;
   const float* weights = nullptr;
-  if (!check_weights(a[6], o, &weights)) return nullptr;
+  if (!check_weights(a[3], o, &weights)) return nullptr;
   const at::Tensor dy = empty({o.pairs, y->size(1)}, at::kBFloat16);
   const at::Tensor dweights = empty({o.tokens, o.top_k}, at::kFloat);
   const ar_status_t status = ar_expert_combine_grad(
       dout->const_data_ptr(), dout_stride, y->const_data_ptr(), y_stride, static_cast<size_t>(o.pairs),
-      static_cast<size_t>(y->size(1)), AR_BFLOAT16, static_cast<const int32_t*>(o.position->const_data_ptr()),
-      static_cast<const int32_t*>(o.offsets->const_data_ptr()), o.experts, weights, static_cast<size_t>(o.tokens),
-      o.top_k, dy.data_ptr(), static_cast<float*>(dweights.data_ptr()), stream_of(a[7]));
-  return result(status, {&dy, &dweights});
+      static_cast<size_t>(y->size(1)), AR_BFLOAT16, static_cast<const int32_t*>(o.position.const_data_ptr()),
+      static_cast<const int32_t*>(o.offsets.const_data_ptr()), o.experts, weights, static_cast<size_t>(o.tokens),
+      o.top_k, dy.data_ptr(), static_cast<float*>(dweights.data_ptr()), stream);
+  return checked(status, "expert_combine_grad", {&dy, &dweights});
   END_HANDLE_TH_ERRORS
 }
 
@@ -515,6 +605,7 @@ PyMethodDef methods[] = {
     {"route", as_function(route), METH_FASTCALL, nullptr},
     {"route_grad", as_function(route_grad), METH_FASTCALL, nullptr},
     {"dequantize", as_function(dequantize), METH_FASTCALL, nullptr},
+    {"hooks", as_function(set_hooks), METH_FASTCALL, nullptr},
     {"expert_order", as_function(expert_order), METH_FASTCALL, nullptr},
     {"expert_matmul", as_function(expert_matmul), METH_FASTCALL, nullptr},
     {"expert_weight_grad", as_function(expert_weight_grad), METH_FASTCALL, nullptr},

@@ -25,7 +25,7 @@ stream, or on ``stream``, which is treated as in ``training``.
 
 import torch
 
-from .binding import SUCCESS, ArError
+from .binding import ArError
 from .training import _current_device, _current_stream, _in_use, _stream_of, _training
 
 
@@ -40,36 +40,21 @@ class ExpertOrder:
     def __init__(self, order, position, offsets, top_k):
         self.order, self.position, self.offsets, self.top_k = order, position, offsets, top_k
 
-    def _parts(self):
-        return self.order, self.position, self.offsets, self.top_k
+
+_training.hooks(_current_device, _current_stream, ExpertOrder, ArError)
 
 
-def _device(t, what):
-    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
-    if dev < 0:
-        raise TypeError(f"{what} must be GPU tensors")
-    return dev
-
-
-def _elsewhere(call, dev, stream, used):
-    """`call()` with `stream` (or the current one of `dev`) current; `used` are
-    the tensors that it reads or writes there."""
-    with torch.cuda.stream(_stream_of(stream, dev)):
+def _elsewhere(call, first, stream, used, order=None):
+    """`call()` with `stream` current, or (None) the current stream of the device
+    of `first`; `used` and the order's tensors are what it reads or writes."""
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise TypeError("tensors must be GPU tensors")
+    with torch.cuda.stream(_stream_of(stream, first.get_device())):
         result = call()
+    if order is not None:
+        used += (order.order, order.position, order.offsets)
     _in_use(stream, [t for t in used if isinstance(t, torch.Tensor)])
     return result
-
-
-def _checked(result, what):
-    if result[0] != SUCCESS:
-        raise ArError(result[0], what)
-    return result[1:] if len(result) > 2 else result[1]
-
-
-def _order_of(order):
-    if not isinstance(order, ExpertOrder):
-        raise TypeError("order must be what expert_order returned")
-    return order._parts()
 
 
 def expert_order(indices, experts, stream=None):
@@ -78,10 +63,9 @@ def expert_order(indices, experts, stream=None):
     contiguous int32 GPU tensor [..., top_k], for instance a routing's or one
     rank's of it; a number outside [0, experts) is no expert.  Up to 1,024
     experts."""
-    dev = _device(indices, "indices")
-    if stream is not None or _current_device() != dev:
-        return _elsewhere(lambda: expert_order(indices, experts), dev, stream, (indices,))
-    found = _checked(_training.expert_order(indices, experts, _current_stream(dev)), "expert_order")
+    found = _training.expert_order(indices, experts) if stream is None else None
+    if found is None:
+        return _elsewhere(lambda: expert_order(indices, experts), indices, stream, (indices,))
     return ExpertOrder(*found, indices.shape[-1])
 
 
@@ -93,12 +77,10 @@ def expert_matmul(x, weight, order, gather=False, stream=None):
     which each pair takes its token's row; rows may be strided.  ``weight`` is
     [experts, in, out], an expert's rows or its columns contiguous, so that
     ``weight.transpose(1, 2)`` gives the gradient with respect to the rows."""
-    parts = _order_of(order)
-    dev = _device(x, "x")
-    if stream is not None or _current_device() != dev:
-        return _elsewhere(lambda: expert_matmul(x, weight, order, gather), dev, stream,
-                          (x, weight, *parts[:3]))
-    return _checked(_training.expert_matmul(x, weight, *parts, gather, _current_stream(dev)), "expert_matmul")
+    y = _training.expert_matmul(x, weight, order, gather) if stream is None else None
+    if y is None:
+        return _elsewhere(lambda: expert_matmul(x, weight, order, gather), x, stream, (x, weight), order)
+    return y
 
 
 def expert_weight_grad(x, dy, order, gather=False, dtype=torch.float32, out=None, stream=None):
@@ -108,15 +90,12 @@ def expert_weight_grad(x, dy, order, gather=False, dtype=torch.float32, out=None
     ``x`` and ``gather`` are those of the product, ``dy`` [pairs, out] is the
     gradient of its rows.  ``dtype`` is float32 or bfloat16; ``out``, contiguous
     and of either type, is overwritten instead of a new tensor."""
-    parts = _order_of(order)
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"dtype must be float32 or bfloat16, not {dtype}")
-    dev = _device(x, "x")
-    if stream is not None or _current_device() != dev:
-        return _elsewhere(lambda: expert_weight_grad(x, dy, order, gather, dtype, out), dev, stream,
-                          (x, dy, out, *parts[:3]))
-    dw = _checked(_training.expert_weight_grad(x, dy, *parts, gather, dtype == torch.float32, out,
-                                               _current_stream(dev)), "expert_weight_grad")
+    dw = _training.expert_weight_grad(x, dy, order, gather, dtype is torch.float32, out) if stream is None else None
+    if dw is None:
+        return _elsewhere(lambda: expert_weight_grad(x, dy, order, gather, dtype, out), x, stream, (x, dy, out),
+                          order)
     return dw if out is None else out
 
 
@@ -125,11 +104,10 @@ def expert_combine(y, order, weights=None, stream=None):
     token's choices, times ``weights`` (float32, one a pair; None: 1), added up
     in float32 in the order of the choices (see ar_expert_combine).  Without
     weights it is also the gradient of the rows that ``gather`` takes."""
-    parts = _order_of(order)
-    dev = _device(y, "y")
-    if stream is not None or _current_device() != dev:
-        return _elsewhere(lambda: expert_combine(y, order, weights), dev, stream, (y, weights, *parts[:3]))
-    return _checked(_training.expert_combine(y, *parts, weights, _current_stream(dev)), "expert_combine")
+    sums = _training.expert_combine(y, order, weights) if stream is None else None
+    if sums is None:
+        return _elsewhere(lambda: expert_combine(y, order, weights), y, stream, (y, weights), order)
+    return sums
 
 
 def expert_combine_grad(dout, y, order, weights, stream=None):
@@ -137,10 +115,8 @@ def expert_combine_grad(dout, y, order, weights, stream=None):
     size]: those of the rows, [pairs, size] bfloat16 (0 for rows without a
     pair), and of the weights, [tokens, top_k] float32 (0 for a choice without
     an expert)."""
-    parts = _order_of(order)
-    dev = _device(dout, "dout")
-    if stream is not None or _current_device() != dev:
-        return _elsewhere(lambda: expert_combine_grad(dout, y, order, weights), dev, stream,
-                          (dout, y, weights, *parts[:3]))
-    return _checked(_training.expert_combine_grad(dout, y, *parts, weights, _current_stream(dev)),
-                    "expert_combine_grad")
+    grads = _training.expert_combine_grad(dout, y, order, weights) if stream is None else None
+    if grads is None:
+        return _elsewhere(lambda: expert_combine_grad(dout, y, order, weights), dout, stream, (dout, y, weights),
+                          order)
+    return grads
