@@ -301,6 +301,67 @@ def test_sums_of_views():
         assert torch.equal(a, b)
 
 
+# --- the ends of the ranges ---------------------------------------------------------
+
+def test_no_tokens():
+    o = ar.expert_order(torch.zeros(0, 4, dtype=torch.int32, device=DEV), 5)
+    x, w = torch.empty(0, 24, dtype=BF16, device=DEV), torch.randn(5, 24, 32, device=DEV).to(BF16)
+    y = ar.expert_matmul(x, w, o, gather=True)
+    assert y.shape == (0, 32) and ar.expert_matmul(x, w, o).shape == (0, 32)
+    g = torch.empty(0, 4, device=DEV)
+    assert ar.expert_combine(y, o, g).shape == (0, 32)
+    dy, dg = ar.expert_combine_grad(torch.empty(0, 32, dtype=BF16, device=DEV), y, o, g)
+    assert dy.shape == (0, 32) and dg.shape == (0, 4)
+    dw = ar.expert_weight_grad(x, dy, o, gather=True)
+    assert dw.shape == (5, 24, 32) and not dw.any()
+
+
+def test_many_choices_of_few_tokens():
+    """pairs * top_k past 32 bits: a pair's token by division."""
+    idx = choices(3, 60_000, 7, "even", 4)
+    order, _, offsets = order_of(idx, 7)
+    o = ar.expert_order(torch.from_numpy(idx).to(DEV), 7)
+    rng = np.random.default_rng(6)
+    x, w = bf16(rng, 3, 16), bf16(rng, 7, 16, 8)
+    want, size = grouped(x, w, order, offsets, 60_000, True)
+    near(ar.expert_matmul(x, w, o, gather=True), want, size, 16, "y")
+    dy = bf16(rng, 180_000, 8)
+    dw = ar.expert_weight_grad(x, dy, o, gather=True)
+    token = torch.from_numpy(order.astype(np.int64)).to(DEV) // 60_000
+    for e in range(7):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        xs, d = x[token[lo:hi]].double().t().contiguous(), dy[lo:hi].double()
+        near(dw[e], xs @ d, xs.abs() @ d.abs(), hi - lo, f"dw {e}", stored=False)
+
+
+@pytest.mark.parametrize("n_in", [64, 61])
+def test_rows_past_32_bits(n_in):
+    """x's and dy's rows beyond 4 GiB from their beginning, y's too."""
+    tokens, k, experts, n_out, far = 40_000, 2, 3, 32_768, 65_536
+    idx = choices(tokens, k, experts, "even", 7)
+    order, _, offsets = order_of(idx, experts)
+    o = ar.expert_order(torch.from_numpy(idx).to(DEV), experts)
+    rng = np.random.default_rng(8)
+    small = bf16(rng, tokens, n_in)
+    x = torch.zeros(tokens, far, dtype=BF16, device=DEV)[:, :n_in].copy_(small)
+    w = bf16(rng, experts, n_in, n_out)
+    y = ar.expert_matmul(x, w, o, gather=True)              # 80,000 x 32,768: 5.2 GB
+    pairs = torch.from_numpy(order.astype(np.int64)).to(DEV)
+    for i in (0, 1, 39_999, 65_536, 79_999):
+        e = int(np.searchsorted(offsets, i, side="right")) - 1
+        row = small[pairs[i] // k].double()
+        near(y[i:i + 1], (row @ w[e].double())[None], (row.abs() @ w[e].double().abs())[None], n_in, f"y {i}")
+    out = ar.expert_combine(y, o)
+    position = torch.from_numpy(order_of(idx, experts)[1].astype(np.int64)).to(DEV).view(tokens, k)
+    for t in (0, 20_000, 39_999):
+        rows = y[position[t]].double()
+        near(out[t:t + 1], rows.sum(0)[None], rows.abs().sum(0)[None], k, f"out {t}")
+    dw = ar.expert_weight_grad(x, y[:, :24], o, gather=True)      # dy's rows 65,536 bytes apart
+    lo, hi = int(offsets[2]), int(offsets[3])
+    xs, d = small[pairs[lo:hi] // k].double().t().contiguous(), y[lo:hi, :24].double()
+    near(dw[2], xs @ d, xs.abs() @ d.abs(), hi - lo, "dw", stored=False)
+
+
 # --- a layer, as it is used -----------------------------------------------------------
 
 def test_gradients_of_a_layer():
@@ -346,9 +407,10 @@ def test_gradients_of_a_layer():
     # one direction of W1 by differences of the formula
     V = torch.from_numpy(rng.standard_normal(w1.shape)).to(DEV)
     eps = 1e-6
-    slope = ((layer(X, W1 + eps * V, W2, gate) - layer(X, W1 - eps * V, W2, gate)) * dout.double()).sum() / (2 * eps)
+    with torch.no_grad():
+        slope = ((layer(X, W1 + eps * V, W2, gate) - layer(X, W1 - eps * V, W2, gate)) * dout.double()).sum() / (2 * eps)
     scale = float((dw1.double() * V).norm())
-    assert abs(float((dw1.double() * V).sum() - slope)) <= 2 * 3 * HALF * scale * 3
+    assert abs(float((dw1.double() * V).sum()) - float(slope)) <= 2 * 3 * HALF * scale * 3
 
 
 # --- streams, graphs, refusals -----------------------------------------------------------

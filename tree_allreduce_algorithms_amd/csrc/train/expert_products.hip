@@ -686,27 +686,13 @@ template <class T, bool BR, bool DIRECT> void launch_product(ProductArgs a, hipS
         <<<grid, T::kThreads, 0, stream>>>(a);
 }
 
-template <class T, class OUT, bool DIRECT>
-hipError_t launch_weight_grad(WeightGradArgs a, void* workspace, hipStream_t stream) {
+template <class T, class OUT, bool DIRECT> void launch_weight_grad(WeightGradArgs a, hipStream_t stream) {
   a.tiles_n = static_cast<uint32_t>(tiles_n<T>(a.out));
   a.tiles = static_cast<uint32_t>(weight_grad_tiles<T>(a.in, a.out));
   a.tiles_xcd = (a.tiles - 1) / kXcds + 1;
-  const dim3 grid(a.experts * a.tiles_xcd * kXcds, a.parts);
-  if (a.parts == 1) {
-    (past_caches(a.dw, static_cast<uint64_t>(a.experts) * a.in, a.out * sizeof(OUT)) ? expert_weight_grad<T, OUT, DIRECT, true>
-                                                                                     : expert_weight_grad<T, OUT, DIRECT, false>)
-        <<<grid, T::kThreads, 0, stream>>>(a);
-    return hipGetLastError();
-  }
-  OUT* to = static_cast<OUT*>(a.dw);
-  a.dw = workspace;
-  expert_weight_grad<T, float, DIRECT, false><<<grid, T::kThreads, 0, stream>>>(a);
-  const hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  const uint64_t n = static_cast<uint64_t>(a.experts) * a.in * a.out;
-  add_parts<OUT><<<static_cast<uint32_t>((n + kAddThreads * 4 - 1) / (kAddThreads * 4)), kAddThreads, 0, stream>>>(
-      static_cast<const float*>(workspace), to, n, a.parts);
-  return hipGetLastError();
+  const bool past = a.parts == 1 && past_caches(a.dw, static_cast<uint64_t>(a.experts) * a.in, a.out * sizeof(OUT));
+  (past ? expert_weight_grad<T, OUT, DIRECT, true> : expert_weight_grad<T, OUT, DIRECT, false>)
+      <<<dim3(a.experts * a.tiles_xcd * kXcds, a.parts), T::kThreads, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -762,13 +748,23 @@ hipError_t launch_expert_product(const ProductArgs& a, bool out_contiguous, bool
   return hipGetLastError();
 }
 
-hipError_t launch_expert_weight_grad(const WeightGradArgs& a, ar_dtype_t dw_dtype, bool direct, void* workspace,
-                                     hipStream_t stream) {
+hipError_t launch_expert_weight_grad(const WeightGradArgs& a, ar_dtype_t dw_dtype, bool direct, hipStream_t stream) {
   if (dw_dtype == AR_FLOAT32)
-    return (direct ? launch_weight_grad<LargeGrad, float, true> : launch_weight_grad<Middle, float, false>)(a, workspace,
-                                                                                                            stream);
-  return (direct ? launch_weight_grad<LargeGrad, uint16_t, true> : launch_weight_grad<Middle, uint16_t, false>)(
-      a, workspace, stream);
+    (direct ? launch_weight_grad<LargeGrad, float, true> : launch_weight_grad<Middle, float, false>)(a, stream);
+  else
+    (direct ? launch_weight_grad<LargeGrad, uint16_t, true> : launch_weight_grad<Middle, uint16_t, false>)(a, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_add_parts(const WeightGradArgs& a, void* dw, ar_dtype_t dw_dtype, hipStream_t stream) {
+  const uint64_t n = static_cast<uint64_t>(a.experts) * a.in * a.out;
+  const dim3 grid(static_cast<uint32_t>((n + kAddThreads * 4 - 1) / (kAddThreads * 4)));
+  const float* from = static_cast<const float*>(a.dw);
+  if (dw_dtype == AR_FLOAT32)
+    add_parts<float><<<grid, kAddThreads, 0, stream>>>(from, static_cast<float*>(dw), n, a.parts);
+  else
+    add_parts<uint16_t><<<grid, kAddThreads, 0, stream>>>(from, static_cast<uint16_t*>(dw), n, a.parts);
+  return hipGetLastError();
 }
 
 }  // namespace ar

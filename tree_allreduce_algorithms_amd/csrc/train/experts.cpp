@@ -93,7 +93,10 @@ ar_status_t ar_expert_order(const int32_t* indices, size_t pairs, int experts, i
   a.block_pairs = static_cast<uint32_t>(((pairs + blocks - 1) / blocks + unit - 1) / unit * unit);
   if (a.block_pairs == 0) a.block_pairs = unit;
   a.blocks = pairs == 0 ? 1 : static_cast<uint32_t>((pairs - 1) / a.block_pairs + 1);
-  return ar::launch_status(ar::enqueue([&] { return ar::launch_expert_order(a, stream); }));
+  hipError_t err = hipSuccess;
+  if (a.blocks > 1) err = ar::enqueue([&] { return ar::launch_expert_order_count(a, stream); });
+  if (err == hipSuccess) err = ar::enqueue([&] { return ar::launch_expert_order_place(a, stream); });
+  return ar::launch_status(err);
 }
 
 ar_status_t ar_expert_matmul(const ar_expert_rows_t* r, const void* weight, size_t expert_stride,
@@ -182,8 +185,12 @@ ar_status_t ar_expert_weight_grad(const ar_expert_rows_t* r, const void* dy, siz
   a.parts = parts;
   a.experts = r->experts;
   a.token = ar::token_of(r->pairs, r->order != nullptr ? r->top_k : 1);
-  return ar::launch_status(
-      ar::enqueue([&] { return ar::launch_expert_weight_grad(a, dw_dtype, direct, workspace, stream); }));
+  if (parts > 1) a.dw = workspace;
+  hipError_t err = ar::enqueue(
+      [&] { return ar::launch_expert_weight_grad(a, parts > 1 ? AR_FLOAT32 : dw_dtype, direct, stream); });
+  if (err == hipSuccess && parts > 1)
+    err = ar::enqueue([&] { return ar::launch_expert_add_parts(a, dw, dw_dtype, stream); });
+  return ar::launch_status(err);
 }
 
 ar_status_t ar_expert_combine(const void* y, size_t y_stride, size_t pairs, size_t size, ar_dtype_t dtype,

@@ -29,7 +29,9 @@ struct OrderArgs {
   int32_t* offsets;
   uint32_t* counts;       // [blocks][experts], more than one block
 };
-hipError_t launch_expert_order(const OrderArgs& a, hipStream_t stream);
+// Each block's pairs of each expert (more than one block); the order itself.
+hipError_t launch_expert_order_count(const OrderArgs& a, hipStream_t stream);
+hipError_t launch_expert_order_place(const OrderArgs& a, hipStream_t stream);
 
 // The token of a pair, pair / top_k: by a product with `reciprocal` = ceil(2^32 /
 // top_k) where pairs * top_k <= 2^32 makes that exact, else (0) by a division.
@@ -79,9 +81,10 @@ struct WeightGradArgs {
   TokenOf token;
 };
 uint32_t expert_weight_grad_parts(uint64_t pairs, int experts, uint64_t in, uint64_t out);
-// `workspace`: with more than one part, that many float32 arrays of dw's size.
-hipError_t launch_expert_weight_grad(const WeightGradArgs& a, ar_dtype_t dw_dtype, bool direct, void* workspace,
-                                     hipStream_t stream);
+// With more than one part a.dw has that many float32 arrays of its size, which the
+// second call adds up into dw.
+hipError_t launch_expert_weight_grad(const WeightGradArgs& a, ar_dtype_t dw_dtype, bool direct, hipStream_t stream);
+hipError_t launch_expert_add_parts(const WeightGradArgs& a, void* dw, ar_dtype_t dw_dtype, hipStream_t stream);
 
 struct CombineArgs {
   const void* y;

@@ -283,14 +283,13 @@ __global__ __launch_bounds__(kSumThreads) void combine_grad(CombineArgs a) {
 constexpr uint64_t kPastBytes = 32ull << 20;
 static bool past_caches(const CombineArgs& a) { return static_cast<uint64_t>(a.pairs) * a.size * 2 >= kPastBytes; }
 
-hipError_t launch_expert_order(const OrderArgs& a, hipStream_t stream) {
-  const size_t row = static_cast<size_t>(a.experts) * sizeof(uint32_t);
-  if (a.blocks > 1) {
-    order_count<<<a.blocks, kOrderThreads, row, stream>>>(a);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
-  }
-  order_place<<<a.blocks, kOrderThreads, row * kOrderWaves, stream>>>(a);
+hipError_t launch_expert_order_count(const OrderArgs& a, hipStream_t stream) {
+  order_count<<<a.blocks, kOrderThreads, static_cast<size_t>(a.experts) * sizeof(uint32_t), stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_order_place(const OrderArgs& a, hipStream_t stream) {
+  order_place<<<a.blocks, kOrderThreads, static_cast<size_t>(a.experts) * kOrderWaves * sizeof(uint32_t), stream>>>(a);
   return hipGetLastError();
 }
 

@@ -130,7 +130,7 @@ template <int SIDE, class G> __global__ __launch_bounds__(kElementThreads) void 
   constexpr uint32_t kPart = 64, kParts = SIDE / kPart;
   __shared__ float turned[kPart][kPart + 1];
   const MuonTile t = reinterpret_cast<const MuonTile*>(a.plan + a.tiles_at)[blockIdx.x];
-  if (t.matrix == kMuonNoMatrix) return;
+  if (t.matrix == kMuonNoMatrix || t.part != 0) return;
   const MuonMatrix& x = matrix_of(a, t.matrix);
   const double scale = norm_of(a, t.matrix)->inverse * kScale;   // float32 would lose the far norms
   const uint32_t m0 = t.m * SIDE + blockIdx.y / kParts * kPart, n0 = t.n * SIDE + blockIdx.y % kParts * kPart;   // of X
