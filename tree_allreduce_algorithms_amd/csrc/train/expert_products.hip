@@ -97,6 +97,10 @@ using Large = Tile<128, 256, 2, 4, 32, 4, 3>;
 using Huge = Tile<256, 256, 2, 4, 64, 2, 2>;
 using LargeGrad = Tile<128, 256, 2, 4, 32, 4, 2>;
 using Middle = Tile<128, 128, 2, 2, 64, 2, 2>;
+// The weights' gradient of odd sizes: its blocks wait for loads and stores, so many
+// small ones.  4,084 pairs of 61 experts, 515 x 1,030, 36 us, 46 in Middle; 16,336
+// pairs 76 and 99.
+using OddGrad = Tile<64, 128, 2, 2, 32, 4, 2>;
 using Small = Tile<64, 128, 2, 2, 64, 3, 2>;
 
 __device__ __forceinline__ uint32_t token_of(const TokenOf& t, uint32_t pair) {
@@ -451,7 +455,10 @@ __global__ __launch_bounds__(kThinThreads, 2) void expert_product_thin(ProductAr
 // blocks (blockIdx.y), whose sums, a matrix each, add_parts() joins.
 //
 // A tile costs what its expert has rows, so every XCD gets a part of each
-// expert's tiles (neighbours, of the same rows of dW).
+// expert's tiles (neighbours, of the same rows of dW).  Where the parts are not
+// equal they are dealt in turn, by expert; not elsewhere, since it spreads what an
+// XCD writes (64 matrices of 1,024 x 2,048 float32 of zeros: 101 us in turn, 88
+// not; of 64 experts with 64 rows each, 2,048 x 1,024, 105 and 90).
 template <class T, class OUT, bool DIRECT, bool PAST>
 __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(WeightGradArgs a) {
   using SA = Staged<T::M, true, T::STEP, false>;
@@ -461,7 +468,8 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(W
   __shared__ __attribute__((aligned(1024))) char lds[T::STAGES * kStage];
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const uint32_t turn = blockIdx.x / kXcds, e = turn / a.tiles_xcd;
-  const uint32_t tile = (blockIdx.x + e) % kXcds * a.tiles_xcd + turn % a.tiles_xcd;
+  const uint32_t xcd = (blockIdx.x + (a.tiles % kXcds != 0 ? e : 0)) % kXcds;
+  const uint32_t tile = xcd * a.tiles_xcd + turn % a.tiles_xcd;
   if (tile >= a.tiles) return;
   const uint32_t m0 = tile / a.tiles_n * T::M, n0 = tile % a.tiles_n * T::N;
   uint32_t lo, hi;
@@ -707,7 +715,7 @@ uint64_t expert_product_blocks(uint64_t pairs, int experts, uint64_t out, bool b
 }
 
 uint64_t expert_weight_grad_blocks(int experts, uint64_t in, uint64_t out, bool direct) {
-  const uint64_t tiles = direct ? weight_grad_tiles<LargeGrad>(in, out) : weight_grad_tiles<Middle>(in, out);
+  const uint64_t tiles = direct ? weight_grad_tiles<LargeGrad>(in, out) : weight_grad_tiles<OddGrad>(in, out);
   return experts * ((tiles - 1) / kXcds + 1) * kXcds;
 }
 
@@ -750,9 +758,9 @@ hipError_t launch_expert_product(const ProductArgs& a, bool out_contiguous, bool
 
 hipError_t launch_expert_weight_grad(const WeightGradArgs& a, ar_dtype_t dw_dtype, bool direct, hipStream_t stream) {
   if (dw_dtype == AR_FLOAT32)
-    (direct ? launch_weight_grad<LargeGrad, float, true> : launch_weight_grad<Middle, float, false>)(a, stream);
+    (direct ? launch_weight_grad<LargeGrad, float, true> : launch_weight_grad<OddGrad, float, false>)(a, stream);
   else
-    (direct ? launch_weight_grad<LargeGrad, uint16_t, true> : launch_weight_grad<Middle, uint16_t, false>)(a, stream);
+    (direct ? launch_weight_grad<LargeGrad, uint16_t, true> : launch_weight_grad<OddGrad, uint16_t, false>)(a, stream);
   return hipGetLastError();
 }
 
