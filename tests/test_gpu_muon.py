@@ -135,6 +135,16 @@ def test_types_of_many_tensors(pd, gd, copy):
     check([(100, 61), (7, 200), (4, 64, 128), (256, 64), (1, 9)], "strong", pd, gd, copy)
 
 
+@pytest.mark.parametrize("shapes", [
+    [(128, 64), (64, 128), (16, 16), (2, 31, 127)], [(128, 65), (65, 66), (1, 1), (128, 128)],
+    [(64, 64), (33, 7), (3, 17, 48)],
+])
+@pytest.mark.parametrize("pd,gd,copy", [(F32, F32, True), (BF16, BF16, False)])
+def test_small_matrices_together(shapes, pd, gd, copy):
+    announce(f"{shapes} {pd}")
+    check(shapes, "noise", pd, gd, copy)
+
+
 @pytest.mark.parametrize("kind", ["rank 1", "rows", "large", "tiny"])
 def test_values(kind):
     announce(kind)

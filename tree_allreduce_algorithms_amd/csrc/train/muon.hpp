@@ -41,7 +41,7 @@ struct MuonHead {
   int32_t param_dtype;
   int32_t grad_dtype;
   int32_t has_copy;
-  uint32_t whole;            // 64 or 128: every matrix fits one block of so many rows and columns; 0
+  uint32_t longest, shortest;      // 64 or 128: no matrix' longer and shorter side is more; 0, 0
   uint64_t bytes;
   uint64_t workspace;        // bytes
   uint64_t matrices_at, chunks_at, squares_at, polys_at, tiles_at, norms_at, sums_at, arrived_at;
@@ -109,8 +109,8 @@ hipError_t launch_muon_poly(const MuonStepArgs& a, uint32_t squares, uint32_t si
 hipError_t launch_muon_apply(const MuonStepArgs& a, uint32_t tiles, uint32_t side, ar_dtype_t param_dtype, bool copy,
                              hipStream_t stream);
 
-// Steps of matrices of up to side x side (64 or 128), a block each.
-hipError_t launch_muon_whole(const MuonStepArgs& a, uint32_t matrices, uint32_t side, ar_dtype_t param_dtype,
-                             ar_dtype_t grad_dtype, bool copy, hipStream_t stream);
+// Steps of matrices of up to `longest` by `shortest` (64 or 128), a block each.
+hipError_t launch_muon_whole(const MuonStepArgs& a, uint32_t matrices, uint32_t longest, uint32_t shortest,
+                             ar_dtype_t param_dtype, ar_dtype_t grad_dtype, bool copy, hipStream_t stream);
 
 }  // namespace ar

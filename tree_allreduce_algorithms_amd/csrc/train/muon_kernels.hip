@@ -446,16 +446,28 @@ __global__ __launch_bounds__(kProductThreads<SIDE>, kPerSimd<SIDE>) void muon_ap
 
 // --- small matrices -----------------------------------------------------------------
 
-// A whole step of a matrix of up to MOST x MOST in one block, X and X X^T in LDS:
+// A whole step of a matrix of up to MOST x SHORT in one block, X and X X^T in LDS:
 // fifteen products whose launches would take longer than they do.
 //
 // Both are [line][k] in 16-byte chunks, permuted by the line; a product reads X's
-// lines along k, or across it by transposing loads.
-template <int MOST> struct Whole {
-  static constexpr int kThreads = MOST == 128 ? 1024 : 256, kWaves = kThreads / kWave;
-  static_assert(kWaves == (MOST / 32) * (MOST / 32));     // a wave has 32 x 32 of a result
+// lines along k, or across it by transposing loads.  What binds is the reading of
+// LDS, whose wait only other waves fill: matrices with a short side of up to 64
+// are shared out in parts of 16 x 32, so that every SIMD has some (64 x 64 22 us in
+// parts of 32 x 32, 18 so; 100 x 61 25 and 24); reading a step ahead leaves no
+// registers (28 % more time).
+template <int MOST, int SHORT> struct Whole {
+  static constexpr int TM = SHORT == 128 ? 2 : 1, kRows = 16 * TM;      // a wave has kRows x 32 of a result
+  static constexpr int kThreads = SHORT / kRows * (MOST / 32) * kWave;
+  typedef f32x4 Sums[TM][2];
 
-  static __device__ __forceinline__ int place(int line, int k) { return line * MOST + ((k / 8 ^ (line & 7)) * 8 | k % 8); }
+  // Eight lines' chunks of one k meet all banks, and so do two neighbouring chunks
+  // of the lines that a transposing load reads: four whose pitch is that of the
+  // banks, or two of half that (100 x 61: 25.0 us with the permutation of 64, 23.5
+  // so; 64 x 64: 19.6 us with that of 128, 17.9 so).
+  static __device__ __forceinline__ int place(int line, int k) {
+    const int by = MOST == 128 ? (line & 3) * 2 | (line >> 2 & 1) : line & 7;
+    return line * MOST + ((k / 8 ^ by) * 8 | k % 8);
+  }
 
   // 8 k of row r0 + lane % 16, from lines or across them
   template <bool ACROSS> static __device__ __forceinline__ f16x8 fragment(const _Float16* x, int r0, int k0, int lane) {
@@ -479,7 +491,7 @@ template <int MOST> struct Whole {
     int m, n;
     __device__ __forceinline__ Part(int rows, int columns) {
       const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wide = columns / 32;
-      m = wave / wide * 32;
+      m = wave / wide * kRows;
       n = wave % wide * 32;
       any = m < rows;
     }
@@ -488,24 +500,24 @@ template <int MOST> struct Whole {
   // This part of A B^T (or A B where ACROSS), k in steps of 32.
   template <bool ACROSS>
   static __device__ __forceinline__ void product(const _Float16* a, const _Float16* b, const Part& part, int k,
-                                                 f32x4 (&acc)[2][2]) {
+                                                 Sums& acc) {
     const int lane = threadIdx.x % kWave;
     clear(acc);
     if (!part.any) return;
     for (int k0 = 0; k0 < k; k0 += 32) {
-      f16x8 fa[2][2], fb[2][2];
+      f16x8 fa[2][TM], fb[2][2];
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int p = 0; p < 2; ++p) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          fa[p][i] = fragment<false>(a + p * (MOST * MOST), part.m + 16 * i, k0, lane);
-          fb[p][i] = fragment<ACROSS>(b + p * (MOST * MOST), part.n + 16 * i, k0, lane);
-        }
+        for (int i = 0; i < TM; ++i) fa[p][i] = fragment<false>(a + p * (MOST * MOST), part.m + 16 * i, k0, lane);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) fb[p][j] = fragment<ACROSS>(b + p * (MOST * MOST), part.n + 16 * j, k0, lane);
+      }
       // large by large, and large by small either way
 #pragma unroll
       for (int t = 0; t < 3; ++t)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
           for (int j = 0; j < 2; ++j) acc[i][j] = multiply(fb[t == 0][j], fa[t == 1][i], acc[i][j]);
     }
@@ -513,11 +525,11 @@ template <int MOST> struct Whole {
 
   // Calls f(row, first column, values) for what product() left in the thread.
   template <class F>
-  static __device__ __forceinline__ void each(const Part& part, const f32x4 (&acc)[2][2], F&& f) {
+  static __device__ __forceinline__ void each(const Part& part, const Sums& acc, F&& f) {
     const int lane = threadIdx.x % kWave;
     if (!part.any) return;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) f(part.m + 16 * i + lane % 16, part.n + 16 * j + 4 * (lane / 16), acc[i][j]);
   }
@@ -540,9 +552,9 @@ template <int MOST> struct Whole {
   }
 };
 
-template <int MOST, class T, class G, bool COPY>
-__global__ __launch_bounds__(Whole<MOST>::kThreads, 4) void muon_whole(MuonStepArgs a) {
-  using W = Whole<MOST>;
+template <int MOST, int SHORT, class T, class G, bool COPY>
+__global__ __launch_bounds__((Whole<MOST, SHORT>::kThreads), 4) void muon_whole(MuonStepArgs a) {
+  using W = Whole<MOST, SHORT>;
   __shared__ __attribute__((aligned(16))) _Float16 held[4 * MOST * MOST];
   _Float16 *x = held, *gram = held + 2 * MOST * MOST;
   const MuonMatrix& matrix = matrix_of(a, blockIdx.x);
@@ -591,7 +603,7 @@ __global__ __launch_bounds__(Whole<MOST>::kThreads, 4) void muon_whole(MuonStepA
   __syncthreads();
 
   const typename W::Part square(height, height), wide(height, width);
-  f32x4 acc[2][2];
+  typename W::Sums acc;
   const float lr = a.lr * (a.rms != 0.0f ? a.rms * matrix.by_size : matrix.by_shape) * (kUnscale * kUnscale);
   for (int step = 0; step < a.steps; ++step) {
     W::template product<false>(x, x, square, width, acc);
@@ -620,10 +632,10 @@ __global__ __launch_bounds__(Whole<MOST>::kThreads, 4) void muon_whole(MuonStepA
   if (!wide.any) return;
   // p' = (1 - lr wd) p - lr s x; all of a thread's are read at once
   T* p = static_cast<T*>(matrix.p);
-  float old[2][2][4];
-  int at[2][2][4];
+  float old[W::TM][2][4];
+  int at[W::TM][2][4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < W::TM; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -634,7 +646,7 @@ __global__ __launch_bounds__(Whole<MOST>::kThreads, 4) void muon_whole(MuonStepA
         old[i][j][q] = at[i][j][q] >= 0 ? static_cast<float>(p[at[i][j][q]]) : 0.0f;
       }
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < W::TM; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -648,20 +660,26 @@ __global__ __launch_bounds__(Whole<MOST>::kThreads, 4) void muon_whole(MuonStepA
 
 }  // namespace
 
-template <int MOST, class G>
+template <int MOST, int SHORT, class G>
 static hipError_t whole(const MuonStepArgs& a, uint32_t matrices, ar_dtype_t param_dtype, bool copy, hipStream_t stream) {
-  const auto kernel = param_dtype == AR_BFLOAT16 ? muon_whole<MOST, __bf16, G, false>
-                      : copy                     ? muon_whole<MOST, float, G, true>
-                                                 : muon_whole<MOST, float, G, false>;
-  kernel<<<matrices, Whole<MOST>::kThreads, 0, stream>>>(a);
+  const auto kernel = param_dtype == AR_BFLOAT16 ? muon_whole<MOST, SHORT, __bf16, G, false>
+                      : copy                     ? muon_whole<MOST, SHORT, float, G, true>
+                                                 : muon_whole<MOST, SHORT, float, G, false>;
+  kernel<<<matrices, Whole<MOST, SHORT>::kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-hipError_t launch_muon_whole(const MuonStepArgs& a, uint32_t matrices, uint32_t side, ar_dtype_t param_dtype,
-                             ar_dtype_t grad_dtype, bool copy, hipStream_t stream) {
-  const bool wide = grad_dtype == AR_FLOAT32;
-  return (side == 128 ? (wide ? whole<128, float> : whole<128, __bf16>)
-                      : (wide ? whole<64, float> : whole<64, __bf16>))(a, matrices, param_dtype, copy, stream);
+template <class G>
+static hipError_t whole(const MuonStepArgs& a, uint32_t matrices, uint32_t longest, uint32_t shortest, ar_dtype_t param_dtype, bool copy,
+                        hipStream_t stream) {
+  return (longest <= 64    ? whole<64, 64, G>
+          : shortest <= 64 ? whole<128, 64, G>
+                           : whole<128, 128, G>)(a, matrices, param_dtype, copy, stream);
+}
+
+hipError_t launch_muon_whole(const MuonStepArgs& a, uint32_t matrices, uint32_t longest, uint32_t shortest,
+                             ar_dtype_t param_dtype, ar_dtype_t grad_dtype, bool copy, hipStream_t stream) {
+  return (grad_dtype == AR_FLOAT32 ? whole<float> : whole<__bf16>)(a, matrices, longest, shortest, param_dtype, copy, stream);
 }
 
 hipError_t launch_muon_momentum(const MuonStepArgs& a, uint32_t chunks, ar_dtype_t grad_dtype, hipStream_t stream) {
