@@ -500,7 +500,8 @@ ar_status_t ar_route_grad(const void* const* logits, const uint8_t* const* masks
  * all others.  The counts stay on the GPU, no call waits for them.  Matrices
  * are bfloat16, products are added up in float32 and rounded once.  What the
  * device arrays `order`, `position` and `offsets` hold is bounds-checked by the
- * kernels (a row or token out of range is none).
+ * kernels (a row or token out of range is none).  What a call writes may not
+ * overlap what it reads or writes elsewhere.
  */
 
 /* Device memory that ar_expert_order needs for so many pairs and experts, in
@@ -540,7 +541,7 @@ typedef struct {
  * expert_stride + k * in_stride + n * out_stride; one of in_stride and
  * out_stride is 1 and the other at least the size along the first.  With the
  * two sizes and strides exchanged this is also the gradient with respect to x's
- * rows.  AR_ERROR_UNSUPPORTED: another dtype, or 2^23 tiles (of 16 x 64 to 128 x 256)
+ * rows.  AR_ERROR_UNSUPPORTED: another dtype, or 2^23 tiles (of 16 x 64 to 256 x 256)
  * or more. */
 ar_status_t ar_expert_matmul(const ar_expert_rows_t* rows, const void* weight,
                              size_t expert_stride, size_t in_stride, size_t out_stride, void* y,
@@ -629,8 +630,8 @@ ar_status_t ar_muon_plan(const ar_muon_tensor_t* tensors, int ntensors, ar_dtype
                          ar_dtype_t grad_dtype, void* plan, size_t bytes);
 
 /* Bytes of device memory (256-byte aligned, any content) that a step on this
- * plan works in: about 8 an element and 8 for each of the shorter sides'
- * squares. */
+ * plan works in: about 8 an element, 8 for each of the shorter sides' squares,
+ * and up to 34 MB for products whose sums several blocks share. */
 size_t ar_muon_workspace(const void* plan);
 
 /* One step in place, per matrix, with G = grad_scale g:
@@ -642,7 +643,7 @@ size_t ar_muon_workspace(const void* plan);
  * rounded once to param's type, and to bfloat16 in `copy`), |u| in float64; X, A
  * and the polynomial are held in 22 bits and multiplied with float32 sums.  A
  * matrix with a NaN or an infinity in u gets NaN throughout; one of zeros is
- * not moved but by its decay.
+ * not moved but by its decay, also where eps is 0.
  * AR_ERROR_INVALID_ARGUMENT: a value that is not finite, lr, eps, weight_decay
  * or match_rms negative, momentum outside [0, 1), ns_steps out of range.
  * May be captured into a graph (a replay repeats the step with these values). */

@@ -181,6 +181,21 @@ def test_zeros_and_values_that_are_not_finite():
     assert bool(p[0][2].isnan().all() and p[0][3].isnan().all())
 
 
+@pytest.mark.parametrize("shape", [(8, 8), (100, 61), (200, 300)])
+def test_zeros_without_an_eps(shape):
+    p, g = [torch.ones(shape, device=DEV)], [torch.zeros(shape, device=DEV)]
+    ar.Muon(p, g, eps=0.0, weight_decay=0.5).step(0.25)
+    assert bool((p[0] == 0.875).all())
+
+
+def test_flat_gradients_and_state():
+    p = [torch.randn(40, 30, device=DEV)]
+    q, g, m = [p[0].clone()], torch.randn(1200, device=DEV), torch.randn(1200, device=DEV)
+    ar.Muon(p, [g.view(40, 30)], state={"momentum": [m.view(40, 30).clone()]}).step(0.1)
+    ar.Muon(q, [g], state={"momentum": [m]}).step(0.1)
+    assert torch.equal(p[0], q[0])
+
+
 def test_empty_tensors_and_odd_addresses():
     flat = torch.randn(100 * 61 + 3, device=DEV)
     p = [flat[3:].view(100, 61).clone(), torch.empty(0, 5, 6, device=DEV), torch.empty(3, 0, 6, device=DEV)]
@@ -272,6 +287,9 @@ def test_refusals():
         (TypeError, lambda: ar.Muon([p], [m(8, 8)], state={"momentum": [m(8, 8, dt=BF16)]})),
         (ar.ArError, lambda: ar.Muon([p], [p])),                              # a gradient in the parameter
         (ar.ArError, lambda: ar.Muon([p], [m(8, 8)], state={"momentum": [p]})),
+        (ValueError, lambda: ar.Muon([p], [m(4, 16)])),                       # as many elements, another matrix
+        (ValueError, lambda: ar.Muon([p], [m(8, 8)], [m(1, 8, 8, dt=BF16)])),
+        (ValueError, lambda: ar.Muon([p], [m(8, 8)], state={"momentum": [m(16, 4)]})),
         (ValueError, lambda: ar.Muon([p], [m(8, 8)], ns_steps=2.5)),
         (ValueError, lambda: ar.Muon([p], [m(8, 8)], match_rms=0.0)),
     ]

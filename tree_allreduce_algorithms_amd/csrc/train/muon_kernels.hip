@@ -38,6 +38,12 @@ __device__ __forceinline__ void split(float v, _Float16* large, _Float16* small)
 
 // --- momentum and norm --------------------------------------------------------------
 
+// 1 / (|u| + eps), given |u|^2; a matrix of zeros has X = 0 without an eps too.
+__device__ __forceinline__ double inverse(double square, double eps) {
+  const double norm = sqrt(square) + eps;
+  return norm == 0 ? 0 : 1.0 / norm;
+}
+
 constexpr int kElementThreads = 256;
 
 // N elements from p on; `vec`: p allows them at once.
@@ -102,7 +108,7 @@ template <class G> __global__ __launch_bounds__(kElementThreads) void muon_momen
   for (uint32_t i = threadIdx.x; i < x.chunks; i += kElementThreads) all += shared_load(sums + i);
   all = block_sum<kElementThreads>(all);
   if (threadIdx.x == 0) {
-    norm->inverse = 1.0 / (sqrt(all) + a.eps);
+    norm->inverse = inverse(all, a.eps);
     norm->arrived = 0;
   }
 }
@@ -588,7 +594,7 @@ __global__ __launch_bounds__((Whole<MOST, SHORT>::kThreads), 4) void muon_whole(
   double sum = 0;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) sum += static_cast<double>(u[e]) * u[e];
-  const double scale = 1.0 / (sqrt(block_sum<W::kThreads>(sum)) + a.eps) * kScale;
+  const double scale = inverse(block_sum<W::kThreads>(sum), a.eps) * kScale;
   int r = threadIdx.x / cols, c = threadIdx.x % cols;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {

@@ -23,22 +23,22 @@ class Muon:
     dimensions; the last two are a matrix's rows and columns, those before count
     matrices that are treated one by one, as in the weights [experts, in, out]
     of a mixture of experts.  ``grads`` (float32 or bfloat16) have the same
-    sizes; ``copies`` optionally lists bfloat16 working copies of float32
+    shapes, or are flat; ``copies`` optionally lists bfloat16 working copies of float32
     params, rewritten by every step.  Everything is checked once, here; the
     tensors' storage must not move while the object is in use, and every step
     reads the gradients from the same ``grads``.
 
-    ``state`` hands over an existing ``{"momentum": [...]}`` (float32, the
-    params' sizes), updated in place; by default it starts at zero.  A step
+    ``state`` hands over an existing ``{"momentum": [...]}`` (float32, shaped
+    like ``grads``), updated in place; by default it starts at zero.  A step
     moves a matrix by ``lr`` times ``sqrt(max(1, rows / cols))``, or with
     ``match_rms`` times ``match_rms * sqrt(max(rows, cols))`` (0.2 gives updates
     of about AdamW's size), along the orthogonalised momentum.  ``grad_scale``
     multiplies every gradient first, e.g. ``1 / N`` where they are sums over N
     ranks.
 
-    The object keeps about 8 bytes an element and 8 for each element of the
-    shorter sides' squares on the GPU to work in, which the steps share: they
-    must be ordered.  A step may be captured into a graph, whose replays repeat
+    The object keeps about 8 bytes an element, 8 for each element of the shorter
+    sides' squares, and up to 34 MB more on the GPU to work in, which the steps
+    share: they must be ordered.  A step may be captured into a graph, whose replays repeat
     it with its ``lr`` and are ordered with the other steps by the caller.
     """
 
@@ -66,6 +66,10 @@ class Muon:
         if set(state) != {"momentum"}:
             raise ValueError(f"state must hold ['momentum'], not {sorted(state)}")
         self.state = {"momentum": _flat(state["momentum"], "momentum", dev, (torch.float32,), sizes)}
+        for what, tensors in (("grads", self.grads), ("copies", self.copies or []),
+                              ("momentum", self.state["momentum"])):
+            if any(t.dim() != 1 and t.shape != p.shape for t, p in zip(tensors, params)):
+                raise ValueError(f"{what} must have the parameters' shapes, or be flat")
         if int(ns_steps) != ns_steps:
             raise ValueError("ns_steps must be a whole number")
         if match_rms is not None and not match_rms > 0:
