@@ -110,7 +110,8 @@ struct Table {
 
 struct Layout {
   uint64_t matrices = 0, chunks = 0;
-  uint32_t side = 0, square_side = 0, longest = 0, shortest = 0;
+  uint32_t side = 0, square_side = 0;
+  uint16_t longest = 0, shortest = 0;
   Table squares, polys, tiles;
   uint64_t matrices_at = 0, chunks_at = 0, squares_at = 0, polys_at = 0, tiles_at = 0, norms_at = 0, sums_at = 0,
            arrived_at = 0;

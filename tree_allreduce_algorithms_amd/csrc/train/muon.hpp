@@ -41,7 +41,7 @@ struct MuonHead {
   int32_t param_dtype;
   int32_t grad_dtype;
   int32_t has_copy;
-  uint32_t longest, shortest;      // 64 or 128: no matrix' longer and shorter side is more; 0, 0
+  uint16_t longest, shortest;      // 64 or 128: no matrix's longer and shorter side is more; 0, 0
   uint64_t bytes;
   uint64_t workspace;        // bytes
   uint64_t matrices_at, chunks_at, squares_at, polys_at, tiles_at, norms_at, sums_at, arrived_at;
