@@ -193,8 +193,11 @@ constexpr int kSumThreads = 256;
 // up in float32 in the order of k.  A thread has eight columns of a token; a
 // block has `lanes` of a token's threads, so whole tokens where they are short.
 // 131,072 rows of 1,024: 49 us with the rows read past the caches, 70 through them;
-// the rows' reading at 6.2 TB/s takes 48.
-template <bool PAST>
+// the rows' reading at 6.2 TB/s takes 48.  The rows of WAY choices are under way at
+// a time: 8,192 pairs, two a token, 5.4 us with two, 6.6 with four; 131,072, eight a
+// token, 58 with two, 55 with four, 54 with eight, which cost tokens of four a
+// microsecond.
+template <int WAY, bool PAST>
 __global__ __launch_bounds__(kSumThreads) void combine(CombineArgs a, uint32_t lanes) {
   const uint32_t per_block = kSumThreads / lanes, in_block = threadIdx.x / lanes;
   const uint64_t c = (static_cast<uint64_t>(blockIdx.y) * lanes + threadIdx.x % lanes) * 8;
@@ -206,20 +209,19 @@ __global__ __launch_bounds__(kSumThreads) void combine(CombineArgs a, uint32_t l
        t += static_cast<uint64_t>(gridDim.x) * per_block) {
     const uint64_t first = t * a.top_k;
     float sum[8] = {};
-    // four choices' rows under way at a time
-    for (int k = 0; k < a.top_k; k += 4) {
-      uint32_t row[4];
-      float w[4];
-      Eight r[4];
+    for (int k = 0; k < a.top_k; k += WAY) {
+      uint32_t row[WAY];
+      float w[WAY];
+      Eight r[WAY];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < WAY; ++q) {
         row[q] = k + q < a.top_k ? static_cast<uint32_t>(a.position[first + k + q]) : kNone;
         w[q] = a.weights == nullptr || k + q >= a.top_k ? 1.0f : a.weights[first + k + q];
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) r[q] = read<PAST>(y + row[q] * a.y_stride, row[q] < a.pairs ? n : 0);
+      for (int q = 0; q < WAY; ++q) r[q] = read<PAST>(y + row[q] * a.y_stride, row[q] < a.pairs ? n : 0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < WAY; ++q)
         if (row[q] < a.pairs)
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w[q], to_float(r[q].v[i]), sum[i]);
@@ -297,7 +299,9 @@ hipError_t launch_expert_combine(const CombineArgs& a, hipStream_t stream) {
   const uint32_t per = (a.size - 1) / 8 + 1, lanes = per < kSumThreads ? per : kSumThreads;
   const uint32_t tokens = kSumThreads / lanes, blocks = (a.tokens - 1) / tokens + 1;
   const dim3 grid(blocks < 65536 ? blocks : 65536, (per - 1) / lanes + 1);
-  (past_caches(a) ? combine<true> : combine<false>)<<<grid, kSumThreads, 0, stream>>>(a, lanes);
+  const auto kernel = a.top_k <= 2 ? (past_caches(a) ? combine<2, true> : combine<2, false>)
+                                   : (past_caches(a) ? combine<4, true> : combine<4, false>);
+  kernel<<<grid, kSumThreads, 0, stream>>>(a, lanes);
   return hipGetLastError();
 }
 
