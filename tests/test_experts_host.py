@@ -55,7 +55,7 @@ def order(pairs=200, experts=8, indices=at(0), out=at(1), position=at(2), offset
 
 def test_order_workspace():
     size = ar.lib().ar_expert_order_workspace
-    assert size(0, 8) == size(4096, 1024) == 0 and size(4097, 8) == 2 * 8 * 4
+    assert size(0, 8) == size(32768, 1024) == 0 and size(32769, 8) == 9 * 8 * 4
     assert size(2 ** 31 - 1, 1024) == 64 * 1024 * 4
     assert size(100, 0) == size(100, 1025) == size(2 ** 31, 8) == 0
 
@@ -64,8 +64,8 @@ def test_order_workspace():
     ({}, HIP), ({"pairs": 0, "indices": None, "out": None, "position": None}, HIP), ({"experts": 0}, INVALID),
     ({"experts": 1025}, UNSUPPORTED), ({"pairs": 2 ** 31}, UNSUPPORTED), ({"offsets": None}, INVALID),
     ({"indices": None}, INVALID), ({"out": None}, INVALID), ({"position": None}, INVALID),
-    ({"indices": at(0) + 2}, INVALID), ({"offsets": at(3) + 1}, INVALID), ({"pairs": 5000}, INVALID),
-    ({"pairs": 5000, "workspace": at(4)}, HIP), ({"pairs": 5000, "workspace": at(4) + 8}, INVALID),
+    ({"indices": at(0) + 2}, INVALID), ({"offsets": at(3) + 1}, INVALID), ({"pairs": 50000}, INVALID),
+    ({"pairs": 50000, "workspace": at(4)}, HIP), ({"pairs": 50000, "workspace": at(4) + 8}, INVALID),
 ])
 def test_order_arguments(change, want):
     assert order(**change) == want

@@ -97,6 +97,7 @@ def near(got, want, size, n, what, stored=True):
 @pytest.mark.parametrize("tokens,k,experts,kind", [
     (1, 1, 1, "even"), (1, 8, 8, "even"), (1, 2, 1024, "even"), (5, 3, 7, "masked"), (63, 1, 64, "skewed"),
     (1000, 4, 61, "masked"), (512, 8, 256, "skewed"), (4096, 1, 3, "one"), (700, 2, 16, "none"),
+    (1024, 1, 5, "masked"), (1025, 1, 5, "skewed"), (32768, 1, 1024, "masked"), (32769, 1, 9, "masked"),
     (16384, 8, 1024, "skewed"), (16384, 8, 128, "masked"), (40000, 6, 64, "even"), (12289, 1, 1000, "masked"),
 ])
 def test_order(tokens, k, experts, kind):

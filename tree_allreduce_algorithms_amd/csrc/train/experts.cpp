@@ -66,8 +66,7 @@ extern "C" {
 
 size_t ar_expert_order_workspace(size_t pairs, int experts) {
   if (experts < 1 || experts > AR_MAX_EXPERTS || pairs > kMost) return 0;
-  const uint32_t blocks = ar::order_blocks(pairs);
-  return blocks > 1 ? static_cast<size_t>(blocks) * experts * sizeof(uint32_t) : 0;
+  return static_cast<size_t>(ar::order_blocks(pairs)) * experts * sizeof(uint32_t);
 }
 
 ar_status_t ar_expert_order(const int32_t* indices, size_t pairs, int experts, int32_t* order,
@@ -87,14 +86,13 @@ ar_status_t ar_expert_order(const int32_t* indices, size_t pairs, int experts, i
   a.order = order;
   a.position = position;
   a.offsets = offsets;
-  a.counts = static_cast<uint32_t*>(workspace);
   // whole rounds of a block's waves, and no block without pairs
   const uint64_t blocks = ar::order_blocks(pairs), unit = ar::kOrderWaves * 64;
-  a.block_pairs = static_cast<uint32_t>(((pairs + blocks - 1) / blocks + unit - 1) / unit * unit);
-  if (a.block_pairs == 0) a.block_pairs = unit;
+  a.counts = blocks != 0 ? static_cast<uint32_t*>(workspace) : nullptr;
+  a.block_pairs = static_cast<uint32_t>(blocks == 0 ? unit : ((pairs + blocks - 1) / blocks + unit - 1) / unit * unit);
   a.blocks = pairs == 0 ? 1 : static_cast<uint32_t>((pairs - 1) / a.block_pairs + 1);
   hipError_t err = hipSuccess;
-  if (a.blocks > 1) err = ar::enqueue([&] { return ar::launch_expert_order_count(a, stream); });
+  if (a.counts != nullptr) err = ar::enqueue([&] { return ar::launch_expert_order_count(a, stream); });
   if (err == hipSuccess) err = ar::enqueue([&] { return ar::launch_expert_order_place(a, stream); });
   return ar::launch_status(err);
 }

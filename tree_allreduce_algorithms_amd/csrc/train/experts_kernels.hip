@@ -33,7 +33,7 @@ __device__ __forceinline__ void count_pairs(const OrderArgs& a, uint32_t* mine, 
   }
 }
 
-// A block's pairs of each expert, for lists of more than one block.
+// A block's pairs of each expert, for long lists.
 __global__ __launch_bounds__(kOrderThreads) void order_count(OrderArgs a) {
   extern __shared__ uint32_t counts[];
   for (int e = threadIdx.x; e < a.experts; e += kOrderThreads) counts[e] = 0;
@@ -51,16 +51,37 @@ __global__ __launch_bounds__(kOrderThreads) void order_count(OrderArgs a) {
 // blocks and waves before, plus those of the wave's lower lanes (found by
 // comparing the number's bits across the lanes).
 __global__ __launch_bounds__(kOrderThreads) void order_place(OrderArgs a) {
-  extern __shared__ uint32_t next[];       // [waves][experts]
+  extern __shared__ uint32_t next[];       // [waves][experts]; of pairs of other blocks, before and behind
   __shared__ uint32_t part[kOrderWaves];
   const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int experts = a.experts;
-  for (int i = threadIdx.x; i < experts * static_cast<int>(kOrderWaves); i += kOrderThreads) next[i] = 0;
+  const bool once = a.counts == nullptr;
+  uint32_t *const lower_blocks = next + kOrderWaves * experts, *const upper_blocks = lower_blocks + experts;
+  for (int i = threadIdx.x; i < experts * static_cast<int>(kOrderWaves + (once ? 2 : 0)); i += kOrderThreads) next[i] = 0;
   __syncthreads();
   uint32_t begin, end;
   span_of(a, wave, &begin, &end);
   uint32_t* mine = next + wave * experts;
-  count_pairs(a, mine, begin, end);
+  if (once) {
+    // (a wave has 64 pairs)
+    const uint32_t first = blockIdx.x * kOrderThreads;
+    for (uint32_t p0 = threadIdx.x; p0 < a.pairs; p0 += 4 * kOrderThreads) {
+      uint32_t key[4];
+#pragma unroll
+      for (uint32_t q = 0; q < 4; ++q) {
+        const uint32_t p = p0 + q * kOrderThreads;
+        key[q] = p < a.pairs ? expert_of(a, p) : kNone;
+      }
+#pragma unroll
+      for (uint32_t q = 0; q < 4; ++q) {
+        const uint32_t p = p0 - threadIdx.x + q * kOrderThreads;      // a whole block's or none
+        if (key[q] != kNone)
+          atomicAdd((p < first ? lower_blocks : p > first ? upper_blocks : mine) + key[q], 1u);
+      }
+    }
+  } else {
+    count_pairs(a, mine, begin, end);
+  }
   __syncthreads();
 
   // thread e has expert e (at most 1,024 of both): its pairs in all blocks, and
@@ -68,7 +89,9 @@ __global__ __launch_bounds__(kOrderThreads) void order_place(OrderArgs a) {
   const int e = threadIdx.x;
   uint32_t all = 0, before = 0;
   if (e < experts) {
-    if (a.blocks == 1) {
+    if (once) {
+      before = lower_blocks[e];
+      all = before + upper_blocks[e];
       for (uint32_t w = 0; w < kOrderWaves; ++w) all += next[w * experts + e];
     } else {
       for (uint32_t b = 0; b < a.blocks; b += 8) {
@@ -291,7 +314,7 @@ hipError_t launch_expert_order_count(const OrderArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_expert_order_place(const OrderArgs& a, hipStream_t stream) {
-  order_place<<<a.blocks, kOrderThreads, static_cast<size_t>(a.experts) * kOrderWaves * sizeof(uint32_t), stream>>>(a);
+  order_place<<<a.blocks, kOrderThreads, static_cast<size_t>(a.experts) * (kOrderWaves + (a.counts == nullptr ? 2 : 0)) * sizeof(uint32_t), stream>>>(a);
   return hipGetLastError();
 }
 
