@@ -260,6 +260,8 @@ def test_weight_grad_into_a_tensor():
 @pytest.mark.parametrize("tokens,k,experts,size,kind", [
     (1, 1, 1, 1, "even"), (1, 8, 8, 1024, "even"), (33, 3, 7, 61, "masked"), (5, 2, 4, 4096, "masked"),
     (1000, 4, 16, 520, "masked"), (64, 2, 4, 128, "none"), (300, 6, 64, 2049, "skewed"),
+    (100, 2, 8, 7, "even"), (100, 2, 8, 9, "masked"), (50, 4, 8, 515, "even"), (40, 3, 8, 1030, "masked"),
+    (8200, 4, 8, 1026, "masked"), (16400, 8, 8, 520, "even"), (8200, 2, 8, 1024, "masked"),
 ])
 def test_combine_and_its_gradient(tokens, k, experts, size, kind):
     announce(f"combine {tokens} {k} {experts} {size} {kind}")
