@@ -456,9 +456,10 @@ __global__ __launch_bounds__(kThinThreads, 2) void expert_product_thin(ProductAr
 // blocks (blockIdx.y), whose sums, a matrix each, add_parts() joins.
 //
 // A tile costs what its expert has rows, so every XCD gets a part of each
-// expert's tiles (neighbours, of the same rows of dW).  Where the parts are not
-// equal they are dealt in turn, by expert; not elsewhere, since it spreads what an
-// XCD writes (64 matrices of 1,024 x 2,048 float32 of zeros: 101 us in turn, 88
+// expert's tiles (neighbours, of the same rows of dW), or of each second one's where
+// there are enough of them to come out even: each XCD of an expert reads its rows
+// once (see weight_grad_xcds).  Where the parts are not equal they are dealt in
+// turn, by expert; not elsewhere, since it spreads what an XCD writes (64 matrices of 1,024 x 2,048 float32 of zeros: 101 us in turn, 88
 // not; of 64 experts with 64 rows each, 2,048 x 1,024, 105 and 90).
 template <class T, class OUT, bool DIRECT, bool PAST>
 __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(WeightGradArgs a) {
@@ -468,10 +469,11 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(W
   constexpr int kA = SA::kChunks / T::kThreads, kB = SB::kChunks / T::kThreads;
   __shared__ __attribute__((aligned(1024))) char lds[T::STAGES * kStage];
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const uint32_t turn = blockIdx.x / kXcds, e = turn / a.tiles_xcd;
-  const uint32_t xcd = (blockIdx.x + (a.tiles % kXcds != 0 ? e : 0)) % kXcds;
-  const uint32_t tile = xcd * a.tiles_xcd + turn % a.tiles_xcd;
-  if (tile >= a.tiles) return;
+  const uint32_t turn = blockIdx.x / kXcds, xcd = blockIdx.x % kXcds, round = turn / a.tiles_xcd;
+  const uint32_t e = a.xcds == kXcds ? round : round * 2 + xcd / (kXcds / 2);
+  const uint32_t part = (xcd + (a.tiles % a.xcds != 0 ? round : 0)) % a.xcds;
+  const uint32_t tile = part * a.tiles_xcd + turn % a.tiles_xcd;
+  if (tile >= a.tiles || e >= static_cast<uint32_t>(a.experts)) return;
   const uint32_t m0 = tile / a.tiles_n * T::M, n0 = tile % a.tiles_n * T::N;
   uint32_t lo, hi;
   rows_of(a.offsets, a.experts, e, a.pairs, &lo, &hi);
@@ -661,6 +663,16 @@ template <class T> uint64_t weight_grad_tiles(uint64_t in, uint64_t out) {
   return (in + T::M - 1) / T::M * tiles_n<T>(out);
 }
 
+// The XCDs that share an expert's tiles of the weights' gradient.  32,768 pairs of 64
+// experts, 1,024 x 2,048, 218 us with half of them, 243 with all; 131,072 of 256,
+// 1,024 x 512, 232 and 269; but 16,384 of 16, 2,048 x 2,048, whose rows are uneven, 185
+// and 173, and 131,072 of 128, 2,048 x 1,024, which matrix instructions bind, 874 and 864.
+uint32_t weight_grad_xcds(int experts) { return experts >= 32 ? kXcds / 2 : kXcds; }
+uint64_t weight_grad_blocks(int experts, uint64_t tiles) {
+  const uint64_t xcds = weight_grad_xcds(experts), at_once = kXcds / xcds;
+  return (experts + at_once - 1) / at_once * ((tiles - 1) / xcds + 1) * kXcds;
+}
+
 // So many wide tiles give every CU one.  With fewer, smaller ones are faster: 2,048
 // pairs of 8 experts, 1,024 x 1,024, 14 us in 64 x 128 and 21 in 128 x 256, 8,192
 // pairs 33 either way.
@@ -699,10 +711,11 @@ template <class T, bool BR, bool DIRECT> void launch_product(ProductArgs a, hipS
 template <class T, class OUT, bool DIRECT> void launch_weight_grad(WeightGradArgs a, hipStream_t stream) {
   a.tiles_n = static_cast<uint32_t>(tiles_n<T>(a.out));
   a.tiles = static_cast<uint32_t>(weight_grad_tiles<T>(a.in, a.out));
-  a.tiles_xcd = (a.tiles - 1) / kXcds + 1;
+  a.xcds = weight_grad_xcds(a.experts);
+  a.tiles_xcd = (a.tiles - 1) / a.xcds + 1;
   const bool past = a.parts == 1 && past_caches(a.dw, static_cast<uint64_t>(a.experts) * a.in, a.out * sizeof(OUT));
   (past ? expert_weight_grad<T, OUT, DIRECT, true> : expert_weight_grad<T, OUT, DIRECT, false>)
-      <<<dim3(a.experts * a.tiles_xcd * kXcds, a.parts), T::kThreads, 0, stream>>>(a);
+      <<<dim3(static_cast<uint32_t>(weight_grad_blocks(a.experts, a.tiles)), a.parts), T::kThreads, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -718,7 +731,7 @@ uint64_t expert_product_blocks(uint64_t pairs, int experts, uint64_t out, bool b
 
 uint64_t expert_weight_grad_blocks(int experts, uint64_t in, uint64_t out, bool direct) {
   const uint64_t tiles = direct ? weight_grad_tiles<LargeGrad>(in, out) : weight_grad_tiles<OddGrad>(in, out);
-  return experts * ((tiles - 1) / kXcds + 1) * kXcds;
+  return weight_grad_blocks(experts, tiles);
 }
 
 // Where the tiles leave places on the CUs free and have many rows to go over, the

@@ -179,7 +179,7 @@ ar_status_t ar_expert_weight_grad(const ar_expert_rows_t* r, const void* dy, siz
   a.pairs = static_cast<uint32_t>(r->pairs);
   a.in = static_cast<uint32_t>(r->in);
   a.out = static_cast<uint32_t>(r->out);
-  a.tiles_n = a.tiles = a.tiles_xcd = 0;
+  a.tiles_n = a.tiles = a.tiles_xcd = a.xcds = 0;
   a.parts = parts;
   a.experts = r->experts;
   a.token = ar::token_of(r->pairs, r->order != nullptr ? r->top_k : 1);

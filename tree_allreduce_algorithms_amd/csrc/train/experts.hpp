@@ -82,6 +82,7 @@ struct WeightGradArgs {
   uint64_t x_stride, dy_stride;
   uint32_t x_rows, pairs, in, out, tiles_n;
   uint32_t tiles, tiles_xcd;    // of an expert; an XCD's of these
+  uint32_t xcds;                // that share an expert's tiles: all or half
   uint32_t parts;               // blocks that share a tile's rows
   int32_t experts;
   TokenOf token;
