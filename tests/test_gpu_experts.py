@@ -127,7 +127,7 @@ SHAPES = [
     (1, 2, 8, 64, 64, "even"), (1, 1, 1, 1, 1, "even"), (3, 2, 4, 7, 5, "masked"), (40, 4, 61, 72, 136, "masked"),
     (130, 1, 1, 200, 129, "even"), (129, 2, 3, 64, 128, "one"), (64, 8, 16, 1000, 24, "skewed"),
     (300, 2, 5, 33, 300, "skewed"), (257, 3, 1000, 65, 66, "masked"), (20, 2, 4, 128, 256, "none"),
-    (2000, 2, 8, 256, 512, "skewed"), (513, 8, 64, 520, 392, "masked"), (7, 2, 8, 2048, 1024, "even"),
+    (3000, 2, 40, 128, 264, "skewed"), (2000, 2, 8, 256, 512, "skewed"), (513, 8, 64, 520, 392, "masked"), (7, 2, 8, 2048, 1024, "even"),
 ]
 
 
