@@ -463,8 +463,9 @@ __global__ __launch_bounds__(kThinThreads, 2) void expert_product_thin(ProductAr
 // expert's tiles (neighbours, of the same rows of dW), or of each second one's where
 // there are enough of them to come out even: each XCD of an expert reads its rows
 // once (see weight_grad_xcds).  Where the parts are not equal they are dealt in
-// turn, by expert; not elsewhere, since it spreads what an XCD writes (64 matrices of 1,024 x 2,048 float32 of zeros: 101 us in turn, 88
-// not; of 64 experts with 64 rows each, 2,048 x 1,024, 105 and 90).
+// turn, by expert; not elsewhere, since it spreads what an XCD writes (64 matrices of
+// 1,024 x 2,048 float32 of zeros: 101 us in turn, 88 not; of 64 experts with 64 rows
+// each, 2,048 x 1,024, 105 and 90).
 template <class T, class OUT, bool DIRECT, bool PAST>
 __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void expert_weight_grad(WeightGradArgs a) {
   using SA = Staged<T::M, true, T::STEP, false>;

@@ -11,11 +11,11 @@
 // line by the line's number, so that the lanes of one access meet different
 // banks.
 //
-// Steps are double-buffered: the loads of step k + 1 are under way while step k
-// is multiplied; one barrier a step.  More stages measured slower (8192^3: 1,276
-// TFLOP/s with four half steps against 1,310 with two whole ones): it is not the
-// loads' latency that binds but what L2 and LDS move, so tiles are as wide as
-// the registers of two blocks on a CU allow.
+// Two or more steps are in LDS: the loads of later ones are under way while one is
+// multiplied; one barrier a step.  For operands in the caches more than two measured
+// slower (8192^3: 1,276 TFLOP/s with four half steps against 1,310 with two whole
+// ones): it is not the loads' latency that binds but what L2 and LDS move, so tiles
+// are as wide as the registers of two blocks on a CU allow.
 //
 // B's columns are dealt to the fragments so that a lane holds 16 consecutive
 // ones in four fragments (`turned`), four of each, and so that the lanes of a
