@@ -125,7 +125,7 @@ struct Source {
 __device__ __forceinline__ void load_to_lds(const Source& s, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                ::"s"(lds), "v"(offset), "s"(s.words)
-               : "memory");
+               : "m0", "memory");
 }
 
 // Waits until all of the wave's loads to LDS have arrived and its own LDS reads
