@@ -184,7 +184,7 @@ uint32_t steps_each(const std::vector<Rest>& rest, uint64_t room) {
 // The table of a product: the tiles with most steps first, neighbours together,
 // each group to the XCD that has least so far; entry i is XCD (i mod 8)'s, so
 // lists of unequal lengths leave entries of no matrix.
-Table deal(const ar_muon_tensor_t* t, int n, uint32_t pad, uint32_t side, Kind kind, uint64_t total) {
+Table deal(const ar_muon_tensor_t* t, int n, uint32_t pad, uint32_t side, Kind kind) {
   const bool upper = kind != Kind::kTiles;
   // each tensor's tiles in order
   std::vector<std::vector<MuonTile>> order;
@@ -209,7 +209,9 @@ Table deal(const ar_muon_tensor_t* t, int n, uint32_t pad, uint32_t side, Kind k
                    [&](uint32_t a, uint32_t b) { return steps_of[shape_of[a]] > steps_of[shape_of[b]]; });
 
   // whole tiles up to a multiple of the places, parts of the others
-  uint64_t whole = total - total % kPlaces, seen = 0;
+  uint64_t total = 0, seen = 0;
+  for (uint32_t shape : shape_of) total += order[shape].size();
+  uint64_t whole = total - total % kPlaces;
   std::vector<Rest> rest;
   for (uint32_t k : matrices) {
     const uint64_t tiles = order[shape_of[k]].size();
@@ -278,10 +280,9 @@ Layout layout_of(const ar_muon_tensor_t* t, int n) {
   if (!l.fits) return l;
   l.matrices = at.matrices;
   l.chunks = at.chunks;
-  const uint64_t squares = (l.square_side == 128 ? wide : narrow).squares;
-  l.squares = deal(t, n, l.side, l.square_side, Kind::kSquares, squares);
-  l.polys = deal(t, n, l.side, l.square_side, Kind::kPolys, squares);
-  l.tiles = deal(t, n, l.side, l.side, Kind::kTiles, at.tiles);
+  l.squares = deal(t, n, l.side, l.square_side, Kind::kSquares);
+  l.polys = deal(t, n, l.side, l.square_side, Kind::kPolys);
+  l.tiles = deal(t, n, l.side, l.side, Kind::kTiles);
   l.fits = l.tiles.fits && l.squares.fits && l.polys.fits;
   for (int i = 0; i < n; ++i) {
     if (empty(t[i])) continue;
