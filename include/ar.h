@@ -629,10 +629,17 @@ size_t ar_muon_plan_bytes(const ar_muon_tensor_t* tensors, int ntensors, ar_dtyp
 ar_status_t ar_muon_plan(const ar_muon_tensor_t* tensors, int ntensors, ar_dtype_t param_dtype,
                          ar_dtype_t grad_dtype, void* plan, size_t bytes);
 
-/* Bytes of device memory (256-byte aligned, any content) that a step on this
- * plan works in: about 8 an element, 8 for each of the shorter sides' squares,
- * and up to 34 MB for products whose sums several blocks share. */
+/* Bytes of device memory (256-byte aligned, any content) for a step on this plan
+ * to work in: 8 an element and 8 for each of the shorter sides' squares, all
+ * sides rounded up to a multiple of 64, or of 128 from 256 tiles of 128 x 128 in
+ * all on (so a matrix of 16 x 4,096 has that of 64 or 128 rows), and up to 34 MB
+ * for products whose sums several blocks share. */
 size_t ar_muon_workspace(const void* plan);
+
+/* How many of them a step reads or writes: all, or none where every matrix has at
+ * most 128 rows and 128 columns.  With none, any address that is aligned so, for
+ * instance the device plan's, may be passed as the workspace. */
+size_t ar_muon_workspace_used(const void* plan);
 
 /* One step in place, per matrix, with G = grad_scale g:
  *   m' = momentum m + G;   u = G + momentum m' (nesterov) or m'

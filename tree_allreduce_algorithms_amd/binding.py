@@ -113,6 +113,7 @@ SIGNATURES = {
     "ar_muon_plan_bytes": (_SZ, [ctypes.POINTER(MuonTensor), _I, _I, _I]),
     "ar_muon_plan": (_I, [ctypes.POINTER(MuonTensor), _I, _I, _I, _VP, _SZ]),
     "ar_muon_workspace": (_SZ, [_VP]),
+    "ar_muon_workspace_used": (_SZ, [_VP]),
     "ar_muon_step": (_I, [_VP, _VP, _VP, ctypes.POINTER(MuonStep), _VP]),
     "ar_debug_fail_launch": (_I, [_I]),
 }

@@ -426,6 +426,11 @@ size_t ar_muon_workspace(const void* plan) {
   return plan_ok(h) ? h->workspace : 0;
 }
 
+size_t ar_muon_workspace_used(const void* plan) {
+  const MuonHead* h = static_cast<const MuonHead*>(plan);
+  return plan_ok(h) && h->longest == 0 ? h->workspace : 0;
+}
+
 ar_status_t ar_muon_step(const void* plan, void* device_plan, void* workspace, const ar_muon_step_t* s,
                          hipStream_t stream) {
   const MuonHead* h = static_cast<const MuonHead*>(plan);

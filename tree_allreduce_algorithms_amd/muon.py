@@ -36,10 +36,14 @@ class Muon:
     multiplies every gradient first, e.g. ``1 / N`` where they are sums over N
     ranks.
 
-    The object keeps about 8 bytes an element, 8 for each element of the shorter
-    sides' squares, and up to 34 MB more on the GPU to work in, which the steps
-    share: they must be ordered.  A step may be captured into a graph, whose replays repeat
-    it with its ``lr`` and are ordered with the other steps by the caller.
+    The object keeps memory on the GPU to work in, which the steps share: they
+    must be ordered.  It is 8 bytes an element and 8 for each element of the
+    shorter sides' squares, for all matrices at once, sides rounded up to a
+    multiple of 64, or of 128 from 256 tiles of 128 x 128 in all on, and up to
+    34 MB more; none where no matrix has more than 128 rows or columns.  The
+    plan takes some 300 bytes a matrix or more.  A step may be captured into a
+    graph, whose replays repeat it with its ``lr`` and are ordered with the
+    other steps by the caller.
     """
 
     def __init__(self, params, grads, copies=None, *, state=None, momentum=0.95, nesterov=True,
@@ -94,7 +98,8 @@ class Muon:
         self._dev = dev
         with binding._on_device(dev):
             self._device = torch.frombuffer(self._host, dtype=torch.uint8).to(params[0].device)
-            self._workspace = torch.empty(lib().ar_muon_workspace(self._host), dtype=torch.uint8,
+            # (a step takes an address also where it works in none)
+            self._workspace = torch.empty(max(lib().ar_muon_workspace_used(self._host), 256), dtype=torch.uint8,
                                           device=params[0].device)
         self._host_ptr, self._device_ptr = ctypes.addressof(self._host), self._device.data_ptr()
         self._workspace_ptr = self._workspace.data_ptr()
