@@ -462,7 +462,10 @@ ar_status_t ar_muon_step(const void* plan, void* device_plan, void* workspace, c
   a.lr = static_cast<float>(s->lr);
   a.lr_wd = static_cast<float>(s->lr * s->weight_decay);
   a.eps = s->eps;
-  a.rms = static_cast<float>(s->match_rms);
+  // (0 is none, so what float32 cannot hold becomes the smallest that it can)
+  a.rms = s->match_rms > 0
+              ? std::max(static_cast<float>(s->match_rms), std::numeric_limits<float>::denorm_min())
+              : 0.0f;
   a.nesterov = s->nesterov != 0;
   a.last = 0;
   a.from = 0;
