@@ -562,7 +562,8 @@ ar_status_t ar_expert_weight_grad(const ar_expert_rows_t* rows, const void* dy, 
 
 /* out [tokens][size] (contiguous): out_t = the sum over the choices k of token t
  * that have a row of weights[t][k] * y_row, in the order of k (weights NULL: 1).
- * y has `pairs` rows, y_stride apart; position is [tokens][top_k]. */
+ * y has `pairs` rows, y_stride apart; position is [tokens][top_k].
+ * AR_ERROR_UNSUPPORTED also for top_k > 2^31 - 4. */
 ar_status_t ar_expert_combine(const void* y, size_t y_stride, size_t pairs, size_t size,
                               ar_dtype_t dtype, const int32_t* position, const float* weights,
                               size_t tokens, int top_k, void* out, hipStream_t stream);

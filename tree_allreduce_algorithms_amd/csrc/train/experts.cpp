@@ -196,6 +196,8 @@ ar_status_t ar_expert_combine(const void* y, size_t y_stride, size_t pairs, size
                               void* out, hipStream_t stream) {
   const ar_status_t st = check_sums(y, y_stride, pairs, size, dtype, position, tokens, top_k);
   if (st != AR_SUCCESS) return st;
+  // the kernel counts the choices by up to four at a time in an int
+  if (static_cast<uint64_t>(top_k) > kMost - 3) return AR_ERROR_UNSUPPORTED;
   if (tokens == 0) return AR_SUCCESS;
   if (out == nullptr || !aligned(out, 2) || !aligned(weights, 4) || !fits(out, tokens, size, size, 2))
     return AR_ERROR_INVALID_ARGUMENT;
