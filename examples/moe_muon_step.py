@@ -55,8 +55,9 @@ class Trainer:
         self.grads = [[torch.zeros_like(w) for _ in range(RANKS)] for w in start]
         own = [slice(r * OWN, (r + 1) * OWN) for r in range(RANKS)]
         shards = lambda ts: [t[s] for matrix in ts for t, s in zip(matrix, own)]  # noqa: E731
+        # match_rms, since the matrices stand as [in, out]: the other scale is for [out, in]
         self.muon = ar.Muon([w[s].clone() for w in start for s in own], shards(self.grads), shards(self.copies),
-                            momentum=0.9, grad_scale=1.0 / RANKS)
+                            momentum=0.9, match_rms=0.2, grad_scale=1.0 / RANKS)
         # the router is small: its gradient's sum is updated once and copied
         self.router = torch.randn(DIM, EXPERTS, device=device) * DIM ** -0.5
         self.router_grads = [torch.zeros_like(self.router) for _ in range(RANKS)]
@@ -100,7 +101,7 @@ class Trainer:
 def main(steps=100):
     trainer = Trainer()
     for k in range(steps):
-        error, balance = trainer.step(lr=0.05 * (1 - k / steps))
+        error, balance = trainer.step(lr=0.03 * (1 - k / steps))
         if k % max(1, steps // 10) == 0 or k == steps - 1:
             print(f"step {k:4d}  error {float(error):.4f}  balance {float(balance):.3f}", flush=True)
     return float(error)

@@ -607,7 +607,8 @@ typedef struct {
   double eps;            /* added to the norm */
   double weight_decay;
   double grad_scale;     /* the gradients' factor, e.g. 1/N for a mean over N ranks */
-  double match_rms;      /* 0: s = sqrt(max(1, rows / cols)); else s = match_rms sqrt(max(rows, cols)) */
+  double match_rms;      /* 0: s = sqrt(max(1, rows / cols)), for matrices that stand as [out][in];
+                          * else s = match_rms sqrt(max(rows, cols)), for either layout */
   int nesterov;
   int ns_steps;          /* 1 to 32 */
 } ar_muon_step_t;

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import tree_allreduce_algorithms_amd as ar
-from test_gpu_muon import gpu_ready  # noqa: F401
+from test_gpu_muon import H, HYPER, expected, gpu_ready  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -19,3 +19,24 @@ def test_a_match_rms_below_float32_moves_nothing(shape):
     assert torch.equal(p, old)
     ar.Muon([p], [g], match_rms=1e-50, weight_decay=0.5).step(0.5)
     assert torch.equal(p, old * 0.75)
+
+
+@pytest.mark.parametrize("shape", [(64, 96), (100, 30), (700, 200)])
+def test_match_rms_is_the_same_for_either_layout(shape):
+    """The update of [in, out] is that of [out, in], turned: each is within its
+    bound of the formula, whose two results are the same."""
+    gen = torch.Generator("cuda").manual_seed(6)
+    p = torch.randn(shape, device="cuda", generator=gen)
+    g = torch.randn(shape, device="cuda", generator=gen)
+    q, gq = p.t().contiguous(), g.t().contiguous()
+    h = {**HYPER, "lr": 0.02, "match_rms": 0.2}
+    results = []
+    for w, grad in ((p, g), (q, gq)):
+        want, _, bound = expected(w.cpu(), grad.cpu(), torch.zeros(w.shape), h)
+        ar.Muon([w], [grad], weight_decay=h["weight_decay"], match_rms=0.2).step(0.02)
+        bound += H * float(want.norm())
+        assert float((w.cpu().double() - want).norm()) <= bound
+        results.append((want, bound))
+    (a, bound), (b, other) = results
+    assert float((p - q.t()).double().norm()) <= bound + other
+    assert float((a - b.t()).norm()) <= 1e-10 * float(a.norm())      # products of float64 in another order

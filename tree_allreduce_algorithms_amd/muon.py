@@ -32,9 +32,12 @@ class Muon:
     like ``grads``), updated in place; by default it starts at zero.  A step
     moves a matrix by ``lr`` times ``sqrt(max(1, rows / cols))``, or with
     ``match_rms`` times ``match_rms * sqrt(max(rows, cols))`` (0.2 gives updates
-    of about AdamW's size), along the orthogonalised momentum.  ``grad_scale``
-    multiplies every gradient first, e.g. ``1 / N`` where they are sums over N
-    ranks.
+    of about AdamW's size), along the orthogonalised momentum.  The first is
+    meant for weights that stand as [out, in], as torch's linear layers keep
+    theirs; for [in, out], as in the experts' [experts, in, out], it gives its
+    factor to the wrong ones of two matrices.  Take ``match_rms`` there, which is
+    the same for both.  ``grad_scale`` multiplies every gradient first, e.g.
+    ``1 / N`` where they are sums over N ranks.
 
     The object keeps memory on the GPU to work in, which the steps share: they
     must be ordered.  It is 8 bytes an element and 8 for each element of the
