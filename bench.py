@@ -117,10 +117,10 @@ KERNEL_FILE = {  # kernel -> the source file that defines it
     "adamw8_step_kernel": "train/adamw_kernels.hip",
     "adamw_dequantize_kernel": "train/adamw_kernels.hip",
     "route_kernel": "train/route_kernels.hip", "route_grad_kernel": "train/route_kernels.hip",
-    "order_place": "train/experts_kernels.hip", "combine": "train/experts_kernels.hip",
-    "combine_grad": "train/experts_kernels.hip",
+    "order_count": "train/experts_kernels.hip", "order_place": "train/experts_kernels.hip",
+    "combine": "train/experts_kernels.hip", "combine_grad": "train/experts_kernels.hip",
     "expert_product": "train/expert_products.hip", "expert_product_thin": "train/expert_products.hip",
-    "expert_weight_grad": "train/expert_products.hip",
+    "expert_weight_grad": "train/expert_products.hip", "add_parts": "train/expert_products.hip",
     "muon_whole": "train/muon_kernels.hip", "muon_momentum": "train/muon_kernels.hip",
     "muon_start": "train/muon_kernels.hip", "muon_square": "train/muon_kernels.hip",
     "muon_apply": "train/muon_kernels.hip",

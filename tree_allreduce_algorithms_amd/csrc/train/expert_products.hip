@@ -97,8 +97,10 @@ using Large = Tile<128, 256, 2, 4, 32, 4, 3>;
 using Huge = Tile<256, 256, 2, 4, 64, 2, 2>;
 using LargeGrad = Tile<128, 256, 2, 4, 32, 4, 2>;
 // Two steps under way for the rows of many experts, of which few come from L2: 131,072
-// pairs of 128 experts, 2,048 x 1,024, 774 us instead of 804; but 16,384 of 16, 2,048 x
-// 2,048, 205 instead of 195.
+// pairs of 128 experts, 2,048 x 1,024, 785 us instead of 826.  Where an expert has fewer
+// rows or a smaller matrix they cost 2 % (32 and 64 experts, 32,768 pairs, 1,024 x 2,048,
+// 202 instead of 199 and 228 instead of 222), for 16 experts 9 % (16,384 pairs, 2,048 x
+// 2,048, 202 instead of 185).
 using DeepGrad = Tile<128, 256, 2, 4, 32, 4, 3>;
 using Middle = Tile<128, 128, 2, 2, 64, 2, 2>;
 // The weights' gradient of odd sizes: its blocks wait for loads and stores, so many
@@ -668,10 +670,13 @@ template <class T> uint64_t weight_grad_tiles(uint64_t in, uint64_t out) {
   return (in + T::M - 1) / T::M * tiles_n<T>(out);
 }
 
-// The XCDs that share an expert's tiles of the weights' gradient.  32,768 pairs of 64
-// experts, 1,024 x 2,048, 218 us with half of them, 243 with all; 131,072 of 256,
-// 1,024 x 512, 232 and 269; but 16,384 of 16, 2,048 x 2,048, whose rows are uneven, 185
-// and 173, and 131,072 of 128, 2,048 x 1,024, which matrix instructions bind, 874 and 864.
+// The XCDs that share an expert's tiles of the weights' gradient, half or all, with one
+// step under way: 32 experts, 32,768 pairs, 1,024 x 2,048, 199 us and 215 (even rows
+// 173 and 187); 64 experts 222 and 243; 131,072 pairs of 256, 1,024 x 512, 240 and 283;
+// of 128, 2,048 x 1,024, 826 and 775, but 785 with two steps (see DeepGrad).  Below 32
+// experts half is no slower either on a later card (16,384 pairs of 16, 2,048 x 2,048,
+// 185 and 186; an earlier one had 185 and 173; 65,536 pairs of 16 327 and 355), so 32 is
+// a border on the safe side, not where the two cross.
 constexpr int kManyExperts = 32;
 uint32_t weight_grad_xcds(int experts) { return experts >= kManyExperts ? kXcds / 2 : kXcds; }
 uint64_t weight_grad_blocks(int experts, uint64_t tiles) {
@@ -684,7 +689,9 @@ uint64_t weight_grad_blocks(int experts, uint64_t tiles) {
 // pairs 33 either way.
 constexpr uint64_t kFull = 256;
 
-// Which tiles a product has, by the rows of an expert if all have as many.
+// Which tiles a product has, by the rows of an expert if all have as many (the counts
+// stay on the GPU): 4,096 pairs of 256 experts that all go to 16 take 90 us in 16 x 64,
+// 25 if only those 16 are there.
 enum class Rows { kFew, kSome, kMany, kMost };
 Rows rows_of_product(uint64_t pairs, int experts, uint64_t out, bool by_out, bool direct) {
   const uint64_t each = pairs / (static_cast<uint64_t>(experts) < pairs ? experts : pairs);
